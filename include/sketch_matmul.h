@@ -211,6 +211,143 @@ size_t sketch_matmul_bwd_workspace(int64_t m, int64_t n, int64_t d, int b, int g
                                    int io_dtype, int lut_dtype);
 
 /*
+ * 8-bit activation checkpoints: what a layer keeps of its input X for the
+ * table gradient, at 8.25 bits per value instead of 16 (or 32).
+ *   codes  int8  [m][d]       q
+ *   scales uint8 [m][d / 32]  s, one per block of 32 columns
+ *   value = q * 2^(s - 127)
+ * With M the block's largest magnitude, e = s - 127 is the smallest integer
+ * with 127 * 2^e >= M, clamped to [-24, 9] for F16 and [-126, 121] for BF16
+ * and F32 (so that every value is a finite number of that dtype and exact in
+ * it); q = x * 2^-e rounded to nearest even and clamped to [-127, 127]. A
+ * value is off by at most half a step 2^e, except in F16 blocks with
+ * M > 65024 (and BF16 / F32 blocks with M > 127 * 2^121), whose largest
+ * values are off by less than one step. A block that holds an infinity or a
+ * NaN is stored as s = 255, q = 0 and reads back as NaN in all its columns.
+ *   sketch_act_quant    X [m][d] x_dtype (F32, F16, BF16) -> codes, scales
+ *   sketch_act_dequant  codes, scales -> X [m][d] x_dtype (the dtype that was
+ *                       quantised; a narrower one rounds)
+ * d >= 32 and a multiple of 32, m >= 0 (0 is a no-op), m * d <= 2^42. All
+ * pointers 16-byte aligned; outputs must not overlap inputs or each other.
+ */
+int sketch_act_quant(const void* X, int x_dtype, int64_t m, int64_t d,
+                     int8_t* codes, uint8_t* scales, hipStream_t stream);
+
+int sketch_act_dequant(const int8_t* codes, const uint8_t* scales, int64_t m, int64_t d,
+                       void* X, int x_dtype, hipStream_t stream);
+
+/*
+ * sketch_matmul_bwd with X given as its 8-bit checkpoint (the values above in
+ * io_dtype, exact): same results as dequantising into X first. codes and
+ * scales may be NULL when dLUT is NULL. workspace: at least
+ * sketch_matmul_bwd_ckpt_workspace(...) bytes (that of sketch_matmul_bwd, and
+ * one X [m][d] in io_dtype that lives during the call only; need_dlut = 0
+ * when dLUT is NULL).
+ */
+int sketch_matmul_bwd_ckpt(const void* dY, const int8_t* codes, const uint8_t* scales, int io_dtype,
+                           const uint8_t* idx_packed, const void* lut, int lut_dtype,
+                           int64_t m, int64_t n, int64_t d, int b, int gpr,
+                           float* dX, float* dLUT, int accumulate,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t sketch_matmul_bwd_ckpt_workspace(int64_t m, int64_t n, int64_t d, int b, int gpr,
+                                        int io_dtype, int lut_dtype, int need_dlut);
+
+/*
+ * The norm in front of a sketched layer, over the rows of X [m][d]:
+ *   SKM_NORM_LAYER  mu = mean(x), r = 1 / sqrt(mean((x - mu)^2) + eps)
+ *   SKM_NORM_RMS    mu = 0,       r = 1 / sqrt(mean(x^2) + eps)
+ *   xh = (x - mu) * r,  Y = xh * weight + bias
+ * Statistics and sums in fp32; Y is rounded once to x_dtype.
+ *   X, Y           [m][d] x_dtype (F32, F16 or BF16)
+ *   weight, bias   [d] param_dtype (F32 or x_dtype); NULL = ones / zeros
+ *   mean, rstd     [m] fp32, written (mean may be NULL for SKM_NORM_RMS,
+ *                  where nothing is written to it)
+ *   codes, scales  both or neither: the 8-bit checkpoint of Y as stored, in
+ *                  the same pass (d a multiple of 32)
+ * 1 <= d <= 65536 of any width (whole 8-column chunks are the fast case),
+ * 0 <= m < 2^31, eps >= 0. Pointers 16-byte aligned; outputs must not overlap
+ * inputs or each other.
+ */
+enum { SKM_NORM_RMS = 0, SKM_NORM_LAYER = 1 };
+
+int sketch_norm_fwd(const void* X, int x_dtype, const void* weight, const void* bias, int param_dtype,
+                    int64_t m, int64_t d, int kind, float eps,
+                    void* Y, float* mean, float* rstd, int8_t* codes, uint8_t* scales,
+                    hipStream_t stream);
+
+/*
+ * Its backward pass, from mean and rstd as written by sketch_norm_fwd (mean
+ * NULL and unread for SKM_NORM_RMS), g = dY * weight:
+ *   dX = r * (g - xh * mean(g * xh) - [layer] mean(g))   [m][d] x_dtype
+ *   dweight = sum over rows of dY * xh                    [d] fp32
+ *   dbias   = sum over rows of dY                         [d] fp32
+ * each NULL = skip; accumulate == 1 adds to dweight and dbias. dY [m][d] in
+ * dy_dtype (F32, e.g. the dX of sketch_matmul_bwd, or x_dtype). X is given
+ * either as X [m][d] x_dtype, or (X NULL) as its 8-bit checkpoint codes and
+ * scales (d a multiple of 32). The row sums are taken in a fixed order
+ * (deterministic). workspace: sketch_norm_bwd_workspace(m, d) bytes when
+ * dweight or dbias is given. With m == 0 and accumulate == 0 dweight and
+ * dbias are written as zeros. Sizes and alignment as for sketch_norm_fwd.
+ */
+int sketch_norm_bwd(const void* dY, int dy_dtype, const void* X, int x_dtype,
+                    const int8_t* codes, const uint8_t* scales,
+                    const void* weight, int param_dtype, const float* mean, const float* rstd,
+                    int64_t m, int64_t d, int kind,
+                    void* dX, float* dweight, float* dbias, int accumulate,
+                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t sketch_norm_bwd_workspace(int64_t m, int64_t d);
+
+/*
+ * Softmax cross entropy of a sketched vocabulary projection Z = X * W^T (W the
+ * sketched head of n words), without storing the logits Z:
+ *   lse[t]  = log sum_v exp(Z[t][v])
+ *   loss[t] = lse[t] - Z[t][targets[t]]
+ *   targets [m] int64 (device). A token whose target is ignore_index is left
+ *           out: its loss and lse are 0 and its row of X is not used (it may
+ *           hold infinities or NaN). Any other target outside [0, n) gives
+ *           loss NaN and NaN gradients.
+ *   loss, lse [m] fp32.
+ * Dtype pairs (x_dtype, lut_dtype): (F16, F16), (BF16, F16), (BF16, BF16)
+ * (matrix cores, fp32 logits and statistics; the (BF16, F16) range rule at
+ * the top applies); others return SKM_EUNSUPPORTED. m < 2^31, d <= 2^20; m == 0 is
+ * a no-op. targets 8-byte, other pointers 16-byte aligned. workspace: at least
+ * sketch_xent_fwd_workspace(...) bytes (8 bytes per token and 256 words, and
+ * 8 to 12 per token).
+ */
+int sketch_xent_fwd(const void* X, int x_dtype, const uint8_t* idx_packed, const void* lut, int lut_dtype,
+                    const int64_t* targets, int64_t ignore_index,
+                    int64_t m, int64_t n, int64_t d, int b, int gpr,
+                    float* loss, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t sketch_xent_fwd_workspace(int64_t m, int64_t n, int64_t d, int b, int gpr, int x_dtype, int lut_dtype);
+
+/*
+ * Its backward pass, from lse as written by sketch_xent_fwd and the gradient
+ * dloss [m] fp32 of every token's loss (e.g. 1 / count for a mean; read only
+ * for tokens that are not ignored):
+ *   dZ[t][v] = dloss[t] * (exp(Z[t][v] - lse[t]) - [v == targets[t]])
+ *   dX   = dZ * W              [m][d] x_dtype, zeros for ignored tokens
+ *   dLUT = table gradient      [n][gpr][2^b] fp32; accumulate == 1 adds to it
+ * each NULL = skip. The logits are recomputed a piece of the vocabulary at a
+ * time. dX is the fp32 sum of products with dZ rounded once to the tables'
+ * dtype; dLUT takes dZ to at least 17 bits. Both are deterministic (no
+ * atomics). workspace: at least sketch_xent_bwd_workspace(...) bytes (up to
+ * 256 MiB of dZ, the fp32 dX, and for dLUT one X); need_dx / need_dlut = 0
+ * where the output is NULL. With m == 0 and accumulate == 0 dLUT is written as
+ * zeros. Dtypes, sizes and alignment as for sketch_xent_fwd.
+ */
+int sketch_xent_bwd(const void* X, int x_dtype, const uint8_t* idx_packed, const void* lut, int lut_dtype,
+                    const int64_t* targets, int64_t ignore_index, const float* lse, const float* dloss,
+                    int64_t m, int64_t n, int64_t d, int b, int gpr,
+                    void* dX, float* dLUT, int accumulate,
+                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t sketch_xent_bwd_workspace(int64_t m, int64_t n, int64_t d, int b, int gpr, int x_dtype, int lut_dtype,
+                                 int need_dx, int need_dlut);
+
+/*
  * Dequantise W[i][j] = lut[i][j/G][idx[i][j]] into a dense [n][d] array of
  * lut_dtype (SpaLLM Eq. (1) with groups per row). A checking aid: the matmul
  * entry points never build W.

@@ -63,6 +63,22 @@ _SIGNATURES = {
                             _c_vp]),
     "sketch_hessian_factor_workspace": (_c_size, [_c_i64]),
     "sketch_hessian_factor": (_c_int, [_c_vp, _c_i64, ctypes.c_double, _c_vp, _c_vp, _c_size, _c_vp]),
+    "sketch_act_quant": (_c_int, [_c_vp, _c_int, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp]),
+    "sketch_act_dequant": (_c_int, [_c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_int, _c_vp]),
+    "sketch_matmul_bwd_ckpt": (_c_int, [_c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_int, _c_i64, _c_i64, _c_i64,
+                                        _c_int, _c_int, _c_vp, _c_vp, _c_int, _c_vp, _c_size, _c_vp]),
+    "sketch_matmul_bwd_ckpt_workspace": (_c_size, [_c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_int]),
+    "sketch_norm_fwd": (_c_int, [_c_vp, _c_int, _c_vp, _c_vp, _c_int, _c_i64, _c_i64, _c_int, _c_f32, _c_vp, _c_vp,
+                                 _c_vp, _c_vp, _c_vp, _c_vp]),
+    "sketch_norm_bwd": (_c_int, [_c_vp, _c_int, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_i64,
+                                 _c_i64, _c_int, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_size, _c_vp]),
+    "sketch_norm_bwd_workspace": (_c_size, [_c_i64, _c_i64]),
+    "sketch_xent_fwd": (_c_int, [_c_vp, _c_int, _c_vp, _c_vp, _c_int, _c_vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_int,
+                                 _c_int, _c_vp, _c_vp, _c_vp, _c_size, _c_vp]),
+    "sketch_xent_fwd_workspace": (_c_size, [_c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_int]),
+    "sketch_xent_bwd": (_c_int, [_c_vp, _c_int, _c_vp, _c_vp, _c_int, _c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_i64,
+                                 _c_i64, _c_int, _c_int, _c_vp, _c_vp, _c_int, _c_vp, _c_size, _c_vp]),
+    "sketch_xent_bwd_workspace": (_c_size, [_c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int]),
     "sketch_status_str": (ctypes.c_char_p, [_c_int]),
     "sketch_version": (_c_int, []),
 }
@@ -465,3 +481,333 @@ def sketch_hessian_factor(H, damp: float = 0.01, out=None, workspace=None, strea
                                      ws.numel() if ws is not None else 0, _stream_ptr(stream))
     _check("sketch_hessian_factor", st)
     return out
+
+
+# --------------------------------------------------------------------------
+# 8-bit activation checkpoints, norms
+# --------------------------------------------------------------------------
+
+class _Launch:
+    """The device and stream a call runs on, current while it allocates and launches.
+
+    The tensors must share one device, which becomes current; `stream` (None = the device's current stream)
+    becomes current too, so outputs and workspaces allocated meanwhile belong to the stream that uses them.
+    Ordering the inputs before `stream` is the caller's.
+    """
+
+    __slots__ = ("device", "stream", "stack")
+
+    def __init__(self, stream, *tensors):
+        device = None
+        for t in tensors:
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise ValueError("tensors must live on the GPU")
+            if not t.is_contiguous():
+                raise ValueError("tensors must be contiguous")
+            if device is None:
+                device = t.device
+            elif t.device != device:
+                raise ValueError(f"tensors on {device} and {t.device}")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"a stream of {stream.device} for tensors on {device}")
+        self.device, self.stream, self.stack = device, stream, ()
+
+    def __enter__(self):
+        cuda = _torch().cuda
+        if self.stream is not None:
+            self.stack = (cuda.stream(self.stream),)
+        elif cuda.current_device() != self.device.index:
+            self.stack = (cuda.device(self.device),)
+        for c in self.stack:
+            c.__enter__()
+        return cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for c in self.stack:
+            c.__exit__(*exc)
+
+
+def _ptr(t):
+    """The tensor's address (None for no tensor or an empty one)."""
+    return t.data_ptr() if t is not None and t.numel() else None
+
+
+def _size(t) -> int:
+    return t.numel() * t.element_size() if t is not None else 0
+
+
+def _check_ckpt(codes, scales, m: int, d: int):
+    _expect(codes, "codes", shape=(m, d), dtypes=("int8",))
+    _expect(scales, "scales", shape=(m, d // 32), dtypes=("uint8",))
+
+
+def sketch_act_quant(X, codes=None, scales=None, stream=None) -> Tuple[object, object]:
+    """The 8-bit checkpoint of X [m, d] (f32/f16/bf16, d % 32 == 0): (codes int8 [m, d], scales uint8 [m, d/32]).
+
+    value = codes * 2^(scales - 127), one exponent per 32 columns; a block with an infinity or NaN reads back
+    as NaN. codes / scales: optional outputs.
+    """
+    torch = _torch()
+    m, d = _matrix(X, "X")
+    if d < 32 or d % 32:
+        raise ValueError(f"X has {d} columns: a checkpoint takes whole blocks of 32")
+    _check_ckpt(codes, scales, m, d)
+    with _Launch(stream, X, codes, scales) as sp:
+        if codes is None:
+            codes = torch.empty((m, d), dtype=torch.int8, device=X.device)
+        if scales is None:
+            scales = torch.empty((m, d // 32), dtype=torch.uint8, device=X.device)
+        st = lib().sketch_act_quant(_ptr(X), dtype_code(X), m, d, _ptr(codes), _ptr(scales), sp)
+    _check("sketch_act_quant", st)
+    return codes, scales
+
+
+def sketch_act_dequant(codes, scales, dtype, out=None, stream=None):
+    """X [m, d] in `dtype` from its checkpoint (exact in the dtype that was quantised)."""
+    torch = _torch()
+    m, d = _matrix(codes, "codes")
+    if d < 32 or d % 32:
+        raise ValueError(f"codes has {d} columns: a checkpoint takes whole blocks of 32")
+    _check_ckpt(codes, scales, m, d)
+    if out is None and dtype not in (torch.float32, torch.float16, torch.bfloat16):
+        raise TypeError(f"unsupported dtype {dtype}")
+    _expect(out, "out", shape=(m, d), dtypes=(str(dtype).replace("torch.", ""),))
+    with _Launch(stream, codes, scales, out) as sp:
+        if out is None:
+            out = torch.empty((m, d), dtype=dtype, device=codes.device)
+        st = lib().sketch_act_dequant(_ptr(codes), _ptr(scales), m, d, _ptr(out), dtype_code(out), sp)
+    _check("sketch_act_dequant", st)
+    return out
+
+
+def sketch_matmul_bwd_ckpt_workspace(m: int, n: int, d: int, b: int, gpr: int, io_dtype: int, lut_dtype: int,
+                                     need_dlut: bool = True) -> int:
+    """Bytes of device workspace sketch_matmul_bwd_ckpt needs for these sizes and dtypes."""
+    return int(lib().sketch_matmul_bwd_ckpt_workspace(m, n, d, b, gpr, io_dtype, lut_dtype, 1 if need_dlut else 0))
+
+
+def sketch_matmul_bwd_ckpt(dY, codes, scales, idx_packed, lut, b: int, gpr: int, need_dx: bool = True,
+                           need_dlut: bool = True, dlut_out=None, accumulate: bool = False, workspace=None,
+                           stream=None) -> Tuple[object, object]:
+    """(dX, dLUT) of the sketched matmul, both fp32, with X given as its 8-bit checkpoint.
+
+    dY [m, n] (its dtype is the activations'), codes [m, d] int8 and scales [m, d/32] uint8 of
+    sketch_act_quant or sketch_norm_fwd; the rest as for sketch_matmul_bwd.
+    """
+    torch = _torch()
+    m, n = _matrix(dY, "dY")
+    _, d = _matrix(codes, "codes")
+    _expect(dY, "dY", dtypes=_FLOAT_DTYPES)
+    _check_sketch(idx_packed, lut, n, d, b, gpr)
+    _check_ckpt(codes, scales, m, d)
+    K = 1 << b
+    _expect(dlut_out, "dlut_out", shape=(n, gpr, K), dtypes=("float32",))
+    _expect(workspace, "workspace", dtypes=("uint8",))
+    io, lt = dtype_code(dY), dtype_code(lut)
+    with _Launch(stream, dY, codes, scales, idx_packed, lut, dlut_out, workspace) as sp:
+        dX = torch.empty((m, d), dtype=torch.float32, device=dY.device) if need_dx else None
+        dL = None
+        if need_dlut:
+            dL = dlut_out if dlut_out is not None else torch.empty((n, gpr, K), dtype=torch.float32, device=dY.device)
+        ws = _workspace(workspace, sketch_matmul_bwd_ckpt_workspace(m, n, d, b, gpr, io, lt, need_dlut), dY.device)
+        st = lib().sketch_matmul_bwd_ckpt(_ptr(dY), _ptr(codes), _ptr(scales), io, idx_packed.data_ptr(),
+                                          lut.data_ptr(), lt, m, n, d, b, gpr, _ptr(dX), _ptr(dL),
+                                          1 if accumulate else 0, _ptr(ws), _size(ws), sp)
+    _check("sketch_matmul_bwd_ckpt", st)
+    return dX, dL
+
+
+_NORM_KINDS = {"rms": 0, "layer": 1}
+
+
+def _norm_kind(kind: str) -> int:
+    if kind not in _NORM_KINDS:
+        raise ValueError(f"kind = {kind!r}: supported are 'layer' and 'rms'")
+    return _NORM_KINDS[kind]
+
+
+def _check_params(X, d: int, *named):
+    """weight / bias of a norm: [d], fp32 or X's dtype, one dtype for both. Returns its code."""
+    code = SKM_F32
+    first = None
+    for name, t in named:
+        if t is None:
+            continue
+        _expect(t, name, shape=(d,), dtypes=("float32", _dtype_name(X)))
+        if first is not None and t.dtype != first:
+            raise TypeError("weight and bias must have one dtype")
+        first = t.dtype
+        code = dtype_code(t)
+    return code
+
+
+def sketch_norm_fwd(X, weight=None, bias=None, kind: str = "layer", eps: float = 1e-5, checkpoint: bool = False,
+                    out=None, stream=None):
+    """(Y, mean, rstd, codes, scales): layer norm or rms norm of the rows of X [m, d].
+
+    Y = (x - mean) rstd weight + bias in X's dtype (f32/f16/bf16); mean (None for kind "rms") and rstd fp32 [m].
+    weight / bias: [d] fp32 or X's dtype, None = ones / zeros. checkpoint: also write the 8-bit checkpoint of Y
+    in the same pass (d % 32 == 0), else codes and scales are None.
+    """
+    torch = _torch()
+    m, d = _matrix(X, "X")
+    k = _norm_kind(kind)
+    _expect(X, "X", dtypes=_FLOAT_DTYPES)
+    pc = _check_params(X, d, ("weight", weight), ("bias", bias))
+    if checkpoint and d % 32:
+        raise ValueError(f"X has {d} columns: a checkpoint takes whole blocks of 32")
+    _expect(out, "out", shape=(m, d), dtypes=(_dtype_name(X),))
+    with _Launch(stream, X, weight, bias, out) as sp:
+        dev = X.device
+        if out is None:
+            out = torch.empty((m, d), dtype=X.dtype, device=dev)
+        mean = torch.empty(m, dtype=torch.float32, device=dev) if k else None
+        rstd = torch.empty(m, dtype=torch.float32, device=dev)
+        codes = scales = None
+        if checkpoint:
+            codes = torch.empty((m, d), dtype=torch.int8, device=dev)
+            scales = torch.empty((m, d // 32), dtype=torch.uint8, device=dev)
+        st = lib().sketch_norm_fwd(_ptr(X), dtype_code(X), _ptr(weight), _ptr(bias), pc, m, d, k, eps, _ptr(out),
+                                   _ptr(mean), _ptr(rstd), _ptr(codes), _ptr(scales), sp)
+    _check("sketch_norm_fwd", st)
+    return out, mean, rstd, codes, scales
+
+
+def sketch_norm_bwd_workspace(m: int, d: int) -> int:
+    """Bytes of device workspace sketch_norm_bwd needs for dweight / dbias of these sizes."""
+    return int(lib().sketch_norm_bwd_workspace(m, d))
+
+
+def sketch_norm_bwd(dY, X, weight, mean, rstd, kind: str = "layer", need_dx: bool = True, need_dw: bool = True,
+                    need_db: bool = True, dw_out=None, db_out=None, accumulate: bool = False, x_dtype=None,
+                    workspace=None, stream=None):
+    """(dX, dweight, dbias) of sketch_norm_fwd; None where not asked for.
+
+    X: the forward's input [m, d], or its 8-bit checkpoint as a pair (codes, scales), then x_dtype is the
+    activations' dtype (dY's if omitted). dY [m, d] fp32 or the activations' dtype; dX in the activations'
+    dtype, dweight and dbias fp32 [d] (dw_out / db_out: optional outputs, accumulate=True adds to them). mean
+    is None for kind "rms". workspace: optional uint8 buffer of sketch_norm_bwd_workspace(m, d) bytes.
+    """
+    torch = _torch()
+    k = _norm_kind(kind)
+    m, d = _matrix(dY, "dY")
+    codes = scales = None
+    if isinstance(X, (tuple, list)):
+        codes, scales = X
+        X = None
+        if d % 32:
+            raise ValueError(f"dY has {d} columns: a checkpoint takes whole blocks of 32")
+        _check_ckpt(codes, scales, m, d)
+        xt = x_dtype if x_dtype is not None else dY.dtype
+    else:
+        _expect(X, "X", shape=(m, d))
+        xt = X.dtype
+        if x_dtype is not None and x_dtype != xt:
+            raise TypeError(f"X has dtype {xt}, expected {x_dtype}")
+    like = torch.empty(0, dtype=xt)
+    _expect(like, "X", dtypes=_FLOAT_DTYPES)
+    _expect(dY, "dY", dtypes=("float32", _dtype_name(like)))
+    pc = _check_params(like, d, ("weight", weight))
+    if k and mean is None:
+        raise ValueError("a layer norm's backward needs the mean")
+    if not k:
+        mean = None
+    _expect(mean, "mean", shape=(m,), dtypes=("float32",))
+    _expect(rstd, "rstd", shape=(m,), dtypes=("float32",))
+    _expect(dw_out, "dw_out", shape=(d,), dtypes=("float32",))
+    _expect(db_out, "db_out", shape=(d,), dtypes=("float32",))
+    _expect(workspace, "workspace", dtypes=("uint8",))
+    with _Launch(stream, dY, X, codes, scales, weight, mean, rstd, dw_out, db_out, workspace) as sp:
+        dev = dY.device
+        dX = torch.empty((m, d), dtype=xt, device=dev) if need_dx else None
+        dw = db = None
+        if need_dw:
+            dw = dw_out if dw_out is not None else torch.empty(d, dtype=torch.float32, device=dev)
+        if need_db:
+            db = db_out if db_out is not None else torch.empty(d, dtype=torch.float32, device=dev)
+        need = sketch_norm_bwd_workspace(m, d) if need_dw or need_db else 0
+        ws = _workspace(workspace, need, dev)
+        st = lib().sketch_norm_bwd(_ptr(dY), dtype_code(dY), _ptr(X), dtype_code(like), _ptr(codes), _ptr(scales),
+                                   _ptr(weight), pc, _ptr(mean), _ptr(rstd), m, d, k, _ptr(dX), _ptr(dw), _ptr(db),
+                                   1 if accumulate else 0, _ptr(ws), _size(ws), sp)
+    _check("sketch_norm_bwd", st)
+    return dX, dw, db
+
+
+# --------------------------------------------------------------------------
+# cross entropy of a sketched head
+# --------------------------------------------------------------------------
+
+def _check_xent(X, idx_packed, lut, targets, b: int, gpr: int, **vectors):
+    m, d = _matrix(X, "X")
+    n = idx_packed.shape[0]
+    _expect(X, "X", dtypes=("float16", "bfloat16"))
+    _check_sketch(idx_packed, lut, n, d, b, gpr)
+    _expect(lut, "lut", dtypes=("float16", "bfloat16"))
+    _expect(targets, "targets", shape=(m,), dtypes=("int64",))
+    for name, t in vectors.items():
+        _expect(t, name, shape=(m,), dtypes=("float32",))
+    return m, n, d
+
+
+def sketch_xent_fwd_workspace(m: int, n: int, d: int, b: int, gpr: int, x_dtype: int, lut_dtype: int) -> int:
+    """Bytes of device workspace sketch_xent_fwd needs for these sizes and dtypes."""
+    return int(lib().sketch_xent_fwd_workspace(m, n, d, b, gpr, x_dtype, lut_dtype))
+
+
+def sketch_xent_fwd(X, idx_packed, lut, targets, b: int, gpr: int, ignore_index: int = -100, workspace=None,
+                    stream=None) -> Tuple[object, object]:
+    """(loss, lse), fp32 [m]: softmax cross entropy of the logits X W^T, which are never stored.
+
+    X [m, d] f16/bf16, idx_packed [n, d*b/8] uint8 and lut [n, gpr, 2^b] the sketched head of n words (f16 X
+    needs f16 tables), targets [m] int64. Tokens whose target is ignore_index have loss and lse 0; any other
+    target outside [0, n) gives loss NaN.
+    """
+    torch = _torch()
+    m, n, d = _check_xent(X, idx_packed, lut, targets, b, gpr)
+    _expect(workspace, "workspace", dtypes=("uint8",))
+    xc, lc = dtype_code(X), dtype_code(lut)
+    with _Launch(stream, X, idx_packed, lut, targets, workspace) as sp:
+        loss = torch.empty(m, dtype=torch.float32, device=X.device)
+        lse = torch.empty(m, dtype=torch.float32, device=X.device)
+        ws = _workspace(workspace, sketch_xent_fwd_workspace(m, n, d, b, gpr, xc, lc), X.device)
+        st = lib().sketch_xent_fwd(_ptr(X), xc, idx_packed.data_ptr(), lut.data_ptr(), lc, _ptr(targets), ignore_index,
+                                   m, n, d, b, gpr, _ptr(loss), _ptr(lse), _ptr(ws), _size(ws), sp)
+    _check("sketch_xent_fwd", st)
+    return loss, lse
+
+
+def sketch_xent_bwd_workspace(m: int, n: int, d: int, b: int, gpr: int, x_dtype: int, lut_dtype: int,
+                              need_dx: bool = True, need_dlut: bool = True) -> int:
+    """Bytes of device workspace sketch_xent_bwd needs for these sizes and dtypes."""
+    return int(lib().sketch_xent_bwd_workspace(m, n, d, b, gpr, x_dtype, lut_dtype, 1 if need_dx else 0,
+                                               1 if need_dlut else 0))
+
+
+def sketch_xent_bwd(X, idx_packed, lut, targets, lse, dloss, b: int, gpr: int, ignore_index: int = -100,
+                    need_dx: bool = True, need_dlut: bool = True, dlut_out=None, accumulate: bool = False,
+                    workspace=None, stream=None) -> Tuple[object, object]:
+    """(dX, dLUT) of sketch_xent_fwd's losses: dX [m, d] in X's dtype, dLUT fp32 [n, gpr, 2^b]; None if not asked.
+
+    lse [m] as sketch_xent_fwd gave it, dloss [m] fp32 the gradient of every token's loss. dlut_out: optional
+    fp32 [n, gpr, 2^b] to write (accumulate=True adds to it). The other arguments are the forward's.
+    """
+    torch = _torch()
+    m, n, d = _check_xent(X, idx_packed, lut, targets, b, gpr, lse=lse, dloss=dloss)
+    K = 1 << b
+    _expect(dlut_out, "dlut_out", shape=(n, gpr, K), dtypes=("float32",))
+    _expect(workspace, "workspace", dtypes=("uint8",))
+    xc, lc = dtype_code(X), dtype_code(lut)
+    with _Launch(stream, X, idx_packed, lut, targets, lse, dloss, dlut_out, workspace) as sp:
+        dX = torch.empty((m, d), dtype=X.dtype, device=X.device) if need_dx else None
+        dL = None
+        if need_dlut:
+            dL = dlut_out if dlut_out is not None else torch.empty((n, gpr, K), dtype=torch.float32, device=X.device)
+        ws = _workspace(workspace, sketch_xent_bwd_workspace(m, n, d, b, gpr, xc, lc, need_dx, need_dlut), X.device)
+        st = lib().sketch_xent_bwd(_ptr(X), xc, idx_packed.data_ptr(), lut.data_ptr(), lc, _ptr(targets), ignore_index,
+                                   _ptr(lse), _ptr(dloss), m, n, d, b, gpr, _ptr(dX), _ptr(dL),
+                                   1 if accumulate else 0, _ptr(ws), _size(ws), sp)
+    _check("sketch_xent_bwd", st)
+    return dX, dL

@@ -289,6 +289,261 @@ int sketch_matmul_bwd_noalloc(const void* dY, const void* X, int io_dtype, const
                            ws ? kScratchBytes : 0, stream);
 }
 
+// ---- 8-bit activation checkpoints ----------------------------------------------
+
+static int check_ckpt_shape(int64_t m, int64_t d) {
+  if (m < 0 || d < 32 || d % 32 != 0) return SKM_EINVAL;
+  // the streaming kernels take 2048 values per block; m * d <= 2^42 keeps the grid below 2^31
+  if (m > (int64_t(1) << 31) || d > (int64_t(1) << 31) || (m > 0 && d > (int64_t(1) << 42) / m)) return SKM_EINVAL;
+  return SKM_OK;
+}
+
+int sketch_act_quant(const void* X, int x_dtype, int64_t m, int64_t d, int8_t* codes, uint8_t* scales,
+                     hipStream_t stream) {
+  int st = check_ckpt_shape(m, d);
+  if (st != SKM_OK) return st;
+  if (!valid_dtype(x_dtype)) return SKM_EUNSUPPORTED;
+  if (m == 0) return SKM_OK;
+  if (!X || !codes || !scales) return SKM_EINVAL;
+  if (!aligned16(X) || !aligned16(codes) || !aligned16(scales)) return SKM_EALIGN;
+  const Range x{X, m * d * elem_bytes(x_dtype)}, c{codes, m * d}, s{scales, m * d / 32};
+  if (overlap(x, c) || overlap(x, s) || overlap(c, s)) return SKM_EALIAS;
+  return status_of(skm::launch_act_quant(X, x_dtype, m * d, codes, scales, stream));
+}
+
+int sketch_act_dequant(const int8_t* codes, const uint8_t* scales, int64_t m, int64_t d, void* X, int x_dtype,
+                       hipStream_t stream) {
+  int st = check_ckpt_shape(m, d);
+  if (st != SKM_OK) return st;
+  if (!valid_dtype(x_dtype)) return SKM_EUNSUPPORTED;
+  if (m == 0) return SKM_OK;
+  if (!X || !codes || !scales) return SKM_EINVAL;
+  if (!aligned16(X) || !aligned16(codes) || !aligned16(scales)) return SKM_EALIGN;
+  const Range x{X, m * d * elem_bytes(x_dtype)};
+  if (overlap(x, {codes, m * d}) || overlap(x, {scales, m * d / 32})) return SKM_EALIAS;
+  return status_of(skm::launch_act_dequant(codes, scales, m * d, X, x_dtype, stream));
+}
+
+// Workspace of the backward from a checkpoint: [X in io_dtype, 256-byte
+// aligned] (read by the table gradient), then sketch_matmul_bwd's
+static size_t ckpt_x_bytes(int64_t m, int64_t d, int io_dtype, int need_dlut) {
+  return need_dlut && m > 0 ? align256((size_t)m * (size_t)d * elem_bytes(io_dtype)) : 0;
+}
+
+size_t sketch_matmul_bwd_ckpt_workspace(int64_t m, int64_t n, int64_t d, int b, int gpr, int io_dtype, int lut_dtype,
+                                        int need_dlut) {
+  if (check_shape(m, n, d, b, gpr) != SKM_OK || check_ckpt_shape(m, d) != SKM_OK ||
+      !supported_pair(io_dtype, lut_dtype))
+    return 0;
+  return ckpt_x_bytes(m, d, io_dtype, need_dlut) +
+         sketch_matmul_bwd_workspace(m, n, d, b, gpr, io_dtype, lut_dtype);
+}
+
+int sketch_matmul_bwd_ckpt(const void* dY, const int8_t* codes, const uint8_t* scales, int io_dtype,
+                           const uint8_t* idx_packed, const void* lut, int lut_dtype, int64_t m, int64_t n, int64_t d,
+                           int b, int gpr, float* dX, float* dLUT, int accumulate, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream) {
+  int st = check_shape(m, n, d, b, gpr);
+  if (st == SKM_OK) st = check_ckpt_shape(m, d);
+  if (st != SKM_OK) return st;
+  if (!supported_pair(io_dtype, lut_dtype)) return SKM_EUNSUPPORTED;
+  const size_t xb = ckpt_x_bytes(m, d, io_dtype, dLUT != nullptr);
+  if (xb == 0)
+    return sketch_matmul_bwd(dY, nullptr, io_dtype, idx_packed, lut, lut_dtype, m, n, d, b, gpr, dX, dLUT, accumulate,
+                             workspace, workspace_bytes, stream);
+  if (!codes || !scales || !dY || !idx_packed || !lut) return SKM_EINVAL;
+  if (accumulate != 0 && accumulate != 1) return SKM_EINVAL;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(dY) || !aligned16(idx_packed) || !aligned16(lut) ||
+      !aligned16(dX) || !aligned16(dLUT) || !aligned16(workspace))
+    return SKM_EALIGN;
+  const size_t need = sketch_matmul_bwd_ckpt_workspace(m, n, d, b, gpr, io_dtype, lut_dtype, 1);
+  if (workspace_bytes < need || !workspace) return SKM_EWORKSPACE;
+  // the checkpoint against every buffer that is written, and X's copy against
+  // what sketch_matmul_bwd writes or reads (it checks the rest of its buffers,
+  // but only after X has been written)
+  const int64_t K = int64_t(1) << b;
+  const int xs = elem_bytes(io_dtype), ls = elem_bytes(lut_dtype);
+  const Range w[3] = {{workspace, (int64_t)need}, {dX, m * d * 4}, {dLUT, n * gpr * K * 4}};
+  const Range r[5] = {{codes, m * d}, {scales, m * d / 32}, {dY, m * n * xs}, {idx_packed, n * d * b / 8},
+                      {lut, n * gpr * K * ls}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range& in : r)
+      if (overlap(w[i], in)) return SKM_EALIAS;
+    for (int j = i + 1; j < 3; ++j)
+      if (overlap(w[i], w[j])) return SKM_EALIAS;
+  }
+  st = status_of(skm::launch_act_dequant(codes, scales, m * d, workspace, io_dtype, stream));
+  if (st != SKM_OK) return st;
+  const size_t rest = workspace_bytes - xb;
+  return sketch_matmul_bwd(dY, workspace, io_dtype, idx_packed, lut, lut_dtype, m, n, d, b, gpr, dX, dLUT, accumulate,
+                           static_cast<char*>(workspace) + xb, rest, stream);
+}
+
+// ---- norms -----------------------------------------------------------------------
+
+static int check_norm(int64_t m, int64_t d, int kind, int x_dtype, int param_dtype, bool ckpt) {
+  if (m < 0 || m >= (int64_t(1) << 31) || d < 1 || d > 65536) return SKM_EINVAL;
+  if (kind != SKM_NORM_RMS && kind != SKM_NORM_LAYER) return SKM_EINVAL;
+  if (!valid_dtype(x_dtype)) return SKM_EUNSUPPORTED;
+  if (param_dtype != SKM_F32 && param_dtype != x_dtype) return SKM_EUNSUPPORTED;
+  if (ckpt && d % 32 != 0) return SKM_EINVAL;
+  return SKM_OK;
+}
+
+int sketch_norm_fwd(const void* X, int x_dtype, const void* weight, const void* bias, int param_dtype, int64_t m,
+                    int64_t d, int kind, float eps, void* Y, float* mean, float* rstd, int8_t* codes, uint8_t* scales,
+                    hipStream_t stream) {
+  if (!codes != !scales) return SKM_EINVAL;
+  int st = check_norm(m, d, kind, x_dtype, param_dtype, codes != nullptr);
+  if (st != SKM_OK) return st;
+  if (!finite_in(eps, 0.f)) return SKM_EINVAL;
+  if (m == 0) return SKM_OK;
+  if (!X || !Y || !rstd || (kind == SKM_NORM_LAYER && !mean)) return SKM_EINVAL;
+  if (kind == SKM_NORM_RMS) mean = nullptr;
+  for (const void* p : {X, weight, bias, (const void*)Y, (const void*)mean, (const void*)rstd, (const void*)codes,
+                        (const void*)scales})
+    if (!aligned16(p)) return SKM_EALIGN;
+  const int xs = elem_bytes(x_dtype), ps = elem_bytes(param_dtype);
+  const Range w[5] = {{Y, m * d * xs}, {mean, m * 4}, {rstd, m * 4}, {codes, m * d}, {scales, m * (d / 32)}};
+  const Range r[3] = {{X, m * d * xs}, {weight, d * ps}, {bias, d * ps}};
+  for (int i = 0; i < 5; ++i) {
+    for (const Range& in : r)
+      if (overlap(w[i], in)) return SKM_EALIAS;
+    for (int j = i + 1; j < 5; ++j)
+      if (overlap(w[i], w[j])) return SKM_EALIAS;
+  }
+  const skm::NormArgs a{m, d, kind, eps, weight, bias, param_dtype == SKM_F32};
+  return status_of(skm::launch_norm_fwd(a, X, x_dtype, Y, mean, rstd, codes, scales, stream));
+}
+
+size_t sketch_norm_bwd_workspace(int64_t m, int64_t d) {
+  if (m < 1 || m >= (int64_t(1) << 31) || d < 1 || d > 65536) return 0;
+  return align256(2 * skm::norm_bwd_part_bytes(m, d));
+}
+
+int sketch_norm_bwd(const void* dY, int dy_dtype, const void* X, int x_dtype, const int8_t* codes,
+                    const uint8_t* scales, const void* weight, int param_dtype, const float* mean, const float* rstd,
+                    int64_t m, int64_t d, int kind, void* dX, float* dweight, float* dbias, int accumulate,
+                    void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!codes != !scales) return SKM_EINVAL;
+  int st = check_norm(m, d, kind, x_dtype, param_dtype, codes != nullptr);
+  if (st != SKM_OK) return st;
+  if (dy_dtype != SKM_F32 && dy_dtype != x_dtype) return SKM_EUNSUPPORTED;
+  if (accumulate != 0 && accumulate != 1) return SKM_EINVAL;
+  for (const void* p : {dY, X, (const void*)codes, (const void*)scales, weight, (const void*)mean,
+                        (const void*)rstd, (const void*)dX, (const void*)dweight, (const void*)dbias,
+                        (const void*)workspace})
+    if (!aligned16(p)) return SKM_EALIGN;
+  if (m == 0) {
+    if (!accumulate && dweight) st = status_of(skm::launch_zero_f32(dweight, d, stream));
+    if (st == SKM_OK && !accumulate && dbias) st = status_of(skm::launch_zero_f32(dbias, d, stream));
+    return st;
+  }
+  if (!dX && !dweight && !dbias) return SKM_OK;
+  if (!dY || !rstd || (kind == SKM_NORM_LAYER && !mean)) return SKM_EINVAL;
+  if (!X == !codes) return SKM_EINVAL;  // exactly one form of X
+  if (kind == SKM_NORM_RMS) mean = nullptr;
+  const size_t need = dweight || dbias ? sketch_norm_bwd_workspace(m, d) : 0;
+  if (workspace_bytes < need || (need && !workspace)) return SKM_EWORKSPACE;
+  const int xs = elem_bytes(x_dtype), ps = elem_bytes(param_dtype);
+  const Range w[4] = {{dX, m * d * xs}, {dweight, d * 4}, {dbias, d * 4}, {workspace, (int64_t)need}};
+  const Range r[7] = {{dY, m * d * elem_bytes(dy_dtype)}, {X, m * d * xs}, {codes, m * d}, {scales, m * (d / 32)},
+                      {weight, d * ps}, {mean, m * 4}, {rstd, m * 4}};
+  for (int i = 0; i < 4; ++i) {
+    for (const Range& in : r)
+      if (overlap(w[i], in)) return SKM_EALIAS;
+    for (int j = i + 1; j < 4; ++j)
+      if (overlap(w[i], w[j])) return SKM_EALIAS;
+  }
+  const skm::NormArgs a{m, d, kind, 0.f, weight, nullptr, param_dtype == SKM_F32};
+  return status_of(skm::launch_norm_bwd(a, dY, dy_dtype, X, x_dtype, codes, scales, mean, rstd, dX, dweight, dbias,
+                                        accumulate, (float*)workspace, stream));
+}
+
+// ---- cross entropy of a sketched head ------------------------------------------------
+
+static int check_xent(int64_t m, int64_t n, int64_t d, int b, int gpr, int x_dtype, int lut_dtype) {
+  const int st = check_shape(m, n, d, b, gpr);
+  if (st != SKM_OK) return st;
+  if (m >= (int64_t(1) << 31) || d > (int64_t(1) << 20)) return SKM_EINVAL;
+  // (F16 activations would be rounded to the BF16 tables' 8 bits: the loss is
+  // fp32, so that pair is not provided)
+  const bool ok = (x_dtype == SKM_F16 && lut_dtype == SKM_F16) ||
+                  (x_dtype == SKM_BF16 && (lut_dtype == SKM_F16 || lut_dtype == SKM_BF16));
+  return ok ? SKM_OK : SKM_EUNSUPPORTED;
+}
+
+size_t sketch_xent_fwd_workspace(int64_t m, int64_t n, int64_t d, int b, int gpr, int x_dtype, int lut_dtype) {
+  if (m < 1 || check_xent(m, n, d, b, gpr, x_dtype, lut_dtype) != SKM_OK) return 0;
+  return skm::xent_fwd_bytes(Problem{m, n, d, b, gpr}, x_dtype, lut_dtype);
+}
+
+int sketch_xent_fwd(const void* X, int x_dtype, const uint8_t* idx_packed, const void* lut, int lut_dtype,
+                    const int64_t* targets, int64_t ignore_index, int64_t m, int64_t n, int64_t d, int b, int gpr,
+                    float* loss, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const int st = check_xent(m, n, d, b, gpr, x_dtype, lut_dtype);
+  if (st != SKM_OK) return st;
+  if (!idx_packed || !lut) return SKM_EINVAL;
+  if (m > 0 && (!X || !targets || !loss || !lse)) return SKM_EINVAL;
+  if (!aligned16(X) || !aligned16(idx_packed) || !aligned16(lut) || !aligned16(loss) || !aligned16(lse) ||
+      !aligned16(workspace) || ((uintptr_t)targets & 7u) != 0)
+    return SKM_EALIGN;
+  if (m == 0) return SKM_OK;
+  const size_t need = sketch_xent_fwd_workspace(m, n, d, b, gpr, x_dtype, lut_dtype);
+  if (workspace_bytes < need || !workspace) return SKM_EWORKSPACE;
+  const Range w[3] = {{loss, m * 4}, {lse, m * 4}, {workspace, (int64_t)need}};
+  const Range r[4] = {{X, m * d * 2}, {idx_packed, n * d * b / 8}, {lut, n * gpr * (int64_t(1) << b) * 2},
+                      {targets, m * 8}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range& in : r)
+      if (overlap(w[i], in)) return SKM_EALIAS;
+    for (int j = i + 1; j < 3; ++j)
+      if (overlap(w[i], w[j])) return SKM_EALIAS;
+  }
+  const skm::XentArgs a{X, x_dtype, idx_packed, lut, lut_dtype, targets, ignore_index, Problem{m, n, d, b, gpr}};
+  return status_of(skm::launch_xent_fwd(a, loss, lse, workspace, stream));
+}
+
+size_t sketch_xent_bwd_workspace(int64_t m, int64_t n, int64_t d, int b, int gpr, int x_dtype, int lut_dtype,
+                                 int need_dx, int need_dlut) {
+  if (m < 1 || (!need_dx && !need_dlut) || check_xent(m, n, d, b, gpr, x_dtype, lut_dtype) != SKM_OK) return 0;
+  return skm::xent_bwd_bytes(Problem{m, n, d, b, gpr}, x_dtype, lut_dtype, need_dx != 0, need_dlut != 0);
+}
+
+int sketch_xent_bwd(const void* X, int x_dtype, const uint8_t* idx_packed, const void* lut, int lut_dtype,
+                    const int64_t* targets, int64_t ignore_index, const float* lse, const float* dloss, int64_t m,
+                    int64_t n, int64_t d, int b, int gpr, void* dX, float* dLUT, int accumulate, void* workspace,
+                    size_t workspace_bytes, hipStream_t stream) {
+  const int st = check_xent(m, n, d, b, gpr, x_dtype, lut_dtype);
+  if (st != SKM_OK) return st;
+  if (!idx_packed || !lut) return SKM_EINVAL;
+  if (accumulate != 0 && accumulate != 1) return SKM_EINVAL;
+  if (m > 0 && (!X || !targets || !lse || !dloss)) return SKM_EINVAL;
+  if (!aligned16(X) || !aligned16(idx_packed) || !aligned16(lut) || !aligned16(lse) || !aligned16(dloss) ||
+      !aligned16(dX) || !aligned16(dLUT) || !aligned16(workspace) || ((uintptr_t)targets & 7u) != 0)
+    return SKM_EALIGN;
+  const int64_t K = int64_t(1) << b;
+  if (m == 0) {
+    if (dLUT && !accumulate) return status_of(skm::launch_zero_f32(dLUT, n * gpr * K, stream));
+    return SKM_OK;
+  }
+  if (!dX && !dLUT) return SKM_OK;
+  const size_t need =
+      sketch_xent_bwd_workspace(m, n, d, b, gpr, x_dtype, lut_dtype, dX != nullptr, dLUT != nullptr);
+  if (workspace_bytes < need || !workspace) return SKM_EWORKSPACE;
+  const Range w[3] = {{dX, m * d * 2}, {dLUT, n * gpr * K * 4}, {workspace, (int64_t)need}};
+  const Range r[6] = {{X, m * d * 2}, {idx_packed, n * d * b / 8}, {lut, n * gpr * K * 2},
+                      {targets, m * 8}, {lse, m * 4}, {dloss, m * 4}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range& in : r)
+      if (overlap(w[i], in)) return SKM_EALIAS;
+    for (int j = i + 1; j < 3; ++j)
+      if (overlap(w[i], w[j])) return SKM_EALIAS;
+  }
+  const skm::XentArgs a{X, x_dtype, idx_packed, lut, lut_dtype, targets, ignore_index, Problem{m, n, d, b, gpr}};
+  return status_of(skm::launch_xent_bwd(a, lse, dloss, dX, dLUT, accumulate, workspace, stream));
+}
+
 int sketch_column_weights(const float* U, int64_t d, float* h, hipStream_t stream) {
   if (d < 1 || d > (int64_t(1) << 20)) return SKM_EINVAL;
   if (!U || !h) return SKM_EINVAL;

@@ -218,6 +218,9 @@ __device__ __forceinline__ u32x4 add_quad(u32x4 v, uint32_t k) {
 // compile-time tag of a block's prescale mode (0 none, 1 exponent add, 2 multiply)
 template <int V> struct mode_tag { static constexpr int value = V; };
 
+// compile-time LDS buffer index of a K-step
+template <int V> struct buf_tag { static constexpr uint32_t value = V; };
+
 // Block-uniform prescale mode (skm_common.h scale_mode_of) from each thread's
 // flags: the waves OR their ballots into an LDS word at `word` (an address no
 // thread touches before the block's first K-step), two barriers.

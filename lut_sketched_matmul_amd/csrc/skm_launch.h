@@ -92,6 +92,50 @@ size_t dlut_partial_bytes(const Problem& p);
 hipError_t launch_gemm_dlut(const void* dY, const void* X, int io_dtype, const uint8_t* idx, const Problem& p,
                             float* dLUT, int accumulate, float* part, hipStream_t s);
 
+// 8-bit activation checkpoints (skm_quant.h): `count` values in whole blocks
+// of 32 to codes [count] and exponent bytes [count / 32], and back
+hipError_t launch_act_quant(const void* X, int x_dtype, int64_t count, int8_t* codes, uint8_t* scales, hipStream_t s);
+hipError_t launch_act_dequant(const int8_t* codes, const uint8_t* scales, int64_t count, void* X, int x_dtype,
+                              hipStream_t s);
+
+// layer norm (layer = 1) and root-mean-square norm (layer = 0) of rows of d
+// columns; w, bias: fp32 (p_f32 = 1) or X's dtype, NULL = ones / zeros
+struct NormArgs {
+  int64_t m, d;
+  int layer;
+  float eps;
+  const void* w;
+  const void* bias;
+  int p_f32;
+};
+// codes / scales: also write the 8-bit checkpoint of Y (d a multiple of 32)
+hipError_t launch_norm_fwd(const NormArgs& a, const void* X, int x_dtype, void* Y, float* mean, float* rstd,
+                           int8_t* codes, uint8_t* scales, hipStream_t s);
+// X from codes / scales when codes is given; mean is NULL for the rms norm;
+// dX, dw, db: NULL = skip. part: norm_bwd_part_bytes(m, d) per of dw and db
+size_t norm_bwd_part_bytes(int64_t m, int64_t d);
+hipError_t launch_norm_bwd(const NormArgs& a, const void* dY, int dy_dtype, const void* X, int x_dtype,
+                           const int8_t* codes, const uint8_t* scales, const float* mean, const float* rstd, void* dX,
+                           float* dw, float* db, int accumulate, float* part, hipStream_t s);
+
+// cross entropy of a sketched head (skm_xent.h): 16-bit pairs whose X keeps its
+// precision, (F16, F16), (BF16, F16), (BF16, BF16); p.n is the vocabulary
+struct XentArgs {
+  const void* X;
+  int x_dtype;
+  const uint8_t* idx;
+  const void* lut;
+  int lut_dtype;
+  const int64_t* targets;
+  int64_t ignore;
+  Problem p;
+};
+size_t xent_fwd_bytes(const Problem& p, int x_dtype, int lut_dtype);
+hipError_t launch_xent_fwd(const XentArgs& a, float* loss, float* lse, void* ws, hipStream_t s);
+size_t xent_bwd_bytes(const Problem& p, int x_dtype, int lut_dtype, bool need_dx, bool need_dlut);
+hipError_t launch_xent_bwd(const XentArgs& a, const float* lse, const float* dloss, void* dX, float* dLUT,
+                           int accumulate, void* ws, hipStream_t s);
+
 // sketch construction: column weights 1 / [H^-1]_jj from the factor U, the
 // weighted Lloyd tables, and the error-compensated mapping (Wc is overwritten;
 // E holds map_workspace_bytes(n))

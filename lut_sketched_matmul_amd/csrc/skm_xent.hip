@@ -1,0 +1,350 @@
+// Cross entropy of a sketched head: the small kernels around the tiles (token
+// list, merge of the statistics, gather of X, dX's last sum) and the host
+// side that cuts the vocabulary into pieces. The mathematics is in skm_xent.h.
+#include "skm_xent.h"
+#include "skm_quant.h"
+
+namespace skm {
+
+namespace {
+
+// ---- the list of tokens that have a target -----------------------------------------
+// One block (the list is one scan over m targets, 8 per thread and round).
+// rows[c] = token of listed row c, in token order. Forward: loss and lse of the
+// others are zeroed. Backward: pos[t] = listed row of token t or -1, and the
+// power of two that puts the largest |dloss| into [2^14, 2^15) (1 when there
+// is none or it is not finite).
+template <bool BWD>
+__global__ void __launch_bounds__(1024) k_xent_index(const int64_t* __restrict__ targets, int64_t ignore, int64_t m,
+                                                     const float* __restrict__ dloss, XentHead* __restrict__ head,
+                                                     int32_t* __restrict__ rows, int32_t* __restrict__ pos,
+                                                     float* __restrict__ loss, float* __restrict__ lse) {
+  __shared__ int32_t wsum[16];
+  __shared__ uint32_t wmax[16];
+  const int t = (int)threadIdx.x, lane = t & 63, wave = t >> 6;
+  int32_t base = 0;
+  uint32_t top = 0u;
+  for (int64_t r0 = 0; r0 < m; r0 += 8192) {
+    const int64_t i0 = r0 + 8 * (int64_t)t;
+    uint32_t flags = 0u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (i0 + k < m && targets[i0 + k] != ignore) flags |= 1u << k;
+    const int32_t mine = __popc(flags);
+    int32_t scan = mine;  // inclusive over the wave
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int32_t v = __shfl_up(scan, o, 64);
+      if (lane >= o) scan += v;
+    }
+    if (lane == 63) wsum[wave] = scan;
+    __syncthreads();
+    int32_t before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      const int32_t v = wsum[w];
+      if (w < wave) before += v;
+      total += v;
+    }
+    __syncthreads();  // (the next round writes wsum)
+    int32_t c = base + before + scan - mine;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t i = i0 + k;
+      if (i >= m) continue;
+      const bool on = (flags >> k) & 1u;
+      if (on) rows[c] = (int32_t)i;
+      if constexpr (BWD) {
+        pos[i] = on ? c : -1;
+        if (on) {
+          const uint32_t a = __builtin_bit_cast(uint32_t, dloss[i]) & 0x7FFFFFFFu;
+          if (a < 0x7F800000u && a > top) top = a;
+        }
+      } else if (!on) {
+        loss[i] = 0.0f;
+        lse[i] = 0.0f;
+      }
+      c += on ? 1 : 0;
+    }
+    base += total;
+  }
+  if constexpr (BWD) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) {
+      const uint32_t v = (uint32_t)__shfl_xor((int)top, o, 64);
+      top = top > v ? top : v;
+    }
+    if (lane == 0) wmax[wave] = top;
+    __syncthreads();
+  }
+  if (t == 0) {
+    head->count = base;
+    if constexpr (BWD) {
+      for (int w = 0; w < 16; ++w) top = top > wmax[w] ? top : wmax[w];
+      int e = top >= 0x00800000u ? 14 + 127 - (int)(top >> 23) : 0;
+      e = e > 126 ? 126 : (e < -112 ? -112 : e);
+      head->scale = pow2f(e);
+      head->inv_scale = pow2f(-e);
+    }
+  }
+}
+
+// ---- forward: merge of the blocks' (max, sum) pairs ------------------------------------
+// 16 listed tokens per block, 16 threads each over the vocabulary blocks.
+__global__ void __launch_bounds__(256) k_xent_merge(const float2* __restrict__ part, int64_t stride, int nvb,
+                                                    const XentHead* __restrict__ head,
+                                                    const int32_t* __restrict__ rows,
+                                                    const int64_t* __restrict__ targets, int64_t V,
+                                                    const float* __restrict__ tlogit, float* __restrict__ loss,
+                                                    float* __restrict__ lse) {
+  __shared__ float sm[16][16], ss[16][16];
+  const int tk = (int)(threadIdx.x & 15), sl = (int)(threadIdx.x >> 4);
+  const int64_t c = (int64_t)blockIdx.x * 16 + tk;
+  const int count = head->count;
+  if ((int64_t)blockIdx.x * 16 >= count) return;  // block-uniform
+  float mx = -__builtin_inff(), sum = 0.0f;
+  if (c < count) {
+    for (int v = sl; v < nvb; v += 16) {
+      const float2 p = part[(int64_t)v * stride + c];
+      const float nm = __builtin_fmaxf(mx, p.x);
+      const float ref = nm == -__builtin_inff() ? 0.0f : nm;
+      sum = sum * __expf(mx - ref) + p.y * __expf(p.x - ref);
+      mx = nm;
+    }
+  }
+  sm[sl][tk] = mx;
+  ss[sl][tk] = sum;
+  __syncthreads();
+  if (sl != 0 || c >= count) return;
+  mx = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) mx = __builtin_fmaxf(mx, sm[i][tk]);
+  const float ref = mx == -__builtin_inff() ? 0.0f : mx;
+  sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) sum += ss[i][tk] * __expf(sm[i][tk] - ref);
+  const float l = ref + logf(sum);
+  const int64_t t = rows[c];
+  const int64_t target = targets[t];
+  lse[t] = l;
+  loss[t] = target >= 0 && target < V ? l - tlogit[c] : __builtin_nanf("");
+}
+
+// ---- backward --------------------------------------------------------------------------
+
+// Xc[c] = X[rows[c]] for the listed tokens, zeros up to the next multiple of 32
+// (whole steps of the table gradient's tiles); 16 bytes per thread and round
+__global__ void __launch_bounds__(256) k_xent_gather(const uint16_t* __restrict__ X, const int32_t* __restrict__ rows,
+                                                     const XentHead* __restrict__ head, int64_t d,
+                                                     uint16_t* __restrict__ Xc) {
+  const int64_t c = blockIdx.x;
+  const int count = head->count;
+  if (c >= ((int64_t)count + 31) / 32 * 32) return;
+  const bool live = c < count;
+  const u32x4* src = reinterpret_cast<const u32x4*>(X + (live ? (int64_t)rows[c] : 0) * d);
+  u32x4* dst = reinterpret_cast<u32x4*>(Xc + c * d);
+  for (int64_t j = threadIdx.x; j < d / 8; j += 256) dst[j] = live ? src[j] : u32x4{0u, 0u, 0u, 0u};
+}
+
+// dX[t] = inv_scale * sum of the ranges' dX of t's listed row; zeros for an
+// ignored token
+template <typename TX>
+__global__ void __launch_bounds__(256) k_xent_dx_out(const float* __restrict__ acc, int splits, int64_t part_stride,
+                                                     const int32_t* __restrict__ pos, const XentHead* __restrict__ head,
+                                                     int64_t d, TX* __restrict__ dX) {
+  const int64_t t = blockIdx.x;
+  const int64_t c = pos[t];
+  const float inv = head->inv_scale;
+  for (int64_t j = (int64_t)threadIdx.x * 8; j < d; j += 2048) {
+    float v[8] = {};
+    if (c >= 0) {
+      for (int k = 0; k < splits; ++k) {
+        float a[8];
+        load8<float>(acc + k * part_stride + c * d + j, a);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] += a[q];
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] *= inv;
+    }
+    store8<TX>(dX + t * d + j, v);
+  }
+}
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+bool mixed(int x_dtype, int lut_dtype) { return scaled_pair(x_dtype == DT_BF16, lut_dtype == DT_F16); }
+
+// ---- workspace layouts -----------------------------------------------------------------
+struct FwdPlan {
+  size_t rows, rexp, part, tlogit, bytes;  // byte offsets (the head is at 0)
+};
+FwdPlan fwd_plan(const Problem& p, int x_dtype, int lut_dtype) {
+  FwdPlan f;
+  size_t o = 256;
+  f.rows = o;
+  o += up256((size_t)p.m * 4);
+  f.rexp = o;
+  if (mixed(x_dtype, lut_dtype)) o += up256((size_t)p.m * 4);
+  f.part = o;
+  o += up256((size_t)((p.n + G_BN - 1) / G_BN) * (size_t)p.m * 8);
+  f.tlogit = o;
+  o += up256((size_t)p.m * 4);
+  f.bytes = o;
+  return f;
+}
+
+struct BwdPlan {
+  int64_t cap;         // listed rows, rounded up to 32
+  int64_t P;           // vocabulary rows per piece
+  int splits;          // ranges of a piece's rows with their own dX
+  int64_t split_rows;  // of the first piece
+  size_t rows, pos, rexp, hi, lo, dxv, acc, xc, part, bytes;
+};
+
+// The pieces: dZ of a piece takes 2 bytes per (token, word) and form, and is
+// written once and read by two products; 256 MB of it stays in the memory-side
+// cache, and more rows per piece only save re-reading dX's fp32 sums.
+constexpr size_t XENT_PIECE_BYTES = size_t(256) << 20;
+
+BwdPlan bwd_plan(const Problem& p, int x_dtype, int lut_dtype, bool need_dx, bool need_dlut) {
+  BwdPlan f;
+  const bool mx = mixed(x_dtype, lut_dtype);
+  const bool has_hi = need_dlut || !mx, has_dxv = need_dx && mx;
+  const int forms = (has_hi ? 1 : 0) + (need_dlut ? 1 : 0) + (has_dxv ? 1 : 0);
+  f.cap = (p.m + 31) / 32 * 32;
+  int64_t P = (int64_t)(XENT_PIECE_BYTES / (size_t)(f.cap * 2 * forms)) / G_BN * G_BN;
+  if (P < G_BN) P = G_BN;
+  const int64_t pieces = (p.n + P - 1) / P;
+  P = ((p.n + pieces - 1) / pieces + G_BN - 1) / G_BN * G_BN;
+  f.P = P;
+  // ranges of a piece's rows so that dX's (256-token, 256-column) tiles fill
+  // the 256 CUs: the count that minimises rounds times steps per block
+  const int64_t n1 = p.n < P ? p.n : P, steps = (n1 + 63) / 64;
+  const int64_t nb0 = (p.m + 255) / 256 * ((p.d + 255) / 256);
+  int64_t best = 1, cost = (nb0 + 255) / 256 * steps;
+  for (int64_t c = 2; c <= 64 && c * 4 <= steps && nb0 * c <= 512; ++c) {
+    const int64_t k = (nb0 * c + 255) / 256 * ((steps + c - 1) / c);
+    if (k < cost) {
+      cost = k;
+      best = c;
+    }
+  }
+  f.split_rows = (steps + best - 1) / best * 64;
+  f.splits = (int)((n1 + f.split_rows - 1) / f.split_rows);
+  size_t o = 256;
+  auto take = [&](bool on, size_t bytes) {
+    const size_t at = o;
+    if (on) o += up256(bytes);
+    return at;
+  };
+  const size_t dz = (size_t)f.cap * (size_t)((n1 + 7) / 8 * 8) * 2;
+  f.rows = take(true, (size_t)p.m * 4);
+  f.pos = take(true, (size_t)p.m * 4);
+  f.rexp = take(mx, (size_t)p.m * 4);
+  f.hi = take(has_hi, dz);
+  f.lo = take(need_dlut, dz);
+  f.dxv = take(has_dxv, dz);
+  f.acc = take(need_dx, (size_t)f.splits * (size_t)p.m * (size_t)p.d * 4);
+  f.xc = take(need_dlut, (size_t)f.cap * (size_t)p.d * 2);
+  size_t part = 0;
+  for (int64_t v0 = 0; v0 < p.n; v0 += P) {  // (the last piece may split differently)
+    if (v0 > 0 && v0 + P < p.n) continue;
+    const Problem q{f.cap, p.n - v0 < P ? p.n - v0 : P, p.d, p.b, p.gpr};
+    const size_t b = dlut_partial_bytes(q);
+    part = b > part ? b : part;
+  }
+  f.part = take(need_dlut, part);
+  f.bytes = o;
+  return f;
+}
+
+template <typename T> T* at(void* ws, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(ws) + off); }
+
+}  // namespace
+
+size_t xent_fwd_bytes(const Problem& p, int x_dtype, int lut_dtype) { return fwd_plan(p, x_dtype, lut_dtype).bytes; }
+
+hipError_t launch_xent_fwd(const XentArgs& a, float* loss, float* lse, void* ws, hipStream_t s) {
+  const Problem& p = a.p;
+  const FwdPlan f = fwd_plan(p, a.x_dtype, a.lut_dtype);
+  XentHead* head = at<XentHead>(ws, 0);
+  int32_t* rows = at<int32_t>(ws, f.rows);
+  int32_t* rexp = mixed(a.x_dtype, a.lut_dtype) ? at<int32_t>(ws, f.rexp) : nullptr;
+  float2* part = at<float2>(ws, f.part);
+  float* tlogit = at<float>(ws, f.tlogit);
+  hipLaunchKernelGGL(k_xent_index<false>, dim3(1), dim3(1024), 0, s, a.targets, a.ignore, p.m, nullptr, head, rows,
+                     nullptr, loss, lse);
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && rexp) e = launch_row_exp(a.X, p.m, p.d, rexp, s);
+  if (e != hipSuccess) return e;
+  const XentGemm g{a.X, a.x_dtype, a.idx, a.lut, a.lut_dtype, p, rows, head, a.targets, rexp, 0};
+  e = xent_stats(g, part, p.m, tlogit, s);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_xent_merge, dim3((unsigned)((p.m + 15) / 16)), dim3(256), 0, s, part, p.m,
+                     (int)((p.n + G_BN - 1) / G_BN), head, rows, a.targets, p.n, tlogit, loss, lse);
+  return hipGetLastError();
+}
+
+size_t xent_bwd_bytes(const Problem& p, int x_dtype, int lut_dtype, bool need_dx, bool need_dlut) {
+  return bwd_plan(p, x_dtype, lut_dtype, need_dx, need_dlut).bytes;
+}
+
+hipError_t launch_xent_bwd(const XentArgs& a, const float* lse, const float* dloss, void* dX, float* dLUT,
+                           int accumulate, void* ws, hipStream_t s) {
+  const Problem& p = a.p;
+  const BwdPlan f = bwd_plan(p, a.x_dtype, a.lut_dtype, dX != nullptr, dLUT != nullptr);
+  const bool mx = mixed(a.x_dtype, a.lut_dtype);
+  XentHead* head = at<XentHead>(ws, 0);
+  int32_t* rows = at<int32_t>(ws, f.rows);
+  int32_t* pos = at<int32_t>(ws, f.pos);
+  int32_t* rexp = mx ? at<int32_t>(ws, f.rexp) : nullptr;
+  float* acc = dX ? at<float>(ws, f.acc) : nullptr;
+  void* hi = dLUT || !mx ? at<void>(ws, f.hi) : nullptr;
+  void* lo = dLUT ? at<void>(ws, f.lo) : nullptr;
+  void* dxv = dX && mx ? at<void>(ws, f.dxv) : nullptr;
+  void* xc = dLUT ? at<void>(ws, f.xc) : nullptr;
+  hipLaunchKernelGGL(k_xent_index<true>, dim3(1), dim3(1024), 0, s, a.targets, a.ignore, p.m, dloss, head, rows, pos,
+                     nullptr, nullptr);
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && rexp) e = launch_row_exp(a.X, p.m, p.d, rexp, s);
+  if (e == hipSuccess && dLUT) {
+    hipLaunchKernelGGL(k_xent_gather, dim3((unsigned)f.cap), dim3(256), 0, s, (const uint16_t*)a.X, rows, head, p.d,
+                       (uint16_t*)xc);
+    e = hipGetLastError();
+  }
+  const int es = 2;  // bytes of a table entry (16-bit pairs only)
+  for (int64_t v0 = 0; v0 < p.n && e == hipSuccess; v0 += f.P) {
+    const int64_t n = p.n - v0 < f.P ? p.n - v0 : f.P;
+    const Problem q{p.m, n, p.d, p.b, p.gpr};
+    const uint8_t* idx = a.idx + v0 * p.row_bytes();
+    const void* lut = static_cast<const char*>(a.lut) + v0 * p.gpr * p.k() * es;
+    const int64_t ld = (n + 7) / 8 * 8;
+    const XentGemm g{a.X, a.x_dtype, idx, lut, a.lut_dtype, q, rows, head, a.targets, rexp, v0};
+    e = xent_grad(g, {lse, dloss, p.n, ld, hi, lo, dxv}, s);
+    const XentPiece pc{head, ld};
+    if (e == hipSuccess && dX) {
+      // every range of the first piece is written; later pieces add to some or all
+      const int64_t steps = (n + 63) / 64;
+      const int64_t sr = (steps + f.splits - 1) / f.splits * 64;
+      const int splits = (int)((n + sr - 1) / sr);
+      e = xent_dx(mx ? dxv : hi, idx, lut, a.lut_dtype, q, acc, pc, v0 > 0, splits, sr, s);
+    }
+    if (e == hipSuccess && dLUT) {
+      const Problem qc{f.cap, n, p.d, p.b, p.gpr};
+      e = xent_dlut(hi, lo, xc, a.x_dtype, idx, qc, dLUT + v0 * p.gpr * p.k(), accumulate, at<float>(ws, f.part), pc,
+                    s);
+    }
+  }
+  if (e != hipSuccess || !dX) return e;
+  const dim3 grid((unsigned)p.m);
+  if (a.x_dtype == DT_F16)
+    hipLaunchKernelGGL(k_xent_dx_out<half_t>, grid, dim3(256), 0, s, acc, f.splits, p.m * p.d, pos, head, p.d,
+                       (half_t*)dX);
+  else
+    hipLaunchKernelGGL(k_xent_dx_out<bf16_t>, grid, dim3(256), 0, s, acc, f.splits, p.m * p.d, pos, head, p.d,
+                       (bf16_t*)dX);
+  return hipGetLastError();
+}
+
+}  // namespace skm
