@@ -237,12 +237,14 @@ int sketch_act_dequant(const int8_t* codes, const uint8_t* scales, int64_t m, in
                        void* X, int x_dtype, hipStream_t stream);
 
 /*
- * sketch_matmul_bwd with X given as its 8-bit checkpoint (the values above in
- * io_dtype, exact): same results as dequantising into X first. codes and
- * scales may be NULL when dLUT is NULL. workspace: at least
- * sketch_matmul_bwd_ckpt_workspace(...) bytes (that of sketch_matmul_bwd, and
- * one X [m][d] in io_dtype that lives during the call only; need_dlut = 0
- * when dLUT is NULL).
+ * sketch_matmul_bwd with X given as its 8-bit checkpoint: the gradients of the
+ * values above (exact in io_dtype), up to the order of the fp32 sums, which is
+ * fixed (deterministic). codes and scales may be NULL when dLUT is NULL.
+ * workspace: at least sketch_matmul_bwd_ckpt_workspace(...) bytes (one X in
+ * io_dtype for dLUT, up to 128 MiB of partial sums of dX when its tiles are
+ * few, one dY when n is not a multiple of 8, split table gradients); need_dx /
+ * need_dlut = 0 where the output is NULL. Everything else as for
+ * sketch_matmul_bwd.
  */
 int sketch_matmul_bwd_ckpt(const void* dY, const int8_t* codes, const uint8_t* scales, int io_dtype,
                            const uint8_t* idx_packed, const void* lut, int lut_dtype,
@@ -251,7 +253,7 @@ int sketch_matmul_bwd_ckpt(const void* dY, const int8_t* codes, const uint8_t* s
                            void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 size_t sketch_matmul_bwd_ckpt_workspace(int64_t m, int64_t n, int64_t d, int b, int gpr,
-                                        int io_dtype, int lut_dtype, int need_dlut);
+                                        int io_dtype, int lut_dtype, int need_dx, int need_dlut);
 
 /*
  * The norm in front of a sketched layer, over the rows of X [m][d]:

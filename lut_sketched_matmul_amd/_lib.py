@@ -67,7 +67,8 @@ _SIGNATURES = {
     "sketch_act_dequant": (_c_int, [_c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_int, _c_vp]),
     "sketch_matmul_bwd_ckpt": (_c_int, [_c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_int, _c_i64, _c_i64, _c_i64,
                                         _c_int, _c_int, _c_vp, _c_vp, _c_int, _c_vp, _c_size, _c_vp]),
-    "sketch_matmul_bwd_ckpt_workspace": (_c_size, [_c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_int]),
+    "sketch_matmul_bwd_ckpt_workspace": (_c_size, [_c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                                   _c_int]),
     "sketch_norm_fwd": (_c_int, [_c_vp, _c_int, _c_vp, _c_vp, _c_int, _c_i64, _c_i64, _c_int, _c_f32, _c_vp, _c_vp,
                                  _c_vp, _c_vp, _c_vp, _c_vp]),
     "sketch_norm_bwd": (_c_int, [_c_vp, _c_int, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_i64,
@@ -120,17 +121,25 @@ def _check(fn: str, status: int) -> None:
 # torch-facing wrappers
 # --------------------------------------------------------------------------
 
+_torch_module = None
+_dtype_codes = {}
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _dtype_codes.update({torch.float32: SKM_F32, torch.float16: SKM_F16, torch.bfloat16: SKM_BF16})
+        _torch_module = torch
+    return _torch_module
 
 
 def dtype_code(t) -> int:
-    torch = _torch()
-    m = {torch.float32: SKM_F32, torch.float16: SKM_F16, torch.bfloat16: SKM_BF16}
-    if t.dtype not in m:
+    _torch()
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    return m[t.dtype]
+    return code
 
 
 def _stream_ptr(stream) -> int:
@@ -155,8 +164,14 @@ def _require_device(*ts):
 _FLOAT_DTYPES = ("float32", "float16", "bfloat16")
 
 
+_dtype_names = {}
+
+
 def _dtype_name(t) -> str:
-    return str(t.dtype).replace("torch.", "")
+    name = _dtype_names.get(t.dtype)
+    if name is None:
+        name = _dtype_names[t.dtype] = str(t.dtype).replace("torch.", "")
+    return name
 
 
 def _expect(t, name: str, shape=None, numel=None, dtypes=None):
@@ -495,38 +510,32 @@ class _Launch:
     Ordering the inputs before `stream` is the caller's.
     """
 
-    __slots__ = ("device", "stream", "stack")
+    __slots__ = ("index", "stream", "inner")
 
-    def __init__(self, stream, *tensors):
-        device = None
-        for t in tensors:
-            if t is None:
-                continue
-            if not t.is_cuda:
-                raise ValueError("tensors must live on the GPU")
-            if not t.is_contiguous():
-                raise ValueError("tensors must be contiguous")
-            if device is None:
-                device = t.device
-            elif t.device != device:
-                raise ValueError(f"tensors on {device} and {t.device}")
-        if stream is not None and stream.device != device:
-            raise ValueError(f"a stream of {stream.device} for tensors on {device}")
-        self.device, self.stream, self.stack = device, stream, ()
+    def __init__(self, stream, first, *others):
+        _require_device(first, *others)
+        index = first.get_device()
+        for t in others:
+            if t is not None and t.get_device() != index:
+                raise ValueError(f"tensors on cuda:{index} and cuda:{t.get_device()}")
+        if stream is not None and stream.device_index != index:
+            raise ValueError(f"a stream of cuda:{stream.device_index} for tensors on cuda:{index}")
+        self.index, self.stream, self.inner = index, stream, None
 
     def __enter__(self):
-        cuda = _torch().cuda
+        torch = _torch()
         if self.stream is not None:
-            self.stack = (cuda.stream(self.stream),)
-        elif cuda.current_device() != self.device.index:
-            self.stack = (cuda.device(self.device),)
-        for c in self.stack:
-            c.__enter__()
-        return cuda.current_stream().cuda_stream
+            self.inner = torch.cuda.stream(self.stream)
+        elif torch.cuda.current_device() != self.index:
+            self.inner = torch.cuda.device(self.index)
+        if self.inner is not None:
+            self.inner.__enter__()
+        # (the raw handle: building a Stream object costs as much as half a launch)
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
-        for c in self.stack:
-            c.__exit__(*exc)
+        if self.inner is not None:
+            self.inner.__exit__(*exc)
 
 
 def _ptr(t):
@@ -556,9 +565,9 @@ def sketch_act_quant(X, codes=None, scales=None, stream=None) -> Tuple[object, o
     _check_ckpt(codes, scales, m, d)
     with _Launch(stream, X, codes, scales) as sp:
         if codes is None:
-            codes = torch.empty((m, d), dtype=torch.int8, device=X.device)
+            codes = X.new_empty((m, d), dtype=torch.int8)
         if scales is None:
-            scales = torch.empty((m, d // 32), dtype=torch.uint8, device=X.device)
+            scales = X.new_empty((m, d // 32), dtype=torch.uint8)
         st = lib().sketch_act_quant(_ptr(X), dtype_code(X), m, d, _ptr(codes), _ptr(scales), sp)
     _check("sketch_act_quant", st)
     return codes, scales
@@ -576,16 +585,17 @@ def sketch_act_dequant(codes, scales, dtype, out=None, stream=None):
     _expect(out, "out", shape=(m, d), dtypes=(str(dtype).replace("torch.", ""),))
     with _Launch(stream, codes, scales, out) as sp:
         if out is None:
-            out = torch.empty((m, d), dtype=dtype, device=codes.device)
+            out = codes.new_empty((m, d), dtype=dtype)
         st = lib().sketch_act_dequant(_ptr(codes), _ptr(scales), m, d, _ptr(out), dtype_code(out), sp)
     _check("sketch_act_dequant", st)
     return out
 
 
 def sketch_matmul_bwd_ckpt_workspace(m: int, n: int, d: int, b: int, gpr: int, io_dtype: int, lut_dtype: int,
-                                     need_dlut: bool = True) -> int:
+                                     need_dx: bool = True, need_dlut: bool = True) -> int:
     """Bytes of device workspace sketch_matmul_bwd_ckpt needs for these sizes and dtypes."""
-    return int(lib().sketch_matmul_bwd_ckpt_workspace(m, n, d, b, gpr, io_dtype, lut_dtype, 1 if need_dlut else 0))
+    return int(lib().sketch_matmul_bwd_ckpt_workspace(m, n, d, b, gpr, io_dtype, lut_dtype, 1 if need_dx else 0,
+                                                      1 if need_dlut else 0))
 
 
 def sketch_matmul_bwd_ckpt(dY, codes, scales, idx_packed, lut, b: int, gpr: int, need_dx: bool = True,
@@ -611,7 +621,8 @@ def sketch_matmul_bwd_ckpt(dY, codes, scales, idx_packed, lut, b: int, gpr: int,
         dL = None
         if need_dlut:
             dL = dlut_out if dlut_out is not None else torch.empty((n, gpr, K), dtype=torch.float32, device=dY.device)
-        ws = _workspace(workspace, sketch_matmul_bwd_ckpt_workspace(m, n, d, b, gpr, io, lt, need_dlut), dY.device)
+        ws = _workspace(workspace, sketch_matmul_bwd_ckpt_workspace(m, n, d, b, gpr, io, lt, need_dx, need_dlut),
+                        dY.device)
         st = lib().sketch_matmul_bwd_ckpt(_ptr(dY), _ptr(codes), _ptr(scales), io, idx_packed.data_ptr(),
                                           lut.data_ptr(), lt, m, n, d, b, gpr, _ptr(dX), _ptr(dL),
                                           1 if accumulate else 0, _ptr(ws), _size(ws), sp)
@@ -628,14 +639,14 @@ def _norm_kind(kind: str) -> int:
     return _NORM_KINDS[kind]
 
 
-def _check_params(X, d: int, *named):
-    """weight / bias of a norm: [d], fp32 or X's dtype, one dtype for both. Returns its code."""
+def _check_params(xt, d: int, *named):
+    """weight / bias of a norm: [d], fp32 or the activations' dtype xt, one dtype for both. Returns its code."""
     code = SKM_F32
     first = None
     for name, t in named:
         if t is None:
             continue
-        _expect(t, name, shape=(d,), dtypes=("float32", _dtype_name(X)))
+        _expect(t, name, shape=(d,), dtypes=None if t.dtype == xt else ("float32", str(xt).replace("torch.", "")))
         if first is not None and t.dtype != first:
             raise TypeError("weight and bias must have one dtype")
         first = t.dtype
@@ -655,20 +666,19 @@ def sketch_norm_fwd(X, weight=None, bias=None, kind: str = "layer", eps: float =
     m, d = _matrix(X, "X")
     k = _norm_kind(kind)
     _expect(X, "X", dtypes=_FLOAT_DTYPES)
-    pc = _check_params(X, d, ("weight", weight), ("bias", bias))
+    pc = _check_params(X.dtype, d, ("weight", weight), ("bias", bias))
     if checkpoint and d % 32:
         raise ValueError(f"X has {d} columns: a checkpoint takes whole blocks of 32")
     _expect(out, "out", shape=(m, d), dtypes=(_dtype_name(X),))
     with _Launch(stream, X, weight, bias, out) as sp:
-        dev = X.device
         if out is None:
-            out = torch.empty((m, d), dtype=X.dtype, device=dev)
-        mean = torch.empty(m, dtype=torch.float32, device=dev) if k else None
-        rstd = torch.empty(m, dtype=torch.float32, device=dev)
+            out = torch.empty_like(X)
+        mean = X.new_empty(m, dtype=torch.float32) if k else None
+        rstd = X.new_empty(m, dtype=torch.float32)
         codes = scales = None
         if checkpoint:
-            codes = torch.empty((m, d), dtype=torch.int8, device=dev)
-            scales = torch.empty((m, d // 32), dtype=torch.uint8, device=dev)
+            codes = X.new_empty((m, d), dtype=torch.int8)
+            scales = X.new_empty((m, d // 32), dtype=torch.uint8)
         st = lib().sketch_norm_fwd(_ptr(X), dtype_code(X), _ptr(weight), _ptr(bias), pc, m, d, k, eps, _ptr(out),
                                    _ptr(mean), _ptr(rstd), _ptr(codes), _ptr(scales), sp)
     _check("sketch_norm_fwd", st)
@@ -706,10 +716,12 @@ def sketch_norm_bwd(dY, X, weight, mean, rstd, kind: str = "layer", need_dx: boo
         xt = X.dtype
         if x_dtype is not None and x_dtype != xt:
             raise TypeError(f"X has dtype {xt}, expected {x_dtype}")
-    like = torch.empty(0, dtype=xt)
-    _expect(like, "X", dtypes=_FLOAT_DTYPES)
-    _expect(dY, "dY", dtypes=("float32", _dtype_name(like)))
-    pc = _check_params(like, d, ("weight", weight))
+    xc = _dtype_codes.get(xt)
+    if xc is None:
+        raise TypeError(f"X has dtype {xt}, expected one of {_FLOAT_DTYPES}")
+    if dY.dtype != xt:
+        _expect(dY, "dY", dtypes=("float32", str(xt).replace("torch.", "")))
+    pc = _check_params(xt, d, ("weight", weight))
     if k and mean is None:
         raise ValueError("a layer norm's backward needs the mean")
     if not k:
@@ -729,7 +741,7 @@ def sketch_norm_bwd(dY, X, weight, mean, rstd, kind: str = "layer", need_dx: boo
             db = db_out if db_out is not None else torch.empty(d, dtype=torch.float32, device=dev)
         need = sketch_norm_bwd_workspace(m, d) if need_dw or need_db else 0
         ws = _workspace(workspace, need, dev)
-        st = lib().sketch_norm_bwd(_ptr(dY), dtype_code(dY), _ptr(X), dtype_code(like), _ptr(codes), _ptr(scales),
+        st = lib().sketch_norm_bwd(_ptr(dY), dtype_code(dY), _ptr(X), xc, _ptr(codes), _ptr(scales),
                                    _ptr(weight), pc, _ptr(mean), _ptr(rstd), m, d, k, _ptr(dX), _ptr(dw), _ptr(db),
                                    1 if accumulate else 0, _ptr(ws), _size(ws), sp)
     _check("sketch_norm_bwd", st)

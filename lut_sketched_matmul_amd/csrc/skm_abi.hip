@@ -324,19 +324,13 @@ int sketch_act_dequant(const int8_t* codes, const uint8_t* scales, int64_t m, in
   return status_of(skm::launch_act_dequant(codes, scales, m * d, X, x_dtype, stream));
 }
 
-// Workspace of the backward from a checkpoint: [X in io_dtype, 256-byte
-// aligned] (read by the table gradient), then sketch_matmul_bwd's
-static size_t ckpt_x_bytes(int64_t m, int64_t d, int io_dtype, int need_dlut) {
-  return need_dlut && m > 0 ? align256((size_t)m * (size_t)d * elem_bytes(io_dtype)) : 0;
-}
-
 size_t sketch_matmul_bwd_ckpt_workspace(int64_t m, int64_t n, int64_t d, int b, int gpr, int io_dtype, int lut_dtype,
-                                        int need_dlut) {
-  if (check_shape(m, n, d, b, gpr) != SKM_OK || check_ckpt_shape(m, d) != SKM_OK ||
+                                        int need_dx, int need_dlut) {
+  if (m < 1 || check_shape(m, n, d, b, gpr) != SKM_OK || check_ckpt_shape(m, d) != SKM_OK ||
       !supported_pair(io_dtype, lut_dtype))
     return 0;
-  return ckpt_x_bytes(m, d, io_dtype, need_dlut) +
-         sketch_matmul_bwd_workspace(m, n, d, b, gpr, io_dtype, lut_dtype);
+  if (io_dtype == SKM_F32) return need_dlut ? align256((size_t)m * (size_t)d * 4) : 0;
+  return skm::bwd_ckpt_bytes(Problem{m, n, d, b, gpr}, io_dtype, lut_dtype, need_dx != 0, need_dlut != 0);
 }
 
 int sketch_matmul_bwd_ckpt(const void* dY, const int8_t* codes, const uint8_t* scales, int io_dtype,
@@ -347,21 +341,22 @@ int sketch_matmul_bwd_ckpt(const void* dY, const int8_t* codes, const uint8_t* s
   if (st == SKM_OK) st = check_ckpt_shape(m, d);
   if (st != SKM_OK) return st;
   if (!supported_pair(io_dtype, lut_dtype)) return SKM_EUNSUPPORTED;
-  const size_t xb = ckpt_x_bytes(m, d, io_dtype, dLUT != nullptr);
-  if (xb == 0)
-    return sketch_matmul_bwd(dY, nullptr, io_dtype, idx_packed, lut, lut_dtype, m, n, d, b, gpr, dX, dLUT, accumulate,
-                             workspace, workspace_bytes, stream);
-  if (!codes || !scales || !dY || !idx_packed || !lut) return SKM_EINVAL;
   if (accumulate != 0 && accumulate != 1) return SKM_EINVAL;
-  if (!aligned16(codes) || !aligned16(scales) || !aligned16(dY) || !aligned16(idx_packed) || !aligned16(lut) ||
-      !aligned16(dX) || !aligned16(dLUT) || !aligned16(workspace))
-    return SKM_EALIGN;
-  const size_t need = sketch_matmul_bwd_ckpt_workspace(m, n, d, b, gpr, io_dtype, lut_dtype, 1);
-  if (workspace_bytes < need || !workspace) return SKM_EWORKSPACE;
-  // the checkpoint against every buffer that is written, and X's copy against
-  // what sketch_matmul_bwd writes or reads (it checks the rest of its buffers,
-  // but only after X has been written)
+  if (!idx_packed || !lut) return SKM_EINVAL;
+  if (m > 0 && (dX || dLUT) && !dY) return SKM_EINVAL;
+  if (m > 0 && dLUT && (!codes || !scales)) return SKM_EINVAL;
+  for (const void* p : {dY, (const void*)codes, (const void*)scales, (const void*)idx_packed, lut, (const void*)dX,
+                        (const void*)dLUT, (const void*)workspace})
+    if (!aligned16(p)) return SKM_EALIGN;
   const int64_t K = int64_t(1) << b;
+  if (m == 0) {
+    if (dLUT && !accumulate) return status_of(skm::launch_zero_f32(dLUT, n * gpr * K, stream));
+    return SKM_OK;
+  }
+  if (!dX && !dLUT) return SKM_OK;
+  const size_t need = sketch_matmul_bwd_ckpt_workspace(m, n, d, b, gpr, io_dtype, lut_dtype, dX != nullptr,
+                                                       dLUT != nullptr);
+  if (workspace_bytes < need || (need && !workspace)) return SKM_EWORKSPACE;
   const int xs = elem_bytes(io_dtype), ls = elem_bytes(lut_dtype);
   const Range w[3] = {{workspace, (int64_t)need}, {dX, m * d * 4}, {dLUT, n * gpr * K * 4}};
   const Range r[5] = {{codes, m * d}, {scales, m * d / 32}, {dY, m * n * xs}, {idx_packed, n * d * b / 8},
@@ -372,11 +367,18 @@ int sketch_matmul_bwd_ckpt(const void* dY, const int8_t* codes, const uint8_t* s
     for (int j = i + 1; j < 3; ++j)
       if (overlap(w[i], w[j])) return SKM_EALIAS;
   }
-  st = status_of(skm::launch_act_dequant(codes, scales, m * d, workspace, io_dtype, stream));
-  if (st != SKM_OK) return st;
-  const size_t rest = workspace_bytes - xb;
-  return sketch_matmul_bwd(dY, workspace, io_dtype, idx_packed, lut, lut_dtype, m, n, d, b, gpr, dX, dLUT, accumulate,
-                           static_cast<char*>(workspace) + xb, rest, stream);
+  const Problem p{m, n, d, b, gpr};
+  if (io_dtype == SKM_F32) {
+    if (dX) st = status_of(skm::launch_dx_f32((const float*)dY, idx_packed, (const float*)lut, p, dX, stream));
+    if (st != SKM_OK || !dLUT) return st;
+    st = status_of(skm::launch_act_dequant(codes, scales, m * d, workspace, io_dtype, stream));
+    if (st != SKM_OK) return st;
+    return status_of(skm::launch_dlut_f32((const float*)dY, (const float*)workspace, idx_packed, p, dLUT, accumulate,
+                                          stream));
+  }
+  if (!skm::gemm_bwd_supported(p)) return SKM_EUNSUPPORTED;
+  return status_of(skm::launch_bwd_ckpt(dY, codes, scales, io_dtype, idx_packed, lut, lut_dtype, p, dX, dLUT,
+                                        accumulate, workspace, stream));
 }
 
 // ---- norms -----------------------------------------------------------------------

@@ -58,17 +58,17 @@ using namespace mm;
 // LDS buffer index of a K-step not known at compile time (else mm::buf_tag)
 struct buf_rt { uint32_t value; };
 
-// Both products also run on a piece of the weight rows (a vocabulary whose
-// output gradient is made a range of rows at a time), with PA = DxPiece /
-// DlPiece instead of Whole: dY's rows then have their own stride, and the
-// number of tokens is read on the device.
+// Both products also run with PA = DxPiece / DlPiece instead of Whole, for the
+// operators that own their operands' layout (cross entropy: a range of the
+// vocabulary at a time, tokens counted on the device; the backward from an
+// 8-bit checkpoint: X in a padded workspace).
 struct Whole {
   static constexpr bool PIECE = false;
 };
 struct DxPiece {
   static constexpr bool PIECE = true;
-  const int32_t* count;  // tokens (at most the host's m)
-  int64_t ldy;           // row stride of dY: a multiple of 8, at least n, zeros from n on
+  const int32_t* count;  // tokens (at most the host's m); NULL = m
+  int64_t ldy;           // row stride of dY: a multiple of 8, at least n, finite from n on
   int accumulate;        // add to dX instead of overwriting it
   int splits;            // the weight rows are cut into this many ranges,
   int64_t split_rows;    // of this many rows (a multiple of 64), each with its
@@ -76,10 +76,12 @@ struct DxPiece {
 };
 struct DlPiece {
   static constexpr bool PIECE = true;
-  const int32_t* count;    // tokens, rounded up to 32 here (X and dY hold zeros there)
+  const int32_t* count;    // tokens; NULL = m. X holds zeros up to a multiple of 32
   int64_t ldy;             // row stride of dY, as above
   int64_t lo_off;          // dY + lo_off: a second addend of dY, 0 = none
-  const float* inv_scale;  // the sums are multiplied by *inv_scale
+  const float* inv_scale;  // the sums are multiplied by *inv_scale; NULL = 1
+  const void* zeros;       // 16 zero bytes read in place of dY's rows past the
+                           // tokens; NULL = those rows exist and hold zeros
 };
 
 // ============================================================================
@@ -212,7 +214,7 @@ __device__ __forceinline__ bool dx_piece(const DxPiece& pa, uint32_t& bid, const
   lut += r0 * gpr * (1 << B);
   n = n - r0 < pa.split_rows ? n - r0 : pa.split_rows;
   dX += sp * pa.part_stride;
-  m = *pa.count;
+  if (pa.count) m = *pa.count;
   return (int64_t)(bid % mblocks) * DX_BM < m;
 }
 
@@ -957,10 +959,9 @@ __device__ __forceinline__ void dl_scatter(const f32x16 (&acc)[2][4], uint32_t l
 // One store per gradient entry of the block's rows and group: the four bin
 // copies at `bins` (stride `bcopy` bytes, rows of `brs` floats) summed in a
 // fixed order.
-template <int B, bool SCALED = false>
+template <int B>
 __device__ __forceinline__ void dl_store_bins(float* __restrict__ dLUT, int64_t i0, int64_t n, int gpr, int g,
-                                              uint32_t bins, uint32_t bcopy, uint32_t brs, int accumulate, int t,
-                                              float scale = 1.0f) {
+                                              uint32_t bins, uint32_t bcopy, uint32_t brs, int accumulate, int t) {
   constexpr int K = 1 << B;
   for (uint32_t q = (uint32_t)t; q < 128u * (uint32_t)K; q += 512u) {
     const uint32_t i = q / K, c = q % K;
@@ -968,7 +969,6 @@ __device__ __forceinline__ void dl_store_bins(float* __restrict__ dLUT, int64_t 
     float s = 0.0f;
 #pragma unroll
     for (int w = 0; w < 4; ++w) s += *(const lds_f32*)(uintptr_t)(bins + (uint32_t)w * bcopy + (i * brs + c) * 4u);
-    if constexpr (SCALED) s *= scale;
     float* dst = dLUT + ((i0 + i) * gpr + g) * K + c;
     *dst = accumulate ? *dst + s : s;
   }
@@ -1198,6 +1198,94 @@ __device__ __forceinline__ void dd_wait_vmcnt() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
+// ---- binning with private bins (DlPiece) ------------------------------------
+// The MFMA operands are exchanged, so a lane holds one weight row i = 64 wm +
+// 32 a + lane % 32 and, per 32-column tile b, the 16 columns 8 q + 4 (lane /
+// 32) + k. Every lane adds into its own copy of its row's bins, entry-major /
+// lane-minor ([a][entry][64 lanes] per wave, 64 KB in all, in the operand ring,
+// which is free between chunks): the 64 lanes of an add hit 64 banks whatever
+// the indices are. (With lanes along the columns, as dl_scatter has them, up
+// to 32 lanes add to one of 2^b bins of a row.) A lane's indices are whole
+// 32-column units of its row, loaded straight into registers. The eight copies
+// of an entry (4 column waves x 2 lane halves) are then added in a fixed order
+// into the registers of the thread that owns it: thread t has entries K/4 (t /
+// 128) .. of row t % 128.
+template <int B>
+__device__ __forceinline__ void dl_bins(const f32x16 (&acc)[2][4], const uint8_t* __restrict__ idx_packed,
+                                        uint32_t lane, int wave, int t, int64_t i0, int64_t n, int64_t d, int64_t j0,
+                                        int64_t jend, float (&bins)[4]) {
+  constexpr int K = 1 << B;
+  const int wm = wave & 1, wn = wave >> 1;
+  const uint32_t h = lane >> 5;
+  const uint32_t mine = (uint32_t)wave * 8192u + lane * 4u;
+  uint32_t w[2][4][B];
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    const int64_t i = i0 + 64 * wm + 32 * a + (lane & 31u);
+    const uint8_t* row = idx_packed + (i < n ? i : n - 1) * (d * B / 8);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int64_t j = j0 + 128 * wn + 32 * b;  // (past the range: any unit of the row, its sums are dropped)
+      load_unit<B>(row, (j < jend ? j : j0) / 32, w[a][b]);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 2 * K; ++q) st_w((uint32_t)wave * 8192u + (uint32_t)(q / K) * 4096u + (uint32_t)(q % K) * 256u + lane * 4u, 0u);
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      if (j0 + 128 * wn + 32 * b >= jend) continue;  // wave-uniform
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        // the four fields 8 q + 4 h .. + 3 of the unit, from bit 0 of f on
+        uint32_t f;
+        if constexpr (B == 4) {
+          f = w[a][b][q] >> (16u * h);
+        } else if constexpr (B == 2) {
+          f = w[a][b][q >> 1] >> (16u * (q & 1) + 8u * h);
+        } else {
+          const uint32_t bit = 24u * q + 12u * h;  // at most 84: word and offset of the lane's half
+          const uint32_t w0 = h ? w[a][b][(24 * q + 12) >> 5] : w[a][b][(24 * q) >> 5];
+          const uint32_t w1 = h ? w[a][b][((24 * q + 12) >> 5) < 2 ? ((24 * q + 12) >> 5) + 1 : 2]
+                                : w[a][b][((24 * q) >> 5) < 2 ? ((24 * q) >> 5) + 1 : 2];
+          f = __builtin_amdgcn_alignbit(w1, w0, bit & 31u);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t c = (f >> (B * k)) & (uint32_t)(K - 1);
+          __hip_atomic_fetch_add((lds_f32*)(uintptr_t)(mine + (uint32_t)a * 4096u + (c << 8)), acc[a][b][4 * q + k],
+                                 __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        }
+      }
+    }
+  __syncthreads();
+  const uint32_t r = (uint32_t)t & 127u, c0 = ((uint32_t)t >> 7) * (uint32_t)(K / 4);
+#pragma unroll
+  for (int k = 0; k < K / 4; ++k) {
+    float s = bins[k];
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        s += *(const lds_f32*)(uintptr_t)(((r >> 6) + 2u * v) * 8192u + ((r >> 5) & 1u) * 4096u + (c0 + k) * 256u +
+                                          ((r & 31u) + 32u * g) * 4u);
+    bins[k] = s;
+  }
+}
+
+// the block's entries, times scale
+template <int B>
+__device__ __forceinline__ void dl_put_bins(float* __restrict__ dLUT, int64_t i0, int64_t n, int gpr, int g,
+                                            int accumulate, int t, const float (&bins)[4], float scale) {
+  constexpr int K = 1 << B;
+  const int64_t i = i0 + (t & 127);
+  if (i >= n) return;
+  float* dst = dLUT + (i * gpr + g) * K + (t >> 7) * (K / 4);
+#pragma unroll
+  for (int k = 0; k < K / 4; ++k) dst[k] = accumulate ? dst[k] + bins[k] * scale : bins[k] * scale;
+}
+
 template <int B, typename TX, typename PA>
 __global__ void __launch_bounds__(512, 1)
 k_gemm_dlut_dma(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8_t* __restrict__ idx_packed,
@@ -1207,7 +1295,7 @@ k_gemm_dlut_dma(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8
   int64_t ldy = n;
   if constexpr (PA::PIECE) {
     ldy = pa.ldy;
-    m = ((int64_t)*pa.count + DL_BK - 1) / DL_BK * DL_BK;
+    if (pa.count) m = *pa.count;
   }
   extern __shared__ uint32_t smem[];  // dynamic LDS only: starts at address 0
   (void)smem;
@@ -1239,13 +1327,14 @@ k_gemm_dlut_dma(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8
   const int64_t jg0 = (int64_t)g * G + (int64_t)cr * split_cols;
   const int64_t jend = (int64_t)g * G + G < jg0 + split_cols ? (int64_t)g * G + G : jg0 + split_cols;
   // (a piece's token range may start past the tokens that exist: no step)
-  const int K1 = PA::PIECE && m <= 0 ? 0 : (int)(m / DL_BK);
+  const int K1 = PA::PIECE ? (m <= 0 ? 0 : (int)((m + DL_BK - 1) / DL_BK)) : (int)(m / DL_BK);
   // steps: the tokens once, or with a second addend of dY twice
   int KS = K1;
   if constexpr (PA::PIECE)
     if (pa.lo_off != 0) KS = 2 * K1;
 
-  for (uint32_t q = (uint32_t)t; q < 4u * DD_BCOPY / 4u; q += 512u) st_w(DD_BINS + q * 4u, 0u);
+  if constexpr (!PA::PIECE)
+    for (uint32_t q = (uint32_t)t; q < 4u * DD_BCOPY / 4u; q += 512u) st_w(DD_BINS + q * 4u, 0u);
 
   // ---- DMA roles: this wave's token rows 4 wave .. +3. dY: one 1 KB
   // instruction (lane = row (lane / 16) x slot (lane % 16)); X: one
@@ -1264,7 +1353,10 @@ k_gemm_dlut_dma(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8
         k -= K1;
         lo = pa.lo_off;
       }
-    dd_dma16(ysrc + (lo + (int64_t)k * ystep), stage + ydst);
+    const void* ys = ysrc + (lo + (int64_t)k * ystep);
+    if constexpr (PA::PIECE)
+      if (pa.zeros && k == K1 - 1 && (int64_t)k * DL_BK + 4 * wave + (int)(lane >> 4) >= m) ys = pa.zeros;
+    dd_dma16(ys, stage + ydst);
 #pragma unroll
     for (int h = 0; h < 4; ++h) dd_dma16(xsrc[h] + (int64_t)k * xstep, stage + DD_TA + 1024u * (4u * (uint32_t)wave + h));
   };
@@ -1303,8 +1395,10 @@ k_gemm_dlut_dma(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
-      for (int b = 0; b < 4; ++b) acc[a][b] = MF::run(af[a], bf[b], acc[a][b]);
+      for (int b = 0; b < 4; ++b)
+        acc[a][b] = PA::PIECE ? MF::run(bf[b], af[a], acc[a][b]) : MF::run(af[a], bf[b], acc[a][b]);
   };
+  float bins[PA::PIECE ? 4 : 1] = {};  // PIECE: the thread's entries (dl_bins)
   // a half step's 8 MFMAs interleaved with the other half's 12 reads
   auto interleave = [&]() {
 #pragma unroll
@@ -1363,14 +1457,21 @@ k_gemm_dlut_dma(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8
     }
     dd_wait_vmcnt<0>();  // (no copy is in flight here; the compiler does not count them)
 
-    dl_stage_indices<B>(idx_packed, i0, n, d, j0, jend, t);
-    __syncthreads();
-    dl_scatter<B>(acc, lane, wm, wn, i0, n, j0, jend, DD_BINS + (uint32_t)wn * DD_BCOPY, DD_BRS);
+    if constexpr (PA::PIECE) {
+      dl_bins<B>(acc, idx_packed, lane, wave, t, i0, n, d, j0, jend, bins);
+    } else {
+      dl_stage_indices<B>(idx_packed, i0, n, d, j0, jend, t);
+      __syncthreads();
+      dl_scatter<B>(acc, lane, wm, wn, i0, n, j0, jend, DD_BINS + (uint32_t)wn * DD_BCOPY, DD_BRS);
+    }
   }
-  __syncthreads();
-  float scale = 1.0f;
-  if constexpr (PA::PIECE) scale = *pa.inv_scale;
-  dl_store_bins<B, PA::PIECE>(dLUT, i0, n, gpr, g, DD_BINS, DD_BCOPY, DD_BRS, accumulate, t, scale);
+  if constexpr (PA::PIECE) {
+    const float scale = pa.inv_scale ? *pa.inv_scale : 1.0f;
+    dl_put_bins<B>(dLUT, i0, n, gpr, g, accumulate, t, bins, scale);
+  } else {
+    __syncthreads();
+    dl_store_bins<B>(dLUT, i0, n, gpr, g, DD_BINS, DD_BCOPY, DD_BRS, accumulate, t);
+  }
 }
 
 // ---- launchers ---------------------------------------------------------------

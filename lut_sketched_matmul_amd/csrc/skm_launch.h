@@ -92,11 +92,39 @@ size_t dlut_partial_bytes(const Problem& p);
 hipError_t launch_gemm_dlut(const void* dY, const void* X, int io_dtype, const uint8_t* idx, const Problem& p,
                             float* dLUT, int accumulate, float* part, hipStream_t s);
 
+// the same products with the caller's own operand layout (skm_gemm_bwd.h):
+// token count on the device (count, at most p.m; NULL = p.m), dY's row stride
+// ld (a multiple of 8), dX in ranges of the weight rows (p.m * p.d floats
+// apart), dY for dLUT as hi + lo (lo may be NULL)
+struct DxRanges {
+  int count;
+  int64_t rows;
+};
+DxRanges dx_ranges(const Problem& p);
+hipError_t launch_dx_piece(const void* dY, int io_dtype, const uint8_t* idx, const void* lut, int lut_dtype,
+                           const Problem& p, float* dX, const int32_t* rexp, const int32_t* count, int64_t ld,
+                           int accumulate, const DxRanges& r, hipStream_t s);
+struct DlutPiece {
+  const int32_t* count;
+  int64_t ld;
+  const float* inv_scale;  // NULL = 1
+  const void* zeros;       // see DlPiece
+};
+hipError_t launch_dlut_piece(const void* hi, const void* lo, const void* X, int io_dtype, const uint8_t* idx,
+                             const Problem& p, float* dLUT, int accumulate, float* part, const DlutPiece& q,
+                             hipStream_t s);
+
 // 8-bit activation checkpoints (skm_quant.h): `count` values in whole blocks
 // of 32 to codes [count] and exponent bytes [count / 32], and back
 hipError_t launch_act_quant(const void* X, int x_dtype, int64_t count, int8_t* codes, uint8_t* scales, hipStream_t s);
 hipError_t launch_act_dequant(const int8_t* codes, const uint8_t* scales, int64_t count, void* X, int x_dtype,
                               hipStream_t s);
+// the backward with X from its checkpoint, 16-bit pairs (the fp32 pair
+// dequantises and takes the plain path); dX, dLUT: NULL = skip
+size_t bwd_ckpt_bytes(const Problem& p, int io_dtype, int lut_dtype, bool need_dx, bool need_dlut);
+hipError_t launch_bwd_ckpt(const void* dY, const int8_t* codes, const uint8_t* scales, int io_dtype,
+                           const uint8_t* idx, const void* lut, int lut_dtype, const Problem& p, float* dX,
+                           float* dLUT, int accumulate, void* ws, hipStream_t s);
 
 // layer norm (layer = 1) and root-mean-square norm (layer = 0) of rows of d
 // columns; w, bias: fp32 (p_f32 = 1) or X's dtype, NULL = ones / zeros

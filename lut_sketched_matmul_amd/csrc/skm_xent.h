@@ -226,14 +226,5 @@ struct XentGradOut {
   void *hi, *lo, *dxv;
 };
 hipError_t xent_grad(const XentGemm& g, const XentGradOut& o, hipStream_t s);
-// dX of a piece (dY in the tables' dtype), dLUT of a piece
-struct XentPiece {
-  const XentHead* head;
-  int64_t ld;
-};
-hipError_t xent_dx(const void* dY, const uint8_t* idx, const void* lut, int lut_dtype, const Problem& p, float* dX,
-                   const XentPiece& q, int accumulate, int splits, int64_t split_rows, hipStream_t s);
-hipError_t xent_dlut(const void* hi, const void* lo, const void* Xc, int x_dtype, const uint8_t* idx,
-                     const Problem& p, float* dLUT, int accumulate, float* part, const XentPiece& q, hipStream_t s);
 
 }  // namespace skm

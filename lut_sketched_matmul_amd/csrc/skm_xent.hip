@@ -197,8 +197,7 @@ FwdPlan fwd_plan(const Problem& p, int x_dtype, int lut_dtype) {
 struct BwdPlan {
   int64_t cap;         // listed rows, rounded up to 32
   int64_t P;           // vocabulary rows per piece
-  int splits;          // ranges of a piece's rows with their own dX
-  int64_t split_rows;  // of the first piece
+  DxRanges ranges;     // of the first piece's rows, each with its own dX
   size_t rows, pos, rexp, hi, lo, dxv, acc, xc, part, bytes;
 };
 
@@ -218,20 +217,8 @@ BwdPlan bwd_plan(const Problem& p, int x_dtype, int lut_dtype, bool need_dx, boo
   const int64_t pieces = (p.n + P - 1) / P;
   P = ((p.n + pieces - 1) / pieces + G_BN - 1) / G_BN * G_BN;
   f.P = P;
-  // ranges of a piece's rows so that dX's (256-token, 256-column) tiles fill
-  // the 256 CUs: the count that minimises rounds times steps per block
-  const int64_t n1 = p.n < P ? p.n : P, steps = (n1 + 63) / 64;
-  const int64_t nb0 = (p.m + 255) / 256 * ((p.d + 255) / 256);
-  int64_t best = 1, cost = (nb0 + 255) / 256 * steps;
-  for (int64_t c = 2; c <= 64 && c * 4 <= steps && nb0 * c <= 512; ++c) {
-    const int64_t k = (nb0 * c + 255) / 256 * ((steps + c - 1) / c);
-    if (k < cost) {
-      cost = k;
-      best = c;
-    }
-  }
-  f.split_rows = (steps + best - 1) / best * 64;
-  f.splits = (int)((n1 + f.split_rows - 1) / f.split_rows);
+  const int64_t n1 = p.n < P ? p.n : P;
+  f.ranges = dx_ranges(Problem{p.m, n1, p.d, p.b, p.gpr});
   size_t o = 256;
   auto take = [&](bool on, size_t bytes) {
     const size_t at = o;
@@ -245,7 +232,7 @@ BwdPlan bwd_plan(const Problem& p, int x_dtype, int lut_dtype, bool need_dx, boo
   f.hi = take(has_hi, dz);
   f.lo = take(need_dlut, dz);
   f.dxv = take(has_dxv, dz);
-  f.acc = take(need_dx, (size_t)f.splits * (size_t)p.m * (size_t)p.d * 4);
+  f.acc = take(need_dx, (size_t)f.ranges.count * (size_t)p.m * (size_t)p.d * 4);
   f.xc = take(need_dlut, (size_t)f.cap * (size_t)p.d * 2);
   size_t part = 0;
   for (int64_t v0 = 0; v0 < p.n; v0 += P) {  // (the last piece may split differently)
@@ -322,27 +309,26 @@ hipError_t launch_xent_bwd(const XentArgs& a, const float* lse, const float* dlo
     const int64_t ld = (n + 7) / 8 * 8;
     const XentGemm g{a.X, a.x_dtype, idx, lut, a.lut_dtype, q, rows, head, a.targets, rexp, v0};
     e = xent_grad(g, {lse, dloss, p.n, ld, hi, lo, dxv}, s);
-    const XentPiece pc{head, ld};
     if (e == hipSuccess && dX) {
       // every range of the first piece is written; later pieces add to some or all
       const int64_t steps = (n + 63) / 64;
-      const int64_t sr = (steps + f.splits - 1) / f.splits * 64;
-      const int splits = (int)((n + sr - 1) / sr);
-      e = xent_dx(mx ? dxv : hi, idx, lut, a.lut_dtype, q, acc, pc, v0 > 0, splits, sr, s);
+      const int64_t sr = (steps + f.ranges.count - 1) / f.ranges.count * 64;
+      e = launch_dx_piece(mx ? dxv : hi, a.lut_dtype, idx, lut, a.lut_dtype, q, acc, nullptr, &head->count, ld, v0 > 0,
+                          {(int)((n + sr - 1) / sr), sr}, s);
     }
     if (e == hipSuccess && dLUT) {
       const Problem qc{f.cap, n, p.d, p.b, p.gpr};
-      e = xent_dlut(hi, lo, xc, a.x_dtype, idx, qc, dLUT + v0 * p.gpr * p.k(), accumulate, at<float>(ws, f.part), pc,
-                    s);
+      e = launch_dlut_piece(hi, lo, xc, a.x_dtype, idx, qc, dLUT + v0 * p.gpr * p.k(), accumulate,
+                            at<float>(ws, f.part), {&head->count, ld, &head->inv_scale, nullptr}, s);
     }
   }
   if (e != hipSuccess || !dX) return e;
   const dim3 grid((unsigned)p.m);
   if (a.x_dtype == DT_F16)
-    hipLaunchKernelGGL(k_xent_dx_out<half_t>, grid, dim3(256), 0, s, acc, f.splits, p.m * p.d, pos, head, p.d,
+    hipLaunchKernelGGL(k_xent_dx_out<half_t>, grid, dim3(256), 0, s, acc, f.ranges.count, p.m * p.d, pos, head, p.d,
                        (half_t*)dX);
   else
-    hipLaunchKernelGGL(k_xent_dx_out<bf16_t>, grid, dim3(256), 0, s, acc, f.splits, p.m * p.d, pos, head, p.d,
+    hipLaunchKernelGGL(k_xent_dx_out<bf16_t>, grid, dim3(256), 0, s, acc, f.ranges.count, p.m * p.d, pos, head, p.d,
                        (bf16_t*)dX);
   return hipGetLastError();
 }

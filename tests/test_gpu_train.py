@@ -107,32 +107,61 @@ def test_act_quant_empty_and_outputs():
     assert (buf[0] == 7).all() and (buf[5] == 7).all()     # rows outside the output stay as they were
 
 
-@pytest.mark.parametrize("b,gpr", [(2, 1), (3, 4), (4, 8)])
-@pytest.mark.parametrize("io,ldt", [("f16", "f16"), ("bf16", "f16"), ("bf16", "bf16"), ("f16", "bf16"), ("f32", "f32")])
-@pytest.mark.parametrize("m", [1, 33, 96])
-def test_bwd_from_checkpoint(m, io, ldt, b, gpr):
-    """Bit for bit the backward of the values the checkpoint stands for, and dLUT within the bound of float64."""
-    n, d = 136, 512
-    name = f"bwdck/{m}/{io}/{ldt}/{b}"
+PAIRS = [("f16", "f16"), ("bf16", "f16"), ("bf16", "bf16"), ("f16", "bf16"), ("f32", "f32")]
+
+
+@pytest.mark.parametrize("io,ldt", PAIRS)
+@pytest.mark.parametrize("m,n,d,b,gpr", [
+    (1, 136, 512, 2, 1), (33, 136, 512, 3, 4), (96, 136, 512, 4, 8), (31, 131, 96, 4, 1), (64, 1, 64, 3, 1),
+    (40, 1000, 256, 4, 1), (5, 1100, 2048, 2, 2), (290, 520, 1088, 4, 2), (300, 77, 640, 3, 20),
+])
+def test_bwd_from_checkpoint(m, n, d, b, gpr, io, ldt):
+    """Both gradients of the values the checkpoint stands for against float64; ragged tokens, rows and columns."""
+    t = torch()
+    name = f"bwdck/{m}/{n}/{d}/{io}/{ldt}/{b}"
     idx = syn.random_packed_indices(name + "/i", n, d, b)
     lut = syn.random_lut(name + "/l", n, gpr, b, 0.02, ldt)
     X, _ = dev(name + "/x", (m, d), 1.0, io)
     dY, dY64 = dev(name + "/y", (m, n), 0.1, io)
     gi, gl = to_dev(idx, "u8"), to_dev(lut, ldt)
     codes, scales = skm().sketch_act_quant(X)
-    Xq = skm().sketch_act_dequant(codes, scales, X.dtype)
-    want = skm().sketch_matmul_bwd(dY, Xq, gi, gl, b, gpr)
-    acc = torch().ones_like(want[1])
-    got = skm().sketch_matmul_bwd_ckpt(dY, codes, scales, gi, gl, b, gpr)
-    assert torch().equal(got[0], want[0]) and torch().equal(got[1], want[1])
-    assert skm().sketch_matmul_bwd_ckpt(dY, codes, scales, gi, gl, b, gpr, need_dlut=False)[1] is None
-    got = skm().sketch_matmul_bwd_ckpt(dY, codes, scales, gi, gl, b, gpr, need_dx=False, dlut_out=acc, accumulate=True)
-    assert got[0] is None and got[1] is acc
-    x64 = to_f64(Xq)
+    x64 = to.act_dequant(codes.cpu().numpy(), scales.cpu().numpy())
+    dX, dL = skm().sketch_matmul_bwd_ckpt(dY, codes, scales, gi, gl, b, gpr)
     ref = oracle.backward_dlut(dY64, x64, idx, b, gpr)
     mag = oracle.backward_dlut(np.abs(dY64), np.abs(x64), idx, b, gpr)
-    # tokens in chains of at most m, a bin's entries in chains of at most d / gpr, plus the two last sums
-    within(to_f64(got[1]) - 1.0, ref, (m + d // gpr + 8) * U * (mag + 1.0), "dLUT")
+    # tokens in chains of at most m, a bin's entries in chains of at most d / gpr, split sums
+    tol = (m + d // gpr + 80) * U * mag
+    within(to_f64(dL), ref, tol, "dLUT")
+    W = oracle.dequantize(idx, syn.to_float64(lut, ldt), d, b, gpr)
+    sx = (np.abs(dY64) @ np.abs(W)) * (n + 80) * U
+    if (io, ldt) == ("bf16", "f16"):       # operands below 2^-14 of f16: 2^-23 of the row's largest
+        sx = sx + 2.0 ** -23 * np.abs(dY64).max(1, keepdims=True) * np.abs(W).sum(0)
+    elif (io, ldt) == ("f16", "bf16"):     # dY is rounded to the tables' dtype
+        sx = sx + H["bf16"] * (np.abs(dY64) @ np.abs(W))
+    within(to_f64(dX), dY64 @ W, sx, "dX")
+    one = skm().sketch_matmul_bwd_ckpt(dY, codes, scales, gi, gl, b, gpr, need_dlut=False)
+    assert one[1] is None and t.equal(one[0], dX)
+    acc = t.ones_like(dL)
+    two = skm().sketch_matmul_bwd_ckpt(dY, codes, scales, gi, gl, b, gpr, need_dx=False, dlut_out=acc, accumulate=True)
+    assert two[0] is None and two[1] is acc
+    within(to_f64(acc), to_f64(dL) + 1.0, 80 * U * (mag + 1.0), "accumulate")
+
+
+@pytest.mark.parametrize("m", [33, 64])
+def test_bwd_from_checkpoint_infinite_gradient_stays_in_its_row(m):
+    """Padding rows are zeros, not copies: an infinity in the last token's dY stays an infinity of its table row."""
+    t = torch()
+    n, d = 136, 64
+    idx = syn.random_packed_indices("bwdinf/i", n, d, 4)
+    gi, gl = to_dev(idx, "u8"), t.randn((n, 1, 16), device="cuda").half()
+    codes, scales = skm().sketch_act_quant(t.ones((m, d), device="cuda").half())
+    dY = t.ones((m, n), device="cuda").half()
+    dY[m - 1, 5] = float("inf")
+    dL = to_f64(skm().sketch_matmul_bwd_ckpt(dY, codes, scales, gi, gl, 4, 1)[1])
+    used = oracle.backward_dlut(np.ones((1, n)), np.ones((1, d)), idx, 4, 1)
+    assert np.isposinf(dL[5][used[5] > 0]).all()
+    rest = [i for i in range(n) if i != 5]
+    assert np.array_equal(dL[rest], m * used[rest])
 
 
 # ---------------------------------------------------------------------------------------------------------

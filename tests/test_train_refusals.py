@@ -60,10 +60,12 @@ def test_bwd_ckpt_refusals(lib):
         for k in range(5):
             assert bwd(lib, **{out: addr(k)}) == EALIAS, (out, k)
     assert bwd(lib, dL=addr(5)) == EALIAS and bwd(lib, ws=addr(6)) == EALIAS
-    # without dLUT no checkpoint is read: the plain backward's own refusals
+    # without dLUT no checkpoint is read, without either output nothing is done
+    less = _lib.sketch_matmul_bwd_ckpt_workspace(4, 6400, 512, 4, 2, BF16, F16, need_dlut=False)
+    assert 0 < less < _lib.sketch_matmul_bwd_ckpt_workspace(4, 6400, 512, 4, 2, BF16, F16)
+    assert bwd(lib, dt=BF16, n=6400, dL=None, codes=None, scales=None, wsb=less - 1) == EWS
     assert bwd(lib, dL=None, codes=None, scales=None, dY=None) == EINVAL
-    assert _lib.sketch_matmul_bwd_ckpt_workspace(4, 64, 512, 4, 2, F16, F16, need_dlut=False) == \
-        _lib.sketch_matmul_bwd_workspace(4, 64, 512, 4, 2, F16, F16)
+    assert bwd(lib, dX=None, dL=None) == 0 and bwd(lib, m=0, acc=1, dY=None, codes=None, scales=None) == 0
 
 
 def nfwd(lib, X=addr(0), dt=F16, w=addr(1), bias=addr(2), pdt=F32, m=4, d=64, kind=1, eps=1e-5, Y=addr(3),
