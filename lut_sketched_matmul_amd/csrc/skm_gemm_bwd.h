@@ -57,6 +57,7 @@ using namespace mm;
 
 // LDS buffer index of a K-step not known at compile time (else mm::buf_tag)
 struct buf_rt { uint32_t value; };
+template <bool V> struct bool_tag { static constexpr bool value = V; };
 
 // Both products also run with PA = DxPiece / DlPiece instead of Whole, for the
 // operators that own their operands' layout (cross entropy: a range of the
@@ -1183,6 +1184,21 @@ __device__ __forceinline__ void dd_dma16(const void* src, uint32_t lds) {
       : "memory");
 }
 
+// The same without a compiler fence, for copies placed between reads of other
+// stages and MFMAs (dd_barrier and the waits keep them apart from the reads of
+// their own stage).
+__device__ __forceinline__ void dd_dma16_free(const void* src, uint32_t lds) {
+  uint32_t keep;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %2\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, off\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(keep)
+      : "v"(src), "s"(lds));
+}
+
 // raw barrier, with compiler-only fences so that no LDS access moves across it
 __device__ __forceinline__ void dd_barrier() {
   asm volatile("" ::: "memory");
@@ -1216,6 +1232,9 @@ __device__ __forceinline__ void dl_bins(const f32x16 (&acc)[2][4], const uint8_t
                                         int64_t jend, float (&bins)[4]) {
   constexpr int K = 1 << B;
   const int wm = wave & 1, wn = wave >> 1;
+  // (opaque copies: the addresses below would be hoisted out of the chunk loop
+  // and stay live across the K loop)
+  asm volatile("" : "+v"(lane), "+v"(t));
   const uint32_t h = lane >> 5;
   const uint32_t mine = (uint32_t)wave * 8192u + lane * 4u;
   uint32_t w[2][4][B];
@@ -1436,24 +1455,88 @@ k_gemm_dlut_dma(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8
     u32x4 a0[2], b0[4], a1[2], b1[4];
     uint32_t st = 0u;  // stage of step k
     read_half(st, 0, a0, b0);
-    for (int k = 0; k < KS; ++k) {
-      const uint32_t st2 = st >= DD_STAGE ? st - DD_STAGE : st + 2u * DD_STAGE;  // stage of step k+2
-      // (stage k+2 = stage k-1: every wave finished reading it before the last barrier)
-      if (k + 2 < KS) dma(k + 2, st2);
-      read_half(st, 1, a1, b1);
-      mfma_half(a0, b0);
-      interleave();
-      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): every read of stage k has landed
-      // this wave's DMA of step k+1 has landed (the one of step k+2 may not)
-      if (k + 2 < KS) dd_wait_vmcnt<5>();
-      else dd_wait_vmcnt<0>();
-      dd_barrier();
-      st = st + DD_STAGE == 3u * DD_STAGE ? 0u : st + DD_STAGE;
-      // (unconditional, so that the reads interleave with the MFMAs: after
-      // the last step they read a stale stage and the values go unused)
-      read_half(st, 0, a0, b0);
-      mfma_half(a1, b1);
-      interleave();
+    if constexpr (PA::PIECE) {
+      // The copies of step k+2 are issued between the MFMAs of the first half:
+      // issued together at the head of the step they held the matrix core up
+      // (both waves of a SIMD are there at the same time). Their addresses
+      // advance by a step's worth of rows, and go back to the first rows of X
+      // (and on to dY's second addend) after the last step of the first addend.
+      const char* ys = reinterpret_cast<const char*>(ysrc + (K1 > 2 ? 2 * ystep : pa.lo_off + (2 - K1) * ystep));
+      const char* xs[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        xs[h] = reinterpret_cast<const char*>(xsrc[h] + (K1 > 2 ? 2 * xstep : (2 - K1) * xstep));
+      // lanes whose row of dY in the last step is past the tokens
+      const bool past = pa.zeros && (int64_t)(K1 - 1) * DL_BK + 4 * wave + (int)(lane >> 4) >= m;
+      auto step = [&](int k, auto more) __attribute__((always_inline)) {
+        constexpr bool MORE = decltype(more)::value;
+        const uint32_t st2 = st >= DD_STAGE ? st - DD_STAGE : st + 2u * DD_STAGE;  // stage of step k+2
+        const void* yl = ys;
+        if constexpr (MORE)
+          if (pa.zeros && k + 2 == K1 - 1) yl = past ? pa.zeros : yl;
+        // (each group pinned: three reads, two MFMAs, the copies)
+        u32x2 lo[6], hi[6];  // of a1[0], a1[1], b1[0] .. b1[3]
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+#pragma unroll
+          for (int r = 3 * q; r < 3 * q + 3; ++r) {
+            const int f = r >> 1;  // fragment
+            const uint32_t p = f < 2 ? st + fa[f] + 16u * 256u : st + fb[f - 2] + 16u * 1024u;
+            (r & 1 ? hi : lo)[f] = ld_tr(p + (r & 1 ? (f < 2 ? 4u * 256u : 4u * 1024u) : 0u));
+          }
+          const int a = q >> 1, b = 2 * (q & 1);
+          acc[a][b] = MF::run(b0[b], a0[a], acc[a][b]);
+          acc[a][b + 1] = MF::run(b0[b + 1], a0[a], acc[a][b + 1]);
+          if constexpr (MORE) {
+            if (q == 0) dd_dma16_free(yl, st2 + ydst);
+            dd_dma16_free(xs[q], st2 + DD_TA + 1024u * (4u * (uint32_t)wave + q));
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int f = 0; f < 6; ++f) (f < 2 ? a1[f & 1] : b1[(f - 2) & 3]) = u32x4{lo[f].x, lo[f].y, hi[f].x, hi[f].y};
+        if constexpr (MORE) {
+          ys += ystep * 2;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) xs[h] += xstep * 2;
+          if (k + 3 == K1) {  // step k+3 is the first of the second addend
+            ys += (pa.lo_off - (int64_t)K1 * ystep) * 2;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) xs[h] -= (int64_t)K1 * xstep * 2;
+          }
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): every read of stage k has landed
+        if constexpr (MORE) dd_wait_vmcnt<5>();
+        else dd_wait_vmcnt<0>();
+        dd_barrier();
+        st = st + DD_STAGE == 3u * DD_STAGE ? 0u : st + DD_STAGE;
+        read_half(st, 0, a0, b0);
+        mfma_half(a1, b1);
+        interleave();
+      };
+      int k = 0;
+      for (; k + 2 < KS; ++k) step(k, bool_tag<true>{});
+      for (; k < KS; ++k) step(k, bool_tag<false>{});
+    } else {
+      for (int k = 0; k < KS; ++k) {
+        const uint32_t st2 = st >= DD_STAGE ? st - DD_STAGE : st + 2u * DD_STAGE;  // stage of step k+2
+        // (stage k+2 = stage k-1: every wave finished reading it before the last barrier)
+        if (k + 2 < KS) dma(k + 2, st2);
+        read_half(st, 1, a1, b1);
+        mfma_half(a0, b0);
+        interleave();
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): every read of stage k has landed
+        // this wave's DMA of step k+1 has landed (the one of step k+2 may not)
+        if (k + 2 < KS) dd_wait_vmcnt<5>();
+        else dd_wait_vmcnt<0>();
+        dd_barrier();
+        st = st + DD_STAGE == 3u * DD_STAGE ? 0u : st + DD_STAGE;
+        // (unconditional, so that the reads interleave with the MFMAs: after
+        // the last step they read a stale stage and the values go unused)
+        read_half(st, 0, a0, b0);
+        mfma_half(a1, b1);
+        interleave();
+      }
     }
     dd_wait_vmcnt<0>();  // (no copy is in flight here; the compiler does not count them)
 
