@@ -201,13 +201,17 @@ __device__ __forceinline__ void dx_lut_store(const DxLutWord<B>& L, uint32_t eba
 }
 
 // A piece's share of one block: its range of the weight rows, the tokens that
-// exist. False when the block has no token (block-uniform).
+// exist. The blocks that have tokens come first (evenly over the XCDs); false
+// for the others (block-uniform).
 template <int B, typename TX, typename TL>
 __device__ __forceinline__ bool dx_piece(const DxPiece& pa, uint32_t& bid, const TX* __restrict__& dY,
                                          const uint8_t* __restrict__& idx_packed, const TL* __restrict__& lut,
-                                         int64_t& m, int64_t& n, int64_t d, int gpr, int64_t mblocks,
+                                         int64_t& m, int64_t& n, int64_t d, int gpr, int64_t& mblocks,
                                          float* __restrict__& dX) {
-  const uint32_t nb0 = gridDim.x / (uint32_t)pa.splits;
+  if (pa.count) m = *pa.count;
+  mblocks = (m + DX_BM - 1) / DX_BM;
+  const uint32_t nb0 = (uint32_t)(mblocks * ((d + DX_BN - 1) / DX_BN));
+  if (bid >= nb0 * (uint32_t)pa.splits) return false;
   const int64_t sp = bid / nb0, r0 = sp * pa.split_rows;
   bid %= nb0;
   dY += r0;
@@ -215,8 +219,7 @@ __device__ __forceinline__ bool dx_piece(const DxPiece& pa, uint32_t& bid, const
   lut += r0 * gpr * (1 << B);
   n = n - r0 < pa.split_rows ? n - r0 : pa.split_rows;
   dX += sp * pa.part_stride;
-  if (pa.count) m = *pa.count;
-  return (int64_t)(bid % mblocks) * DX_BM < m;
+  return true;
 }
 
 template <int B, int NG, typename TX, typename TL, typename PA>
@@ -1217,15 +1220,23 @@ __device__ __forceinline__ void dd_wait_vmcnt() {
 // ---- binning with private bins (DlPiece) ------------------------------------
 // The MFMA operands are exchanged, so a lane holds one weight row i = 64 wm +
 // 32 a + lane % 32 and, per 32-column tile b, the 16 columns 8 q + 4 (lane /
-// 32) + k. Every lane adds into its own copy of its row's bins, entry-major /
-// lane-minor ([a][entry][64 lanes] per wave, 64 KB in all, in the operand ring,
-// which is free between chunks): the 64 lanes of an add hit 64 banks whatever
-// the indices are. (With lanes along the columns, as dl_scatter has them, up
-// to 32 lanes add to one of 2^b bins of a row.) A lane's indices are whole
-// 32-column units of its row, loaded straight into registers. The eight copies
-// of an entry (4 column waves x 2 lane halves) are then added in a fixed order
-// into the registers of the thread that owns it: thread t has entries K/4 (t /
-// 128) .. of row t % 128.
+// 32) + k. Every lane adds into its own copies of its row's bins, entry-major
+// / lane-minor (per wave [a][b / 2][entry][64 lanes], 128 KB in all, over the
+// operand ring, which is free between chunks): the 64 lanes of an access hit
+// 64 banks whatever the indices are, and since no other lane touches a copy,
+// an addition is a read, an add and a write. (An LDS fp32 atomic add takes 3
+// cycles per lane: 92 us for the 65536 additions of a block, the whole cost of
+// a call with few tokens; with 8192 tokens a chunk's matrix work takes 200 us.)
+// The four copies of a wave are four independent chains of 32 additions, which
+// hides most of the read latency. A lane's indices are whole 32-column units
+// of its row, loaded straight into registers. The sixteen copies of an entry
+// (4 column waves x 2 x 2 lane halves) are then added in a fixed order into
+// the registers of the thread that owns it: thread t has entries K/4 (t / 128)
+// .. of row t % 128.
+constexpr uint32_t DP_COPY = 16u * 256u;      // one copy: 16 entries x 64 lanes
+constexpr uint32_t DP_WAVE = 4u * DP_COPY;
+static_assert(8u * DP_WAVE <= DD_LDS, "the bins of 8 waves fit the block's LDS");
+
 template <int B>
 __device__ __forceinline__ void dl_bins(const f32x16 (&acc)[2][4], const uint8_t* __restrict__ idx_packed,
                                         uint32_t lane, int wave, int t, int64_t i0, int64_t n, int64_t d, int64_t j0,
@@ -1236,7 +1247,7 @@ __device__ __forceinline__ void dl_bins(const f32x16 (&acc)[2][4], const uint8_t
   // and stay live across the K loop)
   asm volatile("" : "+v"(lane), "+v"(t));
   const uint32_t h = lane >> 5;
-  const uint32_t mine = (uint32_t)wave * 8192u + lane * 4u;
+  const uint32_t mine = (uint32_t)wave * DP_WAVE + lane * 4u;
   uint32_t w[2][4][B];
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
@@ -1249,46 +1260,60 @@ __device__ __forceinline__ void dl_bins(const f32x16 (&acc)[2][4], const uint8_t
     }
   }
 #pragma unroll
-  for (int q = 0; q < 2 * K; ++q) st_w((uint32_t)wave * 8192u + (uint32_t)(q / K) * 4096u + (uint32_t)(q % K) * 256u + lane * 4u, 0u);
+  for (int v = 0; v < 4; ++v)
 #pragma unroll
-  for (int a = 0; a < 2; ++a)
+    for (int c = 0; c < K; ++c) st_w(mine + (uint32_t)v * DP_COPY + (uint32_t)c * 256u, 0u);
+  // the four fields 8 q + 4 h .. + 3 of tile (a, b)'s unit, from bit 0 on
+  auto fields = [&](int a, int b, int q) -> uint32_t {
+    if constexpr (B == 4) {
+      return w[a][b][q] >> (16u * h);
+    } else if constexpr (B == 2) {
+      return w[a][b][q >> 1] >> (16u * (q & 1) + 8u * h);
+    } else {
+      const int b0 = 24 * q, b1 = 24 * q + 12;  // first bit for either half
+      const uint32_t w0 = h ? w[a][b][b1 >> 5] : w[a][b][b0 >> 5];
+      const uint32_t w1 = h ? w[a][b][(b1 >> 5) < 2 ? (b1 >> 5) + 1 : 2] : w[a][b][(b0 >> 5) < 2 ? (b0 >> 5) + 1 : 2];
+      return __builtin_amdgcn_alignbit(w1, w0, (24u * q + 12u * h) & 31u);
+    }
+  };
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      if (j0 + 128 * wn + 32 * b >= jend) continue;  // wave-uniform
+  for (int bb = 0; bb < 2; ++bb) {
+    // tiles bb and 2 + bb; a tile is inside the range or not as a whole
+    // (wave-uniform), and the second one is not when the first is not
+    if (j0 + 128 * wn + 32 * bb >= jend) break;
+    const bool two = j0 + 128 * wn + 64 + 32 * bb < jend;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        // the four fields 8 q + 4 h .. + 3 of the unit, from bit 0 of f on
-        uint32_t f;
-        if constexpr (B == 4) {
-          f = w[a][b][q] >> (16u * h);
-        } else if constexpr (B == 2) {
-          f = w[a][b][q >> 1] >> (16u * (q & 1) + 8u * h);
-        } else {
-          const uint32_t bit = 24u * q + 12u * h;  // at most 84: word and offset of the lane's half
-          const uint32_t w0 = h ? w[a][b][(24 * q + 12) >> 5] : w[a][b][(24 * q) >> 5];
-          const uint32_t w1 = h ? w[a][b][((24 * q + 12) >> 5) < 2 ? ((24 * q + 12) >> 5) + 1 : 2]
-                                : w[a][b][((24 * q) >> 5) < 2 ? ((24 * q) >> 5) + 1 : 2];
-          f = __builtin_amdgcn_alignbit(w1, w0, bit & 31u);
+    for (int q = 0; q < 4; ++q) {
+      uint32_t f[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) f[v] = fields(v >> 1, 2 * (v & 1) + bb, q);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t at[4];
+        float s[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          at[v] = mine + (uint32_t)v * DP_COPY + (((f[v] >> (B * k)) & (uint32_t)(K - 1)) << 8);
+          s[v] = __builtin_bit_cast(float, ld_w(at[v]));
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t c = (f >> (B * k)) & (uint32_t)(K - 1);
-          __hip_atomic_fetch_add((lds_f32*)(uintptr_t)(mine + (uint32_t)a * 4096u + (c << 8)), acc[a][b][4 * q + k],
-                                 __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        for (int v = 0; v < 4; ++v) {
+          const float x = acc[v >> 1][2 * (v & 1) + bb][4 * q + k];
+          st_w(at[v], __builtin_bit_cast(uint32_t, s[v] + ((v & 1) && !two ? 0.0f : x)));
         }
       }
     }
+  }
   __syncthreads();
   const uint32_t r = (uint32_t)t & 127u, c0 = ((uint32_t)t >> 7) * (uint32_t)(K / 4);
 #pragma unroll
   for (int k = 0; k < K / 4; ++k) {
     float s = bins[k];
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-        s += *(const lds_f32*)(uintptr_t)(((r >> 6) + 2u * v) * 8192u + ((r >> 5) & 1u) * 4096u + (c0 + k) * 256u +
-                                          ((r & 31u) + 32u * g) * 4u);
+    for (int v = 0; v < 16; ++v)  // column wave, copy, lane half
+      s += __builtin_bit_cast(float, ld_w(((r >> 6) + 2u * (v >> 2)) * DP_WAVE +
+                                          (2u * ((r >> 5) & 1u) + ((v >> 1) & 1)) * DP_COPY + (c0 + k) * 256u +
+                                          ((r & 31u) + 32u * (v & 1)) * 4u));
     bins[k] = s;
   }
 }

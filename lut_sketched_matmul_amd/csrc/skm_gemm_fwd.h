@@ -234,7 +234,7 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[4][2], TX* __rest
 //              is weight row r, token c: a lane then holds 32 outputs of one
 //              token (per 32-token tile) instead of 64 tokens of one row;
 //   EP::ROWS   the tokens are rows ep.rows[0 .. *ep.count - 1] of X (the count
-//              is read on the device; blocks past it leave at once);
+//              is read on the device; blocks without tokens leave at once);
 //   EP::run    takes the accumulators after the last K-step's barrier (all of
 //              the LDS is free).
 // EpStore is the plain matmul: Y rounded to TX.
@@ -266,8 +266,11 @@ k_gemm_fwd(const TX* __restrict__ X, const uint8_t* __restrict__ idx_packed, con
            const int32_t* __restrict__ rexp) {
   constexpr bool SC = scaled_pair(__is_same(TX, bf16_t), __is_same(TL, half_t));
   if constexpr (EP::ROWS) {
+    // the blocks that have tokens come first, so that they spread evenly over
+    // the XCDs (consecutive blocks go to different ones); the rest leave
     m = *ep.count;
-    if ((int64_t)(blockIdx.x % mblocks) * G_BM >= m) return;  // block-uniform
+    mblocks = (m + G_BM - 1) / G_BM;
+    if (blockIdx.x >= mblocks * ((n + G_BN - 1) / G_BN)) return;  // block-uniform
   }
   // The block's conversion mode of its activation rows (bf16 with f16 tables:
   // block_scale_mode). Everything after it is compiled once per mode (run<MD>),
@@ -531,8 +534,11 @@ k_gemm_fwd64(const TX* __restrict__ X, const uint8_t* __restrict__ idx_packed, c
              const int32_t* __restrict__ rexp) {
   constexpr bool SC = scaled_pair(__is_same(TX, bf16_t), __is_same(TL, half_t));
   if constexpr (EP::ROWS) {
+    // the blocks that have tokens come first, so that they spread evenly over
+    // the XCDs (consecutive blocks go to different ones); the rest leave
     m = *ep.count;
-    if ((int64_t)(blockIdx.x % mblocks) * G_BM >= m) return;  // block-uniform
+    mblocks = (m + G_BM - 1) / G_BM;
+    if (blockIdx.x >= mblocks * ((n + G_BN - 1) / G_BN)) return;  // block-uniform
   }
   // The block's conversion mode of its activation rows (bf16 with f16 tables:
   // block_scale_mode). Everything after it is compiled once per mode (run<MD>),

@@ -1,12 +1,14 @@
 // Cross entropy of a sketched head: the small kernels around the tiles (token
 // list, merge of the statistics, gather of X, dX's last sum) and the host
 // side that cuts the vocabulary into pieces. The mathematics is in skm_xent.h.
-#include "skm_xent.h"
 #include "skm_quant.h"
+#include "skm_xent.h"
 
 namespace skm {
 
 namespace {
+
+constexpr int XENT_BN = 256;  // vocabulary rows of a tile
 
 // ---- the list of tokens that have a target -----------------------------------------
 // One block (the list is one scan over m targets, 8 per thread and round).
@@ -130,6 +132,47 @@ __global__ void __launch_bounds__(256) k_xent_merge(const float2* __restrict__ p
   loss[t] = target >= 0 && target < V ? l - tlogit[c] : __builtin_nanf("");
 }
 
+// The same for few tokens: a block per token over its [blocks] pairs, ignored
+// tokens included.
+__global__ void __launch_bounds__(1024) k_xent_merge_few(const float2* __restrict__ part, int64_t blocks,
+                                                         const int64_t* __restrict__ targets, int64_t ignore,
+                                                         int64_t V, const float* __restrict__ tlogit,
+                                                         float* __restrict__ loss, float* __restrict__ lse) {
+  __shared__ float sm[16], ss[16];
+  const int64_t t = blockIdx.x;
+  const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
+  float mx = -__builtin_inff(), sum = 0.0f;
+  auto add = [&](float m2, float s2) {
+    const float nm = __builtin_fmaxf(mx, m2);
+    const float ref = nm == -__builtin_inff() ? 0.0f : nm;
+    sum = sum * __expf(mx - ref) + s2 * __expf(m2 - ref);
+    mx = nm;
+  };
+  for (int64_t v = threadIdx.x; v < blocks; v += 1024) {
+    const float2 p = part[t * blocks + v];
+    add(p.x, p.y);
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    const float m2 = __shfl_xor(mx, o, 64), s2 = __shfl_xor(sum, o, 64);
+    add(m2, s2);
+  }
+  if (lane == 0) {
+    sm[wave] = mx;
+    ss[wave] = sum;
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  mx = sm[0];
+  sum = ss[0];
+  for (int w = 1; w < 16; ++w) add(sm[w], ss[w]);
+  const int64_t target = targets[t];
+  const bool live = target != ignore;
+  const float l = (mx == -__builtin_inff() ? 0.0f : mx) + logf(sum);
+  lse[t] = live ? l : 0.0f;
+  loss[t] = !live ? 0.0f : (target >= 0 && target < V ? l - tlogit[t] : __builtin_nanf(""));
+}
+
 // ---- backward --------------------------------------------------------------------------
 
 // Xc[c] = X[rows[c]] for the listed tokens, zeros up to the next multiple of 32
@@ -173,21 +216,30 @@ __global__ void __launch_bounds__(256) k_xent_dx_out(const float* __restrict__ a
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// whether every launch of few tokens stages its activations (the largest does)
+bool few_stages(const Problem& p) {
+  return xent_decode_stages(Problem{p.m < 16 ? p.m : 16, p.n, p.d, p.b, p.gpr});
+}
+
 bool mixed(int x_dtype, int lut_dtype) { return scaled_pair(x_dtype == DT_BF16, lut_dtype == DT_F16); }
 
 // ---- workspace layouts -----------------------------------------------------------------
 struct FwdPlan {
+  bool few;
+  int64_t blocks;                          // vocabulary blocks of the statistics
   size_t rows, rexp, part, tlogit, bytes;  // byte offsets (the head is at 0)
 };
 FwdPlan fwd_plan(const Problem& p, int x_dtype, int lut_dtype) {
   FwdPlan f;
+  f.few = xent_few(p);
+  f.blocks = f.few ? (p.n + 15) / 16 : (p.n + XENT_BN - 1) / XENT_BN;
   size_t o = 256;
   f.rows = o;
   o += up256((size_t)p.m * 4);
   f.rexp = o;
   if (mixed(x_dtype, lut_dtype)) o += up256((size_t)p.m * 4);
   f.part = o;
-  o += up256((size_t)((p.n + G_BN - 1) / G_BN) * (size_t)p.m * 8);
+  o += up256((size_t)f.blocks * (size_t)p.m * 8);
   f.tlogit = o;
   o += up256((size_t)p.m * 4);
   f.bytes = o;
@@ -212,10 +264,10 @@ BwdPlan bwd_plan(const Problem& p, int x_dtype, int lut_dtype, bool need_dx, boo
   const bool has_hi = need_dlut || !mx, has_dxv = need_dx && mx;
   const int forms = (has_hi ? 1 : 0) + (need_dlut ? 1 : 0) + (has_dxv ? 1 : 0);
   f.cap = (p.m + 31) / 32 * 32;
-  int64_t P = (int64_t)(XENT_PIECE_BYTES / (size_t)(f.cap * 2 * forms)) / G_BN * G_BN;
-  if (P < G_BN) P = G_BN;
+  int64_t P = (int64_t)(XENT_PIECE_BYTES / (size_t)(f.cap * 2 * forms)) / XENT_BN * XENT_BN;
+  if (P < XENT_BN) P = XENT_BN;
   const int64_t pieces = (p.n + P - 1) / P;
-  P = ((p.n + pieces - 1) / pieces + G_BN - 1) / G_BN * G_BN;
+  P = ((p.n + pieces - 1) / pieces + XENT_BN - 1) / XENT_BN * XENT_BN;
   f.P = P;
   const int64_t n1 = p.n < P ? p.n : P;
   f.ranges = dx_ranges(Problem{p.m, n1, p.d, p.b, p.gpr});
@@ -250,6 +302,18 @@ template <typename T> T* at(void* ws, size_t off) { return reinterpret_cast<T*>(
 
 }  // namespace
 
+// Tokens for which the decode kernel, 16 per launch, beats the 256-token tiles:
+// each launch streams the indices once more, the tiles take one round of 256
+// blocks whatever the token count. Statistics of 4096 columns, b = 4: 32000
+// words 38 / 70 / 104 us for 16 / 32 / 48 tokens against 101 us, 128256 words
+// 142 / 272 / 400 us against 264 us; with few tiles (4000 words of 1024 columns,
+// b = 2) 18 / 21 / 24 / 27 us up to 64 tokens against 38 us.
+bool xent_few(const Problem& p) {
+  return p.m <= (p.n <= 16384 ? 64 : 32) && decode_supported(Problem{p.m < 16 ? p.m : 16, p.n, p.d, p.b, p.gpr});
+}
+
+bool xent_decode_stages(const Problem& p) { return p.m * p.d <= 32768; }
+
 size_t xent_fwd_bytes(const Problem& p, int x_dtype, int lut_dtype) { return fwd_plan(p, x_dtype, lut_dtype).bytes; }
 
 hipError_t launch_xent_fwd(const XentArgs& a, float* loss, float* lse, void* ws, hipStream_t s) {
@@ -260,16 +324,25 @@ hipError_t launch_xent_fwd(const XentArgs& a, float* loss, float* lse, void* ws,
   int32_t* rexp = mixed(a.x_dtype, a.lut_dtype) ? at<int32_t>(ws, f.rexp) : nullptr;
   float2* part = at<float2>(ws, f.part);
   float* tlogit = at<float>(ws, f.tlogit);
+  const XentGemm g{a.X, a.x_dtype, a.idx, a.lut, a.lut_dtype, p, rows, head, a.targets, rexp, 0};
+  hipError_t e = hipSuccess;
+  if (f.few) {
+    if (rexp && !few_stages(p)) e = launch_row_exp(a.X, p.m, p.d, rexp, s);
+    if (e == hipSuccess) e = xent_few_stats(g, part, f.blocks, tlogit, s);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k_xent_merge_few, dim3((unsigned)p.m), dim3(1024), 0, s, part, f.blocks, a.targets, a.ignore,
+                       p.n, tlogit, loss, lse);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(k_xent_index<false>, dim3(1), dim3(1024), 0, s, a.targets, a.ignore, p.m, nullptr, head, rows,
                      nullptr, loss, lse);
-  hipError_t e = hipGetLastError();
+  e = hipGetLastError();
   if (e == hipSuccess && rexp) e = launch_row_exp(a.X, p.m, p.d, rexp, s);
   if (e != hipSuccess) return e;
-  const XentGemm g{a.X, a.x_dtype, a.idx, a.lut, a.lut_dtype, p, rows, head, a.targets, rexp, 0};
   e = xent_stats(g, part, p.m, tlogit, s);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k_xent_merge, dim3((unsigned)((p.m + 15) / 16)), dim3(256), 0, s, part, p.m,
-                     (int)((p.n + G_BN - 1) / G_BN), head, rows, a.targets, p.n, tlogit, loss, lse);
+                     (int)f.blocks, head, rows, a.targets, p.n, tlogit, loss, lse);
   return hipGetLastError();
 }
 
@@ -300,6 +373,7 @@ hipError_t launch_xent_bwd(const XentArgs& a, const float* lse, const float* dlo
                        (uint16_t*)xc);
     e = hipGetLastError();
   }
+  const bool few = xent_few(p);
   const int es = 2;  // bytes of a table entry (16-bit pairs only)
   for (int64_t v0 = 0; v0 < p.n && e == hipSuccess; v0 += f.P) {
     const int64_t n = p.n - v0 < f.P ? p.n - v0 : f.P;
@@ -308,7 +382,8 @@ hipError_t launch_xent_bwd(const XentArgs& a, const float* lse, const float* dlo
     const void* lut = static_cast<const char*>(a.lut) + v0 * p.gpr * p.k() * es;
     const int64_t ld = (n + 7) / 8 * 8;
     const XentGemm g{a.X, a.x_dtype, idx, lut, a.lut_dtype, q, rows, head, a.targets, rexp, v0};
-    e = xent_grad(g, {lse, dloss, p.n, ld, hi, lo, dxv}, s);
+    const XentGradOut out{lse, dloss, p.n, ld, hi, lo, dxv};
+    e = few ? xent_few_grad(g, out, pos, s) : xent_grad(g, out, s);
     if (e == hipSuccess && dX) {
       // every range of the first piece is written; later pieces add to some or all
       const int64_t steps = (n + 63) / 64;

@@ -1,0 +1,113 @@
+// Cross entropy of few tokens: the decode kernel (skm_decode.h) ends in softmax
+// statistics (EpDecodeStats) or in the logits' gradient (EpDecodeGrad). It
+// reads the indices once per 16 tokens, where the 256-token tiles would spend
+// most of their matrix work on padding.
+#pragma once
+
+#include "skm_decode.h"
+#include "skm_xent.h"
+
+namespace skm {
+
+namespace {
+
+// part[t0 + token][block] = (max, sum of exp(z - max)) over the block's 16 words
+template <typename TX> struct EpDecodeStats {
+  struct Args {
+    const int64_t* targets;  // [m]
+    float2* part;
+    int64_t blocks;
+    float* tlogit;
+    int64_t t0;
+  };
+  static __device__ __forceinline__ void put(const Args& ep, bool ok, int token, int64_t row, float v, int m,
+                                             int64_t n) {
+    const float z = ok ? v : -__builtin_inff();
+    float mx = z;
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) mx = __builtin_fmaxf(mx, __shfl_xor(mx, o, 64));
+    const float ref = mx == -__builtin_inff() ? 0.0f : mx;
+    float sum = ok ? __expf(z - ref) : 0.0f;
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
+    if (token >= m) return;
+    if (row % DEC_ROWS == 0) ep.part[(ep.t0 + token) * ep.blocks + row / DEC_ROWS] = float2{mx, sum};
+    if (ok && ep.targets[ep.t0 + token] == row) ep.tlogit[ep.t0 + token] = v;
+  }
+};
+
+// dZ of the listed tokens among t0 .. t0 + m - 1, in the forms of EpGrad;
+// the first launch also writes the zero rows that pad the list
+template <typename TX, typename TL> struct EpDecodeGrad {
+  struct Args {
+    const int32_t* pos;  // listed row of every token, -1 = ignored
+    const XentHead* head;
+    const int64_t* targets;
+    const float* lse;
+    const float* dloss;
+    int64_t V, v0, ld, t0;
+    TX* hi;
+    TX* lo;
+    TL* dxv;
+  };
+  static __device__ __forceinline__ void store(const Args& ep, int64_t at, float g) {
+    if (ep.hi) {
+      const TX h = from_f32<TX>(g);
+      ep.hi[at] = h;
+      if (ep.lo) ep.lo[at] = from_f32<TX>(g - to_f32(h));
+    }
+    if (ep.dxv) ep.dxv[at] = from_f32<TL>(g);
+  }
+  static __device__ __forceinline__ void put(const Args& ep, bool ok, int token, int64_t row, float v, int m,
+                                             int64_t n) {
+    if (row >= ep.ld) return;
+    if (ep.t0 == 0) {
+      const int64_t count = ep.head->count, pad = (count + 31) / 32 * 32;
+      for (int64_t c = count + token; c < pad; c += 16) store(ep, c * ep.ld + row, 0.0f);
+    }
+    if (token >= m) return;
+    const int64_t t = ep.t0 + token;
+    const int64_t c = ep.pos[t];
+    if (c < 0) return;
+    const int64_t target = ep.targets[t];
+    const float gs = target >= 0 && target < ep.V ? ep.dloss[t] * ep.head->scale : __builtin_nanf("");
+    const float p = __expf(v - ep.lse[t]) - (ep.v0 + row == target ? 1.0f : 0.0f);
+    store(ep, c * ep.ld + row, ok ? p * gs : 0.0f);
+  }
+};
+
+// one launch of at most 16 tokens. The vocabulary has many 16-row blocks: 8
+// waves each, two or more blocks per CU (as the plain decode above 384 blocks)
+template <int B, typename TX, typename TL, typename EP>
+hipError_t xent_decode_b(const TX* X, const uint8_t* idx, const TL* lut, const Problem& p,
+                         const typename EP::Args& ep, const int32_t* rexp, hipStream_t s) {
+  const uint32_t ug = (uint32_t)(p.group_cols() / 32);
+  const uint32_t magic = ug == 1 ? 0u : (uint32_t)((((uint64_t)1) << 32) / ug + 1);
+  SetArgs sa;
+  sa.rexp = rexp;
+  const bool xl = xent_decode_stages(p), xt = !xl && p.m >= DEC_XT_MIN_M;
+  if (p.units() % 4 != 0)
+    return xl ? decode_launch<B, 8, TX, TL, true, true, false, EP>(X, idx, lut, p, ep, s, magic, sa)
+              : (xt ? decode_launch<B, 8, TX, TL, true, false, true, EP>(X, idx, lut, p, ep, s, magic, sa)
+                    : decode_launch<B, 8, TX, TL, true, false, false, EP>(X, idx, lut, p, ep, s, magic, sa));
+  return xl ? decode_launch<B, 8, TX, TL, false, true, false, EP>(X, idx, lut, p, ep, s, magic, sa)
+            : (xt ? decode_launch<B, 8, TX, TL, false, false, true, EP>(X, idx, lut, p, ep, s, magic, sa)
+                  : decode_launch<B, 8, TX, TL, false, false, false, EP>(X, idx, lut, p, ep, s, magic, sa));
+}
+
+// all m tokens, 16 per launch; `ep` with t0 = 0
+template <int B, typename TX, typename TL, typename EP>
+hipError_t xent_decode_all(const XentGemm& g, typename EP::Args ep, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  for (int64_t t0 = 0; t0 < g.p.m && e == hipSuccess; t0 += 16) {
+    const Problem q{g.p.m - t0 < 16 ? g.p.m - t0 : 16, g.p.n, g.p.d, g.p.b, g.p.gpr};
+    ep.t0 = t0;
+    e = xent_decode_b<B, TX, TL, EP>((const TX*)g.X + t0 * g.p.d, g.idx, (const TL*)g.lut, q, ep,
+                                     g.rexp ? g.rexp + t0 : nullptr, s);
+  }
+  return e;
+}
+
+}  // namespace
+
+}  // namespace skm

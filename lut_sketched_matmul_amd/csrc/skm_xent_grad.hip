@@ -1,6 +1,6 @@
 // Cross entropy backward: the instances of the matmul's tiles that end in the
 // logits' gradient (EpGrad).
-#include "skm_xent.h"
+#include "skm_xent_tiles.h"
 
 namespace skm {
 

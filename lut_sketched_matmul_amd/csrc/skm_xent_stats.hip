@@ -1,6 +1,6 @@
 // Cross entropy forward: the instances of the matmul's tiles that end in
 // softmax statistics (EpStats).
-#include "skm_xent.h"
+#include "skm_xent_tiles.h"
 
 namespace skm {
 

@@ -389,6 +389,9 @@ def check_xent(name, m, V, d, b, gpr, io, ldt, ignored="some", sigma=1.0, dscale
     (1, 1, 32, 4, 1), (1, 7, 64, 2, 1), (2, 255, 64, 3, 2), (3, 256, 96, 4, 1), (16, 257, 128, 4, 4),
     (17, 300, 512, 4, 1), (31, 1000, 256, 3, 2), (33, 520, 576, 2, 2), (64, 129, 512, 4, 8), (257, 1001, 320, 4, 1),
     (300, 2050, 512, 3, 1),
+    # few tokens: activations per slot (below and from 8 tokens on, ragged slots), the last few tokens and the
+    # first many, tables too large for the decode
+    (5, 300, 8192, 4, 4), (16, 130, 2112, 2, 1), (64, 100, 1024, 3, 4), (65, 257, 128, 4, 2), (4, 90, 512, 4, 16),
 ])
 def test_xent(m, V, d, b, gpr, io, ldt):
     check_xent(f"xent/{m}/{V}/{d}/{b}/{io}/{ldt}", m, V, d, b, gpr, io, ldt, ignored="some" if m > 2 else "none")
