@@ -57,12 +57,10 @@ using namespace mm;
 
 // LDS buffer index of a K-step not known at compile time (else mm::buf_tag)
 struct buf_rt { uint32_t value; };
-template <bool V> struct bool_tag { static constexpr bool value = V; };
 
-// Both products also run with PA = DxPiece / DlPiece instead of Whole, for the
-// operators that own their operands' layout (cross entropy: a range of the
-// vocabulary at a time, tokens counted on the device; the backward from an
-// 8-bit checkpoint: X in a padded workspace).
+// dX also runs with PA = DxPiece instead of Whole, for the operators that own
+// their operands' layout (cross entropy: a range of the vocabulary at a time,
+// tokens counted on the device; the backward from an 8-bit checkpoint).
 struct Whole {
   static constexpr bool PIECE = false;
 };
@@ -74,15 +72,6 @@ struct DxPiece {
   int splits;            // the weight rows are cut into this many ranges,
   int64_t split_rows;    // of this many rows (a multiple of 64), each with its
   int64_t part_stride;   // own dX, part_stride floats apart
-};
-struct DlPiece {
-  static constexpr bool PIECE = true;
-  const int32_t* count;    // tokens; NULL = m. X holds zeros up to a multiple of 32
-  int64_t ldy;             // row stride of dY, as above
-  int64_t lo_off;          // dY + lo_off: a second addend of dY, 0 = none
-  const float* inv_scale;  // the sums are multiplied by *inv_scale; NULL = 1
-  const void* zeros;       // 16 zero bytes read in place of dY's rows past the
-                           // tokens; NULL = those rows exist and hold zeros
 };
 
 // ============================================================================
@@ -1187,21 +1176,6 @@ __device__ __forceinline__ void dd_dma16(const void* src, uint32_t lds) {
       : "memory");
 }
 
-// The same without a compiler fence, for copies placed between reads of other
-// stages and MFMAs (dd_barrier and the waits keep them apart from the reads of
-// their own stage).
-__device__ __forceinline__ void dd_dma16_free(const void* src, uint32_t lds) {
-  uint32_t keep;
-  asm volatile(
-      "s_mov_b32 %0, m0\n\t"
-      "s_mov_b32 m0, %2\n\t"
-      "s_nop 0\n\t"
-      "global_load_lds_dwordx4 %1, off\n\t"
-      "s_mov_b32 m0, %0"
-      : "=&s"(keep)
-      : "v"(src), "s"(lds));
-}
-
 // raw barrier, with compiler-only fences so that no LDS access moves across it
 __device__ __forceinline__ void dd_barrier() {
   asm volatile("" ::: "memory");
@@ -1217,130 +1191,12 @@ __device__ __forceinline__ void dd_wait_vmcnt() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
-// ---- binning with private bins (DlPiece) ------------------------------------
-// The MFMA operands are exchanged, so a lane holds one weight row i = 64 wm +
-// 32 a + lane % 32 and, per 32-column tile b, the 16 columns 8 q + 4 (lane /
-// 32) + k. Every lane adds into its own copies of its row's bins, entry-major
-// / lane-minor (per wave [a][b / 2][entry][64 lanes], 128 KB in all, over the
-// operand ring, which is free between chunks): the 64 lanes of an access hit
-// 64 banks whatever the indices are, and since no other lane touches a copy,
-// an addition is a read, an add and a write. (An LDS fp32 atomic add takes 3
-// cycles per lane: 92 us for the 65536 additions of a block, the whole cost of
-// a call with few tokens; with 8192 tokens a chunk's matrix work takes 200 us.)
-// The four copies of a wave are four independent chains of 32 additions, which
-// hides most of the read latency. A lane's indices are whole 32-column units
-// of its row, loaded straight into registers. The sixteen copies of an entry
-// (4 column waves x 2 x 2 lane halves) are then added in a fixed order into
-// the registers of the thread that owns it: thread t has entries K/4 (t / 128)
-// .. of row t % 128.
-constexpr uint32_t DP_COPY = 16u * 256u;      // one copy: 16 entries x 64 lanes
-constexpr uint32_t DP_WAVE = 4u * DP_COPY;
-static_assert(8u * DP_WAVE <= DD_LDS, "the bins of 8 waves fit the block's LDS");
-
-template <int B>
-__device__ __forceinline__ void dl_bins(const f32x16 (&acc)[2][4], const uint8_t* __restrict__ idx_packed,
-                                        uint32_t lane, int wave, int t, int64_t i0, int64_t n, int64_t d, int64_t j0,
-                                        int64_t jend, float (&bins)[4]) {
-  constexpr int K = 1 << B;
-  const int wm = wave & 1, wn = wave >> 1;
-  // (opaque copies: the addresses below would be hoisted out of the chunk loop
-  // and stay live across the K loop)
-  asm volatile("" : "+v"(lane), "+v"(t));
-  const uint32_t h = lane >> 5;
-  const uint32_t mine = (uint32_t)wave * DP_WAVE + lane * 4u;
-  uint32_t w[2][4][B];
-#pragma unroll
-  for (int a = 0; a < 2; ++a) {
-    const int64_t i = i0 + 64 * wm + 32 * a + (lane & 31u);
-    const uint8_t* row = idx_packed + (i < n ? i : n - 1) * (d * B / 8);
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int64_t j = j0 + 128 * wn + 32 * b;  // (past the range: any unit of the row, its sums are dropped)
-      load_unit<B>(row, (j < jend ? j : j0) / 32, w[a][b]);
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < 4; ++v)
-#pragma unroll
-    for (int c = 0; c < K; ++c) st_w(mine + (uint32_t)v * DP_COPY + (uint32_t)c * 256u, 0u);
-  // the four fields 8 q + 4 h .. + 3 of tile (a, b)'s unit, from bit 0 on
-  auto fields = [&](int a, int b, int q) -> uint32_t {
-    if constexpr (B == 4) {
-      return w[a][b][q] >> (16u * h);
-    } else if constexpr (B == 2) {
-      return w[a][b][q >> 1] >> (16u * (q & 1) + 8u * h);
-    } else {
-      const int b0 = 24 * q, b1 = 24 * q + 12;  // first bit for either half
-      const uint32_t w0 = h ? w[a][b][b1 >> 5] : w[a][b][b0 >> 5];
-      const uint32_t w1 = h ? w[a][b][(b1 >> 5) < 2 ? (b1 >> 5) + 1 : 2] : w[a][b][(b0 >> 5) < 2 ? (b0 >> 5) + 1 : 2];
-      return __builtin_amdgcn_alignbit(w1, w0, (24u * q + 12u * h) & 31u);
-    }
-  };
-#pragma unroll
-  for (int bb = 0; bb < 2; ++bb) {
-    // tiles bb and 2 + bb; a tile is inside the range or not as a whole
-    // (wave-uniform), and the second one is not when the first is not
-    if (j0 + 128 * wn + 32 * bb >= jend) break;
-    const bool two = j0 + 128 * wn + 64 + 32 * bb < jend;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t f[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) f[v] = fields(v >> 1, 2 * (v & 1) + bb, q);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t at[4];
-        float s[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          at[v] = mine + (uint32_t)v * DP_COPY + (((f[v] >> (B * k)) & (uint32_t)(K - 1)) << 8);
-          s[v] = __builtin_bit_cast(float, ld_w(at[v]));
-        }
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float x = acc[v >> 1][2 * (v & 1) + bb][4 * q + k];
-          st_w(at[v], __builtin_bit_cast(uint32_t, s[v] + ((v & 1) && !two ? 0.0f : x)));
-        }
-      }
-    }
-  }
-  __syncthreads();
-  const uint32_t r = (uint32_t)t & 127u, c0 = ((uint32_t)t >> 7) * (uint32_t)(K / 4);
-#pragma unroll
-  for (int k = 0; k < K / 4; ++k) {
-    float s = bins[k];
-#pragma unroll
-    for (int v = 0; v < 16; ++v)  // column wave, copy, lane half
-      s += __builtin_bit_cast(float, ld_w(((r >> 6) + 2u * (v >> 2)) * DP_WAVE +
-                                          (2u * ((r >> 5) & 1u) + ((v >> 1) & 1)) * DP_COPY + (c0 + k) * 256u +
-                                          ((r & 31u) + 32u * (v & 1)) * 4u));
-    bins[k] = s;
-  }
-}
-
-// the block's entries, times scale
-template <int B>
-__device__ __forceinline__ void dl_put_bins(float* __restrict__ dLUT, int64_t i0, int64_t n, int gpr, int g,
-                                            int accumulate, int t, const float (&bins)[4], float scale) {
-  constexpr int K = 1 << B;
-  const int64_t i = i0 + (t & 127);
-  if (i >= n) return;
-  float* dst = dLUT + (i * gpr + g) * K + (t >> 7) * (K / 4);
-#pragma unroll
-  for (int k = 0; k < K / 4; ++k) dst[k] = accumulate ? dst[k] + bins[k] * scale : bins[k] * scale;
-}
-
-template <int B, typename TX, typename PA>
+template <int B, typename TX>
 __global__ void __launch_bounds__(512, 1)
 k_gemm_dlut_dma(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8_t* __restrict__ idx_packed,
                 int64_t m, int64_t n, int64_t d, int gpr, int gband, float* __restrict__ dLUT, int accumulate,
-                int tsplits, int csplits, int64_t split_tokens, int64_t split_cols, int64_t part_stride, PA pa) {
+                int tsplits, int csplits, int64_t split_tokens, int64_t split_cols, int64_t part_stride) {
   typedef mfma32<TX> MF;
-  int64_t ldy = n;
-  if constexpr (PA::PIECE) {
-    ldy = pa.ldy;
-    if (pa.count) m = *pa.count;
-  }
   extern __shared__ uint32_t smem[];  // dynamic LDS only: starts at address 0
   (void)smem;
 
@@ -1357,7 +1213,7 @@ k_gemm_dlut_dma(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8
   const uint32_t cr = sp / (uint32_t)tsplits;  // column range of the group
   {
     const int64_t tok0 = (int64_t)(sp % (uint32_t)tsplits) * split_tokens;
-    dY += tok0 * ldy;
+    dY += tok0 * n;
     X += tok0 * d;
     m = m - tok0 < split_tokens ? m - tok0 : split_tokens;
     dLUT += (int64_t)sp * part_stride;
@@ -1370,37 +1226,22 @@ k_gemm_dlut_dma(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8
   // this block's columns of the group: column range cr (whole chunks)
   const int64_t jg0 = (int64_t)g * G + (int64_t)cr * split_cols;
   const int64_t jend = (int64_t)g * G + G < jg0 + split_cols ? (int64_t)g * G + G : jg0 + split_cols;
-  // (a piece's token range may start past the tokens that exist: no step)
-  const int K1 = PA::PIECE ? (m <= 0 ? 0 : (int)((m + DL_BK - 1) / DL_BK)) : (int)(m / DL_BK);
-  // steps: the tokens once, or with a second addend of dY twice
-  int KS = K1;
-  if constexpr (PA::PIECE)
-    if (pa.lo_off != 0) KS = 2 * K1;
+  const int KS = (int)(m / DL_BK);
 
-  if constexpr (!PA::PIECE)
-    for (uint32_t q = (uint32_t)t; q < 4u * DD_BCOPY / 4u; q += 512u) st_w(DD_BINS + q * 4u, 0u);
+  for (uint32_t q = (uint32_t)t; q < 4u * DD_BCOPY / 4u; q += 512u) st_w(DD_BINS + q * 4u, 0u);
 
   // ---- DMA roles: this wave's token rows 4 wave .. +3. dY: one 1 KB
   // instruction (lane = row (lane / 16) x slot (lane % 16)); X: one
   // instruction per row (lane = slot).
   const uint32_t ycg = (lane & 15u) ^ (((lane >> 4) & 3u) << 2);
-  const int64_t yrow = i0 + 8 * (int64_t)ycg <= ldy - 8 ? i0 + 8 * (int64_t)ycg : ldy - 8;
-  const TX* ysrc = dY + (int64_t)(4u * (uint32_t)wave + (lane >> 4)) * ldy + yrow;
+  const int64_t yrow = i0 + 8 * (int64_t)ycg <= n - 8 ? i0 + 8 * (int64_t)ycg : n - 8;
+  const TX* ysrc = dY + (int64_t)(4u * (uint32_t)wave + (lane >> 4)) * n + yrow;
   const uint32_t ydst = 1024u * (uint32_t)wave;
-  const int64_t ystep = (int64_t)DL_BK * ldy;
+  const int64_t ystep = (int64_t)DL_BK * n;
   const int64_t xstep = (int64_t)DL_BK * d;
   const TX* xsrc[4];
   auto dma = [&](int k, uint32_t stage) {
-    int64_t lo = 0;
-    if constexpr (PA::PIECE)
-      if (k >= K1) {  // uniform
-        k -= K1;
-        lo = pa.lo_off;
-      }
-    const void* ys = ysrc + (lo + (int64_t)k * ystep);
-    if constexpr (PA::PIECE)
-      if (pa.zeros && k == K1 - 1 && (int64_t)k * DL_BK + 4 * wave + (int)(lane >> 4) >= m) ys = pa.zeros;
-    dd_dma16(ys, stage + ydst);
+    dd_dma16(ysrc + (int64_t)k * ystep, stage + ydst);
 #pragma unroll
     for (int h = 0; h < 4; ++h) dd_dma16(xsrc[h] + (int64_t)k * xstep, stage + DD_TA + 1024u * (4u * (uint32_t)wave + h));
   };
@@ -1439,10 +1280,8 @@ k_gemm_dlut_dma(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        acc[a][b] = PA::PIECE ? MF::run(bf[b], af[a], acc[a][b]) : MF::run(af[a], bf[b], acc[a][b]);
+      for (int b = 0; b < 4; ++b) acc[a][b] = MF::run(af[a], bf[b], acc[a][b]);
   };
-  float bins[PA::PIECE ? 4 : 1] = {};  // PIECE: the thread's entries (dl_bins)
   // a half step's 8 MFMAs interleaved with the other half's 12 reads
   auto interleave = [&]() {
 #pragma unroll
@@ -1453,7 +1292,7 @@ k_gemm_dlut_dma(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  for (int64_t j0 = jg0; j0 < jend && (!PA::PIECE || KS > 0); j0 += DL_BN) {
+  for (int64_t j0 = jg0; j0 < jend; j0 += DL_BN) {
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
       const int64_t col = j0 + 8 * (int64_t)(lane ^ ((uint32_t)h << 2));
@@ -1480,106 +1319,33 @@ k_gemm_dlut_dma(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8
     u32x4 a0[2], b0[4], a1[2], b1[4];
     uint32_t st = 0u;  // stage of step k
     read_half(st, 0, a0, b0);
-    if constexpr (PA::PIECE) {
-      // The copies of step k+2 are issued between the MFMAs of the first half:
-      // issued together at the head of the step they held the matrix core up
-      // (both waves of a SIMD are there at the same time). Their addresses
-      // advance by a step's worth of rows, and go back to the first rows of X
-      // (and on to dY's second addend) after the last step of the first addend.
-      const char* ys = reinterpret_cast<const char*>(ysrc + (K1 > 2 ? 2 * ystep : pa.lo_off + (2 - K1) * ystep));
-      const char* xs[4];
-#pragma unroll
-      for (int h = 0; h < 4; ++h)
-        xs[h] = reinterpret_cast<const char*>(xsrc[h] + (K1 > 2 ? 2 * xstep : (2 - K1) * xstep));
-      // lanes whose row of dY in the last step is past the tokens
-      const bool past = pa.zeros && (int64_t)(K1 - 1) * DL_BK + 4 * wave + (int)(lane >> 4) >= m;
-      auto step = [&](int k, auto more) __attribute__((always_inline)) {
-        constexpr bool MORE = decltype(more)::value;
-        const uint32_t st2 = st >= DD_STAGE ? st - DD_STAGE : st + 2u * DD_STAGE;  // stage of step k+2
-        const void* yl = ys;
-        if constexpr (MORE)
-          if (pa.zeros && k + 2 == K1 - 1) yl = past ? pa.zeros : yl;
-        // (each group pinned: three reads, two MFMAs, the copies)
-        u32x2 lo[6], hi[6];  // of a1[0], a1[1], b1[0] .. b1[3]
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-#pragma unroll
-          for (int r = 3 * q; r < 3 * q + 3; ++r) {
-            const int f = r >> 1;  // fragment
-            const uint32_t p = f < 2 ? st + fa[f] + 16u * 256u : st + fb[f - 2] + 16u * 1024u;
-            (r & 1 ? hi : lo)[f] = ld_tr(p + (r & 1 ? (f < 2 ? 4u * 256u : 4u * 1024u) : 0u));
-          }
-          const int a = q >> 1, b = 2 * (q & 1);
-          acc[a][b] = MF::run(b0[b], a0[a], acc[a][b]);
-          acc[a][b + 1] = MF::run(b0[b + 1], a0[a], acc[a][b + 1]);
-          if constexpr (MORE) {
-            if (q == 0) dd_dma16_free(yl, st2 + ydst);
-            dd_dma16_free(xs[q], st2 + DD_TA + 1024u * (4u * (uint32_t)wave + q));
-          }
-          __builtin_amdgcn_sched_barrier(0);
-        }
-#pragma unroll
-        for (int f = 0; f < 6; ++f) (f < 2 ? a1[f & 1] : b1[(f - 2) & 3]) = u32x4{lo[f].x, lo[f].y, hi[f].x, hi[f].y};
-        if constexpr (MORE) {
-          ys += ystep * 2;
-#pragma unroll
-          for (int h = 0; h < 4; ++h) xs[h] += xstep * 2;
-          if (k + 3 == K1) {  // step k+3 is the first of the second addend
-            ys += (pa.lo_off - (int64_t)K1 * ystep) * 2;
-#pragma unroll
-            for (int h = 0; h < 4; ++h) xs[h] -= (int64_t)K1 * xstep * 2;
-          }
-        }
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): every read of stage k has landed
-        if constexpr (MORE) dd_wait_vmcnt<5>();
-        else dd_wait_vmcnt<0>();
-        dd_barrier();
-        st = st + DD_STAGE == 3u * DD_STAGE ? 0u : st + DD_STAGE;
-        read_half(st, 0, a0, b0);
-        mfma_half(a1, b1);
-        interleave();
-      };
-      int k = 0;
-      for (; k + 2 < KS; ++k) step(k, bool_tag<true>{});
-      for (; k < KS; ++k) step(k, bool_tag<false>{});
-    } else {
-      for (int k = 0; k < KS; ++k) {
-        const uint32_t st2 = st >= DD_STAGE ? st - DD_STAGE : st + 2u * DD_STAGE;  // stage of step k+2
-        // (stage k+2 = stage k-1: every wave finished reading it before the last barrier)
-        if (k + 2 < KS) dma(k + 2, st2);
-        read_half(st, 1, a1, b1);
-        mfma_half(a0, b0);
-        interleave();
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): every read of stage k has landed
-        // this wave's DMA of step k+1 has landed (the one of step k+2 may not)
-        if (k + 2 < KS) dd_wait_vmcnt<5>();
-        else dd_wait_vmcnt<0>();
-        dd_barrier();
-        st = st + DD_STAGE == 3u * DD_STAGE ? 0u : st + DD_STAGE;
-        // (unconditional, so that the reads interleave with the MFMAs: after
-        // the last step they read a stale stage and the values go unused)
-        read_half(st, 0, a0, b0);
-        mfma_half(a1, b1);
-        interleave();
-      }
+    for (int k = 0; k < KS; ++k) {
+      const uint32_t st2 = st >= DD_STAGE ? st - DD_STAGE : st + 2u * DD_STAGE;  // stage of step k+2
+      // (stage k+2 = stage k-1: every wave finished reading it before the last barrier)
+      if (k + 2 < KS) dma(k + 2, st2);
+      read_half(st, 1, a1, b1);
+      mfma_half(a0, b0);
+      interleave();
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): every read of stage k has landed
+      // this wave's DMA of step k+1 has landed (the one of step k+2 may not)
+      if (k + 2 < KS) dd_wait_vmcnt<5>();
+      else dd_wait_vmcnt<0>();
+      dd_barrier();
+      st = st + DD_STAGE == 3u * DD_STAGE ? 0u : st + DD_STAGE;
+      // (unconditional, so that the reads interleave with the MFMAs: after
+      // the last step they read a stale stage and the values go unused)
+      read_half(st, 0, a0, b0);
+      mfma_half(a1, b1);
+      interleave();
     }
     dd_wait_vmcnt<0>();  // (no copy is in flight here; the compiler does not count them)
 
-    if constexpr (PA::PIECE) {
-      dl_bins<B>(acc, idx_packed, lane, wave, t, i0, n, d, j0, jend, bins);
-    } else {
-      dl_stage_indices<B>(idx_packed, i0, n, d, j0, jend, t);
-      __syncthreads();
-      dl_scatter<B>(acc, lane, wm, wn, i0, n, j0, jend, DD_BINS + (uint32_t)wn * DD_BCOPY, DD_BRS);
-    }
-  }
-  if constexpr (PA::PIECE) {
-    const float scale = pa.inv_scale ? *pa.inv_scale : 1.0f;
-    dl_put_bins<B>(dLUT, i0, n, gpr, g, accumulate, t, bins, scale);
-  } else {
+    dl_stage_indices<B>(idx_packed, i0, n, d, j0, jend, t);
     __syncthreads();
-    dl_store_bins<B>(dLUT, i0, n, gpr, g, DD_BINS, DD_BCOPY, DD_BRS, accumulate, t);
+    dl_scatter<B>(acc, lane, wm, wn, i0, n, j0, jend, DD_BINS + (uint32_t)wn * DD_BCOPY, DD_BRS);
   }
+  __syncthreads();
+  dl_store_bins<B>(dLUT, i0, n, gpr, g, DD_BINS, DD_BCOPY, DD_BRS, accumulate, t);
 }
 
 // ---- launchers ---------------------------------------------------------------
@@ -1716,10 +1482,10 @@ hipError_t dlut_launch(const TX* dY, const TX* X, const uint8_t* idx, const Prob
   return e;
 }
 
-template <int B, typename TX, typename PA>
+template <int B, typename TX>
 hipError_t dlut_dma_launch(const TX* dY, const TX* X, const uint8_t* idx, const Problem& p, float* dLUT,
-                           int accumulate, float* part, const PA& pa, hipStream_t s) {
-  const auto kern = k_gemm_dlut_dma<B, TX, PA>;
+                           int accumulate, float* part, hipStream_t s) {
+  const auto kern = k_gemm_dlut_dma<B, TX>;
   static const hipError_t prep = prepare_kernel((const void*)kern, DD_LDS);
   if (prep != hipSuccess) return prep;
   const int64_t rb = (p.n + DL_BM - 1) / DL_BM;
@@ -1730,7 +1496,7 @@ hipError_t dlut_dma_launch(const TX* dY, const TX* X, const uint8_t* idx, const 
   const bool split = sp.parts() > 1;
   hipLaunchKernelGGL(kern, dim3((unsigned)(rb * p.gpr * sp.parts())), dim3(512), DD_LDS, s, dY, X, idx, p.m, p.n,
                      p.d, p.gpr, gband, split ? part : dLUT, split ? 0 : accumulate, sp.tsplits, sp.csplits,
-                     sp.tokens, sp.cols, count, pa);
+                     sp.tokens, sp.cols, count);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && split) e = dlut_reduce(part, sp.parts(), count, dLUT, accumulate, s);
   return e;

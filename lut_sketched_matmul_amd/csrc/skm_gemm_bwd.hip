@@ -21,7 +21,7 @@ hipError_t dlut_b(const TX* dY, const TX* X, const uint8_t* idx, const Problem& 
                   float* part, hipStream_t s) {
   // DMA staging: whole 32-token steps and 16-byte aligned dY rows
   if (p.m % DL_BK == 0 && p.n % 8 == 0)
-    return dlut_dma_launch<B, TX>(dY, X, idx, p, dLUT, accumulate, part, Whole{}, s);
+    return dlut_dma_launch<B, TX>(dY, X, idx, p, dLUT, accumulate, part, s);
   if (p.n % 8 == 0) return dlut_launch<B, TX, true>(dY, X, idx, p, dLUT, accumulate, part, s);
   return dlut_launch<B, TX, false>(dY, X, idx, p, dLUT, accumulate, part, s);
 }

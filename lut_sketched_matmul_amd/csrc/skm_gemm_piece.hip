@@ -1,7 +1,7 @@
-// The backward products with the caller's own operand layout (DxPiece,
-// DlPiece of skm_gemm_bwd.h): ranges of the weight rows, padded token rows, a
-// token count on the device.
-#include "skm_gemm_bwd.h"
+// The backward products with the caller's own operand layout (DxPiece of
+// skm_gemm_bwd.h, DlPiece of skm_gemm_dlut.h): ranges of the weight rows,
+// padded token rows, a token count on the device.
+#include "skm_gemm_dlut.h"
 
 namespace skm {
 
@@ -23,9 +23,9 @@ hipError_t dlut_piece_t(const void* hi, const void* lo, const void* X, const uin
   const TX* y = (const TX*)hi;
   const TX* x = (const TX*)X;
   const DlPiece pa{q.count, q.ld, lo ? (const TX*)lo - y : 0, q.inv_scale, q.zeros};
-  if (p.b == 2) return dlut_dma_launch<2, TX>(y, x, idx, p, dLUT, accumulate, part, pa, s);
-  if (p.b == 3) return dlut_dma_launch<3, TX>(y, x, idx, p, dLUT, accumulate, part, pa, s);
-  return dlut_dma_launch<4, TX>(y, x, idx, p, dLUT, accumulate, part, pa, s);
+  if (p.b == 2) return dlut_piece_launch<2, TX>(y, x, idx, p, dLUT, accumulate, part, pa, s);
+  if (p.b == 3) return dlut_piece_launch<3, TX>(y, x, idx, p, dLUT, accumulate, part, pa, s);
+  return dlut_piece_launch<4, TX>(y, x, idx, p, dLUT, accumulate, part, pa, s);
 }
 
 }  // namespace
