@@ -663,7 +663,8 @@ k_gemm_dx64(const TX* __restrict__ dY, const uint8_t* __restrict__ idx_packed, c
         mm::Planes16 P;
         mm::planes16(S.lut, P);
   #pragma unroll
-        for (int q = 0; q < 4; ++q) st_q(bst + buf * D6_TB + 16u * q, ok ? mm::dequant8_b4(S.w[q], P) : z);
+        for (int q = 0; q < 4; ++q)
+          st_q(bst + buf * D6_TB + 16u * (q ^ (r & 3)), ok ? mm::dequant8_b4(S.w[q], P) : z);
       } else {
       const uint32_t gk = (buf * NG + gsel) * T;
       uint32_t o0[8], o1[8];
@@ -719,8 +720,14 @@ k_gemm_dx64(const TX* __restrict__ dY, const uint8_t* __restrict__ idx_packed, c
   #pragma unroll
     for (int ks = 0; ks < 4; ++ks) ard[ks] = D6_A + swz128(arow, (uint32_t)(2 * ks) + khalf);
     const uint32_t ls = (uint32_t)lane & 15u;
-    const uint32_t btr = D6_B + (8u * ((uint32_t)lane >> 5) + (ls >> 2)) * DX_RSB +
-                         (16u * (((uint32_t)lane >> 4) & 1u) + 4u * (ls & 3u)) * 2u + 128u * (uint32_t)wn;
+    // b = 4: 16-byte chunk c of weight row r sits at c ^ (r % 4). 16 lanes write
+    // 4 chunks of 4 rows, whose starts are 16 banks apart: with the exchange they
+    // hit 64 banks once (4 lanes per bank without), and so do the 32 lanes of a
+    // transposing read (4 rows x 4 chunks), whose row is ls / 4 mod 4.
+    const uint32_t brow = (8u * ((uint32_t)lane >> 5) + (ls >> 2)) * DX_RSB;
+    const uint32_t bchunk = 2u * (((uint32_t)lane >> 4) & 1u) + ((ls & 3u) >> 1);
+    const uint32_t btr = D6_B + brow + ((B == 4 ? bchunk ^ (ls >> 2) : bchunk) << 4) + 8u * (ls & 1u) +
+                         128u * (uint32_t)wn;
     auto load_frags = [&](u32x4* fa, u32x4* fb, uint32_t buf, int ks) __attribute__((always_inline)) {
   #pragma unroll
       for (int i = 0; i < 4; ++i) fa[i] = ld_q(ard[ks] + buf * D6_TA + 4096u * i);

@@ -25,6 +25,9 @@ __device__ __forceinline__ int target_in_wave(int64_t target, int64_t c0, int la
 
 static_assert(G_BN == 256, "the statistics are laid out per 256 words");
 
+// the lane's output e (0 .. 31) of a token, as a column after its first one
+constexpr int col_of_output(int e) { return 32 * (e >> 4) + 8 * ((e & 15) >> 2) + (e & 3); }
+
 // EpStats: part[(n0 / 256) * stride + c] = (max, sum of exp(z - max)) over the
 // block's columns for listed token c; tlogit[c] = the target's logit (written
 // by the one lane that holds it).
@@ -41,6 +44,7 @@ template <typename TX> struct EpStats {
                                              int64_t n0, int wm, int wn, int lane, int t) {
     const int64_t c0 = n0 + 64 * wn;
     const int cols = (int)(n - c0 < 64 ? n - c0 : 64) - 4 * (lane >> 5);  // valid columns from the lane's first
+    const bool ragged = n - c0 < 64;  // wave-uniform
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = 128 * wm + 32 * i + (lane & 31);
@@ -48,29 +52,28 @@ template <typename TX> struct EpStats {
       const int64_t src = ep.rows[tok < m ? tok : m - 1];
       const float u = SC ? pow2f(rexp[src]) : 1.0f;
       const int tgt = target_in_wave(ep.targets[src], ep.v0 + c0, lane);
-      float mx = -__builtin_inff();
-      float tl = 0.0f;
+      float mx = -__builtin_inff(), sum = 0.0f;
+      float z[32];
 #pragma unroll
-      for (int jj = 0; jj < 2; ++jj)
+      for (int e = 0; e < 32; ++e) z[e] = SC ? acc[i][e >> 4][e & 15] * u : acc[i][e >> 4][e & 15];
+      // few waves hold a target of one of their tokens, one column block is ragged
+      if (__ballot(tgt >= 0) != 0) {
+        float tl = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int col = 32 * jj + 8 * (e >> 2) + (e & 3);
-          const float z = SC ? acc[i][jj][e] * u : acc[i][jj][e];
-          if (col < cols) mx = __builtin_fmaxf(mx, z);
-          if (col == tgt) tl = z;
-        }
-      if (tgt >= 0 && (tgt & 4) == 0 && tok < m) ep.tlogit[tok] = tl;
+        for (int e = 0; e < 32; ++e)
+          if (col_of_output(e) == tgt) tl = z[e];
+        if (tgt >= 0 && (tgt & 4) == 0 && tok < m) ep.tlogit[tok] = tl;
+      }
+      if (ragged) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) z[e] = col_of_output(e) < cols ? z[e] : -__builtin_inff();
+      }
+#pragma unroll
+      for (int e = 0; e < 32; ++e) mx = __builtin_fmaxf(mx, z[e]);
       mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32, 64));
       const float ref = mx == -__builtin_inff() ? 0.0f : mx;
-      float sum = 0.0f;
 #pragma unroll
-      for (int jj = 0; jj < 2; ++jj)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int col = 32 * jj + 8 * (e >> 2) + (e & 3);
-          const float z = SC ? acc[i][jj][e] * u : acc[i][jj][e];
-          sum += col < cols ? __expf(z - ref) : 0.0f;
-        }
+      for (int e = 0; e < 32; ++e) sum += __expf(z[e] - ref);
       sum += __shfl_xor(sum, 32, 64);
       if (lane < 32) {
         mm::st_w((uint32_t)(wn * G_BM + row) * 8u, __builtin_bit_cast(uint32_t, mx));
@@ -96,6 +99,14 @@ template <typename TX> struct EpStats {
   }
 };
 
+// (a0, a1): four 16-bit values of columns 8 q + 4 (lane / 32) .., (b0, b1): of
+// q + 1. Lanes 0 .. 31 get all eight of q, lanes 32 .. 63 of q + 1.
+__device__ __forceinline__ u32x4 pair_up(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1) {
+  const auto s0 = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
+  const auto s1 = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
+  return u32x4{s0[0], s1[0], s0[1], s1[1]};
+}
+
 // EpGrad: dZ of the block, [listed token][ld] in up to three forms (NULL =
 // not wanted): hi + lo in TX for dLUT (hi also for dX when the tables have
 // that dtype) and dxv in TL for dX. Columns n .. ld - 1 and listed rows past
@@ -118,12 +129,13 @@ template <typename TX, typename TL> struct EpGrad {
     const int64_t c0 = n0 + 64 * wn;
     const int64_t mpad = (m + 31) / 32 * 32;
     const int cols = (int)(n - c0 < 64 ? n - c0 : 64) - 4 * (lane >> 5);
-    const int stored = (int)(ep.ld - c0 < 64 ? ep.ld - c0 : 64) - 4 * (lane >> 5);
+    const int stored = (int)(ep.ld - c0 < 64 ? ep.ld - c0 : 64);
+    const bool ragged = n - c0 < 64 || m0 + G_BM > m;  // wave-uniform
     const float scale = *ep.scale;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t tok = m0 + 128 * wm + 32 * i + (lane & 31);
-      if (tok >= mpad) continue;
+      if (m0 + 128 * wm + 32 * i >= mpad) break;  // wave-uniform: whole groups of 32 tokens
       const bool live = tok < m;
       const int64_t src = ep.rows[live ? tok : m - 1];
       const float u = SC ? pow2f(rexp[src]) : 1.0f;
@@ -132,36 +144,57 @@ template <typename TX, typename TL> struct EpGrad {
       const float lse = ep.lse[src];
       // a target outside the vocabulary gives NaN gradients (its loss is NaN)
       const float gs = target >= 0 && target < ep.V ? ep.dloss[src] * scale : __builtin_nanf("");
-      const int64_t at = tok * ep.ld + c0 + 4 * (lane >> 5);
+      // g[e] = dZ of output e. (The target's 1 and the masks only where the wave
+      // has one: few waves hold a target of one of their tokens, one column and
+      // one token block are ragged.)
+      float g[32];
 #pragma unroll
-      for (int jj = 0; jj < 2; ++jj)
+      for (int e = 0; e < 32; ++e) {
+        const float z = SC ? acc[i][e >> 4][e & 15] * u : acc[i][e >> 4][e & 15];
+        g[e] = __expf(z - lse);
+      }
+      if (__ballot(tgt >= 0) != 0) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int cq = 32 * jj + 8 * q;
-          if (cq >= stored) continue;
-          float g[4];
+        for (int e = 0; e < 32; ++e) g[e] -= col_of_output(e) == tgt ? 1.0f : 0.0f;
+      }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float z = SC ? acc[i][jj][4 * q + k] * u : acc[i][jj][4 * q + k];
-            const float p = __expf(z - lse) - (cq + k == tgt ? 1.0f : 0.0f);
-            g[k] = live && cq + k < cols ? p * gs : 0.0f;
+      for (int e = 0; e < 32; ++e) g[e] *= gs;
+      if (ragged) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) g[e] = live && col_of_output(e) < cols ? g[e] : 0.0f;
+      }
+      // A lane and its partner 32 lanes away hold columns 8 q .. + 3 and + 4 .. 7
+      // of their token: after an exchange the lower one has all eight of an even
+      // q and the upper one those of the next q, 16 bytes for one store each.
+      // (ld is a multiple of 8: eight columns are stored or not together.)
+      const int64_t at = tok * ep.ld + c0 + 8 * (lane >> 5);
+#pragma unroll
+      for (int q = 0; q < 8; q += 2) {
+        const bool on = 32 * (q >> 2) + 8 * (q & 3) + 8 * (lane >> 5) < stored;
+        const int64_t o = at + 32 * (q >> 2) + 8 * (q & 3);
+        const float* v = g + 4 * q;  // 8 values: columns of q, then of q + 1
+        uint32_t h[4];
+        if (ep.hi) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) h[k] = mm::pack_tc<TX>(v[2 * k], v[2 * k + 1]);
+          if (ep.lo) {
+            float r[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              r[k] = v[k] - to_f32(__builtin_bit_cast(TX, (uint16_t)(h[k >> 1] >> (16 * (k & 1)))));
+            const u32x4 w = pair_up(mm::pack_tc<TX>(r[0], r[1]), mm::pack_tc<TX>(r[2], r[3]),
+                                    mm::pack_tc<TX>(r[4], r[5]), mm::pack_tc<TX>(r[6], r[7]));
+            if (on) *reinterpret_cast<u32x4*>(ep.lo + o) = w;
           }
-          if (ep.hi) {
-            uint32_t h[2] = {mm::pack_tc<TX>(g[0], g[1]), mm::pack_tc<TX>(g[2], g[3])};
-            *reinterpret_cast<u32x2*>(ep.hi + at + cq) = u32x2{h[0], h[1]};
-            if (ep.lo) {
-              float r[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                r[k] = g[k] - to_f32(__builtin_bit_cast(TX, (uint16_t)(h[k >> 1] >> (16 * (k & 1)))));
-              *reinterpret_cast<u32x2*>(ep.lo + at + cq) =
-                  u32x2{mm::pack_tc<TX>(r[0], r[1]), mm::pack_tc<TX>(r[2], r[3])};
-            }
-          }
-          if (ep.dxv)
-            *reinterpret_cast<u32x2*>(ep.dxv + at + cq) =
-                u32x2{mm::pack_tc<TL>(g[0], g[1]), mm::pack_tc<TL>(g[2], g[3])};
+          const u32x4 w = pair_up(h[0], h[1], h[2], h[3]);
+          if (on) *reinterpret_cast<u32x4*>(ep.hi + o) = w;
         }
+        if (ep.dxv) {
+          const u32x4 w = pair_up(mm::pack_tc<TL>(v[0], v[1]), mm::pack_tc<TL>(v[2], v[3]),
+                                  mm::pack_tc<TL>(v[4], v[5]), mm::pack_tc<TL>(v[6], v[7]));
+          if (on) *reinterpret_cast<u32x4*>(ep.dxv + o) = w;
+        }
+      }
     }
   }
 };
