@@ -14,9 +14,9 @@
 // the same kernels with column j TPR + t in element j of thread t.
 //
 // Backward: each block walks rows blockIdx, blockIdx + grid, ... and keeps its
-// columns' dw and db sums in registers; the block's sums go to the workspace
-// and k_norm_reduce adds them per column in block order (deterministic, no
-// atomics).
+// columns' dw and db sums in registers, the next row's loads in flight while a
+// row is worked on; the block's sums go to the workspace and k_norm_reduce adds
+// them per column in block order (deterministic, no atomics).
 #include <type_traits>
 
 #include "skm_launch.h"
@@ -52,6 +52,61 @@ __device__ __forceinline__ void load_row(const T* row, int d, int t, float (&v)[
         v[c][j] = col < d ? to_f32(row[col]) : 0.0f;
       }
     }
+  }
+}
+
+// a row as loaded: the conversion to fp32 waits until the row is worked on
+template <typename T, bool AL, int NCH> struct RawRow {
+  static constexpr int Q = __is_same(T, float) ? 2 : 1;
+  u32x4 v[AL ? NCH * Q : 1];
+  T e[AL ? 1 : NCH * 8];
+};
+template <typename T, bool AL, int TPR, int NCH>
+__device__ __forceinline__ void load_raw(const T* row, int d, int t, RawRow<T, AL, NCH>& r) {
+  typedef RawRow<T, AL, NCH> R;
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    if constexpr (AL) {
+      const int j0 = col_of<AL, TPR>(t, c, 0);
+#pragma unroll
+      for (int q = 0; q < R::Q; ++q)
+        r.v[c * R::Q + q] = j0 < d ? reinterpret_cast<const u32x4*>(row + j0)[q] : u32x4{0u, 0u, 0u, 0u};
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int col = col_of<AL, TPR>(t, c, j);
+        r.e[c * 8 + j] = col < d ? row[col] : from_f32<T>(0.0f);
+      }
+    }
+  }
+}
+template <typename T, bool AL, int NCH>
+__device__ __forceinline__ void from_raw(const RawRow<T, AL, NCH>& r, float (&v)[NCH][8]) {
+  typedef RawRow<T, AL, NCH> R;
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    if constexpr (AL) {
+      load8<T>(reinterpret_cast<const T*>(&r.v[c * R::Q]), v[c]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[c][j] = to_f32(r.e[c * 8 + j]);
+    }
+  }
+}
+// the same for a checkpoint's row (AL only)
+template <int NCH> struct RawCodes {
+  u32x2 v[NCH];
+  uint32_t s[NCH];
+};
+template <int TPR, int NCH>
+__device__ __forceinline__ void load_codes(const int8_t* codes, const uint8_t* scales, int64_t r, int d, int t,
+                                           RawCodes<NCH>& o) {
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    const int j0 = col_of<true, TPR>(t, c, 0);
+    const bool in = j0 < d;
+    o.v[c] = in ? *reinterpret_cast<const u32x2*>(codes + r * d + j0) : u32x2{0u, 0u};
+    o.s[c] = in ? scales[(r * d + j0) >> 5] : 1u;
   }
 }
 
@@ -183,47 +238,55 @@ k_norm_fwd(const T* __restrict__ X, const void* __restrict__ w, const void* __re
   }
 }
 
-template <typename T, bool AL, int TPR, int NCH>
+// DYF: dY is fp32 (else T); CK: X is a checkpoint
+template <typename T, bool AL, int TPR, int NCH, bool DYF, bool CK>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
-k_norm_bwd(const void* __restrict__ dY, int dy_f32, const T* __restrict__ X, const int8_t* __restrict__ codes,
+k_norm_bwd(const void* __restrict__ dY, const T* __restrict__ X, const int8_t* __restrict__ codes,
            const uint8_t* __restrict__ scales, const void* __restrict__ w, int p_f32, const float* __restrict__ mean,
            const float* __restrict__ rstd, int64_t m, int d, T* __restrict__ dX, float* __restrict__ part_w,
            float* __restrict__ part_b) {
   constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+  typedef std::conditional_t<DYF, float, T> TY;
   __shared__ float red[2 * (TPR / 64)];
   const int t = (int)(threadIdx.x % TPR);
   const float inv_d = 1.0f / (float)d;
   float p[NCH][8], aw[NCH][8], ab[NCH][8];
-  load_param<T, AL, TPR, NCH>(w, p_f32, d, t, 1.0f, p);
 #pragma unroll
   for (int c = 0; c < NCH; ++c)
 #pragma unroll
     for (int j = 0; j < 8; ++j) aw[c][j] = ab[c][j] = 0.0f;
-  for (int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; r < m; r += (int64_t)gridDim.x * RPB) {
+  RawRow<TY, AL, NCH> rg;
+  RawRow<T, AL, NCH> rx;
+  RawCodes<NCH> rc;
+  float mu = 0.0f, rs = 0.0f;
+  auto load = [&](int64_t r) {
+    load_raw<TY, AL, TPR, NCH>((const TY*)dY + r * d, d, t, rg);
+    if constexpr (CK) load_codes<TPR, NCH>(codes, scales, r, d, t, rc);
+    else load_raw<T, AL, TPR, NCH>(X + r * d, d, t, rx);
+    mu = mean ? mean[r] : 0.0f;
+    rs = rstd[r];
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+  if (r < m) load(r);
+  load_param<T, AL, TPR, NCH>(w, p_f32, d, t, 1.0f, p);
+  for (; r < m; r += step) {
     float x[NCH][8], g[NCH][8];
-    if (dy_f32) load_row<float, AL, TPR, NCH>((const float*)dY + r * d, d, t, g);
-    else load_row<T, AL, TPR, NCH>((const T*)dY + r * d, d, t, g);
-    if (AL && codes) {
+    from_raw<TY, AL, NCH>(rg, g);
+    if constexpr (CK) {
 #pragma unroll
-      for (int c = 0; c < NCH; ++c) {
-        const int j0 = col_of<AL, TPR>(t, c, 0);
-        if (j0 < d) {
-          ckpt_unpack8(*reinterpret_cast<const u32x2*>(codes + r * d + j0), scales[(r * d + j0) >> 5], x[c]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[c][j] = 0.0f;
-        }
-      }
+      for (int c = 0; c < NCH; ++c) ckpt_unpack8(rc.v[c], rc.s[c], x[c]);
     } else {
-      load_row<T, AL, TPR, NCH>(X + r * d, d, t, x);
+      from_raw<T, AL, NCH>(rx, x);
     }
-    const float mu = mean ? mean[r] : 0.0f, rs = rstd[r];
+    const float m0 = mu, r0 = rs;
+    if (r + step < m) load(r + step);
     float s1 = 0.0f, s2 = 0.0f;  // sums of g xh and of g, g = dy w
 #pragma unroll
     for (int c = 0; c < NCH; ++c)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float xh = (x[c][j] - mu) * rs;  // (past the row's end dy is 0)
+        const float xh = (x[c][j] - m0) * r0;  // (past the row's end dy is 0)
         aw[c][j] = __builtin_fmaf(g[c][j], xh, aw[c][j]);
         ab[c][j] += g[c][j];
         g[c][j] *= p[c][j];
@@ -238,26 +301,56 @@ k_norm_bwd(const void* __restrict__ dY, int dy_f32, const T* __restrict__ X, con
 #pragma unroll
       for (int c = 0; c < NCH; ++c)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[c][j] = rs * (g[c][j] - s2 - x[c][j] * s1);
+        for (int j = 0; j < 8; ++j) x[c][j] = r0 * (g[c][j] - s2 - x[c][j] * s1);
       store_row<T, AL, TPR, NCH>(dX + r * d, d, t, x);
     }
   }
-  // the block's sums, one partial row per row slot of the block
-  const int64_t slot = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
-  if (part_w) store_row<float, AL, TPR, NCH>(part_w + slot * d, d, t, aw);
-  if (part_b) store_row<float, AL, TPR, NCH>(part_b + slot * d, d, t, ab);
+  // the block's sums: with several rows at a time, those of the row slots in order
+  auto put = [&](float* part, float (&a)[NCH][8]) {
+    if constexpr (RPB > 1) {
+      __shared__ float slots[RPB - 1][NCH * 8][64];
+      const int k = (int)(threadIdx.x >> 6);
+      __syncthreads();
+      if (k > 0) {
+#pragma unroll
+        for (int e = 0; e < NCH * 8; ++e) slots[k - 1][e][t] = a[e >> 3][e & 7];
+      }
+      __syncthreads();
+      if (k > 0) return;
+#pragma unroll
+      for (int i = 0; i < RPB - 1; ++i)
+#pragma unroll
+        for (int e = 0; e < NCH * 8; ++e) a[e >> 3][e & 7] += slots[i][e][t];
+    }
+    store_row<float, AL, TPR, NCH>(part + (int64_t)blockIdx.x * d, d, t, a);
+  };
+  if (part_w) put(part_w, aw);
+  if (part_b) put(part_b, ab);
 }
 
-// out[j] = (accumulate ? out[j] : 0) + sum over the partial rows, in order:
-// 64 columns per block, 16 slices of rows summed apart and then in slice order
+// out[j] = (accumulate ? out[j] : 0) + the sum over the blocks' rows of part:
+// 64 columns per block, 16 slices of rows summed apart and then in slice order.
+// blockIdx.y: dw, db (the one that is wanted when there is one)
 __global__ void __launch_bounds__(1024) k_norm_reduce(const float* __restrict__ part, int rows, int d,
-                                                      float* __restrict__ out, int accumulate) {
+                                                      float* __restrict__ out0, float* __restrict__ out1,
+                                                      int accumulate) {
   __shared__ float sm[16][64];
   const int lane = (int)(threadIdx.x & 63), sl = (int)(threadIdx.x >> 6);
   const int j = (int)blockIdx.x * 64 + lane;
+  part += (int64_t)blockIdx.y * rows * d;
+  float* out = blockIdx.y ? out1 : out0;
   float a = 0.0f;
-  if (j < d)
-    for (int r = sl; r < rows; r += 16) a += part[(int64_t)r * d + j];
+  if (j < d) {
+    int r = sl;
+    for (; r + 112 < rows; r += 128) {  // eight loads in flight
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = part[(int64_t)(r + 16 * k) * d + j];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) a += v[k];
+    }
+    for (; r < rows; r += 16) a += part[(int64_t)r * d + j];
+  }
   sm[sl][lane] = a;
   __syncthreads();
   if (sl == 0 && j < d) {
@@ -311,31 +404,41 @@ hipError_t norm_fwd_t(const NormArgs& a, const T* X, T* Y, float* mean, float* r
   });
 }
 
-// blocks of the backward walk
+// Blocks of the backward walk, each with one partial row of dw and of db: at
+// most two per CU.
 int64_t bwd_blocks(int64_t m, int64_t d) {
   const int rpb = shape_of(d).tpr < 256 ? 256 / shape_of(d).tpr : 1;
   const int64_t need = (m + rpb - 1) / rpb;
   return need < 512 ? need : 512;
 }
-int64_t bwd_slots(int64_t m, int64_t d) {
-  const int rpb = shape_of(d).tpr < 256 ? 256 / shape_of(d).tpr : 1;
-  return bwd_blocks(m, d) * rpb;
-}
+
+struct NormBwd {
+  const void* dY;
+  bool dy_f32;
+  const void* X;
+  const int8_t* codes;
+  const uint8_t* scales;
+  const float *mean, *rstd;
+  void* dX;
+  float *part_w, *part_b;
+};
 
 template <typename T>
-hipError_t norm_bwd_t(const NormArgs& a, const void* dY, int dy_f32, const T* X, const int8_t* codes,
-                      const uint8_t* scales, const float* mean, const float* rstd, T* dX, float* part_w, float* part_b,
-                      hipStream_t s) {
+hipError_t norm_bwd_t(const NormArgs& a, const NormBwd& q, hipStream_t s) {
   return with_shape(a.d, [&](auto tpr, auto nch) {
     constexpr int TPR = decltype(tpr)::value, NCH = decltype(nch)::value;
-    const dim3 grid((unsigned)bwd_blocks(a.m, a.d)), block(TPR < 256 ? 256 : TPR);
+    auto go = [&](auto kern) {
+      hipLaunchKernelGGL(kern, dim3((unsigned)bwd_blocks(a.m, a.d)), dim3(TPR < 256 ? 256 : TPR), 0, s, q.dY,
+                         (const T*)q.X, q.codes, q.scales, a.w, a.p_f32, q.mean, q.rstd, a.m, (int)a.d, (T*)q.dX,
+                         q.part_w, q.part_b);
+      return hipGetLastError();
+    };
+    constexpr bool F = __is_same(T, float);  // (an fp32 dY of fp32 rows is of their own type)
+    const bool f = q.dy_f32 && !F;
+    if (q.codes) return f ? go(k_norm_bwd<T, true, TPR, NCH, !F, true>) : go(k_norm_bwd<T, true, TPR, NCH, false, true>);
     if (a.d % 8 == 0)
-      hipLaunchKernelGGL((k_norm_bwd<T, true, TPR, NCH>), grid, block, 0, s, dY, dy_f32, X, codes, scales, a.w,
-                         a.p_f32, mean, rstd, a.m, (int)a.d, dX, part_w, part_b);
-    else
-      hipLaunchKernelGGL((k_norm_bwd<T, false, TPR, NCH>), grid, block, 0, s, dY, dy_f32, X, codes, scales, a.w,
-                         a.p_f32, mean, rstd, a.m, (int)a.d, dX, part_w, part_b);
-    return hipGetLastError();
+      return f ? go(k_norm_bwd<T, true, TPR, NCH, !F, false>) : go(k_norm_bwd<T, true, TPR, NCH, false, false>);
+    return f ? go(k_norm_bwd<T, false, TPR, NCH, !F, false>) : go(k_norm_bwd<T, false, TPR, NCH, false, false>);
   });
 }
 
@@ -348,32 +451,24 @@ hipError_t launch_norm_fwd(const NormArgs& a, const void* X, int x_dtype, void* 
   return norm_fwd_t(a, (const bf16_t*)X, (bf16_t*)Y, mean, rstd, codes, scales, s);
 }
 
-size_t norm_bwd_part_bytes(int64_t m, int64_t d) { return (size_t)bwd_slots(m, d) * (size_t)d * 4; }
+size_t norm_bwd_part_bytes(int64_t m, int64_t d) { return (size_t)bwd_blocks(m, d) * (size_t)d * 4; }
 
 hipError_t launch_norm_bwd(const NormArgs& a, const void* dY, int dy_dtype, const void* X, int x_dtype,
                            const int8_t* codes, const uint8_t* scales, const float* mean, const float* rstd, void* dX,
                            float* dw, float* db, int accumulate, float* part, hipStream_t s) {
-  const int64_t slots = bwd_slots(a.m, a.d);
-  float* pw = dw ? part : nullptr;
-  float* pb = db ? part + (dw ? slots * a.d : 0) : nullptr;
-  const int f32 = dy_dtype == DT_F32;
+  const int64_t rows = bwd_blocks(a.m, a.d);
+  const NormBwd q{dY,   dy_dtype == DT_F32,    X,
+                  codes, scales,                mean,
+                  rstd, dX,                    dw ? part : nullptr,
+                  db ? part + (dw ? rows * a.d : 0) : nullptr};
   hipError_t e;
-  if (x_dtype == DT_F32)
-    e = norm_bwd_t(a, dY, f32, (const float*)X, codes, scales, mean, rstd, (float*)dX, pw, pb, s);
-  else if (x_dtype == DT_F16)
-    e = norm_bwd_t(a, dY, f32, (const half_t*)X, codes, scales, mean, rstd, (half_t*)dX, pw, pb, s);
-  else
-    e = norm_bwd_t(a, dY, f32, (const bf16_t*)X, codes, scales, mean, rstd, (bf16_t*)dX, pw, pb, s);
-  const dim3 grid((unsigned)((a.d + 63) / 64));
-  if (e == hipSuccess && dw) {
-    hipLaunchKernelGGL(k_norm_reduce, grid, dim3(1024), 0, s, pw, (int)slots, (int)a.d, dw, accumulate);
-    e = hipGetLastError();
-  }
-  if (e == hipSuccess && db) {
-    hipLaunchKernelGGL(k_norm_reduce, grid, dim3(1024), 0, s, pb, (int)slots, (int)a.d, db, accumulate);
-    e = hipGetLastError();
-  }
-  return e;
+  if (x_dtype == DT_F32) e = norm_bwd_t<float>(a, q, s);
+  else if (x_dtype == DT_F16) e = norm_bwd_t<half_t>(a, q, s);
+  else e = norm_bwd_t<bf16_t>(a, q, s);
+  if (e != hipSuccess || (!dw && !db)) return e;
+  hipLaunchKernelGGL(k_norm_reduce, dim3((unsigned)((a.d + 63) / 64), dw && db ? 2 : 1), dim3(1024), 0, s, part,
+                     (int)rows, (int)a.d, dw ? dw : db, db, accumulate);
+  return hipGetLastError();
 }
 
 }  // namespace skm
