@@ -18,10 +18,11 @@ __global__ void __launch_bounds__(256) k_act_quant(const T* __restrict__ X, int6
                                                    uint8_t* __restrict__ scales) {
   const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (c >= chunks) return;  // chunks is a multiple of 4: quads stay whole
-  float v[8];
-  load8<T>(X + c * 8, v);
-  const uint32_t s = ckpt_exp_of<T>(quad_max(top8(v)));
-  *reinterpret_cast<u32x2*>(codes + c * 8) = ckpt_pack8(v, s);
+  u32x4 w[sizeof(T) / 2];
+#pragma unroll
+  for (int q = 0; q < (int)sizeof(T) / 2; ++q) w[q] = reinterpret_cast<const u32x4*>(X + c * 8)[q];
+  uint32_t s;
+  *reinterpret_cast<u32x2*>(codes + c * 8) = ckpt_of<T>(w, s);
   if ((threadIdx.x & 3) == 0) scales[c >> 2] = (uint8_t)s;
 }
 

@@ -220,20 +220,23 @@ k_norm_fwd(const T* __restrict__ X, const void* __restrict__ w, const void* __re
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[c][j] += p[c][j];
   }
-  store_row<T, AL, TPR, NCH>(Y + r * d, d, t, x);
-  if constexpr (AL) {
-    if (codes) {  // d is a multiple of 32: the four lanes of a block are in range together
+  if (!AL || !codes) {
+    store_row<T, AL, TPR, NCH>(Y + r * d, d, t, x);
+    return;
+  }
+  if constexpr (AL) {  // d is a multiple of 32: the four lanes of a block are in range together
 #pragma unroll
-      for (int c = 0; c < NCH; ++c) {
-        const int j0 = col_of<AL, TPR>(t, c, 0);
-        if (j0 >= d) continue;
-        // the checkpoint is of Y as stored
+    for (int c = 0; c < NCH; ++c) {
+      const int j0 = col_of<AL, TPR>(t, c, 0);
+      if (j0 >= d) continue;
+      // the checkpoint is of Y as stored
+      u32x4 y[sizeof(T) / 2];
+      store8<T>(reinterpret_cast<T*>(y), x[c]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[c][j] = to_f32(from_f32<T>(x[c][j]));
-        const uint32_t s = ckpt_exp_of<T>(quad_max(top8(x[c])));
-        *reinterpret_cast<u32x2*>(codes + r * d + j0) = ckpt_pack8(x[c], s);
-        if ((t & 3) == 0) scales[(r * d + j0) >> 5] = (uint8_t)s;
-      }
+      for (int q = 0; q < (int)sizeof(T) / 2; ++q) reinterpret_cast<u32x4*>(Y + r * d + j0)[q] = y[q];
+      uint32_t s;
+      *reinterpret_cast<u32x2*>(codes + r * d + j0) = ckpt_of<T>(y, s);
+      if ((t & 3) == 0) scales[(r * d + j0) >> 5] = (uint8_t)s;
     }
   }
 }

@@ -41,6 +41,9 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
   return v > o ? v : o;
 }
 
+// Largest magnitude of eight values as an fp32 bit pattern (NaN above
+// infinity): of fp32 values, or of 16-bit ones packed as stored, whose patterns
+// without the sign order like their magnitudes (four packed maxima).
 __device__ __forceinline__ uint32_t top8(const float* v) {
   uint32_t top = 0u;
 #pragma unroll
@@ -50,20 +53,65 @@ __device__ __forceinline__ uint32_t top8(const float* v) {
   }
   return top;
 }
+__device__ __forceinline__ uint32_t top8_16(u32x4 w) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 m = __builtin_bit_cast(u16x2, w[0] & 0x7FFF7FFFu);
+#pragma unroll
+  for (int q = 1; q < 4; ++q) {
+    const uint32_t a = w[q] & 0x7FFF7FFFu;
+    m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, a));
+  }
+  return m.x > m.y ? m.x : m.y;
+}
+template <typename T> __device__ __forceinline__ uint32_t f32_bits_of(uint32_t p) {
+  return __builtin_bit_cast(uint32_t, to_f32(__builtin_bit_cast(T, (uint16_t)p)));
+}
 
 // Eight values of one lane to eight codes, given the block's exponent byte.
+// x 2^-e + 1.5 2^23 rounds x 2^-e to an integer (nearest even, the product is
+// exact) and holds it in its low byte.
 __device__ __forceinline__ u32x2 ckpt_pack8(const float* v, uint32_t s) {
   // 2^-e as fp32: s in [1, 248]; a NaN block (255) stores zeros
-  const float r = __builtin_bit_cast(float, (254u - (s == kCkptNaN ? 127u : s)) << 23);
-  u32x2 o = {0u, 0u};
+  const bool ok = s != kCkptNaN;
+  const float r = __builtin_bit_cast(float, (254u - (ok ? s : 127u)) << 23);
+  constexpr float M = 12582912.0f;
+  uint32_t c[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float q = __builtin_rintf(v[j] * r);
-    q = __builtin_fminf(__builtin_fmaxf(q, -127.0f), 127.0f);
-    const uint32_t c = s == kCkptNaN ? 0u : (uint32_t)(int)q & 0xFFu;
-    o[j >> 2] |= c << (8 * (j & 3));
+  for (int j = 0; j < 8; ++j)
+    c[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_fmed3f(__builtin_fmaf(v[j], r, M), M - 127.0f, M + 127.0f));
+  u32x2 o;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t a = __builtin_amdgcn_perm(c[4 * q + 1], c[4 * q], 0x0C0C0400u);
+    const uint32_t b = __builtin_amdgcn_perm(c[4 * q + 3], c[4 * q + 2], 0x0C0C0400u);
+    o[q] = ok ? a | b << 16 : 0u;
   }
   return o;
+}
+
+// The checkpoint of eight values as stored in T (`w`, 16 or 32 bytes), one
+// lane's part of its block: codes, and the block's exponent byte in `s`.
+template <typename T>
+__device__ __forceinline__ u32x2 ckpt_of(const u32x4* w, uint32_t& s) {
+  float v[8];
+  if constexpr (__is_same(T, float)) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      // (the vector as a whole: see mm::ld_f4)
+      const f32x4 a = __builtin_bit_cast(f32x4, w[q]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 * q + j] = a[j];
+    }
+    s = ckpt_exp_of<T>(quad_max(top8(v)));
+  } else {
+    s = ckpt_exp_of<T>(f32_bits_of<T>(quad_max(top8_16(w[0]))));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t p = w[0][j >> 1];
+      v[j] = to_f32(__builtin_bit_cast(T, (uint16_t)(j & 1 ? p >> 16 : p & 0xFFFFu)));
+    }
+  }
+  return ckpt_pack8(v, s);
 }
 
 // Eight codes back to values (fp32, exact).
