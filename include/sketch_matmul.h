@@ -350,6 +350,16 @@ size_t sketch_xent_bwd_workspace(int64_t m, int64_t n, int64_t d, int b, int gpr
                                  int need_dx, int need_dlut);
 
 /*
+ * The mean of sketch_xent_fwd's losses over the tokens that are scored (target
+ * != ignore_index): *mean (fp32, on the device) = sum of loss / count, and
+ * weight[t] = 1 / count for those tokens, 0 for the others (so that dloss =
+ * dmean * weight); all 0 when no token is scored. Sums in a fixed order.
+ * m >= 1; targets 8-byte, mean 4-byte, loss and weight 16-byte aligned.
+ */
+int sketch_xent_mean(const float* loss, const int64_t* targets, int64_t ignore_index, int64_t m,
+                     float* mean, float* weight, hipStream_t stream);
+
+/*
  * Dequantise W[i][j] = lut[i][j/G][idx[i][j]] into a dense [n][d] array of
  * lut_dtype (SpaLLM Eq. (1) with groups per row). A checking aid: the matmul
  * entry points never build W.

@@ -36,6 +36,7 @@ from ._lib import (  # noqa: F401
     sketch_xent_bwd_workspace,
     sketch_xent_fwd,
     sketch_xent_fwd_workspace,
+    sketch_xent_mean,
 )
 
 __version__ = "0.1.0"

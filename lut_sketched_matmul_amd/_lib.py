@@ -77,6 +77,7 @@ _SIGNATURES = {
     "sketch_xent_fwd": (_c_int, [_c_vp, _c_int, _c_vp, _c_vp, _c_int, _c_vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_int,
                                  _c_int, _c_vp, _c_vp, _c_vp, _c_size, _c_vp]),
     "sketch_xent_fwd_workspace": (_c_size, [_c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_int]),
+    "sketch_xent_mean": (_c_int, [_c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp]),
     "sketch_xent_bwd": (_c_int, [_c_vp, _c_int, _c_vp, _c_vp, _c_int, _c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_i64,
                                  _c_i64, _c_int, _c_int, _c_vp, _c_vp, _c_int, _c_vp, _c_size, _c_vp]),
     "sketch_xent_bwd_workspace": (_c_size, [_c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int]),
@@ -789,6 +790,24 @@ def sketch_xent_fwd(X, idx_packed, lut, targets, b: int, gpr: int, ignore_index:
                                    m, n, d, b, gpr, _ptr(loss), _ptr(lse), _ptr(ws), _size(ws), sp)
     _check("sketch_xent_fwd", st)
     return loss, lse
+
+
+def sketch_xent_mean(loss, targets, ignore_index: int = -100, stream=None) -> Tuple[object, object]:
+    """(mean, weight): the mean (fp32, 0 dimensions) of the losses whose target is not ignore_index, and every
+    token's weight in it, fp32 [m] (0 for ignored tokens; mean and weights 0 when all are)."""
+    torch = _torch()
+    if loss.dim() != 1 or loss.numel() < 1:
+        raise ValueError(f"loss must be a vector of at least one token, got {tuple(loss.shape)}")
+    m = loss.numel()
+    _expect(loss, "loss", dtypes=("float32",))
+    _expect(targets, "targets", shape=(m,), dtypes=("int64",))
+    with _Launch(stream, loss, targets) as sp:
+        mean = loss.new_empty(())
+        weight = torch.empty_like(loss)
+        st = lib().sketch_xent_mean(loss.data_ptr(), targets.data_ptr(), ignore_index, m, mean.data_ptr(),
+                                    weight.data_ptr(), sp)
+    _check("sketch_xent_mean", st)
+    return mean, weight
 
 
 def sketch_xent_bwd_workspace(m: int, n: int, d: int, b: int, gpr: int, x_dtype: int, lut_dtype: int,

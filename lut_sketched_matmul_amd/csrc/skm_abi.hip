@@ -506,6 +506,19 @@ int sketch_xent_fwd(const void* X, int x_dtype, const uint8_t* idx_packed, const
   return status_of(skm::launch_xent_fwd(a, loss, lse, workspace, stream));
 }
 
+int sketch_xent_mean(const float* loss, const int64_t* targets, int64_t ignore_index, int64_t m, float* mean,
+                     float* weight, hipStream_t stream) {
+  if (m < 1 || m >= (int64_t(1) << 31)) return SKM_EINVAL;
+  if (!loss || !targets || !mean || !weight) return SKM_EINVAL;
+  if (!aligned16(loss) || !aligned16(weight) || ((uintptr_t)targets & 7u) != 0 || ((uintptr_t)mean & 3u) != 0)
+    return SKM_EALIGN;
+  const Range w[2] = {{mean, 4}, {weight, m * 4}};
+  for (const Range& o : w)
+    if (overlap(o, {loss, m * 4}) || overlap(o, {targets, m * 8})) return SKM_EALIAS;
+  if (overlap(w[0], w[1])) return SKM_EALIAS;
+  return status_of(skm::launch_xent_mean(loss, targets, ignore_index, m, mean, weight, stream));
+}
+
 size_t sketch_xent_bwd_workspace(int64_t m, int64_t n, int64_t d, int b, int gpr, int x_dtype, int lut_dtype,
                                  int need_dx, int need_dlut) {
   if (m < 1 || (!need_dx && !need_dlut) || check_xent(m, n, d, b, gpr, x_dtype, lut_dtype) != SKM_OK) return 0;

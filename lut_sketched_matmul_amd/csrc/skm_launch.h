@@ -160,6 +160,8 @@ struct XentArgs {
 };
 size_t xent_fwd_bytes(const Problem& p, int x_dtype, int lut_dtype);
 hipError_t launch_xent_fwd(const XentArgs& a, float* loss, float* lse, void* ws, hipStream_t s);
+hipError_t launch_xent_mean(const float* loss, const int64_t* targets, int64_t ignore, int64_t m, float* mean,
+                            float* weight, hipStream_t s);
 size_t xent_bwd_bytes(const Problem& p, int x_dtype, int lut_dtype, bool need_dx, bool need_dlut);
 hipError_t launch_xent_bwd(const XentArgs& a, const float* lse, const float* dloss, void* dX, float* dLUT,
                            int accumulate, void* ws, hipStream_t s);

@@ -173,6 +173,42 @@ __global__ void __launch_bounds__(1024) k_xent_merge_few(const float2* __restric
   loss[t] = !live ? 0.0f : (target >= 0 && target < V ? l - tlogit[t] : __builtin_nanf(""));
 }
 
+// mean of the scored losses and every token's weight in it: one block, a chain
+// per thread, then the 1024 sums as a tree
+__global__ void __launch_bounds__(1024) k_xent_mean(const float* __restrict__ loss, const int64_t* __restrict__ targets,
+                                                    int64_t ignore, int64_t m, float* __restrict__ mean,
+                                                    float* __restrict__ weight) {
+  __shared__ float ssum[16];
+  __shared__ int32_t scnt[16];
+  float sum = 0.0f;
+  int32_t cnt = 0;
+  for (int64_t t = threadIdx.x; t < m; t += 1024) {
+    const bool on = targets[t] != ignore;
+    sum += on ? loss[t] : 0.0f;
+    cnt += on ? 1 : 0;
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    sum += __shfl_xor(sum, o, 64);
+    cnt += __shfl_xor(cnt, o, 64);
+  }
+  if ((threadIdx.x & 63) == 0) {
+    ssum[threadIdx.x >> 6] = sum;
+    scnt[threadIdx.x >> 6] = cnt;
+  }
+  __syncthreads();
+  sum = 0.0f;
+  cnt = 0;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) {
+    sum += ssum[w];
+    cnt += scnt[w];
+  }
+  const float wt = cnt > 0 ? 1.0f / (float)cnt : 0.0f;
+  if (threadIdx.x == 0) *mean = cnt > 0 ? sum / (float)cnt : 0.0f;
+  for (int64_t t = threadIdx.x; t < m; t += 1024) weight[t] = targets[t] != ignore ? wt : 0.0f;
+}
+
 // ---- backward --------------------------------------------------------------------------
 
 // Xc[c] = X[rows[c]] for the listed tokens, zeros up to the next multiple of 32
@@ -343,6 +379,12 @@ hipError_t launch_xent_fwd(const XentArgs& a, float* loss, float* lse, void* ws,
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k_xent_merge, dim3((unsigned)((p.m + 15) / 16)), dim3(256), 0, s, part, p.m,
                      (int)f.blocks, head, rows, a.targets, p.n, tlogit, loss, lse);
+  return hipGetLastError();
+}
+
+hipError_t launch_xent_mean(const float* loss, const int64_t* targets, int64_t ignore, int64_t m, float* mean,
+                            float* weight, hipStream_t s) {
+  hipLaunchKernelGGL(k_xent_mean, dim3(1), dim3(1024), 0, s, loss, targets, ignore, m, mean, weight);
   return hipGetLastError();
 }
 

@@ -167,6 +167,19 @@ def test_xent_buffer_refusals(lib):
     assert xb(lib, m=0, acc=1, X=None, t=None, lse=None, dl=None) == 0
 
 
+def test_xent_mean_refusals(lib):
+    call = lambda loss=addr(0), t=addr(1), m=4, mean=addr(2), w=addr(3): lib.sketch_xent_mean(loss, t, -100, m, mean, w,
+                                                                                              None)
+    assert call(m=0) == EINVAL and call(m=1 << 31) == EINVAL
+    for k in ("loss", "t", "mean", "w"):
+        assert call(**{k: None}) == EINVAL, k
+    assert call(loss=addr(0) + 8) == EALIGN and call(w=addr(3) + 4) == EALIGN and call(t=addr(1) + 4) == EALIGN
+    assert call(mean=addr(2) + 2) == EALIGN
+    for k in ("mean", "w"):
+        assert call(**{k: addr(0)}) == EALIAS and call(**{k: addr(1)}) == EALIAS
+    assert call(mean=addr(3) + 12) == EALIAS
+
+
 def test_wrappers_check_tensors_before_the_call():
     X = torch.zeros(4, 64, dtype=torch.float16)
     codes, scales = torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4, 2, dtype=torch.uint8)
