@@ -57,9 +57,13 @@ struct XentGemm {
   const int32_t* rows;
   const XentHead* head;
   const int64_t* targets;
-  const int32_t* rexp;
+  const int32_t* rexp;  // row exponents of X, by token (mixed pair)
   int64_t v0;
+  const void* Xp;       // the listed rows in the tables' dtype, in K order (xent_streams)
 };
+// whether the logit tiles read their activations and indices straight into LDS
+// (skm_xent_logits.h), from a copy of the listed rows that xent_rows makes
+inline bool xent_streams(const Problem& p) { return p.b == 4 && p.group_cols() % 64 == 0; }
 hipError_t xent_stats(const XentGemm& g, float2* part, int64_t stride, float* tlogit, hipStream_t s);
 struct XentGradOut {
   const float* lse;

@@ -1,6 +1,7 @@
 // Cross entropy of a sketched head: the small kernels around the tiles (token
 // list, merge of the statistics, gather of X, dX's last sum) and the host
 // side that cuts the vocabulary into pieces. The mathematics is in skm_xent.h.
+#include "skm_gemm_common.h"
 #include "skm_quant.h"
 #include "skm_xent.h"
 
@@ -89,6 +90,57 @@ __global__ void __launch_bounds__(1024) k_xent_index(const int64_t* __restrict__
       head->inv_scale = pow2f(-e);
     }
   }
+}
+
+// ---- the listed rows for the streaming logit tiles --------------------------------------
+// Xp[c] = X[rows[c]] in the tables' dtype TL, every 8 columns in the K order of
+// mm::dequant8_b4. SC (bf16 with f16 tables): prescaled by 2^-e of the row, e
+// written to rexp[token] (skm_common.h). One block per row; the second read of
+// a scaled row comes from the caches.
+template <typename TX, typename TL>
+__global__ void __launch_bounds__(256) k_xent_rows(const TX* __restrict__ X, const int32_t* __restrict__ rows,
+                                                   const XentHead* __restrict__ head, int64_t d, TL* __restrict__ Xp,
+                                                   int32_t* __restrict__ rexp) {
+  constexpr bool SC = scaled_pair(__is_same(TX, bf16_t), __is_same(TL, half_t));
+  __shared__ uint32_t top[4];
+  const int64_t c = blockIdx.x;
+  if (c >= head->count) return;
+  const int64_t t = rows[c];
+  const u32x4* src = reinterpret_cast<const u32x4*>(X + t * d);
+  u32x4* dst = reinterpret_cast<u32x4*>(Xp + c * d);
+  float scale = 1.0f;
+  if constexpr (SC) {
+    uint32_t mx = 0u;
+    for (int64_t j = threadIdx.x; j < d / 8; j += 256) {
+      const uint32_t a = absmax8_bf16(src[j]);
+      mx = mx > a ? mx : a;
+    }
+    mx = wave_max_to_lane63(mx);
+    if ((threadIdx.x & 63) == 63) top[threadIdx.x >> 6] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mx = w == 0 || top[w] > mx ? top[w] : mx;
+    const int e = row_exp_of(mx);
+    scale = pow2f(-e);
+    if (threadIdx.x == 0) rexp[t] = e;
+  }
+  for (int64_t j = threadIdx.x; j < d / 8; j += 256) {
+    if constexpr (SC) dst[j] = mm::cvt_quad_perm_scaled(src[j], scale);
+    else dst[j] = mm::cvt_quad_perm<TX, TL>(src[j]);
+  }
+}
+hipError_t xent_rows(const XentGemm& g, void* Xp, int32_t* rexp, hipStream_t s) {
+  const dim3 grid((unsigned)g.p.m);
+  if (g.x_dtype == DT_F16)
+    hipLaunchKernelGGL((k_xent_rows<half_t, half_t>), grid, dim3(256), 0, s, (const half_t*)g.X, g.rows, g.head, g.p.d,
+                       (half_t*)Xp, rexp);
+  else if (g.lut_dtype == DT_F16)
+    hipLaunchKernelGGL((k_xent_rows<bf16_t, half_t>), grid, dim3(256), 0, s, (const bf16_t*)g.X, g.rows, g.head,
+                       g.p.d, (half_t*)Xp, rexp);
+  else
+    hipLaunchKernelGGL((k_xent_rows<bf16_t, bf16_t>), grid, dim3(256), 0, s, (const bf16_t*)g.X, g.rows, g.head,
+                       g.p.d, (bf16_t*)Xp, rexp);
+  return hipGetLastError();
 }
 
 // ---- forward: merge of the blocks' (max, sum) pairs ------------------------------------
@@ -263,11 +315,13 @@ bool mixed(int x_dtype, int lut_dtype) { return scaled_pair(x_dtype == DT_BF16, 
 struct FwdPlan {
   bool few;
   int64_t blocks;                          // vocabulary blocks of the statistics
-  size_t rows, rexp, part, tlogit, bytes;  // byte offsets (the head is at 0)
+  bool streams;                            // listed rows copied for the streaming tiles
+  size_t rows, rexp, part, tlogit, xp, bytes;  // byte offsets (the head is at 0)
 };
 FwdPlan fwd_plan(const Problem& p, int x_dtype, int lut_dtype) {
   FwdPlan f;
   f.few = xent_few(p);
+  f.streams = !f.few && xent_streams(p);
   f.blocks = f.few ? (p.n + 15) / 16 : (p.n + XENT_BN - 1) / XENT_BN;
   size_t o = 256;
   f.rows = o;
@@ -278,6 +332,8 @@ FwdPlan fwd_plan(const Problem& p, int x_dtype, int lut_dtype) {
   o += up256((size_t)f.blocks * (size_t)p.m * 8);
   f.tlogit = o;
   o += up256((size_t)p.m * 4);
+  f.xp = o;
+  if (f.streams) o += up256((size_t)p.m * (size_t)p.d * 2);
   f.bytes = o;
   return f;
 }
@@ -286,7 +342,8 @@ struct BwdPlan {
   int64_t cap;         // listed rows, rounded up to 32
   int64_t P;           // vocabulary rows per piece
   DxRanges ranges;     // of the first piece's rows, each with its own dX
-  size_t rows, pos, rexp, hi, lo, dxv, acc, xc, part, bytes;
+  bool few, streams;
+  size_t rows, pos, rexp, hi, lo, dxv, acc, xc, xp, part, bytes;
 };
 
 // The pieces: dZ of a piece takes 2 bytes per (token, word) and form, and is
@@ -299,6 +356,8 @@ BwdPlan bwd_plan(const Problem& p, int x_dtype, int lut_dtype, bool need_dx, boo
   const bool mx = mixed(x_dtype, lut_dtype);
   const bool has_hi = need_dlut || !mx, has_dxv = need_dx && mx;
   const int forms = (has_hi ? 1 : 0) + (need_dlut ? 1 : 0) + (has_dxv ? 1 : 0);
+  f.few = xent_few(p);
+  f.streams = !f.few && xent_streams(p);
   f.cap = (p.m + 31) / 32 * 32;
   int64_t P = (int64_t)(XENT_PIECE_BYTES / (size_t)(f.cap * 2 * forms)) / XENT_BN * XENT_BN;
   if (P < XENT_BN) P = XENT_BN;
@@ -330,6 +389,7 @@ BwdPlan bwd_plan(const Problem& p, int x_dtype, int lut_dtype, bool need_dx, boo
     part = b > part ? b : part;
   }
   f.part = take(need_dlut, part);
+  f.xp = take(f.streams, (size_t)p.m * (size_t)p.d * 2);
   f.bytes = o;
   return f;
 }
@@ -360,7 +420,8 @@ hipError_t launch_xent_fwd(const XentArgs& a, float* loss, float* lse, void* ws,
   int32_t* rexp = mixed(a.x_dtype, a.lut_dtype) ? at<int32_t>(ws, f.rexp) : nullptr;
   float2* part = at<float2>(ws, f.part);
   float* tlogit = at<float>(ws, f.tlogit);
-  const XentGemm g{a.X, a.x_dtype, a.idx, a.lut, a.lut_dtype, p, rows, head, a.targets, rexp, 0};
+  void* xp = f.streams ? at<void>(ws, f.xp) : nullptr;
+  const XentGemm g{a.X, a.x_dtype, a.idx, a.lut, a.lut_dtype, p, rows, head, a.targets, rexp, 0, xp};
   hipError_t e = hipSuccess;
   if (f.few) {
     if (rexp && !few_stages(p)) e = launch_row_exp(a.X, p.m, p.d, rexp, s);
@@ -373,7 +434,8 @@ hipError_t launch_xent_fwd(const XentArgs& a, float* loss, float* lse, void* ws,
   hipLaunchKernelGGL(k_xent_index<false>, dim3(1), dim3(1024), 0, s, a.targets, a.ignore, p.m, nullptr, head, rows,
                      nullptr, loss, lse);
   e = hipGetLastError();
-  if (e == hipSuccess && rexp) e = launch_row_exp(a.X, p.m, p.d, rexp, s);
+  if (e == hipSuccess && f.streams) e = xent_rows(g, xp, rexp, s);
+  else if (e == hipSuccess && rexp) e = launch_row_exp(a.X, p.m, p.d, rexp, s);
   if (e != hipSuccess) return e;
   e = xent_stats(g, part, p.m, tlogit, s);
   if (e != hipSuccess) return e;
@@ -409,13 +471,15 @@ hipError_t launch_xent_bwd(const XentArgs& a, const float* lse, const float* dlo
   hipLaunchKernelGGL(k_xent_index<true>, dim3(1), dim3(1024), 0, s, a.targets, a.ignore, p.m, dloss, head, rows, pos,
                      nullptr, nullptr);
   hipError_t e = hipGetLastError();
-  if (e == hipSuccess && rexp) e = launch_row_exp(a.X, p.m, p.d, rexp, s);
+  void* xp = f.streams ? at<void>(ws, f.xp) : nullptr;
+  XentGemm g{a.X, a.x_dtype, a.idx, a.lut, a.lut_dtype, p, rows, head, a.targets, rexp, 0, xp};
+  if (e == hipSuccess && f.streams) e = xent_rows(g, xp, rexp, s);
+  else if (e == hipSuccess && rexp) e = launch_row_exp(a.X, p.m, p.d, rexp, s);
   if (e == hipSuccess && dLUT) {
     hipLaunchKernelGGL(k_xent_gather, dim3((unsigned)f.cap), dim3(256), 0, s, (const uint16_t*)a.X, rows, head, p.d,
                        (uint16_t*)xc);
     e = hipGetLastError();
   }
-  const bool few = xent_few(p);
   const int es = 2;  // bytes of a table entry (16-bit pairs only)
   for (int64_t v0 = 0; v0 < p.n && e == hipSuccess; v0 += f.P) {
     const int64_t n = p.n - v0 < f.P ? p.n - v0 : f.P;
@@ -423,9 +487,12 @@ hipError_t launch_xent_bwd(const XentArgs& a, const float* lse, const float* dlo
     const uint8_t* idx = a.idx + v0 * p.row_bytes();
     const void* lut = static_cast<const char*>(a.lut) + v0 * p.gpr * p.k() * es;
     const int64_t ld = (n + 7) / 8 * 8;
-    const XentGemm g{a.X, a.x_dtype, idx, lut, a.lut_dtype, q, rows, head, a.targets, rexp, v0};
+    g.idx = idx;
+    g.lut = lut;
+    g.p = q;
+    g.v0 = v0;
     const XentGradOut out{lse, dloss, p.n, ld, hi, lo, dxv};
-    e = few ? xent_few_grad(g, out, pos, s) : xent_grad(g, out, s);
+    e = f.few ? xent_few_grad(g, out, pos, s) : xent_grad(g, out, s);
     if (e == hipSuccess && dX) {
       // every range of the first piece is written; later pieces add to some or all
       const int64_t steps = (n + 63) / 64;

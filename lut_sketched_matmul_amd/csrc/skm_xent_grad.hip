@@ -1,6 +1,6 @@
 // Cross entropy backward: the instances of the matmul's tiles that end in the
 // logits' gradient (EpGrad).
-#include "skm_xent_tiles.h"
+#include "skm_xent_logits.h"
 
 namespace skm {
 
@@ -22,6 +22,8 @@ hipError_t grad_b(const XentGemm& g, const XentGradOut& o, hipStream_t s) {
   a.hi = (TX*)o.hi;
   a.lo = (TX*)o.lo;
   a.dxv = (TL*)o.dxv;
+  if constexpr (B == 4)
+    if (xent_streams(g.p)) return xent_logits_launch<TL, EP, !__is_same(TX, TL)>(g, a, s);
   return gemm_fwd_b<B, TX, TL, EP>((const TX*)g.X, g.idx, (const TL*)g.lut, g.p, a, g.rexp, s);
 }
 

@@ -1,6 +1,6 @@
 // Cross entropy forward: the instances of the matmul's tiles that end in
 // softmax statistics (EpStats).
-#include "skm_xent_tiles.h"
+#include "skm_xent_logits.h"
 
 namespace skm {
 
@@ -17,6 +17,8 @@ hipError_t stats_b(const XentGemm& g, float2* part, int64_t stride, float* tlogi
   a.part = part;
   a.stride = stride;
   a.tlogit = tlogit;
+  if constexpr (B == 4)
+    if (xent_streams(g.p)) return xent_logits_launch<TL, EP, !__is_same(TX, TL)>(g, a, s);
   return gemm_fwd_b<B, TX, TL, EP>((const TX*)g.X, g.idx, (const TL*)g.lut, g.p, a, g.rexp, s);
 }
 
