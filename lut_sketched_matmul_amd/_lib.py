@@ -503,45 +503,44 @@ def sketch_hessian_factor(H, damp: float = 0.01, out=None, workspace=None, strea
 # 8-bit activation checkpoints, norms
 # --------------------------------------------------------------------------
 
-class _Launch:
-    """The device and stream a call runs on, current while it allocates and launches.
+def _enter(stream, first, *others):
+    """(raw stream, context): makes the tensors' device and the stream a call runs on current.
 
-    The tensors must share one device, which becomes current; `stream` (None = the device's current stream)
-    becomes current too, so outputs and workspaces allocated meanwhile belong to the stream that uses them.
-    Ordering the inputs before `stream` is the caller's.
+    The tensors must live on one GPU and be contiguous. `stream` (None = the device's current stream) becomes
+    current too, so that outputs and workspaces allocated before :func:`_leave` belong to the stream that uses
+    them; ordering the inputs before it is the caller's. The context is None when nothing had to change.
     """
-
-    __slots__ = ("index", "stream", "inner")
-
-    def __init__(self, stream, first, *others):
-        _require_device(first, *others)
-        index = first.get_device()
-        for t in others:
-            if t is not None and t.get_device() != index:
+    torch = _torch()
+    index = first.get_device()
+    for t in (first, *others):
+        if t is not None:
+            if not t.is_cuda:
+                raise ValueError("tensors must live on the GPU")
+            if not t.is_contiguous():
+                raise ValueError("tensors must be contiguous")
+            if t.get_device() != index:
                 raise ValueError(f"tensors on cuda:{index} and cuda:{t.get_device()}")
-        if stream is not None and stream.device_index != index:
+    context = None
+    if stream is not None:
+        if stream.device_index != index:
             raise ValueError(f"a stream of cuda:{stream.device_index} for tensors on cuda:{index}")
-        self.index, self.stream, self.inner = index, stream, None
+        context = torch.cuda.stream(stream)
+    elif torch.cuda.current_device() != index:
+        context = torch.cuda.device(index)
+    if context is not None:
+        context.__enter__()
+    # (the raw handle: building a Stream object costs as much as half a launch)
+    return torch._C._cuda_getCurrentRawStream(index), context
 
-    def __enter__(self):
-        torch = _torch()
-        if self.stream is not None:
-            self.inner = torch.cuda.stream(self.stream)
-        elif torch.cuda.current_device() != self.index:
-            self.inner = torch.cuda.device(self.index)
-        if self.inner is not None:
-            self.inner.__enter__()
-        # (the raw handle: building a Stream object costs as much as half a launch)
-        return torch._C._cuda_getCurrentRawStream(self.index)
 
-    def __exit__(self, *exc):
-        if self.inner is not None:
-            self.inner.__exit__(*exc)
+def _leave(context):
+    if context is not None:
+        context.__exit__(None, None, None)
 
 
 def _ptr(t):
-    """The tensor's address (None for no tensor or an empty one)."""
-    return t.data_ptr() if t is not None and t.numel() else None
+    """The tensor's address (None for no tensor; an empty one's is null too)."""
+    return None if t is None else t.data_ptr()
 
 
 def _size(t) -> int:
@@ -564,12 +563,15 @@ def sketch_act_quant(X, codes=None, scales=None, stream=None) -> Tuple[object, o
     if d < 32 or d % 32:
         raise ValueError(f"X has {d} columns: a checkpoint takes whole blocks of 32")
     _check_ckpt(codes, scales, m, d)
-    with _Launch(stream, X, codes, scales) as sp:
+    sp, context = _enter(stream, X, codes, scales)
+    try:
         if codes is None:
             codes = X.new_empty((m, d), dtype=torch.int8)
         if scales is None:
             scales = X.new_empty((m, d // 32), dtype=torch.uint8)
         st = lib().sketch_act_quant(_ptr(X), dtype_code(X), m, d, _ptr(codes), _ptr(scales), sp)
+    finally:
+        _leave(context)
     _check("sketch_act_quant", st)
     return codes, scales
 
@@ -584,10 +586,13 @@ def sketch_act_dequant(codes, scales, dtype, out=None, stream=None):
     if out is None and dtype not in (torch.float32, torch.float16, torch.bfloat16):
         raise TypeError(f"unsupported dtype {dtype}")
     _expect(out, "out", shape=(m, d), dtypes=(str(dtype).replace("torch.", ""),))
-    with _Launch(stream, codes, scales, out) as sp:
+    sp, context = _enter(stream, codes, scales, out)
+    try:
         if out is None:
             out = codes.new_empty((m, d), dtype=dtype)
         st = lib().sketch_act_dequant(_ptr(codes), _ptr(scales), m, d, _ptr(out), dtype_code(out), sp)
+    finally:
+        _leave(context)
     _check("sketch_act_dequant", st)
     return out
 
@@ -617,7 +622,8 @@ def sketch_matmul_bwd_ckpt(dY, codes, scales, idx_packed, lut, b: int, gpr: int,
     _expect(dlut_out, "dlut_out", shape=(n, gpr, K), dtypes=("float32",))
     _expect(workspace, "workspace", dtypes=("uint8",))
     io, lt = dtype_code(dY), dtype_code(lut)
-    with _Launch(stream, dY, codes, scales, idx_packed, lut, dlut_out, workspace) as sp:
+    sp, context = _enter(stream, dY, codes, scales, idx_packed, lut, dlut_out, workspace)
+    try:
         dX = torch.empty((m, d), dtype=torch.float32, device=dY.device) if need_dx else None
         dL = None
         if need_dlut:
@@ -627,6 +633,8 @@ def sketch_matmul_bwd_ckpt(dY, codes, scales, idx_packed, lut, b: int, gpr: int,
         st = lib().sketch_matmul_bwd_ckpt(_ptr(dY), _ptr(codes), _ptr(scales), io, idx_packed.data_ptr(),
                                           lut.data_ptr(), lt, m, n, d, b, gpr, _ptr(dX), _ptr(dL),
                                           1 if accumulate else 0, _ptr(ws), _size(ws), sp)
+    finally:
+        _leave(context)
     _check("sketch_matmul_bwd_ckpt", st)
     return dX, dL
 
@@ -671,7 +679,8 @@ def sketch_norm_fwd(X, weight=None, bias=None, kind: str = "layer", eps: float =
     if checkpoint and d % 32:
         raise ValueError(f"X has {d} columns: a checkpoint takes whole blocks of 32")
     _expect(out, "out", shape=(m, d), dtypes=(_dtype_name(X),))
-    with _Launch(stream, X, weight, bias, out) as sp:
+    sp, context = _enter(stream, X, weight, bias, out)
+    try:
         if out is None:
             out = torch.empty_like(X)
         mean = X.new_empty(m, dtype=torch.float32) if k else None
@@ -682,6 +691,8 @@ def sketch_norm_fwd(X, weight=None, bias=None, kind: str = "layer", eps: float =
             scales = X.new_empty((m, d // 32), dtype=torch.uint8)
         st = lib().sketch_norm_fwd(_ptr(X), dtype_code(X), _ptr(weight), _ptr(bias), pc, m, d, k, eps, _ptr(out),
                                    _ptr(mean), _ptr(rstd), _ptr(codes), _ptr(scales), sp)
+    finally:
+        _leave(context)
     _check("sketch_norm_fwd", st)
     return out, mean, rstd, codes, scales
 
@@ -732,7 +743,8 @@ def sketch_norm_bwd(dY, X, weight, mean, rstd, kind: str = "layer", need_dx: boo
     _expect(dw_out, "dw_out", shape=(d,), dtypes=("float32",))
     _expect(db_out, "db_out", shape=(d,), dtypes=("float32",))
     _expect(workspace, "workspace", dtypes=("uint8",))
-    with _Launch(stream, dY, X, codes, scales, weight, mean, rstd, dw_out, db_out, workspace) as sp:
+    sp, context = _enter(stream, dY, X, codes, scales, weight, mean, rstd, dw_out, db_out, workspace)
+    try:
         dev = dY.device
         dX = torch.empty((m, d), dtype=xt, device=dev) if need_dx else None
         dw = db = None
@@ -745,6 +757,8 @@ def sketch_norm_bwd(dY, X, weight, mean, rstd, kind: str = "layer", need_dx: boo
         st = lib().sketch_norm_bwd(_ptr(dY), dtype_code(dY), _ptr(X), xc, _ptr(codes), _ptr(scales),
                                    _ptr(weight), pc, _ptr(mean), _ptr(rstd), m, d, k, _ptr(dX), _ptr(dw), _ptr(db),
                                    1 if accumulate else 0, _ptr(ws), _size(ws), sp)
+    finally:
+        _leave(context)
     _check("sketch_norm_bwd", st)
     return dX, dw, db
 
@@ -782,12 +796,15 @@ def sketch_xent_fwd(X, idx_packed, lut, targets, b: int, gpr: int, ignore_index:
     m, n, d = _check_xent(X, idx_packed, lut, targets, b, gpr)
     _expect(workspace, "workspace", dtypes=("uint8",))
     xc, lc = dtype_code(X), dtype_code(lut)
-    with _Launch(stream, X, idx_packed, lut, targets, workspace) as sp:
+    sp, context = _enter(stream, X, idx_packed, lut, targets, workspace)
+    try:
         loss = torch.empty(m, dtype=torch.float32, device=X.device)
         lse = torch.empty(m, dtype=torch.float32, device=X.device)
         ws = _workspace(workspace, sketch_xent_fwd_workspace(m, n, d, b, gpr, xc, lc), X.device)
         st = lib().sketch_xent_fwd(_ptr(X), xc, idx_packed.data_ptr(), lut.data_ptr(), lc, _ptr(targets), ignore_index,
                                    m, n, d, b, gpr, _ptr(loss), _ptr(lse), _ptr(ws), _size(ws), sp)
+    finally:
+        _leave(context)
     _check("sketch_xent_fwd", st)
     return loss, lse
 
@@ -801,11 +818,14 @@ def sketch_xent_mean(loss, targets, ignore_index: int = -100, stream=None) -> Tu
     m = loss.numel()
     _expect(loss, "loss", dtypes=("float32",))
     _expect(targets, "targets", shape=(m,), dtypes=("int64",))
-    with _Launch(stream, loss, targets) as sp:
+    sp, context = _enter(stream, loss, targets)
+    try:
         mean = loss.new_empty(())
         weight = torch.empty_like(loss)
         st = lib().sketch_xent_mean(loss.data_ptr(), targets.data_ptr(), ignore_index, m, mean.data_ptr(),
                                     weight.data_ptr(), sp)
+    finally:
+        _leave(context)
     _check("sketch_xent_mean", st)
     return mean, weight
 
@@ -831,7 +851,8 @@ def sketch_xent_bwd(X, idx_packed, lut, targets, lse, dloss, b: int, gpr: int, i
     _expect(dlut_out, "dlut_out", shape=(n, gpr, K), dtypes=("float32",))
     _expect(workspace, "workspace", dtypes=("uint8",))
     xc, lc = dtype_code(X), dtype_code(lut)
-    with _Launch(stream, X, idx_packed, lut, targets, lse, dloss, dlut_out, workspace) as sp:
+    sp, context = _enter(stream, X, idx_packed, lut, targets, lse, dloss, dlut_out, workspace)
+    try:
         dX = torch.empty((m, d), dtype=X.dtype, device=X.device) if need_dx else None
         dL = None
         if need_dlut:
@@ -840,5 +861,7 @@ def sketch_xent_bwd(X, idx_packed, lut, targets, lse, dloss, b: int, gpr: int, i
         st = lib().sketch_xent_bwd(_ptr(X), xc, idx_packed.data_ptr(), lut.data_ptr(), lc, _ptr(targets), ignore_index,
                                    _ptr(lse), _ptr(dloss), m, n, d, b, gpr, _ptr(dX), _ptr(dL),
                                    1 if accumulate else 0, _ptr(ws), _size(ws), sp)
+    finally:
+        _leave(context)
     _check("sketch_xent_bwd", st)
     return dX, dL

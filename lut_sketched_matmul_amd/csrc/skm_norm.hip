@@ -370,6 +370,7 @@ struct NormShape {
 };
 NormShape shape_of(int64_t d) {
   if (d <= 512) return {64, 1};
+  if (d <= 1024) return {64, 2};
   if (d <= 2048) return {64, 4};
   if (d <= 4096) return {256, 2};
   if (d <= 8192) return {256, 4};
@@ -380,8 +381,11 @@ NormShape shape_of(int64_t d) {
 template <typename F>
 hipError_t with_shape(int64_t d, F&& f) {
   const NormShape s = shape_of(d);
-  if (s.tpr == 64) return s.nch == 1 ? f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{})
-                                     : f(std::integral_constant<int, 64>{}, std::integral_constant<int, 4>{});
+  if (s.tpr == 64) {
+    if (s.nch == 1) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+    if (s.nch == 2) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
+    return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 4>{});
+  }
   if (s.tpr == 256) {
     if (s.nch == 2) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
     if (s.nch == 4) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});

@@ -168,7 +168,7 @@ def test_bwd_from_checkpoint_infinite_gradient_stays_in_its_row(m):
 # norms
 # ---------------------------------------------------------------------------------------------------------
 
-SHAPES = [(1, 1), (2, 7), (3, 32), (5, 100), (4, 513), (7, 512), (9, 1001), (3, 2048), (2, 2056), (3, 4096),
+SHAPES = [(1, 1), (2, 7), (3, 32), (5, 100), (4, 513), (7, 512), (9, 1001), (6, 1024), (3, 1025), (3, 2048), (2, 2056), (3, 4096),
           (2, 5000), (2, 8224), (1, 16384), (2, 17000), (1, 65536), (300, 64)]
 
 
