@@ -227,7 +227,7 @@ size_t sketch_matmul_bwd_workspace(int64_t m, int64_t n, int64_t d, int b, int g
  *   sketch_act_quant    X [m][d] x_dtype (F32, F16, BF16) -> codes, scales
  *   sketch_act_dequant  codes, scales -> X [m][d] x_dtype (the dtype that was
  *                       quantised; a narrower one rounds)
- * d >= 32 and a multiple of 32, m >= 0 (0 is a no-op), m * d <= 2^42. All
+ * d >= 32 and a multiple of 32, m >= 0 (0 is a no-op), m * d <= 2^34. All
  * pointers 16-byte aligned; outputs must not overlap inputs or each other.
  */
 int sketch_act_quant(const void* X, int x_dtype, int64_t m, int64_t d,
@@ -243,8 +243,8 @@ int sketch_act_dequant(const int8_t* codes, const uint8_t* scales, int64_t m, in
  * workspace: at least sketch_matmul_bwd_ckpt_workspace(...) bytes (one X in
  * io_dtype for dLUT, up to 128 MiB of partial sums of dX when its tiles are
  * few, one dY when n is not a multiple of 8, split table gradients); need_dx /
- * need_dlut = 0 where the output is NULL. Everything else as for
- * sketch_matmul_bwd.
+ * need_dlut = 0 where the output is NULL. m * n and m * d at most 2^34.
+ * Everything else as for sketch_matmul_bwd.
  */
 int sketch_matmul_bwd_ckpt(const void* dY, const int8_t* codes, const uint8_t* scales, int io_dtype,
                            const uint8_t* idx_packed, const void* lut, int lut_dtype,
@@ -313,8 +313,8 @@ size_t sketch_norm_bwd_workspace(int64_t m, int64_t d);
  *   loss, lse [m] fp32.
  * Dtype pairs (x_dtype, lut_dtype): (F16, F16), (BF16, F16), (BF16, BF16)
  * (matrix cores, fp32 logits and statistics; the (BF16, F16) range rule at
- * the top applies); others return SKM_EUNSUPPORTED. m < 2^31, d <= 2^20; m == 0 is
- * a no-op. targets 8-byte, other pointers 16-byte aligned. workspace: at least
+ * the top applies); others return SKM_EUNSUPPORTED. m <= 2^22, d <= 2^20, and
+ * at most 2^22 tiles of 256 tokens x 256 words (or columns); m == 0 is a no-op. targets 8-byte, other pointers 16-byte aligned. workspace: at least
  * sketch_xent_fwd_workspace(...) bytes (8 bytes per token and 256 words, and
  * 8 to 12 per token).
  */

@@ -293,8 +293,8 @@ int sketch_matmul_bwd_noalloc(const void* dY, const void* X, int io_dtype, const
 
 static int check_ckpt_shape(int64_t m, int64_t d) {
   if (m < 0 || d < 32 || d % 32 != 0) return SKM_EINVAL;
-  // the streaming kernels take 2048 values per block; m * d <= 2^42 keeps the grid below 2^31
-  if (m > (int64_t(1) << 31) || d > (int64_t(1) << 31) || (m > 0 && d > (int64_t(1) << 42) / m)) return SKM_EINVAL;
+  // the streaming kernels take 8 values per thread and a launch has fewer than 2^32 threads
+  if (m > (int64_t(1) << 31) || d > (int64_t(1) << 31) || (m > 0 && d > (int64_t(1) << 34) / m)) return SKM_EINVAL;
   return SKM_OK;
 }
 
@@ -340,6 +340,7 @@ int sketch_matmul_bwd_ckpt(const void* dY, const int8_t* codes, const uint8_t* s
   int st = check_shape(m, n, d, b, gpr);
   if (st == SKM_OK) st = check_ckpt_shape(m, d);
   if (st != SKM_OK) return st;
+  if (m > 0 && n > (int64_t(1) << 34) / m) return SKM_EINVAL;
   if (!supported_pair(io_dtype, lut_dtype)) return SKM_EUNSUPPORTED;
   if (accumulate != 0 && accumulate != 1) return SKM_EINVAL;
   if (!idx_packed || !lut) return SKM_EINVAL;
@@ -467,7 +468,12 @@ int sketch_norm_bwd(const void* dY, int dy_dtype, const void* X, int x_dtype, co
 static int check_xent(int64_t m, int64_t n, int64_t d, int b, int gpr, int x_dtype, int lut_dtype) {
   const int st = check_shape(m, n, d, b, gpr);
   if (st != SKM_OK) return st;
-  if (m >= (int64_t(1) << 31) || d > (int64_t(1) << 20)) return SKM_EINVAL;
+  // a launch has fewer than 2^32 threads: rows of up to 256 each, tiles (256
+  // tokens x 256 words or columns, 128 words x a group) of 512
+  const int64_t tm = (m + 255) / 256, most = int64_t(1) << 22;
+  if (m > most || d > (int64_t(1) << 20) || tm * ((n + 255) / 256) > most || tm * ((d + 255) / 256) > most ||
+      (n + 127) / 128 * gpr > most)
+    return SKM_EINVAL;
   // (F16 activations would be rounded to the BF16 tables' 8 bits: the loss is
   // fp32, so that pair is not provided)
   const bool ok = (x_dtype == SKM_F16 && lut_dtype == SKM_F16) ||

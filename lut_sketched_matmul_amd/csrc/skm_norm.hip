@@ -400,14 +400,18 @@ hipError_t norm_fwd_t(const NormArgs& a, const T* X, T* Y, float* mean, float* r
   return with_shape(a.d, [&](auto tpr, auto nch) {
     constexpr int TPR = decltype(tpr)::value, NCH = decltype(nch)::value;
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
-    const dim3 grid((unsigned)((a.m + RPB - 1) / RPB)), block(TPR < 256 ? 256 : TPR);
-    if (a.d % 8 == 0)
-      hipLaunchKernelGGL((k_norm_fwd<T, true, TPR, NCH>), grid, block, 0, s, X, a.w, a.bias, a.p_f32, a.m, (int)a.d,
-                         a.layer, a.eps, Y, mean, rstd, codes, scales);
-    else
-      hipLaunchKernelGGL((k_norm_fwd<T, false, TPR, NCH>), grid, block, 0, s, X, a.w, a.bias, a.p_f32, a.m, (int)a.d,
-                         a.layer, a.eps, Y, mean, rstd, codes, scales);
-    return hipGetLastError();
+    const auto kern = a.d % 8 == 0 ? k_norm_fwd<T, true, TPR, NCH> : k_norm_fwd<T, false, TPR, NCH>;
+    // a launch has fewer than 2^32 threads: at most 2^21 rows of up to 1024
+    constexpr int64_t most = int64_t(1) << 21;
+    hipError_t e = hipSuccess;
+    for (int64_t r = 0; r < a.m && e == hipSuccess; r += most) {
+      const int64_t m = a.m - r < most ? a.m - r : most;
+      hipLaunchKernelGGL(kern, dim3((unsigned)((m + RPB - 1) / RPB)), dim3(TPR < 256 ? 256 : TPR), 0, s, X + r * a.d,
+                         a.w, a.bias, a.p_f32, m, (int)a.d, a.layer, a.eps, Y + r * a.d, mean ? mean + r : nullptr,
+                         rstd + r, codes ? codes + r * a.d : nullptr, scales ? scales + r * (a.d / 32) : nullptr);
+      e = hipGetLastError();
+    }
+    return e;
   });
 }
 

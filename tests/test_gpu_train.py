@@ -552,3 +552,80 @@ def test_captured_step_replays():
         t.cuda.synchronize()
         for p, q in zip(got, want):
             assert t.equal(p, q)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 elements: the last rows of the whole give what those rows alone give."""
+    t, k = torch(), skm()
+    m, d = 131200, 32768
+    X = t.zeros((m, d), dtype=t.bfloat16, device="cuda")
+    X[-3:] = t.randn((3, d), device="cuda").bfloat16()
+    Y, mean, rstd, codes, scales = k.sketch_norm_fwd(X, kind="rms", checkpoint=True)
+    y, _, r, c, s = k.sketch_norm_fwd(X[-3:].contiguous(), kind="rms", checkpoint=True)
+    assert t.equal(Y[-3:], y) and t.equal(rstd[-3:], r) and t.equal(codes[-3:], c) and t.equal(scales[-3:], s)
+    back = k.sketch_act_dequant(codes, scales, t.bfloat16, out=Y)
+    assert t.equal(back[-3:], k.sketch_act_dequant(c, s, t.bfloat16)) and not back[:-3].any()
+    dX, dw, db = k.sketch_norm_bwd(X, X, None, None, rstd, kind="rms")
+    dx = k.sketch_norm_bwd(X[-3:].contiguous(), X[-3:].contiguous(), None, None, r, kind="rms")
+    assert t.equal(dX[-3:], dx[0]) and not dX[:-3].any()
+
+
+def test_two_graphs_share_a_workspace():
+    """A workspace holds nothing between calls: two captured calls of different sizes take turns on one."""
+    t, k = torch(), skm()
+    calls = []
+    for name, m, V, d, b in (("a", 96, 700, 256, 4), ("b", 40, 300, 128, 3)):
+        gi, gl, _, _ = head("share/" + name, V, d, b, 1, "f16")
+        X = t.randn((m, d), device="cuda").half()
+        T = t.randint(0, V, (m,), device="cuda")
+        T[::5] = -100
+        calls.append((X, gi, gl, T, b, 1))
+    need = max(k.sketch_xent_bwd_workspace(X.shape[0], gi.shape[0], X.shape[1], b, 1, 1, 1)
+               for X, gi, gl, T, b, _ in calls)
+    need = max([need] + [k.sketch_xent_fwd_workspace(X.shape[0], gi.shape[0], X.shape[1], b, 1, 1, 1)
+                         for X, gi, gl, T, b, _ in calls])
+    ws = t.full((need,), 255, dtype=t.uint8, device="cuda")          # (NaN wherever a call reads before it writes)
+
+    def run(c):
+        loss, lse = k.sketch_xent_fwd(*c, workspace=ws)
+        return (loss, lse, *k.sketch_xent_bwd(c[0], c[1], c[2], c[3], lse, t.ones_like(loss), c[4], c[5], workspace=ws))
+
+    want = [[o.clone() for o in run(c)] for c in calls]
+    graphs, outs = [], []
+    for c in calls:
+        g = t.cuda.CUDAGraph()
+        with t.cuda.graph(g):
+            outs.append(run(c))
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1, 0):
+        ws.fill_(255)
+        graphs[i].replay()
+        t.cuda.synchronize()
+        assert all(t.equal(p, q) for p, q in zip(outs[i], want[i]))
+
+
+def test_two_streams_at_once():
+    """Calls on two streams with their own workspaces do not disturb each other."""
+    t, k = torch(), skm()
+    gi, gl, _, _ = head("two", 1000, 512, 4, 1, "f16")
+    sets = []
+    for i in range(2):
+        X = t.randn((300, 512), device="cuda").half()
+        T = t.randint(0, 1000, (300,), device="cuda")
+        sets.append((X, gi, gl, T, 4, 1))
+    DL = t.ones(300, device="cuda")
+    want = []
+    for c in sets:
+        loss, lse = k.sketch_xent_fwd(*c)
+        want.append((loss, *k.sketch_xent_bwd(c[0], gi, gl, c[3], lse, DL, 4, 1)))
+    t.cuda.synchronize()
+    streams = [t.cuda.Stream() for _ in sets]
+    got = []
+    for _ in range(3):
+        got = []
+        for c, s in zip(sets, streams):
+            loss, lse = k.sketch_xent_fwd(*c, stream=s)
+            got.append((loss, *k.sketch_xent_bwd(c[0], gi, gl, c[3], lse, DL, 4, 1, stream=s)))
+    t.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(t.equal(p, q) for p, q in zip(g, w))

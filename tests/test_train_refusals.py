@@ -31,7 +31,7 @@ def dequant(lib, codes=addr(1), scales=addr(2), m=4, d=64, X=addr(0), dt=F16):
 def test_checkpoint_refusals(lib, call):
     assert call(lib, d=0) == EINVAL and call(lib, d=16) == EINVAL and call(lib, d=48) == EINVAL
     assert call(lib, m=-1) == EINVAL
-    assert call(lib, m=1 << 31, d=1 << 20) == EINVAL          # m * d over 2^42
+    assert call(lib, m=1 << 20, d=(1 << 14) + 32) == EINVAL   # m * d over 2^34
     assert call(lib, dt=3) == EUNSUP
     assert call(lib, X=None) == EINVAL and call(lib, codes=None) == EINVAL and call(lib, scales=None) == EINVAL
     assert call(lib, X=addr(0) + 8) == EALIGN and call(lib, codes=addr(1) + 4) == EALIGN
@@ -132,7 +132,9 @@ def xb(lib, X=addr(0), dt=F16, idx=addr(1), lut=addr(2), ldt=F16, t=addr(3), ign
 def test_xent_shape_and_dtype_refusals(lib, call):
     assert call(lib, n=0) == EINVAL and call(lib, b=1) == EINVAL and call(lib, m=-1) == EINVAL
     assert call(lib, gpr=4) == EINVAL                          # groups of 16 columns
-    assert call(lib, m=1 << 31) == EINVAL and call(lib, d=(1 << 20) + 64) == EINVAL
+    assert call(lib, m=(1 << 22) + 1) == EINVAL and call(lib, d=(1 << 20) + 64) == EINVAL
+    assert call(lib, m=1 << 22, n=1 << 17) == EINVAL           # 2^14 x 2^9 tiles
+    assert call(lib, n=1 << 30, gpr=2) == EINVAL
     for pair in ((F32, F32), (F16, BF16), (F32, F16), (F16, F32), (7, F16)):
         assert call(lib, dt=pair[0], ldt=pair[1]) == EUNSUP, pair
 
