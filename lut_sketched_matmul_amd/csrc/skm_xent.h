@@ -18,13 +18,20 @@
 // and dLUT then run on the piece (skm_gemm_bwd.h).
 //
 // Rounding. dZ is an MFMA operand, so it is 16 bits wide. dX, itself rounded
-// to 16 bits, takes dZ rounded once, in the tables' dtype (one relative error
-// of half a step per term, as its own rounding). dLUT is fp32: it takes dZ as
-// the sum hi + lo of two values of X's dtype, which leaves 2^-18 (bf16) or
-// 2^-24 (f16) of each term. All are scaled by one power of two that puts the
-// largest |dloss| into [2^14, 2^15), so that f16 holds a softmax value down to
-// 2^-28 of the largest gradient at full precision; the results are scaled
-// back in fp32 (exact).
+// to 16 bits, takes dZ rounded once, in the tables' dtype (half a step per
+// term). The target's term, which carries most of a token's gradient, keeps its
+// remainder in fp32 and k_xent_dx_out adds it times the target's weights. dLUT
+// is fp32: it takes dZ as the sum hi + lo of two f16 values, which leaves 2^-23
+// of each term. f16 rather than X's dtype, since two bf16 values leave 2^-17;
+// bf16 rows of X are prescaled by 2^-e to f16 as for a forward pass
+// (skm_common.h) and their rows of dZ multiplied by 2^e. (dX has a form of its
+// own then: a row of X near zero has no gradient to give to the tables, but
+// takes one itself.)
+// The f16 forms are scaled by one power of two that puts the largest row
+// factor, |dloss| 2^e or |dloss|, into [2^14, 2^15), so that f16 holds a
+// softmax value down to 2^-28 of the largest gradient at full precision; the
+// results are scaled back in fp32 (exact). bf16 dZ (dX with bf16 tables) needs
+// no scale.
 //
 // Tokens whose target is ignore_index are left out: the index kernel lists the
 // others, and every kernel works on that list with its length read on the
@@ -40,8 +47,10 @@ namespace skm {
 // at the start of the workspace
 struct XentHead {
   int32_t count;    // tokens that have a target
-  float scale;      // 2^e of the backward's operands
-  float inv_scale;  // 2^-e
+  float scale;      // of dLUT's f16 operands, a power of two, and its inverse
+  float inv_scale;
+  float dx_scale;   // of dX's (equal for f16 X: one form serves both)
+  float dx_inv;
 };
 
 // ---- pieces of the launchers, one translation unit each --------------------------
@@ -69,7 +78,9 @@ struct XentGradOut {
   const float* lse;
   const float* dloss;
   int64_t V, ld;
-  void *hi, *lo, *dxv;
+  void *hi, *lo, *dxv;  // see EpGrad
+  const int32_t* zexp;  // exponents e of dZ's f16 rows, by token (NULL = 0)
+  float* rest;          // [listed row] remainder of the target's term in dX's operand
 };
 hipError_t xent_grad(const XentGemm& g, const XentGradOut& o, hipStream_t s);
 

@@ -15,18 +15,27 @@ constexpr int XENT_BN = 256;  // vocabulary rows of a tile
 // One block (the list is one scan over m targets, 8 per thread and round).
 // rows[c] = token of listed row c, in token order. Forward: loss and lse of the
 // others are zeroed. Backward: pos[t] = listed row of token t or -1, and the
-// power of two that puts the largest |dloss| into [2^14, 2^15) (1 when there
-// is none or it is not finite).
+// powers of two that put the largest finite |dloss| 2^e (e from zexp, NULL = 0)
+// and the largest finite |dloss| into [2^14, 2^15) (1 when there is none).
+__device__ __forceinline__ uint32_t larger_finite(uint32_t top, float f) {
+  const uint32_t a = __builtin_bit_cast(uint32_t, f) & 0x7FFFFFFFu;
+  return a < 0x7F800000u && a > top ? a : top;
+}
+__device__ __forceinline__ int scale_exp(uint32_t top) {
+  const int e = top >= 0x00800000u ? 14 + 127 - (int)(top >> 23) : 0;
+  return e > 126 ? 126 : (e < -112 ? -112 : e);
+}
 template <bool BWD>
 __global__ void __launch_bounds__(1024) k_xent_index(const int64_t* __restrict__ targets, int64_t ignore, int64_t m,
-                                                     const float* __restrict__ dloss, XentHead* __restrict__ head,
+                                                     const float* __restrict__ dloss,
+                                                     const int32_t* __restrict__ zexp, XentHead* __restrict__ head,
                                                      int32_t* __restrict__ rows, int32_t* __restrict__ pos,
                                                      float* __restrict__ loss, float* __restrict__ lse) {
   __shared__ int32_t wsum[16];
-  __shared__ uint32_t wmax[16];
+  __shared__ uint32_t wmax[2][16];
   const int t = (int)threadIdx.x, lane = t & 63, wave = t >> 6;
   int32_t base = 0;
-  uint32_t top = 0u;
+  uint32_t top = 0u, top_dx = 0u;
   for (int64_t r0 = 0; r0 < m; r0 += 8192) {
     const int64_t i0 = r0 + 8 * (int64_t)t;
     uint32_t flags = 0u;
@@ -60,8 +69,9 @@ __global__ void __launch_bounds__(1024) k_xent_index(const int64_t* __restrict__
       if constexpr (BWD) {
         pos[i] = on ? c : -1;
         if (on) {
-          const uint32_t a = __builtin_bit_cast(uint32_t, dloss[i]) & 0x7FFFFFFFu;
-          if (a < 0x7F800000u && a > top) top = a;
+          const float f = dloss[i];
+          top_dx = larger_finite(top_dx, f);
+          top = larger_finite(top, zexp ? f * pow2f(zexp[i]) : f);
         }
       } else if (!on) {
         loss[i] = 0.0f;
@@ -74,20 +84,28 @@ __global__ void __launch_bounds__(1024) k_xent_index(const int64_t* __restrict__
   if constexpr (BWD) {
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) {
-      const uint32_t v = (uint32_t)__shfl_xor((int)top, o, 64);
+      const uint32_t v = (uint32_t)__shfl_xor((int)top, o, 64), w = (uint32_t)__shfl_xor((int)top_dx, o, 64);
       top = top > v ? top : v;
+      top_dx = top_dx > w ? top_dx : w;
     }
-    if (lane == 0) wmax[wave] = top;
+    if (lane == 0) {
+      wmax[0][wave] = top;
+      wmax[1][wave] = top_dx;
+    }
     __syncthreads();
   }
   if (t == 0) {
     head->count = base;
     if constexpr (BWD) {
-      for (int w = 0; w < 16; ++w) top = top > wmax[w] ? top : wmax[w];
-      int e = top >= 0x00800000u ? 14 + 127 - (int)(top >> 23) : 0;
-      e = e > 126 ? 126 : (e < -112 ? -112 : e);
+      for (int w = 0; w < 16; ++w) {
+        top = top > wmax[0][w] ? top : wmax[0][w];
+        top_dx = top_dx > wmax[1][w] ? top_dx : wmax[1][w];
+      }
+      const int e = scale_exp(top), e_dx = scale_exp(top_dx);
       head->scale = pow2f(e);
       head->inv_scale = pow2f(-e);
+      head->dx_scale = pow2f(e_dx);
+      head->dx_inv = pow2f(-e_dx);
     }
   }
 }
@@ -263,43 +281,100 @@ __global__ void __launch_bounds__(1024) k_xent_mean(const float* __restrict__ lo
 
 // ---- backward --------------------------------------------------------------------------
 
-// Xc[c] = X[rows[c]] for the listed tokens, zeros up to the next multiple of 32
-// (whole steps of the table gradient's tiles); 16 bytes per thread and round
-__global__ void __launch_bounds__(256) k_xent_gather(const uint16_t* __restrict__ X, const int32_t* __restrict__ rows,
+// Xc[c] = X[rows[c]] in f16 for the listed tokens (bf16 rows prescaled by 2^-e,
+// e = zexp), zeros up to the next multiple of 32 (whole steps of the table
+// gradient's tiles); 16 bytes per thread and round
+template <typename TX>
+__global__ void __launch_bounds__(256) k_xent_gather(const TX* __restrict__ X, const int32_t* __restrict__ rows,
+                                                     const int32_t* __restrict__ zexp,
                                                      const XentHead* __restrict__ head, int64_t d,
-                                                     uint16_t* __restrict__ Xc) {
+                                                     half_t* __restrict__ Xc) {
   const int64_t c = blockIdx.x;
   const int count = head->count;
   if (c >= ((int64_t)count + 31) / 32 * 32) return;
   const bool live = c < count;
-  const u32x4* src = reinterpret_cast<const u32x4*>(X + (live ? (int64_t)rows[c] : 0) * d);
+  const int64_t t = live ? rows[c] : 0;
+  float scale = 1.0f;
+  if constexpr (__is_same(TX, bf16_t)) scale = live ? pow2f(-zexp[t]) : 1.0f;
+  const u32x4* src = reinterpret_cast<const u32x4*>(X + t * d);
   u32x4* dst = reinterpret_cast<u32x4*>(Xc + c * d);
-  for (int64_t j = threadIdx.x; j < d / 8; j += 256) dst[j] = live ? src[j] : u32x4{0u, 0u, 0u, 0u};
+  for (int64_t j = threadIdx.x; j < d / 8; j += 256) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (live) {
+      v = src[j];
+      if constexpr (__is_same(TX, bf16_t)) v = mm::cvt_quad_scaled(v, scale);
+    }
+    dst[j] = v;
+  }
 }
 
-// dX[t] = inv_scale * sum of the ranges' dX of t's listed row; zeros for an
-// ignored token
-template <typename TX>
-__global__ void __launch_bounds__(256) k_xent_dx_out(const float* __restrict__ acc, int splits, int64_t part_stride,
+// dX[t] = (sum of the ranges' dX of t's listed row + what rounding took from the
+// target's term, times the target's weights), scaled back; zeros for an ignored
+// token. f16 operands (TL) carry the scale, bf16 ones none.
+template <int B, typename TX, typename TL>
+__global__ void __launch_bounds__(256) k_xent_dx_out(const float* __restrict__ acc, int ranges, int64_t part_stride,
                                                      const int32_t* __restrict__ pos, const XentHead* __restrict__ head,
-                                                     int64_t d, TX* __restrict__ dX) {
+                                                     const float* __restrict__ rest, const int64_t* __restrict__ targets,
+                                                     const uint8_t* __restrict__ idx_packed,
+                                                     const TL* __restrict__ lut, int64_t V, int64_t d, int gpr,
+                                                     TX* __restrict__ dX) {
+  constexpr int K = 1 << B;
   const int64_t t = blockIdx.x;
   const int64_t c = pos[t];
-  const float inv = head->inv_scale;
+  const int64_t target = targets[t];
+  const bool fix = c >= 0 && target >= 0 && target < V;
+  const float r = fix ? rest[c] : 0.0f;
+  const float back = __is_same(TL, bf16_t) ? 1.0f : head->dx_inv;
+  const uint8_t* row = idx_packed + (fix ? target : 0) * (d * B / 8);
+  const TL* tab = lut + (fix ? target : 0) * gpr * K;
+  const uint32_t G = (uint32_t)(d / gpr);
   for (int64_t j = (int64_t)threadIdx.x * 8; j < d; j += 2048) {
     float v[8] = {};
     if (c >= 0) {
-      for (int k = 0; k < splits; ++k) {
+      for (int k = 0; k < ranges; ++k) {
         float a[8];
         load8<float>(acc + k * part_stride + c * d + j, a);
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[q] += a[q];
       }
+      if (fix) {  // the 8 indices of columns j .. j + 7 are B bytes (one group: its width is a multiple of 32)
+        uint32_t w = 0u;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] *= inv;
+        for (int q = 0; q < B; ++q) w |= (uint32_t)row[j / 8 * B + q] << (8 * q);
+        const TL* g = tab + (int64_t)((uint32_t)j / G) * K;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = __builtin_fmaf(r, to_f32(g[(w >> (B * q)) & (K - 1)]), v[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] *= back;
     }
     store8<TX>(dX + t * d + j, v);
   }
+}
+
+struct DxOut {
+  const float* acc;
+  int ranges;
+  const int32_t* pos;
+  const XentHead* head;
+  const float* rest;
+};
+template <typename TX, typename TL>
+hipError_t dx_out_t(const XentArgs& a, const DxOut& o, void* dX, hipStream_t s) {
+  const Problem& p = a.p;
+  auto go = [&](auto kern) {
+    hipLaunchKernelGGL(kern, dim3((unsigned)p.m), dim3(256), 0, s, o.acc, o.ranges, p.m * p.d, o.pos, o.head, o.rest,
+                       a.targets, a.idx, (const TL*)a.lut, p.n, p.d, p.gpr, (TX*)dX);
+    return hipGetLastError();
+  };
+  if (p.b == 2) return go(k_xent_dx_out<2, TX, TL>);
+  if (p.b == 3) return go(k_xent_dx_out<3, TX, TL>);
+  return go(k_xent_dx_out<4, TX, TL>);
+}
+hipError_t dx_out(const XentArgs& a, const DxOut& o, void* dX, hipStream_t s) {
+  if (a.x_dtype == DT_F16) return dx_out_t<half_t, half_t>(a, o, dX, s);
+  if (a.lut_dtype == DT_F16) return dx_out_t<bf16_t, half_t>(a, o, dX, s);
+  return dx_out_t<bf16_t, bf16_t>(a, o, dX, s);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -343,7 +418,9 @@ struct BwdPlan {
   int64_t P;           // vocabulary rows per piece
   DxRanges ranges;     // of the first piece's rows, each with its own dX
   bool few, streams;
-  size_t rows, pos, rexp, hi, lo, dxv, acc, xc, xp, part, bytes;
+  bool own;            // dX's operand is a form of its own
+  bool exps;           // row exponents of X are needed: logits' or dLUT's f16 operands of bf16 rows
+  size_t rows, pos, rexp, hi, lo, dxv, rest, acc, xc, xp, part, bytes;
 };
 
 // The pieces: dZ of a piece takes 2 bytes per (token, word) and form, and is
@@ -353,8 +430,9 @@ constexpr size_t XENT_PIECE_BYTES = size_t(256) << 20;
 
 BwdPlan bwd_plan(const Problem& p, int x_dtype, int lut_dtype, bool need_dx, bool need_dlut) {
   BwdPlan f;
-  const bool mx = mixed(x_dtype, lut_dtype);
-  const bool has_hi = need_dlut || !mx, has_dxv = need_dx && mx;
+  f.own = x_dtype == DT_BF16;
+  const bool has_hi = need_dlut || !f.own, has_dxv = need_dx && f.own;
+  f.exps = x_dtype == DT_BF16 && (need_dlut || lut_dtype == DT_F16);
   const int forms = (has_hi ? 1 : 0) + (need_dlut ? 1 : 0) + (has_dxv ? 1 : 0);
   f.few = xent_few(p);
   f.streams = !f.few && xent_streams(p);
@@ -375,7 +453,8 @@ BwdPlan bwd_plan(const Problem& p, int x_dtype, int lut_dtype, bool need_dx, boo
   const size_t dz = (size_t)f.cap * (size_t)((n1 + 7) / 8 * 8) * 2;
   f.rows = take(true, (size_t)p.m * 4);
   f.pos = take(true, (size_t)p.m * 4);
-  f.rexp = take(mx, (size_t)p.m * 4);
+  f.rexp = take(f.exps, (size_t)p.m * 4);
+  f.rest = take(need_dx, (size_t)p.m * 4);
   f.hi = take(has_hi, dz);
   f.lo = take(need_dlut, dz);
   f.dxv = take(has_dxv, dz);
@@ -431,8 +510,8 @@ hipError_t launch_xent_fwd(const XentArgs& a, float* loss, float* lse, void* ws,
                        p.n, tlogit, loss, lse);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(k_xent_index<false>, dim3(1), dim3(1024), 0, s, a.targets, a.ignore, p.m, nullptr, head, rows,
-                     nullptr, loss, lse);
+  hipLaunchKernelGGL(k_xent_index<false>, dim3(1), dim3(1024), 0, s, a.targets, a.ignore, p.m, nullptr, nullptr, head,
+                     rows, nullptr, loss, lse);
   e = hipGetLastError();
   if (e == hipSuccess && f.streams) e = xent_rows(g, xp, rexp, s);
   else if (e == hipSuccess && rexp) e = launch_row_exp(a.X, p.m, p.d, rexp, s);
@@ -458,26 +537,34 @@ hipError_t launch_xent_bwd(const XentArgs& a, const float* lse, const float* dlo
                            int accumulate, void* ws, hipStream_t s) {
   const Problem& p = a.p;
   const BwdPlan f = bwd_plan(p, a.x_dtype, a.lut_dtype, dX != nullptr, dLUT != nullptr);
-  const bool mx = mixed(a.x_dtype, a.lut_dtype);
   XentHead* head = at<XentHead>(ws, 0);
   int32_t* rows = at<int32_t>(ws, f.rows);
   int32_t* pos = at<int32_t>(ws, f.pos);
-  int32_t* rexp = mx ? at<int32_t>(ws, f.rexp) : nullptr;
+  int32_t* rexp = f.exps ? at<int32_t>(ws, f.rexp) : nullptr;
   float* acc = dX ? at<float>(ws, f.acc) : nullptr;
-  void* hi = dLUT || !mx ? at<void>(ws, f.hi) : nullptr;
+  float* rest = dX ? at<float>(ws, f.rest) : nullptr;
+  void* hi = dLUT || !f.own ? at<void>(ws, f.hi) : nullptr;
   void* lo = dLUT ? at<void>(ws, f.lo) : nullptr;
-  void* dxv = dX && mx ? at<void>(ws, f.dxv) : nullptr;
+  void* dxv = dX && f.own ? at<void>(ws, f.dxv) : nullptr;
   void* xc = dLUT ? at<void>(ws, f.xc) : nullptr;
-  hipLaunchKernelGGL(k_xent_index<true>, dim3(1), dim3(1024), 0, s, a.targets, a.ignore, p.m, dloss, head, rows, pos,
-                     nullptr, nullptr);
-  hipError_t e = hipGetLastError();
   void* xp = f.streams ? at<void>(ws, f.xp) : nullptr;
+  // dLUT's operands: bf16 rows of X are scaled by 2^-e, their rows of dZ by 2^e
+  const int32_t* zexp = dLUT ? rexp : nullptr;
+  hipError_t e = hipSuccess;
+  if (rexp) e = launch_row_exp(a.X, p.m, p.d, rexp, s);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_xent_index<true>, dim3(1), dim3(1024), 0, s, a.targets, a.ignore, p.m, dloss, zexp, head, rows,
+                     pos, nullptr, nullptr);
+  e = hipGetLastError();
   XentGemm g{a.X, a.x_dtype, a.idx, a.lut, a.lut_dtype, p, rows, head, a.targets, rexp, 0, xp};
   if (e == hipSuccess && f.streams) e = xent_rows(g, xp, rexp, s);
-  else if (e == hipSuccess && rexp) e = launch_row_exp(a.X, p.m, p.d, rexp, s);
   if (e == hipSuccess && dLUT) {
-    hipLaunchKernelGGL(k_xent_gather, dim3((unsigned)f.cap), dim3(256), 0, s, (const uint16_t*)a.X, rows, head, p.d,
-                       (uint16_t*)xc);
+    if (a.x_dtype == DT_F16)
+      hipLaunchKernelGGL(k_xent_gather<half_t>, dim3((unsigned)f.cap), dim3(256), 0, s, (const half_t*)a.X, rows, zexp,
+                         head, p.d, (half_t*)xc);
+    else
+      hipLaunchKernelGGL(k_xent_gather<bf16_t>, dim3((unsigned)f.cap), dim3(256), 0, s, (const bf16_t*)a.X, rows, zexp,
+                         head, p.d, (half_t*)xc);
     e = hipGetLastError();
   }
   const int es = 2;  // bytes of a table entry (16-bit pairs only)
@@ -491,30 +578,23 @@ hipError_t launch_xent_bwd(const XentArgs& a, const float* lse, const float* dlo
     g.lut = lut;
     g.p = q;
     g.v0 = v0;
-    const XentGradOut out{lse, dloss, p.n, ld, hi, lo, dxv};
+    const XentGradOut out{lse, dloss, p.n, ld, hi, lo, dxv, zexp, rest};
     e = f.few ? xent_few_grad(g, out, pos, s) : xent_grad(g, out, s);
     if (e == hipSuccess && dX) {
       // every range of the first piece is written; later pieces add to some or all
       const int64_t steps = (n + 63) / 64;
       const int64_t sr = (steps + f.ranges.count - 1) / f.ranges.count * 64;
-      e = launch_dx_piece(mx ? dxv : hi, a.lut_dtype, idx, lut, a.lut_dtype, q, acc, nullptr, &head->count, ld, v0 > 0,
+      e = launch_dx_piece(f.own ? dxv : hi, a.lut_dtype, idx, lut, a.lut_dtype, q, acc, nullptr, &head->count, ld, v0 > 0,
                           {(int)((n + sr - 1) / sr), sr}, s);
     }
     if (e == hipSuccess && dLUT) {
       const Problem qc{f.cap, n, p.d, p.b, p.gpr};
-      e = launch_dlut_piece(hi, lo, xc, a.x_dtype, idx, qc, dLUT + v0 * p.gpr * p.k(), accumulate,
+      e = launch_dlut_piece(hi, lo, xc, DT_F16, idx, qc, dLUT + v0 * p.gpr * p.k(), accumulate,
                             at<float>(ws, f.part), {&head->count, ld, &head->inv_scale, nullptr}, s);
     }
   }
   if (e != hipSuccess || !dX) return e;
-  const dim3 grid((unsigned)p.m);
-  if (a.x_dtype == DT_F16)
-    hipLaunchKernelGGL(k_xent_dx_out<half_t>, grid, dim3(256), 0, s, acc, f.ranges.count, p.m * p.d, pos, head, p.d,
-                       (half_t*)dX);
-  else
-    hipLaunchKernelGGL(k_xent_dx_out<bf16_t>, grid, dim3(256), 0, s, acc, f.ranges.count, p.m * p.d, pos, head, p.d,
-                       (bf16_t*)dX);
-  return hipGetLastError();
+  return dx_out(a, {acc, f.ranges.count, pos, head, rest}, dX, s);
 }
 
 }  // namespace skm

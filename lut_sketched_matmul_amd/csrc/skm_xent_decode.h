@@ -39,40 +39,48 @@ template <typename TX> struct EpDecodeStats {
 // dZ of the listed tokens among t0 .. t0 + m - 1, in the forms of EpGrad;
 // the first launch also writes the zero rows that pad the list
 template <typename TX, typename TL> struct EpDecodeGrad {
+  static constexpr bool OWN = __is_same(TX, bf16_t);
   struct Args {
     const int32_t* pos;  // listed row of every token, -1 = ignored
     const XentHead* head;
     const int64_t* targets;
     const float* lse;
     const float* dloss;
+    const int32_t* zexp;
     int64_t V, v0, ld, t0;
-    TX* hi;
-    TX* lo;
+    half_t* hi;
+    half_t* lo;
     TL* dxv;
+    float* rest;
   };
-  static __device__ __forceinline__ void store(const Args& ep, int64_t at, float g) {
+  // dZ as dLUT's forms and dX's hold it
+  static __device__ __forceinline__ void store(const Args& ep, int64_t at, float up, float dx) {
     if (ep.hi) {
-      const TX h = from_f32<TX>(g);
+      const half_t h = from_f32<half_t>(up);
       ep.hi[at] = h;
-      if (ep.lo) ep.lo[at] = from_f32<TX>(g - to_f32(h));
+      if (ep.lo) ep.lo[at] = from_f32<half_t>(up - to_f32(h));
     }
-    if (ep.dxv) ep.dxv[at] = from_f32<TL>(g);
+    if (OWN && ep.dxv) ep.dxv[at] = from_f32<TL>(dx);
   }
   static __device__ __forceinline__ void put(const Args& ep, bool ok, int token, int64_t row, float v, int m,
                                              int64_t n) {
     if (row >= ep.ld) return;
     if (ep.t0 == 0) {
       const int64_t count = ep.head->count, pad = (count + 31) / 32 * 32;
-      for (int64_t c = count + token; c < pad; c += 16) store(ep, c * ep.ld + row, 0.0f);
+      for (int64_t c = count + token; c < pad; c += 16) store(ep, c * ep.ld + row, 0.0f, 0.0f);
     }
     if (token >= m) return;
     const int64_t t = ep.t0 + token;
     const int64_t c = ep.pos[t];
     if (c < 0) return;
     const int64_t target = ep.targets[t];
-    const float gs = target >= 0 && target < ep.V ? ep.dloss[t] * ep.head->scale : __builtin_nanf("");
-    const float p = __expf(v - ep.lse[t]) - (ep.v0 + row == target ? 1.0f : 0.0f);
-    store(ep, c * ep.ld + row, ok ? p * gs : 0.0f);
+    const float dl = target >= 0 && target < ep.V ? ep.dloss[t] : __builtin_nanf("");
+    const float up = ep.zexp ? dl * pow2f(ep.zexp[t]) * ep.head->scale : dl * ep.head->scale;
+    const float dx = OWN ? (__is_same(TL, bf16_t) ? dl : dl * ep.head->dx_scale) : up;
+    const bool mine = ok && ep.v0 + row == target;
+    const float p = __expf(v - ep.lse[t]) - (mine ? 1.0f : 0.0f);
+    store(ep, c * ep.ld + row, ok ? p * up : 0.0f, ok ? p * dx : 0.0f);
+    if (mine && ep.rest) ep.rest[c] = p * dx - to_f32(from_f32<TL>(p * dx));
   }
 };
 

@@ -9,8 +9,8 @@ namespace {
 template <typename TX, typename TL>
 hipError_t few_t(const XentGemm& g, const XentGradOut& o, const int32_t* pos, hipStream_t s) {
   typedef EpDecodeGrad<TX, TL> EP;
-  const typename EP::Args a{pos, g.head, g.targets, o.lse, o.dloss, o.V, g.v0, o.ld, 0, (TX*)o.hi, (TX*)o.lo,
-                            (TL*)o.dxv};
+  const typename EP::Args a{pos,        g.head, g.targets, o.lse, o.dloss,      o.zexp,        o.V, g.v0,
+                            o.ld,       0,      (half_t*)o.hi,   (half_t*)o.lo, (TL*)o.dxv, o.rest};
   if (g.p.b == 2) return xent_decode_all<2, TX, TL, EP>(g, a, s);
   if (g.p.b == 3) return xent_decode_all<3, TX, TL, EP>(g, a, s);
   return xent_decode_all<4, TX, TL, EP>(g, a, s);

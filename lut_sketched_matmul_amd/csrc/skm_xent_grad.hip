@@ -16,12 +16,14 @@ hipError_t grad_b(const XentGemm& g, const XentGradOut& o, hipStream_t s) {
   a.v0 = g.v0;
   a.lse = o.lse;
   a.dloss = o.dloss;
-  a.scale = &g.head->scale;
+  a.head = g.head;
+  a.zexp = o.zexp;
   a.V = o.V;
   a.ld = o.ld;
-  a.hi = (TX*)o.hi;
-  a.lo = (TX*)o.lo;
+  a.hi = (half_t*)o.hi;
+  a.lo = (half_t*)o.lo;
   a.dxv = (TL*)o.dxv;
+  a.rest = o.rest;
   if constexpr (B == 4)
     if (xent_streams(g.p)) return xent_logits_launch<TL, EP, !__is_same(TX, TL)>(g, a, s);
   return gemm_fwd_b<B, TX, TL, EP>((const TX*)g.X, g.idx, (const TL*)g.lut, g.p, a, g.rexp, s);

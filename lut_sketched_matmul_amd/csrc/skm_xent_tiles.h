@@ -107,20 +107,25 @@ __device__ __forceinline__ u32x4 pair_up(uint32_t a0, uint32_t a1, uint32_t b0, 
   return u32x4{s0[0], s1[0], s0[1], s1[1]};
 }
 
-// EpGrad: dZ of the block, [listed token][ld] in up to three forms (NULL =
-// not wanted): hi + lo in TX for dLUT (hi also for dX when the tables have
-// that dtype) and dxv in TL for dX. Columns n .. ld - 1 and listed rows past
-// the count up to the next multiple of 32 are written as zeros.
+// EpGrad: dZ of the block, [listed token][ld] in up to three forms (NULL = not
+// wanted): hi + lo in f16 for dLUT, scaled by head->scale 2^e of the token, and
+// dxv in the tables' dtype for dX, f16 scaled by head->dx_scale (f16 X: e = 0
+// and hi serves both). Columns n .. ld - 1 and listed rows past the count up to the next
+// multiple of 32 are written as zeros. rest[c]: what rounding took from the
+// target's term in dX's operand.
 template <typename TX, typename TL> struct EpGrad {
+  static constexpr bool OWN = __is_same(TX, bf16_t);  // dX's operand is dxv, not hi
   static constexpr bool SWAP = true, ROWS = true;
   struct Args : XentRows {
     const float* lse;    // [m]
     const float* dloss;  // [m]
-    const float* scale;
+    const XentHead* head;
+    const int32_t* zexp;
     int64_t V, ld;
-    TX* hi;
-    TX* lo;
+    half_t* hi;
+    half_t* lo;
     TL* dxv;
+    float* rest;
   };
   template <bool SC>
   static __device__ __forceinline__ void run(const f32x16 (&acc)[4][2], const Args& ep,
@@ -131,7 +136,7 @@ template <typename TX, typename TL> struct EpGrad {
     const int cols = (int)(n - c0 < 64 ? n - c0 : 64) - 4 * (lane >> 5);
     const int stored = (int)(ep.ld - c0 < 64 ? ep.ld - c0 : 64);
     const bool ragged = n - c0 < 64 || m0 + G_BM > m;  // wave-uniform
-    const float scale = *ep.scale;
+    const float scale = ep.head->scale, dx_scale = __is_same(TL, bf16_t) ? 1.0f : ep.head->dx_scale;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t tok = m0 + 128 * wm + 32 * i + (lane & 31);
@@ -143,10 +148,12 @@ template <typename TX, typename TL> struct EpGrad {
       const int tgt = target_in_wave(target, ep.v0 + c0, lane);
       const float lse = ep.lse[src];
       // a target outside the vocabulary gives NaN gradients (its loss is NaN)
-      const float gs = target >= 0 && target < ep.V ? ep.dloss[src] * scale : __builtin_nanf("");
-      // g[e] = dZ of output e. (The target's 1 and the masks only where the wave
-      // has one: few waves hold a target of one of their tokens, one column and
-      // one token block are ragged.)
+      const float dl = target >= 0 && target < ep.V ? ep.dloss[src] : __builtin_nanf("");
+      const float up = ep.zexp ? dl * pow2f(ep.zexp[src]) * scale : dl * scale;
+      const float dx = OWN ? dl * dx_scale : up;
+      // g[e] = dZ of output e over its row's factor. (The target's 1 and the
+      // masks only where the wave has one: few waves hold a target of one of
+      // their tokens, one column and one token block are ragged.)
       float g[32];
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
@@ -154,14 +161,21 @@ template <typename TX, typename TL> struct EpGrad {
         g[e] = __expf(z - lse);
       }
       if (__ballot(tgt >= 0) != 0) {
+        float gt = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) g[e] -= col_of_output(e) == tgt ? 1.0f : 0.0f;
+        for (int e = 0; e < 32; ++e)
+          if (col_of_output(e) == tgt) {
+            g[e] -= 1.0f;
+            gt = g[e];
+          }
+        if (ep.rest && tgt >= 0 && (tgt & 4) == 0 && live) {
+          const float f = gt * dx;
+          ep.rest[tok] = f - to_f32(from_f32<TL>(f));
+        }
       }
-#pragma unroll
-      for (int e = 0; e < 32; ++e) g[e] *= gs;
       if (ragged) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) g[e] = live && col_of_output(e) < cols ? g[e] : 0.0f;
+        for (int e = 0; e < 32; ++e) g[e] = col_of_output(e) < cols ? g[e] : 0.0f;
       }
       // A lane and its partner 32 lanes away hold columns 8 q .. + 3 and + 4 .. 7
       // of their token: after an exchange the lower one has all eight of an even
@@ -173,26 +187,33 @@ template <typename TX, typename TL> struct EpGrad {
         const bool on = 32 * (q >> 2) + 8 * (q & 3) + 8 * (lane >> 5) < stored;
         const int64_t o = at + 32 * (q >> 2) + 8 * (q & 3);
         const float* v = g + 4 * q;  // 8 values: columns of q, then of q + 1
-        uint32_t h[4];
         if (ep.hi) {
+          uint32_t h[4];
+          float s[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) h[k] = mm::pack_tc<TX>(v[2 * k], v[2 * k + 1]);
+          for (int k = 0; k < 8; ++k) s[k] = live ? v[k] * up : 0.0f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) h[k] = mm::pack_tc<half_t>(s[2 * k], s[2 * k + 1]);
           if (ep.lo) {
-            float r[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              r[k] = v[k] - to_f32(__builtin_bit_cast(TX, (uint16_t)(h[k >> 1] >> (16 * (k & 1)))));
-            const u32x4 w = pair_up(mm::pack_tc<TX>(r[0], r[1]), mm::pack_tc<TX>(r[2], r[3]),
-                                    mm::pack_tc<TX>(r[4], r[5]), mm::pack_tc<TX>(r[6], r[7]));
+              s[k] -= to_f32(__builtin_bit_cast(half_t, (uint16_t)(h[k >> 1] >> (16 * (k & 1)))));
+            const u32x4 w = pair_up(mm::pack_tc<half_t>(s[0], s[1]), mm::pack_tc<half_t>(s[2], s[3]),
+                                    mm::pack_tc<half_t>(s[4], s[5]), mm::pack_tc<half_t>(s[6], s[7]));
             if (on) *reinterpret_cast<u32x4*>(ep.lo + o) = w;
           }
           const u32x4 w = pair_up(h[0], h[1], h[2], h[3]);
           if (on) *reinterpret_cast<u32x4*>(ep.hi + o) = w;
         }
-        if (ep.dxv) {
-          const u32x4 w = pair_up(mm::pack_tc<TL>(v[0], v[1]), mm::pack_tc<TL>(v[2], v[3]),
-                                  mm::pack_tc<TL>(v[4], v[5]), mm::pack_tc<TL>(v[6], v[7]));
-          if (on) *reinterpret_cast<u32x4*>(ep.dxv + o) = w;
+        if constexpr (OWN) {
+          if (ep.dxv) {
+            float s[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s[k] = live ? v[k] * dx : 0.0f;
+            const u32x4 w = pair_up(mm::pack_tc<TL>(s[0], s[1]), mm::pack_tc<TL>(s[2], s[3]),
+                                    mm::pack_tc<TL>(s[4], s[5]), mm::pack_tc<TL>(s[6], s[7]));
+            if (on) *reinterpret_cast<u32x4*>(ep.dxv + o) = w;
+          }
         }
       }
     }

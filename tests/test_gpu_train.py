@@ -476,6 +476,38 @@ def test_xent_other_ignore_index_and_accumulate():
     within(to_f64(acc), to_f64(ga[1]) + 2.0, 4 * U * (2.0 + np.abs(to_f64(ga[1]))), "accumulate")
 
 
+@pytest.mark.parametrize("V", [40, 20000])
+def test_xent_table_gradient_keeps_fp32_of_bf16(V):
+    """dLUT takes bf16 activations' dZ as precisely as f16's.
+
+    Activations of +-1 are exact in both types and scaling them by a power of two changes no logit, so both calls start
+    from the same dZ, and an entry is dZ times a whole number: each side is off by 2^-23 (two f16 values) and by the
+    rounding of three fp32 operations at the most. (f16's floor: 2^-39 of the gradient, 1.)
+    """
+    t = torch()
+    d = 256
+    gi, gl, idx, _ = head(f"xentq/{V}", V, d, 4, 1, "f16")
+    X = t.sign(t.randn((1, d), device="cuda") + 0.1)
+    T = t.full((1,), V - 3, device="cuda", dtype=t.int64)
+    DL = t.ones(1, device="cuda")
+    _, lse = skm().sketch_xent_fwd(X.half(), gi, gl, T, 4, 1)
+    a = skm().sketch_xent_bwd(X.half(), gi, gl, T, lse, DL, 4, 1, need_dx=False)[1]
+    b = skm().sketch_xent_bwd(X.bfloat16(), gi, gl, T, lse, DL, 4, 1, need_dx=False)[1]
+    ref = to_f64(a)
+    within(to_f64(b), ref, 2 * (2.0 ** -23 + 3 * U) * np.abs(ref) + 2 * d * 2.0 ** -39, "dLUT")
+
+
+@pytest.mark.parametrize("io,ldt", [("f16", "f16"), ("bf16", "f16"), ("bf16", "bf16")])
+def test_xent_zero_rows_have_gradients(io, ldt):
+    """A row of zeros (or nearly) gives the tables nothing but takes the gradient sum_v (1/V - [target]) W itself."""
+    m, d = 40, 256
+    x = syn.to_float64(syn.random_normal("xentz", (m, d), 1.0, "f32"), "f32")
+    x[::3] = 0.0
+    x[1::6] *= 2.0 ** -60 if io == "bf16" else 2.0 ** -12
+    dX = check_xent(f"xentz/{io}/{ldt}", m, 500, d, 4, 1, io, ldt, ignored="none", x=x)[2]
+    assert (to_f64(dX)[::3] != 0).any(1).all()
+
+
 def test_xent_empty_batch():
     t = torch()
     gi, gl, _, _ = head("xente", 64, 64, 4, 1, "f16")

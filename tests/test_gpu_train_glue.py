@@ -126,7 +126,7 @@ def test_head_is_its_calls(io, ldt):
     loss = head(X, T)
     tok, lse = k.sketch_xent_fwd(X.detach(), gi, head.lut, T, b, gpr)
     count = int((T != -100).sum())
-    assert loss.dim() == 0 and abs(float(loss) - float(tok.double().sum()) / count) <= 64 * 2.0 ** -24 * float(loss)
+    assert loss.dim() == 0 and abs(float(loss.detach()) - float(tok.double().sum()) / count) <= 64 * 2.0 ** -24 * float(loss.detach())
     assert t.equal(head.token_losses(X, T), tok)
     (3.0 * loss).backward()
     weight = t.where(T != -100, t.tensor(1.0, device="cuda") / count, t.tensor(0.0, device="cuda"))
