@@ -359,8 +359,12 @@ __device__ __forceinline__ u32x4 lds_q16(uint32_t a) {
 // What the block does with an output is its epilogue EP: 256 threads hold the
 // sums, thread t that of token t / 16 and weight row t % 16 of the block, and
 // call EP::put (whole waves, so lanes may exchange values; `ok` is false for
-// tokens and rows that do not exist). EpDecodeStore is the plain matmul.
+// tokens and rows that do not exist). EpDecodeStore is the plain matmul. With
+// EP::GROUPS any number of tokens runs in one launch, 16 per block (ep.t0 = the
+// block's first): the groups of a row block are consecutive blocks of one XCD
+// (ids go round the 8 XCDs), so its L2 holds the indices for all but the first.
 template <typename TX> struct EpDecodeStore {
+  static constexpr bool GROUPS = false;
   struct Args {
     TX* Y;
   };
@@ -393,7 +397,16 @@ k_decode(const TX* __restrict__ X, const uint8_t* __restrict__ idx_packed, const
   // wave index as a scalar, so that the slot loop's branches are scalar
   // branches and every path through it is a real path
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t row0 = (int64_t)blockIdx.x * DEC_ROWS;
+  int64_t row0 = (int64_t)blockIdx.x * DEC_ROWS;
+  if constexpr (EP::GROUPS) {
+    const uint32_t groups = (uint32_t)((m + 15) / 16), i = blockIdx.x >> 3;
+    row0 = (int64_t)(i / groups * 8 + (blockIdx.x & 7)) * DEC_ROWS;
+    if (row0 >= n) return;  // (the row blocks are rounded up to 8)
+    ep.t0 = 16 * (int64_t)(i % groups);
+    X += ep.t0 * d;
+    if (rexp) rexp += ep.t0;
+    m = m - (int)ep.t0 < 16 ? m - (int)ep.t0 : 16;
+  }
   const int j = lane & 15;           // weight row within the block (B operand column)
   const int q = lane >> 4;           // contraction quarter
   const int64_t grow = row0 + j;
@@ -860,8 +873,10 @@ hipError_t decode_launch(const TX* X, const uint8_t* idx, const TL* lut, const P
   constexpr bool SC = scaled_pair(__is_same(TX, bf16_t), __is_same(TL, half_t));
   // MULTI + XL stages one pass's tokens: at most min(m, DEC_XL_MAX / d) of them
   const int64_t xl_m = sa.lut_set && !sa.select && p.m > DEC_XL_MAX / p.d ? DEC_XL_MAX / p.d : p.m;
-  const size_t lds = decode_lds_bytes<B, NW>(p.gpr, XL ? xl_m * p.d : 0, SC && XL, XT);
-  const dim3 grid((unsigned)((p.n + DEC_ROWS - 1) / DEC_ROWS));
+  const int64_t block_m = EP::GROUPS && xl_m > 16 ? 16 : xl_m;
+  const size_t lds = decode_lds_bytes<B, NW>(p.gpr, XL ? block_m * p.d : 0, SC && XL, XT);
+  const int64_t row_blocks = (p.n + DEC_ROWS - 1) / DEC_ROWS;
+  const dim3 grid((unsigned)(EP::GROUPS ? (row_blocks + 7) / 8 * 8 * ((p.m + 15) / 16) : row_blocks));
   // element e of the staged activations lies in row e / d = umulhi(e, ceil(2^32 / d)), exact for e * d < 2^32
   // (staged elements number at most 49152 and d <= 49152 when staging)
   const uint32_t d_magic = p.d <= DEC_XL_MAX1 ? (uint32_t)(((uint64_t)1 << 32) / (uint64_t)p.d) + 1u : 0u;

@@ -84,10 +84,10 @@ struct XentGradOut {
 };
 hipError_t xent_grad(const XentGemm& g, const XentGradOut& o, hipStream_t s);
 
-// Few tokens (skm_xent_decode.h): 16 per launch of the decode kernel, rows of
+// Few tokens (skm_xent_decode.h): 16 per block of the decode kernel, rows of
 // X in token order (not listed). part: [token][16-row block]
 bool xent_few(const Problem& p);
-bool xent_decode_stages(const Problem& p);  // p.m <= 16: activations in LDS, no row exponents needed
+bool xent_decode_stages(const Problem& p);  // activations in LDS, no row exponents needed
 hipError_t xent_few_stats(const XentGemm& g, float2* part, int64_t blocks, float* tlogit, hipStream_t s);
 hipError_t xent_few_grad(const XentGemm& g, const XentGradOut& o, const int32_t* pos, hipStream_t s);
 

@@ -310,46 +310,69 @@ __global__ void __launch_bounds__(256) k_xent_gather(const TX* __restrict__ X, c
 
 // dX[t] = (sum of the ranges' dX of t's listed row + what rounding took from the
 // target's term, times the target's weights), scaled back; zeros for an ignored
-// token. f16 operands (TL) carry the scale, bf16 ones none.
+// token. f16 operands (TL) carry the scale, bf16 ones none. A block sums 2048 /
+// lanes columns, 8 per thread, `lanes` threads taking every lanes-th range each:
+// a few rows have up to 256 ranges, which one thread would wait for one by one.
 template <int B, typename TX, typename TL>
 __global__ void __launch_bounds__(256) k_xent_dx_out(const float* __restrict__ acc, int ranges, int64_t part_stride,
-                                                     const int32_t* __restrict__ pos, const XentHead* __restrict__ head,
+                                                     int lanes, const int32_t* __restrict__ pos,
+                                                     const XentHead* __restrict__ head,
                                                      const float* __restrict__ rest, const int64_t* __restrict__ targets,
                                                      const uint8_t* __restrict__ idx_packed,
                                                      const TL* __restrict__ lut, int64_t V, int64_t d, int gpr,
                                                      TX* __restrict__ dX) {
   constexpr int K = 1 << B;
+  __shared__ float part[8][256];  // [column of a thread's eight][thread]
   const int64_t t = blockIdx.x;
   const int64_t c = pos[t];
-  const int64_t target = targets[t];
-  const bool fix = c >= 0 && target >= 0 && target < V;
-  const float r = fix ? rest[c] : 0.0f;
-  const float back = __is_same(TL, bf16_t) ? 1.0f : head->dx_inv;
-  const uint8_t* row = idx_packed + (fix ? target : 0) * (d * B / 8);
-  const TL* tab = lut + (fix ? target : 0) * gpr * K;
-  const uint32_t G = (uint32_t)(d / gpr);
-  for (int64_t j = (int64_t)threadIdx.x * 8; j < d; j += 2048) {
-    float v[8] = {};
-    if (c >= 0) {
-      for (int k = 0; k < ranges; ++k) {
-        float a[8];
-        load8<float>(acc + k * part_stride + c * d + j, a);
+  const int chunks = 256 / lanes, lane = (int)threadIdx.x / chunks;
+  const int64_t j = 8 * ((int64_t)blockIdx.y * chunks + (int)threadIdx.x % chunks);
+  float v[8] = {};
+  if (c >= 0 && j < d) {
+    const float* src = acc + c * d + j;
+    int k = lane;
+    for (; k + 3 * lanes < ranges; k += 4 * lanes) {
+      float a[4][8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] += a[q];
-      }
-      if (fix) {  // the 8 indices of columns j .. j + 7 are B bytes (one group: its width is a multiple of 32)
-        uint32_t w = 0u;
+      for (int u = 0; u < 4; ++u) load8<float>(src + (k + u * lanes) * part_stride, a[u]);
 #pragma unroll
-        for (int q = 0; q < B; ++q) w |= (uint32_t)row[j / 8 * B + q] << (8 * q);
-        const TL* g = tab + (int64_t)((uint32_t)j / G) * K;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = __builtin_fmaf(r, to_f32(g[(w >> (B * q)) & (K - 1)]), v[q]);
-      }
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] *= back;
+      for (int q = 0; q < 8; ++q) v[q] += (a[0][q] + a[1][q]) + (a[2][q] + a[3][q]);
     }
-    store8<TX>(dX + t * d + j, v);
+    for (; k < ranges; k += lanes) {
+      float a[8];
+      load8<float>(src + k * part_stride, a);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] += a[q];
+    }
   }
+  if (lanes > 1) {  // block-uniform
+#pragma unroll
+    for (int q = 0; q < 8; ++q) part[q][threadIdx.x] = v[q];
+    __syncthreads();
+    if (lane > 0) return;
+    for (int k = 1; k < lanes; ++k)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] += part[q][k * chunks + threadIdx.x];
+  }
+  if (j >= d) return;
+  const int64_t target = targets[t];
+  if (c >= 0 && target >= 0 && target < V) {
+    // the 8 indices of columns j .. j + 7 are B bytes (one group: its width is a multiple of 32)
+    const uint8_t* row = idx_packed + target * (d * B / 8) + j / 8 * B;
+    const TL* g = lut + (target * gpr + (uint32_t)j / (uint32_t)(d / gpr)) * K;
+    const float r = rest[c];
+    uint32_t w = 0u;
+#pragma unroll
+    for (int q = 0; q < B; ++q) w |= (uint32_t)row[q] << (8 * q);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = __builtin_fmaf(r, to_f32(g[(w >> (B * q)) & (K - 1)]), v[q]);
+  }
+  if constexpr (!__is_same(TL, bf16_t)) {
+    const float back = head->dx_inv;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] *= back;
+  }
+  store8<TX>(dX + t * d + j, v);
 }
 
 struct DxOut {
@@ -362,9 +385,13 @@ struct DxOut {
 template <typename TX, typename TL>
 hipError_t dx_out_t(const XentArgs& a, const DxOut& o, void* dX, hipStream_t s) {
   const Problem& p = a.p;
+  // two or more ranges per lane, and at most 2048 blocks' worth of threads
+  int lanes = 1;
+  while (lanes < 32 && lanes * 2 <= o.ranges && p.m * p.d * lanes < 2048 * 2048) lanes *= 2;
+  const int64_t cols = 2048 / lanes;
   auto go = [&](auto kern) {
-    hipLaunchKernelGGL(kern, dim3((unsigned)p.m), dim3(256), 0, s, o.acc, o.ranges, p.m * p.d, o.pos, o.head, o.rest,
-                       a.targets, a.idx, (const TL*)a.lut, p.n, p.d, p.gpr, (TX*)dX);
+    hipLaunchKernelGGL(kern, dim3((unsigned)p.m, (unsigned)((p.d + cols - 1) / cols)), dim3(256), 0, s, o.acc,
+                       o.ranges, p.m * p.d, lanes, o.pos, o.head, o.rest, a.targets, a.idx, (const TL*)a.lut, p.n, p.d, p.gpr, (TX*)dX);
     return hipGetLastError();
   };
   if (p.b == 2) return go(k_xent_dx_out<2, TX, TL>);
@@ -378,11 +405,6 @@ hipError_t dx_out(const XentArgs& a, const DxOut& o, void* dX, hipStream_t s) {
 }
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-
-// whether every launch of few tokens stages its activations (the largest does)
-bool few_stages(const Problem& p) {
-  return xent_decode_stages(Problem{p.m < 16 ? p.m : 16, p.n, p.d, p.b, p.gpr});
-}
 
 bool mixed(int x_dtype, int lut_dtype) { return scaled_pair(x_dtype == DT_BF16, lut_dtype == DT_F16); }
 
@@ -477,17 +499,26 @@ template <typename T> T* at(void* ws, size_t off) { return reinterpret_cast<T*>(
 
 }  // namespace
 
-// Tokens for which the decode kernel, 16 per launch, beats the 256-token tiles:
-// each launch streams the indices once more, the tiles take one round of 256
-// blocks whatever the token count. Statistics of 4096 columns, b = 4: 32000
-// words 38 / 70 / 104 us for 16 / 32 / 48 tokens against 101 us, 128256 words
-// 142 / 272 / 400 us against 264 us; with few tiles (4000 words of 1024 columns,
-// b = 2) 18 / 21 / 24 / 27 us up to 64 tokens against 38 us.
+// Whether the decode kernel, 16 tokens per block, beats the 256 x 256 tiles: it
+// dequantises for every 16 tokens, about 0.4 + 0.00014 d ns per word and group of
+// them with the chip full; the tiles take about 10 + 0.021 d us per round of 256
+// blocks however few of a block's tokens exist. Both sides measured for b = 2, 3
+// and 4 and 1 to 8 groups (statistics, us, decode against tiles): 32000 words of
+// 4096 columns, 16 / 32 / 64 tokens 36 / 64 / 117 against 105; 16000 of 2048, 32
+// / 64 / 160 tokens 31 / 54 / 121 against 59; 4000 of 4096, 64 / 160 / 300 / 500
+// tokens 23 / 45 / 77 / 124 against 100; 2048 of 1024, 160 / 500 tokens 19 / 46
+// against 38.
 bool xent_few(const Problem& p) {
-  return p.m <= (p.n <= 16384 ? 64 : 32) && decode_supported(Problem{p.m < 16 ? p.m : 16, p.n, p.d, p.b, p.gpr});
+  const int64_t groups = (p.m + 15) / 16, tiles = (p.m + 255) / 256 * ((p.n + XENT_BN - 1) / XENT_BN);
+  const double decode = (double)(groups * p.n) * (0.4e-3 + 0.14e-6 * (double)p.d);
+  return decode <= (double)((tiles + 255) / 256) * (10.0 + 0.021 * (double)p.d) &&
+         decode_supported(Problem{p.m < 16 ? p.m : 16, p.n, p.d, p.b, p.gpr});
 }
 
-bool xent_decode_stages(const Problem& p) { return p.m * p.d <= 32768; }
+// 32 KB of a block's LDS: two blocks or more share a CU then (8 tokens of 4096
+// columns, 32000 words: 53 us staged, 36 us from memory; 64 of 2048, 16000
+// words: 85 against 54)
+bool xent_decode_stages(const Problem& p) { return (p.m < 16 ? p.m : 16) * p.d <= 16384; }
 
 size_t xent_fwd_bytes(const Problem& p, int x_dtype, int lut_dtype) { return fwd_plan(p, x_dtype, lut_dtype).bytes; }
 
@@ -503,7 +534,7 @@ hipError_t launch_xent_fwd(const XentArgs& a, float* loss, float* lse, void* ws,
   const XentGemm g{a.X, a.x_dtype, a.idx, a.lut, a.lut_dtype, p, rows, head, a.targets, rexp, 0, xp};
   hipError_t e = hipSuccess;
   if (f.few) {
-    if (rexp && !few_stages(p)) e = launch_row_exp(a.X, p.m, p.d, rexp, s);
+    if (rexp && !xent_decode_stages(p)) e = launch_row_exp(a.X, p.m, p.d, rexp, s);
     if (e == hipSuccess) e = xent_few_stats(g, part, f.blocks, tlogit, s);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(k_xent_merge_few, dim3((unsigned)p.m), dim3(1024), 0, s, part, f.blocks, a.targets, a.ignore,

@@ -13,6 +13,7 @@ namespace {
 
 // part[t0 + token][block] = (max, sum of exp(z - max)) over the block's 16 words
 template <typename TX> struct EpDecodeStats {
+  static constexpr bool GROUPS = true;
   struct Args {
     const int64_t* targets;  // [m]
     float2* part;
@@ -37,8 +38,9 @@ template <typename TX> struct EpDecodeStats {
 };
 
 // dZ of the listed tokens among t0 .. t0 + m - 1, in the forms of EpGrad;
-// the first launch also writes the zero rows that pad the list
+// the first group also writes the zero rows that pad the list
 template <typename TX, typename TL> struct EpDecodeGrad {
+  static constexpr bool GROUPS = true;
   static constexpr bool OWN = __is_same(TX, bf16_t);
   struct Args {
     const int32_t* pos;  // listed row of every token, -1 = ignored
@@ -84,36 +86,26 @@ template <typename TX, typename TL> struct EpDecodeGrad {
   }
 };
 
-// one launch of at most 16 tokens. The vocabulary has many 16-row blocks: 8
-// waves each, two or more blocks per CU (as the plain decode above 384 blocks)
+// All m tokens in one launch, 16 per block. The vocabulary has many 16-row
+// blocks: 8 waves each, two or more blocks per CU (as the plain decode above 384
+// blocks)
 template <int B, typename TX, typename TL, typename EP>
-hipError_t xent_decode_b(const TX* X, const uint8_t* idx, const TL* lut, const Problem& p,
-                         const typename EP::Args& ep, const int32_t* rexp, hipStream_t s) {
+hipError_t xent_decode(const XentGemm& g, const typename EP::Args& ep, hipStream_t s) {
+  const Problem& p = g.p;
+  const TX* X = (const TX*)g.X;
+  const TL* lut = (const TL*)g.lut;
   const uint32_t ug = (uint32_t)(p.group_cols() / 32);
   const uint32_t magic = ug == 1 ? 0u : (uint32_t)((((uint64_t)1) << 32) / ug + 1);
   SetArgs sa;
-  sa.rexp = rexp;
+  sa.rexp = g.rexp;
   const bool xl = xent_decode_stages(p), xt = !xl && p.m >= DEC_XT_MIN_M;
   if (p.units() % 4 != 0)
-    return xl ? decode_launch<B, 8, TX, TL, true, true, false, EP>(X, idx, lut, p, ep, s, magic, sa)
-              : (xt ? decode_launch<B, 8, TX, TL, true, false, true, EP>(X, idx, lut, p, ep, s, magic, sa)
-                    : decode_launch<B, 8, TX, TL, true, false, false, EP>(X, idx, lut, p, ep, s, magic, sa));
-  return xl ? decode_launch<B, 8, TX, TL, false, true, false, EP>(X, idx, lut, p, ep, s, magic, sa)
-            : (xt ? decode_launch<B, 8, TX, TL, false, false, true, EP>(X, idx, lut, p, ep, s, magic, sa)
-                  : decode_launch<B, 8, TX, TL, false, false, false, EP>(X, idx, lut, p, ep, s, magic, sa));
-}
-
-// all m tokens, 16 per launch; `ep` with t0 = 0
-template <int B, typename TX, typename TL, typename EP>
-hipError_t xent_decode_all(const XentGemm& g, typename EP::Args ep, hipStream_t s) {
-  hipError_t e = hipSuccess;
-  for (int64_t t0 = 0; t0 < g.p.m && e == hipSuccess; t0 += 16) {
-    const Problem q{g.p.m - t0 < 16 ? g.p.m - t0 : 16, g.p.n, g.p.d, g.p.b, g.p.gpr};
-    ep.t0 = t0;
-    e = xent_decode_b<B, TX, TL, EP>((const TX*)g.X + t0 * g.p.d, g.idx, (const TL*)g.lut, q, ep,
-                                     g.rexp ? g.rexp + t0 : nullptr, s);
-  }
-  return e;
+    return xl ? decode_launch<B, 8, TX, TL, true, true, false, EP>(X, g.idx, lut, p, ep, s, magic, sa)
+              : (xt ? decode_launch<B, 8, TX, TL, true, false, true, EP>(X, g.idx, lut, p, ep, s, magic, sa)
+                    : decode_launch<B, 8, TX, TL, true, false, false, EP>(X, g.idx, lut, p, ep, s, magic, sa));
+  return xl ? decode_launch<B, 8, TX, TL, false, true, false, EP>(X, g.idx, lut, p, ep, s, magic, sa)
+            : (xt ? decode_launch<B, 8, TX, TL, false, false, true, EP>(X, g.idx, lut, p, ep, s, magic, sa)
+                  : decode_launch<B, 8, TX, TL, false, false, false, EP>(X, g.idx, lut, p, ep, s, magic, sa));
 }
 
 }  // namespace

@@ -11,9 +11,9 @@ hipError_t few_t(const XentGemm& g, const XentGradOut& o, const int32_t* pos, hi
   typedef EpDecodeGrad<TX, TL> EP;
   const typename EP::Args a{pos,        g.head, g.targets, o.lse, o.dloss,      o.zexp,        o.V, g.v0,
                             o.ld,       0,      (half_t*)o.hi,   (half_t*)o.lo, (TL*)o.dxv, o.rest};
-  if (g.p.b == 2) return xent_decode_all<2, TX, TL, EP>(g, a, s);
-  if (g.p.b == 3) return xent_decode_all<3, TX, TL, EP>(g, a, s);
-  return xent_decode_all<4, TX, TL, EP>(g, a, s);
+  if (g.p.b == 2) return xent_decode<2, TX, TL, EP>(g, a, s);
+  if (g.p.b == 3) return xent_decode<3, TX, TL, EP>(g, a, s);
+  return xent_decode<4, TX, TL, EP>(g, a, s);
 }
 
 }  // namespace

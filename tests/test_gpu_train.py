@@ -389,8 +389,8 @@ def check_xent(name, m, V, d, b, gpr, io, ldt, ignored="some", sigma=1.0, dscale
     (1, 1, 32, 4, 1), (1, 7, 64, 2, 1), (2, 255, 64, 3, 2), (3, 256, 96, 4, 1), (16, 257, 128, 4, 4),
     (17, 300, 512, 4, 1), (31, 1000, 256, 3, 2), (33, 520, 576, 2, 2), (64, 129, 512, 4, 8), (257, 1001, 320, 4, 1),
     (300, 2050, 512, 3, 1),
-    # few tokens: activations per slot (below and from 8 tokens on, ragged slots), the last few tokens and the
-    # first many, tables too large for the decode
+    # few tokens: activations per slot (below and from 8 tokens on, ragged slots), many tokens, tables too large for
+    # the decode
     (5, 300, 8192, 4, 4), (16, 130, 2112, 2, 1), (64, 100, 1024, 3, 4), (65, 257, 128, 4, 2), (4, 90, 512, 4, 16),
 ])
 def test_xent(m, V, d, b, gpr, io, ldt):
@@ -495,6 +495,17 @@ def test_xent_table_gradient_keeps_fp32_of_bf16(V):
     b = skm().sketch_xent_bwd(X.bfloat16(), gi, gl, T, lse, DL, 4, 1, need_dx=False)[1]
     ref = to_f64(a)
     within(to_f64(b), ref, 2 * (2.0 ** -23 + 3 * U) * np.abs(ref) + 2 * d * 2.0 ** -39, "dLUT")
+
+
+@pytest.mark.parametrize("m,V,d,b,gpr", [
+    # many groups of 16 tokens in one launch: a last group of 4 and of 15 tokens, row blocks that are no whole number
+    # of 8, activations in LDS and from memory; and the first shapes past them, which take the tiles
+    (500, 130, 256, 4, 2), (175, 1000, 1056, 3, 3), (300, 2048, 1536, 2, 2), (120, 3300, 2048, 4, 1),
+    (1000, 2048, 320, 4, 1), (48, 12000, 256, 4, 2),
+])
+@pytest.mark.parametrize("io,ldt", [("f16", "f16"), ("bf16", "f16"), ("bf16", "bf16")])
+def test_xent_groups_of_tokens(m, V, d, b, gpr, io, ldt):
+    check_xent(f"xentgr/{m}/{V}/{io}/{ldt}", m, V, d, b, gpr, io, ldt)
 
 
 @pytest.mark.parametrize("io,ldt", [("f16", "f16"), ("bf16", "f16"), ("bf16", "bf16")])
