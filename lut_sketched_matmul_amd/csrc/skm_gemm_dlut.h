@@ -31,7 +31,7 @@ struct DlPiece {
   static constexpr bool PIECE = true;
   const int32_t* count;    // tokens; NULL = m. X holds zeros up to a multiple of 32
   int64_t ldy;             // row stride of dY, as above
-  int64_t lo_off;          // dY + lo_off: a second addend of dY, 0 = none
+  int64_t lo_off;          // dY + lo_off: a second addend of dY (k_dlut_piece's TWO)
   const float* inv_scale;  // the sums are multiplied by *inv_scale; NULL = 1
   const void* zeros;       // 16 zero bytes read in place of dY's rows past the
                            // tokens; NULL = those rows exist and hold zeros
@@ -177,7 +177,17 @@ __device__ __forceinline__ void dl_put_bins(float* __restrict__ dLUT, int64_t i0
 template <int V> struct tiles_tag { static constexpr int value = V; };
 template <bool V> struct bool_tag { static constexpr bool value = V; };
 
-template <int B, typename TX>
+// TWO: dY is the sum of two addends. A step holds both and multiplies them by
+// the same X fragments, 1 LDS read per MFMA instead of 1.5 (and X is copied
+// once), as against the tokens once per addend.
+template <bool TWO> struct DpStage {
+  static constexpr uint32_t X0 = (TWO ? 2u : 1u) * DD_TA;       // X behind dY
+  static constexpr uint32_t BYTES = DD_STAGE - DD_TA + X0;
+  static constexpr uint32_t LDS = 3u * BYTES > DD_LDS ? 3u * BYTES : DD_LDS;
+};
+static_assert(DpStage<true>::LDS <= 160u * 1024u, "three stages fit the CU's LDS");
+
+template <int B, typename TX, bool TWO>
 __global__ void __launch_bounds__(512, 1)
 k_dlut_piece(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8_t* __restrict__ idx_packed, int64_t m,
              int64_t n, int64_t d, int gpr, int gband, float* __restrict__ dLUT, int accumulate, int tsplits,
@@ -210,10 +220,12 @@ k_dlut_piece(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8_t*
   const int64_t G = d / gpr;
   const int64_t jg0 = (int64_t)g * G + (int64_t)cr * split_cols;
   const int64_t jend = (int64_t)g * G + G < jg0 + split_cols ? (int64_t)g * G + G : jg0 + split_cols;
-  // steps of 32 tokens: the tokens once, or with a second addend of dY twice
-  // (a token range may start past the tokens that exist: no step, zeros)
-  const int K1 = m <= 0 ? 0 : (int)((m + DL_BK - 1) / DL_BK);
-  const int KS = pa.lo_off != 0 ? 2 * K1 : K1;
+  // steps of 32 tokens (a token range may start past the tokens that exist: no
+  // step, zeros)
+  const int KS = m <= 0 ? 0 : (int)((m + DL_BK - 1) / DL_BK);
+  constexpr uint32_t X0 = DpStage<TWO>::X0, STAGE = DpStage<TWO>::BYTES;
+  constexpr int NA = TWO ? 4 : 2;      // fragments of dY in a half step
+  constexpr int NC = TWO ? 6 : 5;      // copies of a wave in a step
 
   // ---- DMA roles: this wave's token rows 4 wave .. +3. dY: one 1 KB
   // instruction (lane = row (lane / 16) x slot (lane % 16)); X: one
@@ -222,11 +234,11 @@ k_dlut_piece(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8_t*
   const int64_t yrow = i0 + 8 * (int64_t)ycg <= pa.ldy - 8 ? i0 + 8 * (int64_t)ycg : pa.ldy - 8;
   const TX* ysrc = dY + (int64_t)(4u * (uint32_t)wave + (lane >> 4)) * pa.ldy + yrow;
   const uint32_t ydst = 1024u * (uint32_t)wave;
-  const uint32_t xdst = DD_TA + 4096u * (uint32_t)wave;
+  const uint32_t xdst = X0 + 4096u * (uint32_t)wave;
   const int64_t ystep = (int64_t)DL_BK * pa.ldy;
   const int64_t xstep = (int64_t)DL_BK * d;
   // lanes whose row of dY in the last step is past the tokens
-  const bool past = pa.zeros && (int64_t)(K1 - 1) * DL_BK + 4 * wave + (int)(lane >> 4) >= m;
+  const bool past = !TWO && pa.zeros && (int64_t)(KS - 1) * DL_BK + 4 * wave + (int)(lane >> 4) >= m;
 
   // ---- matrix roles: fragment addresses relative to a stage
   const int wm = wave & 1, wn = wave >> 1;
@@ -244,17 +256,18 @@ k_dlut_piece(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8_t*
   // one chunk of up to 128 NBT columns from j0 on
   auto chunk = [&](int64_t j0, auto nbt) __attribute__((always_inline)) {
     constexpr int NBT = decltype(nbt)::value;
-    constexpr int NF = 2 + NBT;  // fragments of a half step: 2 of dY, NBT of X
+    constexpr int NF = NA + NBT;  // fragments of a half step: dY, X
     uint32_t fb[NBT];
 #pragma unroll
     for (int b = 0; b < NBT; ++b)
-      fb[b] = DD_TA + frow * 1024u + (((4u * NBT * wn + 4u * b + fin) ^ fx) << 4) + fw;
+      fb[b] = X0 + frow * 1024u + (((4u * NBT * wn + 4u * b + fin) ^ fx) << 4) + fw;
     // address of read r (0 .. 2 NF - 1) of a half step: fragment r / 2, first
     // or second four token rows
     auto rd = [&](uint32_t stage, int ks, int r) __attribute__((always_inline)) -> u32x2 {
       const int f = r >> 1;
-      const uint32_t rs = f < 2 ? 256u : 1024u;
-      return ld_tr(stage + (f < 2 ? fa[f & 1] : fb[f < 2 ? 0 : f - 2]) + (16u * (uint32_t)ks + 4u * (r & 1)) * rs);
+      const uint32_t rs = f < NA ? 256u : 1024u;
+      return ld_tr(stage + (f < NA ? fa[f & 1] + DD_TA * (uint32_t)(f >> 1) : fb[f < NA ? 0 : f - NA]) +
+                   (16u * (uint32_t)ks + 4u * (r & 1)) * rs);
     };
     f32x16 acc[2][4];
 #pragma unroll
@@ -269,33 +282,32 @@ k_dlut_piece(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8_t*
       const int64_t col = j0 + 8 * (int64_t)(lane ^ ((uint32_t)h << 2));
       xs[h] = reinterpret_cast<const char*>(X + (int64_t)(4u * (uint32_t)wave + h) * d + (col <= d - 8 ? col : d - 8));
     }
-    // the copies of step k, one at a time (c = 0: dY, c = 1 .. 4: X rows), then
-    // the addresses of step k + 1: a step's worth of rows further, or back at
-    // the first rows of X and at dY's second addend
+    // the copies of step k, one at a time (dY, its second addend, 4 rows of X),
+    // then the addresses of step k + 1, a step's worth of rows further
     auto copy = [&](int k, uint32_t stage, int c) __attribute__((always_inline)) {
       if (c == 0) {
         const void* yl = ys;
-        if (pa.zeros && k == K1 - 1) yl = past ? pa.zeros : yl;
+        if (!TWO && pa.zeros && k == KS - 1) yl = past ? pa.zeros : yl;
         dd_dma16_free(yl, stage + ydst);
+      } else if (TWO && c == 1) {
+        dd_dma16_free(ys + 2 * pa.lo_off, stage + DD_TA + ydst);
       } else if (NBT == 4 || lane < 16u * NBT) {
-        dd_dma16_free(xs[c - 1], stage + xdst + 1024u * (c - 1));
+        dd_dma16_free(xs[c - NC + 4], stage + xdst + 1024u * (uint32_t)(c - NC + 4));
       }
     };
-    auto advance = [&](int k) __attribute__((always_inline)) {
-      const bool wrap = k + 1 == K1;
-      ys += wrap ? (pa.lo_off - (int64_t)(K1 - 1) * ystep) * 2 : ystep * 2;
-      const int64_t dx = wrap ? -(int64_t)(K1 - 1) * xstep * 2 : xstep * 2;
+    auto advance = [&]() __attribute__((always_inline)) {
+      ys += ystep * 2;
 #pragma unroll
-      for (int h = 0; h < 4; ++h) xs[h] += dx;
+      for (int h = 0; h < 4; ++h) xs[h] += xstep * 2;
     };
 #pragma unroll
-    for (int c = 0; c < 5; ++c) copy(0, 0u, c);
-    advance(0);
+    for (int c = 0; c < NC; ++c) copy(0, 0u, c);
+    advance();
     if (KS > 1) {
 #pragma unroll
-      for (int c = 0; c < 5; ++c) copy(1, DD_STAGE, c);
-      advance(1);
-      dd_wait_vmcnt<5>();
+      for (int c = 0; c < NC; ++c) copy(1, STAGE, c);
+      advance();
+      dd_wait_vmcnt<NC>();
     } else {
       dd_wait_vmcnt<0>();
     }
@@ -311,7 +323,7 @@ k_dlut_piece(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8_t*
     auto frag = [](const u32x2* v, int f) __attribute__((always_inline)) -> u32x4 {
       return u32x4{v[2 * f].x, v[2 * f].y, v[2 * f + 1].x, v[2 * f + 1].y};
     };
-    // MFMAs of half v (2 NBT of them) with the reads of the next half into w
+    // MFMAs of half v (NA NBT of them) with the reads of the next half into w
     // and, MORE, the copies of step k + 2: pinned group by group
     auto half = [&](const u32x2* v, u32x2* w, uint32_t rst, int ks, int k, uint32_t cst, auto more)
         __attribute__((always_inline)) {
@@ -321,23 +333,23 @@ k_dlut_piece(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8_t*
 #pragma unroll
         for (int r = 2 * NF * b / NBT; r < 2 * NF * (b + 1) / NBT; ++r) w[r] = rd(rst, ks, r);
 #pragma unroll
-        for (int a = 0; a < 2; ++a) acc[a][b] = MF::run(frag(v, 2 + b), frag(v, a), acc[a][b]);
+        for (int a = 0; a < NA; ++a) acc[a & 1][b] = MF::run(frag(v, NA + b), frag(v, a), acc[a & 1][b]);
         if constexpr (MORE) {
 #pragma unroll
-          for (int c = 5 * b / NBT; c < 5 * (b + 1) / NBT; ++c) copy(k + 2, cst, c);
+          for (int c = NC * b / NBT; c < NC * (b + 1) / NBT; ++c) copy(k + 2, cst, c);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
     };
     auto step = [&](int k, auto more) __attribute__((always_inline)) {
       constexpr bool MORE = decltype(more)::value;
-      half(p, q, st, 1, k, st >= DD_STAGE ? st - DD_STAGE : st + 2u * DD_STAGE, more);
-      if constexpr (MORE) advance(k + 2);
+      half(p, q, st, 1, k, st >= STAGE ? st - STAGE : st + 2u * STAGE, more);
+      if constexpr (MORE) advance();
       __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): every read of stage k has landed
-      if constexpr (MORE) dd_wait_vmcnt<5>();
+      if constexpr (MORE) dd_wait_vmcnt<NC>();
       else dd_wait_vmcnt<0>();
       dd_barrier();
-      st = st + DD_STAGE == 3u * DD_STAGE ? 0u : st + DD_STAGE;
+      st = st + STAGE == 3u * STAGE ? 0u : st + STAGE;
       // (after the last step this reads a stale stage and the values go unused)
       half(q, p, st, 0, k, 0u, bool_tag<false>{});
     };
@@ -360,11 +372,11 @@ k_dlut_piece(const TX* __restrict__ dY, const TX* __restrict__ X, const uint8_t*
   dl_put_bins<B>(dLUT, i0, n, gpr, g, accumulate, t, bins, pa.inv_scale ? *pa.inv_scale : 1.0f);
 }
 
-template <int B, typename TX>
+template <int B, typename TX, bool TWO>
 hipError_t dlut_piece_launch(const TX* dY, const TX* X, const uint8_t* idx, const Problem& p, float* dLUT,
                            int accumulate, float* part, const DlPiece& pa, hipStream_t s) {
-  const auto kern = k_dlut_piece<B, TX>;
-  static const hipError_t prep = prepare_kernel((const void*)kern, DD_LDS);
+  const auto kern = k_dlut_piece<B, TX, TWO>;
+  static const hipError_t prep = prepare_kernel((const void*)kern, DpStage<TWO>::LDS);
   if (prep != hipSuccess) return prep;
   const int64_t rb = (p.n + DL_BM - 1) / DL_BM;
   // bands of 4 groups (or 2, or 1) in the XCD-local block order
@@ -372,7 +384,7 @@ hipError_t dlut_piece_launch(const TX* dY, const TX* X, const uint8_t* idx, cons
   const DlutSplit sp = dlut_split_of(p);
   const int64_t count = p.n * p.gpr * p.k();
   const bool split = sp.parts() > 1;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(rb * p.gpr * sp.parts())), dim3(512), DD_LDS, s, dY, X, idx, p.m, p.n,
+  hipLaunchKernelGGL(kern, dim3((unsigned)(rb * p.gpr * sp.parts())), dim3(512), DpStage<TWO>::LDS, s, dY, X, idx, p.m, p.n,
                      p.d, p.gpr, gband, split ? part : dLUT, split ? 0 : accumulate, sp.tsplits, sp.csplits,
                      sp.tokens, sp.cols, count, pa);
   hipError_t e = hipGetLastError();

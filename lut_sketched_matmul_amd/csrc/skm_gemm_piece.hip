@@ -17,15 +17,15 @@ hipError_t dx_piece_t(const void* dY, const uint8_t* idx, const void* lut, const
   return dx_b<4, TX, TL>(y, idx, l, p, dX, rexp, pa, s);
 }
 
-template <typename TX>
+template <typename TX, bool TWO>
 hipError_t dlut_piece_t(const void* hi, const void* lo, const void* X, const uint8_t* idx, const Problem& p,
                         float* dLUT, int accumulate, float* part, const DlutPiece& q, hipStream_t s) {
   const TX* y = (const TX*)hi;
   const TX* x = (const TX*)X;
-  const DlPiece pa{q.count, q.ld, lo ? (const TX*)lo - y : 0, q.inv_scale, q.zeros};
-  if (p.b == 2) return dlut_piece_launch<2, TX>(y, x, idx, p, dLUT, accumulate, part, pa, s);
-  if (p.b == 3) return dlut_piece_launch<3, TX>(y, x, idx, p, dLUT, accumulate, part, pa, s);
-  return dlut_piece_launch<4, TX>(y, x, idx, p, dLUT, accumulate, part, pa, s);
+  const DlPiece pa{q.count, q.ld, TWO ? (const TX*)lo - y : 0, q.inv_scale, q.zeros};
+  if (p.b == 2) return dlut_piece_launch<2, TX, TWO>(y, x, idx, p, dLUT, accumulate, part, pa, s);
+  if (p.b == 3) return dlut_piece_launch<3, TX, TWO>(y, x, idx, p, dLUT, accumulate, part, pa, s);
+  return dlut_piece_launch<4, TX, TWO>(y, x, idx, p, dLUT, accumulate, part, pa, s);
 }
 
 }  // namespace
@@ -64,8 +64,11 @@ hipError_t launch_dx_piece(const void* dY, int io_dtype, const uint8_t* idx, con
 hipError_t launch_dlut_piece(const void* hi, const void* lo, const void* X, int io_dtype, const uint8_t* idx,
                              const Problem& p, float* dLUT, int accumulate, float* part, const DlutPiece& q,
                              hipStream_t s) {
-  if (io_dtype == DT_F16) return dlut_piece_t<half_t>(hi, lo, X, idx, p, dLUT, accumulate, part, q, s);
-  return dlut_piece_t<bf16_t>(hi, lo, X, idx, p, dLUT, accumulate, part, q, s);
+  // (two addends are f16 and their rows past the tokens zeros)
+  if (lo && (io_dtype != DT_F16 || q.zeros)) return hipErrorNotSupported;
+  if (lo) return dlut_piece_t<half_t, true>(hi, lo, X, idx, p, dLUT, accumulate, part, q, s);
+  if (io_dtype == DT_F16) return dlut_piece_t<half_t, false>(hi, lo, X, idx, p, dLUT, accumulate, part, q, s);
+  return dlut_piece_t<bf16_t, false>(hi, lo, X, idx, p, dLUT, accumulate, part, q, s);
 }
 
 }  // namespace skm
