@@ -159,7 +159,8 @@ hipError_t launch_bwd_ckpt(const void* dY, const int8_t* codes, const uint8_t* s
     const bool ranges = f.r.count > 1;
     float* parts = reinterpret_cast<float*>(base + f.dx);
     if (e == hipSuccess)
-      e = launch_dx_piece(y, io_dtype, idx, lut, lut_dtype, p, ranges ? parts : dX, rexp, nullptr, f.ld, 0, f.r, s);
+      e = launch_dx_piece(y, io_dtype, idx, lut, lut_dtype, p, ranges ? parts : dX, rexp, nullptr, f.ld, 0, f.r,
+                          nullptr, 0, s);
     if (e == hipSuccess && ranges) {
       const int64_t count = p.m * p.d;
       hipLaunchKernelGGL(k_sum_ranges, dim3((unsigned)((count / 4 + 255) / 256)), dim3(256), 0, s, parts, f.r.count,

@@ -72,6 +72,8 @@ struct DxPiece {
   int splits;            // the weight rows are cut into this many ranges,
   int64_t split_rows;    // of this many rows (a multiple of 64), each with its
   int64_t part_stride;   // own dX, part_stride floats apart
+  const DxPlan* plan;    // instead of the three above
+  unsigned blocks;       // of the launch
 };
 
 // ============================================================================
@@ -190,8 +192,9 @@ __device__ __forceinline__ void dx_lut_store(const DxLutWord<B>& L, uint32_t eba
 }
 
 // A piece's share of one block: its range of the weight rows, the tokens that
-// exist. The blocks that have tokens come first (evenly over the XCDs); false
-// for the others (block-uniform).
+// exist. The blocks that have tokens come first (evenly over the XCDs), the
+// longest ranges before the others; false for blocks without work
+// (block-uniform).
 template <int B, typename TX, typename TL>
 __device__ __forceinline__ bool dx_piece(const DxPiece& pa, uint32_t& bid, const TX* __restrict__& dY,
                                          const uint8_t* __restrict__& idx_packed, const TL* __restrict__& lut,
@@ -199,15 +202,27 @@ __device__ __forceinline__ bool dx_piece(const DxPiece& pa, uint32_t& bid, const
                                          float* __restrict__& dX) {
   if (pa.count) m = *pa.count;
   mblocks = (m + DX_BM - 1) / DX_BM;
-  const uint32_t nb0 = (uint32_t)(mblocks * ((d + DX_BN - 1) / DX_BN));
-  if (bid >= nb0 * (uint32_t)pa.splits) return false;
-  const int64_t sp = bid / nb0, r0 = sp * pa.split_rows;
-  bid %= nb0;
+  const uint32_t tiles = (uint32_t)(mblocks * ((d + DX_BN - 1) / DX_BN));
+  uint32_t cut = 0, ranges = (uint32_t)pa.splits;
+  int64_t rows = pa.split_rows, stride = pa.part_stride;
+  if (pa.plan) {
+    const DxPlan q = *pa.plan;
+    cut = (uint32_t)q.cut_from;
+    ranges = (uint32_t)q.ranges;
+    rows = ((n + 63) / 64 * q.first + q.parts - 1) / q.parts * 64;
+    stride = m * d;
+  }
+  if (bid < cut) return true;  // a whole tile
+  if (tiles == cut) return false;
+  const uint32_t sp = (bid - cut) / (tiles - cut);
+  const int64_t r0 = sp * rows;
+  if (sp >= ranges || r0 >= n) return false;
+  bid = cut + (bid - cut) % (tiles - cut);
   dY += r0;
   idx_packed += r0 * (d * B / 8);
   lut += r0 * gpr * (1 << B);
-  n = n - r0 < pa.split_rows ? n - r0 : pa.split_rows;
-  dX += sp * pa.part_stride;
+  n = n - r0 < rows ? n - r0 : rows;
+  dX += sp * stride;
   return true;
 }
 
@@ -1362,10 +1377,10 @@ uint32_t ug_magic_of(const Problem& p) {
   return ug == 1 ? 0u : (uint32_t)((((uint64_t)1) << 32) / ug + 1);
 }
 
-// blocks of one launch: a piece's ranges of the weight rows each have their own
+// blocks of one launch
 template <typename PA>
 unsigned dx_blocks(int64_t mb, int64_t nb, const PA& pa) {
-  if constexpr (PA::PIECE) return (unsigned)(mb * nb * pa.splits);
+  if constexpr (PA::PIECE) return pa.blocks;
   else return (unsigned)(mb * nb);
 }
 

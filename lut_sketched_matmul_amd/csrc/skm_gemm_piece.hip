@@ -51,8 +51,9 @@ DxRanges dx_ranges(const Problem& p) {
 
 hipError_t launch_dx_piece(const void* dY, int io_dtype, const uint8_t* idx, const void* lut, int lut_dtype,
                            const Problem& p, float* dX, const int32_t* rexp, const int32_t* count, int64_t ld,
-                           int accumulate, const DxRanges& r, hipStream_t s) {
-  const DxPiece pa{count, ld, accumulate, r.count, r.rows, p.m * p.d};
+                           int accumulate, const DxRanges& r, const DxPlan* plan, int64_t blocks, hipStream_t s) {
+  if (!plan) blocks = (p.m + DX_BM - 1) / DX_BM * ((p.d + DX_BN - 1) / DX_BN) * r.count;
+  const DxPiece pa{count, ld, accumulate, r.count, r.rows, p.m * p.d, plan, (unsigned)blocks};
   if (io_dtype == DT_F16 && lut_dtype == DT_F16)
     return dx_piece_t<half_t, half_t>(dY, idx, lut, p, dX, nullptr, pa, s);
   if (io_dtype == DT_BF16 && lut_dtype == DT_F16)

@@ -101,9 +101,17 @@ struct DxRanges {
   int64_t rows;
 };
 DxRanges dx_ranges(const Problem& p);
+// Ranges made on the device, from the token count: dX's (256-token, 256-column)
+// tiles from cut_from on are cut into `ranges` ranges of ceil(steps first /
+// parts) 64-row steps (the last one takes the rest; it may have none after a
+// first piece), range k's sums k count d floats behind dX.
+struct DxPlan {
+  int32_t cut_from, ranges, first, parts;
+};
+// plan: NULL = the ranges r, else those of *plan in at most `blocks` blocks
 hipError_t launch_dx_piece(const void* dY, int io_dtype, const uint8_t* idx, const void* lut, int lut_dtype,
                            const Problem& p, float* dX, const int32_t* rexp, const int32_t* count, int64_t ld,
-                           int accumulate, const DxRanges& r, hipStream_t s);
+                           int accumulate, const DxRanges& r, const DxPlan* plan, int64_t blocks, hipStream_t s);
 struct DlutPiece {
   const int32_t* count;
   int64_t ld;

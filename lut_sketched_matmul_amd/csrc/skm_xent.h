@@ -51,6 +51,7 @@ struct XentHead {
   float inv_scale;
   float dx_scale;   // of dX's (equal for f16 X: one form serves both)
   float dx_inv;
+  DxPlan dx;        // ranges of dX's tiles (dx_plan)
 };
 
 // ---- pieces of the launchers, one translation unit each --------------------------

@@ -11,8 +11,47 @@ namespace {
 
 constexpr int XENT_BN = 256;  // vocabulary rows of a tile
 
+// ---- the ranges of dX ---------------------------------------------------------------
+// The ranges of dX's tiles for the tokens there are. Up to half a round of 256
+// tiles: as many equal ranges as make rounds of 256 blocks times 64-row steps
+// per block least (at least 4 steps each, two rounds at the most, `cap` token
+// rows of sums for all ranges). Otherwise the tiles past whole rounds, R of them
+// (R <= 224), are cut in two: with q = ceil(R / (256 - R)) short ranges for each
+// CU left over, a long range takes q steps of q + 1. (3 / 4 of 4096 tokens, 4096
+// columns: 192 tiles, 192 ranges of 3 / 4 of the steps beside 64 CUs with three
+// of 1 / 4 each.) Thread t looks at t + 1 equal ranges.
+struct DxShape {
+  int32_t nb, steps;  // column tiles, steps of the first piece
+  int64_t cap;
+};
+constexpr int DX_CUT_STEPS = 32;  // fewest steps of a tile cut in two: none of 7 / 8 and 1 / 8 of them is empty
+__device__ __forceinline__ DxPlan dx_plan(int32_t count, const DxShape& q, unsigned long long* slot) {
+  const uint32_t tiles = (uint32_t)(count + 255) / 256u * (uint32_t)q.nb, steps = (uint32_t)q.steps;
+  if (tiles > 128u || count == 0) {  // block-uniform
+    const uint32_t R = tiles % 256u;
+    if (R == 0 || R > 224u || q.steps < DX_CUT_STEPS || q.cap < 2 * (int64_t)count) return {(int32_t)tiles, 1, 1, 1};
+    const int32_t c = (int32_t)(255u / (256u - R));  // ceil(R / (256 - R))
+    return {(int32_t)(tiles - R), 2, c, c + 1};
+  }
+  const uint32_t t = threadIdx.x + 1;
+  unsigned long long best = ~0ull;
+  if (t == 1 || (4 * t <= steps && tiles * t <= 512u && count * (int64_t)t <= q.cap))
+    best = ((unsigned long long)((tiles * t + 255u) / 256u) * ((steps + t - 1) / t)) << 10 | t;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    const unsigned long long v = __shfl_xor(best, o, 64);
+    best = v < best ? v : best;
+  }
+  if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = best;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 16; ++w) best = slot[w] < best ? slot[w] : best;
+  const uint32_t c = (uint32_t)best & 1023u, len = (steps + c - 1) / c, k = (steps + len - 1) / len;
+  return {0, (int32_t)k, 1, (int32_t)k};
+}
+
 // ---- the list of tokens that have a target -----------------------------------------
-// One block (the list is one scan over m targets, 8 per thread and round).
+// One block (the list is one scan over m targets, 8192 per round).
 // rows[c] = token of listed row c, in token order. Forward: loss and lse of the
 // others are zeroed. Backward: pos[t] = listed row of token t or -1, and the
 // powers of two that put the largest finite |dloss| 2^e (e from zexp, NULL = 0)
@@ -30,56 +69,65 @@ __global__ void __launch_bounds__(1024) k_xent_index(const int64_t* __restrict__
                                                      const float* __restrict__ dloss,
                                                      const int32_t* __restrict__ zexp, XentHead* __restrict__ head,
                                                      int32_t* __restrict__ rows, int32_t* __restrict__ pos,
-                                                     float* __restrict__ loss, float* __restrict__ lse) {
-  __shared__ int32_t wsum[16];
+                                                     DxShape dx, float* __restrict__ loss, float* __restrict__ lse) {
+  __shared__ int32_t before[129];  // listed tokens of a round in front of wave w's k-th 64: [16 k + w]
+  __shared__ unsigned long long slot[16];
   __shared__ uint32_t wmax[2][16];
   const int t = (int)threadIdx.x, lane = t & 63, wave = t >> 6;
   int32_t base = 0;
   uint32_t top = 0u, top_dx = 0u;
   for (int64_t r0 = 0; r0 < m; r0 += 8192) {
-    const int64_t i0 = r0 + 8 * (int64_t)t;
-    uint32_t flags = 0u;
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (i0 + k < m && targets[i0 + k] != ignore) flags |= 1u << k;
-    const int32_t mine = __popc(flags);
-    int32_t scan = mine;  // inclusive over the wave
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int32_t v = __shfl_up(scan, o, 64);
-      if (lane >= o) scan += v;
-    }
-    if (lane == 63) wsum[wave] = scan;
-    __syncthreads();
-    int32_t before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < 16; ++w) {
-      const int32_t v = wsum[w];
-      if (w < wave) before += v;
-      total += v;
-    }
-    __syncthreads();  // (the next round writes wsum)
-    int32_t c = base + before + scan - mine;
+    unsigned long long on[8];
+    float f[8] = {};
+    int32_t z[8] = {};
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int64_t i = i0 + k;
-      if (i >= m) continue;
-      const bool on = (flags >> k) & 1u;
-      if (on) rows[c] = (int32_t)i;
-      if constexpr (BWD) {
-        pos[i] = on ? c : -1;
-        if (on) {
-          const float f = dloss[i];
-          top_dx = larger_finite(top_dx, f);
-          top = larger_finite(top, zexp ? f * pow2f(zexp[i]) : f);
+      const int64_t i = r0 + 1024 * k + t;
+      bool mine = false;
+      if (i < m) {
+        mine = targets[i] != ignore;
+        if constexpr (BWD) {
+          f[k] = dloss[i];
+          if (zexp) z[k] = zexp[i];
         }
-      } else if (!on) {
+      }
+      on[k] = __ballot(mine);
+      if (lane == 0) before[16 * k + wave] = __popcll(on[k]);
+    }
+    __syncthreads();
+    if (wave == 0) {
+      const int32_t a = before[2 * lane], s = a + before[2 * lane + 1];
+      int32_t scan = s;  // inclusive over the wave
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int32_t v = __shfl_up(scan, o, 64);
+        if (lane >= o) scan += v;
+      }
+      before[2 * lane] = scan - s;
+      before[2 * lane + 1] = scan - s + a;
+      if (lane == 63) before[128] = scan;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t i = r0 + 1024 * k + t;
+      if (i >= m) continue;
+      const bool mine = (on[k] >> lane) & 1u;
+      const int32_t c = base + before[16 * k + wave] + __popcll(on[k] & ((1ull << lane) - 1u));
+      if (mine) rows[c] = (int32_t)i;
+      if constexpr (BWD) {
+        pos[i] = mine ? c : -1;
+        if (mine) {
+          top_dx = larger_finite(top_dx, f[k]);
+          top = larger_finite(top, f[k] * pow2f(z[k]));
+        }
+      } else if (!mine) {
         loss[i] = 0.0f;
         lse[i] = 0.0f;
       }
-      c += on ? 1 : 0;
     }
-    base += total;
+    base += before[128];
+    __syncthreads();  // (the next round writes before)
   }
   if constexpr (BWD) {
 #pragma unroll
@@ -94,8 +142,12 @@ __global__ void __launch_bounds__(1024) k_xent_index(const int64_t* __restrict__
     }
     __syncthreads();
   }
+  DxPlan plan{0, 1, 1, 1};
+  if constexpr (BWD)
+    if (dx.nb > 0) plan = dx_plan(base, dx, slot);
   if (t == 0) {
     head->count = base;
+    head->dx = plan;
     if constexpr (BWD) {
       for (int w = 0; w < 16; ++w) {
         top = top > wmax[0][w] ? top : wmax[0][w];
@@ -314,8 +366,8 @@ __global__ void __launch_bounds__(256) k_xent_gather(const TX* __restrict__ X, c
 // lanes columns, 8 per thread, `lanes` threads taking every lanes-th range each:
 // a few rows have up to 256 ranges, which one thread would wait for one by one.
 template <int B, typename TX, typename TL>
-__global__ void __launch_bounds__(256) k_xent_dx_out(const float* __restrict__ acc, int ranges, int64_t part_stride,
-                                                     int lanes, const int32_t* __restrict__ pos,
+__global__ void __launch_bounds__(256) k_xent_dx_out(const float* __restrict__ acc, int lanes,
+                                                     const int32_t* __restrict__ pos,
                                                      const XentHead* __restrict__ head,
                                                      const float* __restrict__ rest, const int64_t* __restrict__ targets,
                                                      const uint8_t* __restrict__ idx_packed,
@@ -330,6 +382,9 @@ __global__ void __launch_bounds__(256) k_xent_dx_out(const float* __restrict__ a
   float v[8] = {};
   if (c >= 0 && j < d) {
     const float* src = acc + c * d + j;
+    const int64_t count = head->count, part_stride = count * d;
+    const DxPlan q = head->dx;
+    const int ranges = j / 256 * ((count + 255) / 256) + c / 256 >= q.cut_from ? q.ranges : 1;
     int k = lane;
     for (; k + 3 * lanes < ranges; k += 4 * lanes) {
       float a[4][8];
@@ -385,13 +440,13 @@ struct DxOut {
 template <typename TX, typename TL>
 hipError_t dx_out_t(const XentArgs& a, const DxOut& o, void* dX, hipStream_t s) {
   const Problem& p = a.p;
-  // two or more ranges per lane, and at most 2048 blocks' worth of threads
+  // two or more of the most ranges per lane, and at most 2048 blocks' worth of threads
   int lanes = 1;
   while (lanes < 32 && lanes * 2 <= o.ranges && p.m * p.d * lanes < 2048 * 2048) lanes *= 2;
   const int64_t cols = 2048 / lanes;
   auto go = [&](auto kern) {
     hipLaunchKernelGGL(kern, dim3((unsigned)p.m, (unsigned)((p.d + cols - 1) / cols)), dim3(256), 0, s, o.acc,
-                       o.ranges, p.m * p.d, lanes, o.pos, o.head, o.rest, a.targets, a.idx, (const TL*)a.lut, p.n, p.d, p.gpr, (TX*)dX);
+                       lanes, o.pos, o.head, o.rest, a.targets, a.idx, (const TL*)a.lut, p.n, p.d, p.gpr, (TX*)dX);
     return hipGetLastError();
   };
   if (p.b == 2) return go(k_xent_dx_out<2, TX, TL>);
@@ -438,7 +493,9 @@ FwdPlan fwd_plan(const Problem& p, int x_dtype, int lut_dtype) {
 struct BwdPlan {
   int64_t cap;         // listed rows, rounded up to 32
   int64_t P;           // vocabulary rows per piece
-  DxRanges ranges;     // of the first piece's rows, each with its own dX
+  int64_t slots;       // dX sums of m tokens in the workspace (the most ranges when all have a target, or 2)
+  int64_t dx_blocks;   // the most blocks of dX's ranges for any number of listed tokens
+  DxShape dx;
   bool few, streams;
   bool own;            // dX's operand is a form of its own
   bool exps;           // row exponents of X are needed: logits' or dLUT's f16 operands of bf16 rows
@@ -465,7 +522,12 @@ BwdPlan bwd_plan(const Problem& p, int x_dtype, int lut_dtype, bool need_dx, boo
   P = ((p.n + pieces - 1) / pieces + XENT_BN - 1) / XENT_BN * XENT_BN;
   f.P = P;
   const int64_t n1 = p.n < P ? p.n : P;
-  f.ranges = dx_ranges(Problem{p.m, n1, p.d, p.b, p.gpr});
+  const int64_t nb = (p.d + 255) / 256, tiles = (p.m + 255) / 256 * nb;
+  f.slots = dx_ranges(Problem{p.m, n1, p.d, p.b, p.gpr}).count;
+  if (f.slots < 2) f.slots = 2;
+  f.dx = DxShape{need_dx ? (int32_t)nb : 0, (int32_t)((n1 + 63) / 64), f.slots * p.m};
+  const int64_t most = f.dx.steps < 8 ? 1 : f.dx.steps / 4;  // equal ranges
+  f.dx_blocks = tiles <= 128 ? (tiles * most < 512 ? tiles * most : 512) : (tiles + 224 > 512 ? tiles + 224 : 512);
   size_t o = 256;
   auto take = [&](bool on, size_t bytes) {
     const size_t at = o;
@@ -480,7 +542,7 @@ BwdPlan bwd_plan(const Problem& p, int x_dtype, int lut_dtype, bool need_dx, boo
   f.hi = take(has_hi, dz);
   f.lo = take(need_dlut, dz);
   f.dxv = take(has_dxv, dz);
-  f.acc = take(need_dx, (size_t)f.ranges.count * (size_t)p.m * (size_t)p.d * 4);
+  f.acc = take(need_dx, (size_t)f.slots * (size_t)p.m * (size_t)p.d * 4);
   f.xc = take(need_dlut, (size_t)f.cap * (size_t)p.d * 2);
   size_t part = 0;
   for (int64_t v0 = 0; v0 < p.n; v0 += P) {  // (the last piece may split differently)
@@ -542,7 +604,7 @@ hipError_t launch_xent_fwd(const XentArgs& a, float* loss, float* lse, void* ws,
     return hipGetLastError();
   }
   hipLaunchKernelGGL(k_xent_index<false>, dim3(1), dim3(1024), 0, s, a.targets, a.ignore, p.m, nullptr, nullptr, head,
-                     rows, nullptr, loss, lse);
+                     rows, nullptr, DxShape{}, loss, lse);
   e = hipGetLastError();
   if (e == hipSuccess && f.streams) e = xent_rows(g, xp, rexp, s);
   else if (e == hipSuccess && rexp) e = launch_row_exp(a.X, p.m, p.d, rexp, s);
@@ -585,7 +647,7 @@ hipError_t launch_xent_bwd(const XentArgs& a, const float* lse, const float* dlo
   if (rexp) e = launch_row_exp(a.X, p.m, p.d, rexp, s);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k_xent_index<true>, dim3(1), dim3(1024), 0, s, a.targets, a.ignore, p.m, dloss, zexp, head, rows,
-                     pos, nullptr, nullptr);
+                     pos, f.dx, nullptr, nullptr);
   e = hipGetLastError();
   XentGemm g{a.X, a.x_dtype, a.idx, a.lut, a.lut_dtype, p, rows, head, a.targets, rexp, 0, xp};
   if (e == hipSuccess && f.streams) e = xent_rows(g, xp, rexp, s);
@@ -613,10 +675,8 @@ hipError_t launch_xent_bwd(const XentArgs& a, const float* lse, const float* dlo
     e = f.few ? xent_few_grad(g, out, pos, s) : xent_grad(g, out, s);
     if (e == hipSuccess && dX) {
       // every range of the first piece is written; later pieces add to some or all
-      const int64_t steps = (n + 63) / 64;
-      const int64_t sr = (steps + f.ranges.count - 1) / f.ranges.count * 64;
       e = launch_dx_piece(f.own ? dxv : hi, a.lut_dtype, idx, lut, a.lut_dtype, q, acc, nullptr, &head->count, ld, v0 > 0,
-                          {(int)((n + sr - 1) / sr), sr}, s);
+                          {}, &head->dx, f.dx_blocks, s);
     }
     if (e == hipSuccess && dLUT) {
       const Problem qc{f.cap, n, p.d, p.b, p.gpr};
@@ -625,7 +685,7 @@ hipError_t launch_xent_bwd(const XentArgs& a, const float* lse, const float* dlo
     }
   }
   if (e != hipSuccess || !dX) return e;
-  return dx_out(a, {acc, f.ranges.count, pos, head, rest}, dX, s);
+  return dx_out(a, {acc, (int)f.slots, pos, head, rest}, dX, s);
 }
 
 }  // namespace skm

@@ -508,6 +508,21 @@ def test_xent_groups_of_tokens(m, V, d, b, gpr, io, ldt):
     check_xent(f"xentgr/{m}/{V}/{io}/{ldt}", m, V, d, b, gpr, io, ldt)
 
 
+@pytest.mark.parametrize("m,V,d,ignored", [
+    # 144 dX tiles, cut 3 : 1; as many that 0.6 of them are equal ranges; 297, the last 41 in halves; too few words to
+    # cut; a single tile in ranges; more tokens than one round of the list's scan
+    (4400, 2100, 2048, "none"), (4400, 2100, 2048, "some"), (8200, 2100, 2304, "none"), (4400, 1000, 2048, "none"),
+    (300, 1500, 256, "some"), (17000, 300, 64, "some"),
+])
+def test_xent_ranges_of_dx(m, V, d, ignored):
+    check_xent(f"xentdx/{m}/{V}/{ignored}", m, V, d, 4, 1, "f16", "f16", ignored=ignored, need=(True, False))
+
+
+def test_xent_pieces_with_cut_tiles():
+    """Two pieces of 36 steps (the second ragged), 160 dX tiles of each in two ranges."""
+    check_xent("xentcut", 10000, 4590, 1024, 4, 1, "bf16", "bf16", ignored="none")
+
+
 @pytest.mark.parametrize("io,ldt", [("f16", "f16"), ("bf16", "f16"), ("bf16", "bf16")])
 def test_xent_zero_rows_have_gradients(io, ldt):
     """A row of zeros (or nearly) gives the tables nothing but takes the gradient sum_v (1/V - [target]) W itself."""
