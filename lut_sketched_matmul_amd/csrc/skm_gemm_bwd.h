@@ -68,7 +68,7 @@ struct DxPiece {
   static constexpr bool PIECE = true;
   const int32_t* count;  // tokens (at most the host's m); NULL = m
   int64_t ldy;           // row stride of dY: a multiple of 8, at least n, finite from n on
-  int accumulate;        // add to dX instead of overwriting it
+  int accumulate;        // add to dX instead of overwriting it (not for the prescaled pair)
   int splits;            // the weight rows are cut into this many ranges,
   int64_t split_rows;    // of this many rows (a multiple of 64), each with its
   int64_t part_stride;   // own dX, part_stride floats apart
@@ -480,16 +480,24 @@ k_gemm_dx(const TX* __restrict__ dY, const uint8_t* __restrict__ idx_packed, con
       for (int jj = 0; jj < 2; ++jj) {
         const int64_t col = n0 + 64 * wn + 32 * jj + (lane & 31);
         if (col >= d) continue;
+        // (the sums so far are read together: a read after each write would wait for it)
+        float sum[16] = {};
+        if constexpr (PA::PIECE && !SC) {
+          if (pa.accumulate) {
+  #pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int64_t tok = m0 + 128 * wm + 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+              sum[e] = dX[(tok < m ? tok : m - 1) * d + col];
+            }
+          }
+        }
   #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int64_t tok = m0 + 128 * wm + 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
           float v = acc[i][jj][e];
           if constexpr (SC && MD != 0) v *= uq[e >> 2][e & 3];
-          if (tok < m) {
-            if constexpr (PA::PIECE)
-              if (pa.accumulate) v += dX[tok * d + col];
-            dX[tok * d + col] = v;
-          }
+          if constexpr (PA::PIECE && !SC) v += sum[e];
+          if (tok < m) dX[tok * d + col] = v;
         }
       }
     }
@@ -840,16 +848,24 @@ k_gemm_dx64(const TX* __restrict__ dY, const uint8_t* __restrict__ idx_packed, c
         const int pc = B == 4 ? (p & ~7) | ((p & 3) << 1) | ((p >> 2) & 1) : p;
         const int64_t col = n0 + pc;
         if (col >= d) continue;
+        // (the sums so far are read together: a read after each write would wait for it)
+        float sum[16] = {};
+        if constexpr (PA::PIECE && !SC) {
+          if (pa.accumulate) {
+  #pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int64_t tok = m0 + 128 * wm + 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+              sum[e] = dX[(tok < m ? tok : m - 1) * d + col];
+            }
+          }
+        }
   #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int64_t tok = m0 + 128 * wm + 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
           float v = acc[i][jj][e];
           if constexpr (SC && MD != 0) v *= uq[e >> 2][e & 3];
-          if (tok < m) {
-            if constexpr (PA::PIECE)
-              if (pa.accumulate) v += dX[tok * d + col];
-            dX[tok * d + col] = v;
-          }
+          if constexpr (PA::PIECE && !SC) v += sum[e];
+          if (tok < m) dX[tok * d + col] = v;
         }
       }
     }

@@ -52,6 +52,7 @@ DxRanges dx_ranges(const Problem& p) {
 hipError_t launch_dx_piece(const void* dY, int io_dtype, const uint8_t* idx, const void* lut, int lut_dtype,
                            const Problem& p, float* dX, const int32_t* rexp, const int32_t* count, int64_t ld,
                            int accumulate, const DxRanges& r, const DxPlan* plan, int64_t blocks, hipStream_t s) {
+  if (accumulate && scaled_pair(io_dtype == DT_BF16, lut_dtype == DT_F16)) return hipErrorNotSupported;
   if (!plan) blocks = (p.m + DX_BM - 1) / DX_BM * ((p.d + DX_BN - 1) / DX_BN) * r.count;
   const DxPiece pa{count, ld, accumulate, r.count, r.rows, p.m * p.d, plan, (unsigned)blocks};
   if (io_dtype == DT_F16 && lut_dtype == DT_F16)

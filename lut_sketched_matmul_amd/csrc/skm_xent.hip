@@ -377,8 +377,19 @@ __global__ void __launch_bounds__(256) k_xent_dx_out(const float* __restrict__ a
   __shared__ float part[8][256];  // [column of a thread's eight][thread]
   const int64_t t = blockIdx.x;
   const int64_t c = pos[t];
+  const int64_t target = targets[t];
   const int chunks = 256 / lanes, lane = (int)threadIdx.x / chunks;
   const int64_t j = 8 * ((int64_t)blockIdx.y * chunks + (int)threadIdx.x % chunks);
+  const bool fix = c >= 0 && target >= 0 && target < V && j < d && lane == 0;
+  // the 8 indices of columns j .. j + 7 are B bytes (one group: its width is a multiple of 32)
+  uint32_t w = 0u;
+  float r = 0.0f;
+  if (fix) {
+    const uint8_t* row = idx_packed + target * (d * B / 8) + j / 8 * B;
+#pragma unroll
+    for (int q = 0; q < B; ++q) w |= (uint32_t)row[q] << (8 * q);
+    r = rest[c];
+  }
   float v[8] = {};
   if (c >= 0 && j < d) {
     const float* src = acc + c * d + j;
@@ -410,15 +421,8 @@ __global__ void __launch_bounds__(256) k_xent_dx_out(const float* __restrict__ a
       for (int q = 0; q < 8; ++q) v[q] += part[q][k * chunks + threadIdx.x];
   }
   if (j >= d) return;
-  const int64_t target = targets[t];
-  if (c >= 0 && target >= 0 && target < V) {
-    // the 8 indices of columns j .. j + 7 are B bytes (one group: its width is a multiple of 32)
-    const uint8_t* row = idx_packed + target * (d * B / 8) + j / 8 * B;
+  if (fix) {
     const TL* g = lut + (target * gpr + (uint32_t)j / (uint32_t)(d / gpr)) * K;
-    const float r = rest[c];
-    uint32_t w = 0u;
-#pragma unroll
-    for (int q = 0; q < B; ++q) w |= (uint32_t)row[q] << (8 * q);
 #pragma unroll
     for (int q = 0; q < 8; ++q) v[q] = __builtin_fmaf(r, to_f32(g[(w >> (B * q)) & (K - 1)]), v[q]);
   }
