@@ -314,9 +314,10 @@ size_t sketch_norm_bwd_workspace(int64_t m, int64_t d);
  * Dtype pairs (x_dtype, lut_dtype): (F16, F16), (BF16, F16), (BF16, BF16)
  * (matrix cores, fp32 logits and statistics; the (BF16, F16) range rule at
  * the top applies); others return SKM_EUNSUPPORTED. m <= 2^22, d <= 2^20, and
- * at most 2^22 tiles of 256 tokens x 256 words (or columns); m == 0 is a no-op. targets 8-byte, other pointers 16-byte aligned. workspace: at least
- * sketch_xent_fwd_workspace(...) bytes (8 bytes per token and 256 words, and
- * 8 to 12 per token).
+ * at most 2^22 tiles of 256 tokens x 256 words (or columns); m == 0 is a no-op.
+ * targets 8-byte, other pointers 16-byte aligned. workspace: at least
+ * sketch_xent_fwd_workspace(...) bytes (8 bytes per token and 256 words, 16 for
+ * few tokens, 8 to 12 per token and for b = 4 up to one 16-bit X).
  */
 int sketch_xent_fwd(const void* X, int x_dtype, const uint8_t* idx_packed, const void* lut, int lut_dtype,
                     const int64_t* targets, int64_t ignore_index,
@@ -334,11 +335,14 @@ size_t sketch_xent_fwd_workspace(int64_t m, int64_t n, int64_t d, int b, int gpr
  *   dLUT = table gradient      [n][gpr][2^b] fp32; accumulate == 1 adds to it
  * each NULL = skip. The logits are recomputed a piece of the vocabulary at a
  * time. dX is the fp32 sum of products with dZ rounded once to the tables'
- * dtype; dLUT takes dZ to at least 17 bits. Both are deterministic (no
- * atomics). workspace: at least sketch_xent_bwd_workspace(...) bytes (up to
- * 256 MiB of dZ, the fp32 dX, and for dLUT one X); need_dx / need_dlut = 0
- * where the output is NULL. With m == 0 and accumulate == 0 dLUT is written as
- * zeros. Dtypes, sizes and alignment as for sketch_xent_fwd.
+ * dtype (the target's term with its fp32 remainder); dLUT takes dZ to 23 bits.
+ * f16 operands hold |dZ| down to 2^-28 of the largest |dloss| (for dLUT of bf16
+ * X: |dloss| times the row's scale of X) at full precision and end at 2^-39 of
+ * it. Both are deterministic (no atomics). workspace: at least
+ * sketch_xent_bwd_workspace(...) bytes (up to 256 MiB of dZ, two or more fp32
+ * dX, and for dLUT one X); need_dx / need_dlut = 0 where the output is NULL.
+ * With m == 0 and accumulate == 0 dLUT is written as zeros. Dtypes, sizes and
+ * alignment as for sketch_xent_fwd.
  */
 int sketch_xent_bwd(const void* X, int x_dtype, const uint8_t* idx_packed, const void* lut, int lut_dtype,
                     const int64_t* targets, int64_t ignore_index, const float* lse, const float* dloss,

@@ -1,6 +1,6 @@
 // Table gradient for operators that own their operands' layout: the cross
 // entropy of a sketched head (a range of the vocabulary at a time, tokens
-// counted on the device, dY as the sum of two 16-bit values) and the backward
+// counted on the device, dY as the sum of two f16 values) and the backward
 // from an 8-bit checkpoint (X in a padded workspace).
 //
 //   dLUT[i][g][c] = sum_{j in g, idx[i][j] = c} sum_t dY[t][i] X[t][j]
@@ -18,7 +18,11 @@
 //     full chunks, one of 128 a quarter of one);
 //   * ragged tokens: the last step's rows of dY past the tokens are read from
 //     16 zero bytes, so every token count takes this kernel.
-// 8192 tokens, 4096 x 11008 in 8 groups, b = 4: see launch_dlut_piece.
+//   * a second addend of dY shares the step's X fragments (k_dlut_piece's TWO).
+// Bound by the K loop's LDS reads (1.5 per MFMA; 1 with two addends). 8192
+// tokens, 4096 x 11008 in 8 groups, b = 4: 717 us as k_gemm_dlut_dma, 603-640 us
+// here (1155-1225 TFLOP/s); two addends, 32000 x 4096, three quarters of 4096
+// tokens: 1447 us with the tokens taken twice, 1219 us (1321 TFLOP/s).
 #pragma once
 
 #include "skm_gemm_bwd.h"

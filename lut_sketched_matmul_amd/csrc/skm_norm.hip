@@ -17,6 +17,12 @@
 // columns' dw and db sums in registers, the next row's loads in flight while a
 // row is worked on; the block's sums go to the workspace and k_norm_reduce adds
 // them per column in block order (deterministic, no atomics).
+//
+// Bound by memory from a few hundred rows on, by launch latency below. 8192 x
+// 4096 bf16: forward with its checkpoint 35 us (4.8 TB/s), layer backward with
+// fp32 dY 48 + 5 us (6 TB/s; a large copy reaches 5.15). 777 x 1001: 7 + 4 us;
+// one row of 4096: 2.9 us. A forward that walks rows like the backward, or that
+// fetches its next row early, measured the same.
 #include <type_traits>
 
 #include "skm_launch.h"

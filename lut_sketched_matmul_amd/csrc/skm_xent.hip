@@ -577,7 +577,9 @@ template <typename T> T* at(void* ws, size_t off) { return reinterpret_cast<T*>(
 bool xent_few(const Problem& p) {
   const int64_t groups = (p.m + 15) / 16, tiles = (p.m + 255) / 256 * ((p.n + XENT_BN - 1) / XENT_BN);
   const double decode = (double)(groups * p.n) * (0.4e-3 + 0.14e-6 * (double)p.d);
+  const int64_t blocks = ((p.n + 15) / 16 + 7) / 8 * 8 * groups;
   return decode <= (double)((tiles + 255) / 256) * (10.0 + 0.021 * (double)p.d) &&
+         blocks <= (int64_t(1) << 22) &&  // (a launch has fewer than 2^32 threads)
          decode_supported(Problem{p.m < 16 ? p.m : 16, p.n, p.d, p.b, p.gpr});
 }
 
