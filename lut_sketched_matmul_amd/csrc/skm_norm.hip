@@ -133,18 +133,46 @@ __device__ __forceinline__ void store_row(T* row, int d, int t, const float (&v)
   }
 }
 
-// a weight or bias row (fp32 or T; NULL gives `fill`)
+// a weight or bias row (fp32 or T; NULL gives `fill`). One assignment per
+// element: with the three sources in branches of their own the compiler merged
+// their stores and kept the array in scratch memory (8192 rows of 4096 columns
+// forward: 6 KB of scratch written per row, 28.6 us instead of 22.6).
 template <typename T, bool AL, int TPR, int NCH>
 __device__ __forceinline__ void load_param(const void* p, int p_f32, int d, int t, float fill, float (&v)[NCH][8]) {
-  if (!p) {
+  const bool f = __is_same(T, float) || p_f32;
+  const char* base = static_cast<const char*>(p);
 #pragma unroll
-    for (int c = 0; c < NCH; ++c)
+  for (int c = 0; c < NCH; ++c) {
+    if constexpr (AL) {
+      const int j0 = col_of<AL, TPR>(t, c, 0);
+      const bool in = p && j0 < d;
+      const u32x4* q = reinterpret_cast<const u32x4*>(base + (int64_t)j0 * (f ? 4 : 2));
+      const u32x4 z = {0u, 0u, 0u, 0u};
+      const u32x4 a = in ? q[0] : z, b = in && f ? q[1] : z;
+      const f32x4 fa = __builtin_bit_cast(f32x4, a), fb = __builtin_bit_cast(f32x4, b);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[c][j] = fill;
-  } else if (p_f32) {
-    load_row<float, AL, TPR, NCH>((const float*)p, d, t, v);
-  } else {
-    load_row<T, AL, TPR, NCH>((const T*)p, d, t, v);
+      for (int j = 0; j < 8; ++j) {
+        float x = j < 4 ? fa[j & 3] : fb[j & 3];
+        if constexpr (!__is_same(T, float)) {
+          const uint32_t w = a[j >> 1];
+          const float h = to_f32(__builtin_bit_cast(T, (uint16_t)(j & 1 ? w >> 16 : w & 0xFFFFu)));
+          x = f ? x : h;
+        }
+        v[c][j] = p ? x : fill;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int col = col_of<AL, TPR>(t, c, j);
+        const bool in = p && col < d;
+        float x = in && f ? reinterpret_cast<const float*>(base)[col] : 0.0f;
+        if constexpr (!__is_same(T, float)) {
+          const float h = in && !f ? to_f32(reinterpret_cast<const T*>(base)[col]) : 0.0f;
+          x = f ? x : h;
+        }
+        v[c][j] = p ? x : fill;
+      }
+    }
   }
 }
 
