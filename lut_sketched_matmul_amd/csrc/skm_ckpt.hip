@@ -7,7 +7,7 @@
 // largest magnitude two quad permutes find), kept in registers between the
 // maximum and the rounding, so every value is read once.
 // Bound by memory: 8192 x 11008 bf16 written in 49 us and read back in 41 (5.6 and
-// 6.7 TB/s of the bytes each has to move; a large copy reaches 5.15). Non-temporal
+// 6.7 TB/s of the bytes each has to move; a large copy reaches 5.15 to 6.2). Non-temporal
 // stores write 8 % faster, but the product that reads the codes next misses them.
 #include "skm_launch.h"
 #include "skm_quant.h"

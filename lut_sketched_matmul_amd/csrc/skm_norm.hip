@@ -19,9 +19,9 @@
 // them per column in block order (deterministic, no atomics).
 //
 // Bound by memory from a few hundred rows on, by launch latency below. 8192 x
-// 4096 bf16: forward with its checkpoint 35 us (4.8 TB/s), layer backward with
-// fp32 dY 48 + 5 us (6 TB/s; a large copy reaches 5.15). 777 x 1001: 7 + 4 us;
-// one row of 4096: 2.9 us. A forward that walks rows like the backward, or that
+// 4096 bf16: forward with its checkpoint 30 us (5.6 TB/s), layer backward with
+// fp32 dY 46 + 5 us (6.2 TB/s; a large copy reaches 5.15 to 6.2). 777 x 1001: 7 + 4 us;
+// one row of 4096: 2.8 us. A forward that walks rows like the backward, or that
 // fetches its next row early, measured the same.
 #include <type_traits>
 
@@ -133,45 +133,42 @@ __device__ __forceinline__ void store_row(T* row, int d, int t, const float (&v)
   }
 }
 
-// a weight or bias row (fp32 or T; NULL gives `fill`). One assignment per
+// chunk c of a weight or bias row (fp32 or T; NULL gives `fill`). One assignment per
 // element: with the three sources in branches of their own the compiler merged
 // their stores and kept the array in scratch memory (8192 rows of 4096 columns
 // forward: 6 KB of scratch written per row, 28.6 us instead of 22.6).
-template <typename T, bool AL, int TPR, int NCH>
-__device__ __forceinline__ void load_param(const void* p, int p_f32, int d, int t, float fill, float (&v)[NCH][8]) {
+template <typename T, bool AL, int TPR>
+__device__ __forceinline__ void load_param(const void* p, int p_f32, int d, int t, int c, float fill, float (&v)[8]) {
   const bool f = __is_same(T, float) || p_f32;
   const char* base = static_cast<const char*>(p);
+  if constexpr (AL) {
+    const int j0 = col_of<AL, TPR>(t, c, 0);
+    const bool in = p && j0 < d;
+    const u32x4* q = reinterpret_cast<const u32x4*>(base + (int64_t)j0 * (f ? 4 : 2));
+    const u32x4 z = {0u, 0u, 0u, 0u};
+    const u32x4 a = in ? q[0] : z, b = in && f ? q[1] : z;
+    const f32x4 fa = __builtin_bit_cast(f32x4, a), fb = __builtin_bit_cast(f32x4, b);
 #pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    if constexpr (AL) {
-      const int j0 = col_of<AL, TPR>(t, c, 0);
-      const bool in = p && j0 < d;
-      const u32x4* q = reinterpret_cast<const u32x4*>(base + (int64_t)j0 * (f ? 4 : 2));
-      const u32x4 z = {0u, 0u, 0u, 0u};
-      const u32x4 a = in ? q[0] : z, b = in && f ? q[1] : z;
-      const f32x4 fa = __builtin_bit_cast(f32x4, a), fb = __builtin_bit_cast(f32x4, b);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float x = j < 4 ? fa[j & 3] : fb[j & 3];
-        if constexpr (!__is_same(T, float)) {
-          const uint32_t w = a[j >> 1];
-          const float h = to_f32(__builtin_bit_cast(T, (uint16_t)(j & 1 ? w >> 16 : w & 0xFFFFu)));
-          x = f ? x : h;
-        }
-        v[c][j] = p ? x : fill;
+    for (int j = 0; j < 8; ++j) {
+      float x = j < 4 ? fa[j & 3] : fb[j & 3];
+      if constexpr (!__is_same(T, float)) {
+        const uint32_t w = a[j >> 1];
+        const float h = to_f32(__builtin_bit_cast(T, (uint16_t)(j & 1 ? w >> 16 : w & 0xFFFFu)));
+        x = f ? x : h;
       }
-    } else {
+      v[j] = p ? x : fill;
+    }
+  } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int col = col_of<AL, TPR>(t, c, j);
-        const bool in = p && col < d;
-        float x = in && f ? reinterpret_cast<const float*>(base)[col] : 0.0f;
-        if constexpr (!__is_same(T, float)) {
-          const float h = in && !f ? to_f32(reinterpret_cast<const T*>(base)[col]) : 0.0f;
-          x = f ? x : h;
-        }
-        v[c][j] = p ? x : fill;
+    for (int j = 0; j < 8; ++j) {
+      const int col = col_of<AL, TPR>(t, c, j);
+      const bool in = p && col < d;
+      float x = in && f ? reinterpret_cast<const float*>(base)[col] : 0.0f;
+      if constexpr (!__is_same(T, float)) {
+        const float h = in && !f ? to_f32(reinterpret_cast<const T*>(base)[col]) : 0.0f;
+        x = f ? x : h;
       }
+      v[j] = p ? x : fill;
     }
   }
 }
@@ -241,18 +238,26 @@ k_norm_fwd(const T* __restrict__ X, const void* __restrict__ w, const void* __re
     rstd[r] = rs;
     if (mean) mean[r] = mu;
   }
-  float p[NCH][8];
-  load_param<T, AL, TPR, NCH>(w, p_f32, d, t, 1.0f, p);
+  // the weights of all chunks together, of longer rows one chunk at a time (fewer
+  // registers: 4096 x 16384 62 -> 52 us, 4096 x 20000 520 -> 160 us)
+  constexpr int STEP = NCH <= 2 ? NCH : 1;
 #pragma unroll
-  for (int c = 0; c < NCH; ++c)
+  for (int c0 = 0; c0 < NCH; c0 += STEP) {
+    float p[STEP][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[c][j] = x[c][j] * rs * p[c][j];
-  if (bias) {
-    load_param<T, AL, TPR, NCH>(bias, p_f32, d, t, 0.0f, p);
+    for (int c = 0; c < STEP; ++c) load_param<T, AL, TPR>(w, p_f32, d, t, c0 + c, 1.0f, p[c]);
 #pragma unroll
-    for (int c = 0; c < NCH; ++c)
+    for (int c = 0; c < STEP; ++c)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[c][j] += p[c][j];
+      for (int j = 0; j < 8; ++j) x[c0 + c][j] = x[c0 + c][j] * rs * p[c][j];
+    if (bias) {
+#pragma unroll
+      for (int c = 0; c < STEP; ++c) load_param<T, AL, TPR>(bias, p_f32, d, t, c0 + c, 0.0f, p[c]);
+#pragma unroll
+      for (int c = 0; c < STEP; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[c0 + c][j] += p[c][j];
+    }
   }
   if (!AL || !codes) {
     store_row<T, AL, TPR, NCH>(Y + r * d, d, t, x);
@@ -275,9 +280,10 @@ k_norm_fwd(const T* __restrict__ X, const void* __restrict__ w, const void* __re
   }
 }
 
-// DYF: dY is fp32 (else T); CK: X is a checkpoint
+// DYF: dY is fp32 (else T); CK: X is a checkpoint. (At least two waves per SIMD:
+// with one, 4096 x 8192 took 50 us instead of 44.)
 template <typename T, bool AL, int TPR, int NCH, bool DYF, bool CK>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, AL && TPR == 256 ? 2 : 1)
 k_norm_bwd(const void* __restrict__ dY, const T* __restrict__ X, const int8_t* __restrict__ codes,
            const uint8_t* __restrict__ scales, const void* __restrict__ w, int p_f32, const float* __restrict__ mean,
            const float* __restrict__ rstd, int64_t m, int d, T* __restrict__ dX, float* __restrict__ part_w,
@@ -306,7 +312,8 @@ k_norm_bwd(const void* __restrict__ dY, const T* __restrict__ X, const int8_t* _
   const int64_t step = (int64_t)gridDim.x * RPB;
   int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
   if (r < m) load(r);
-  load_param<T, AL, TPR, NCH>(w, p_f32, d, t, 1.0f, p);
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) load_param<T, AL, TPR>(w, p_f32, d, t, c, 1.0f, p[c]);
   for (; r < m; r += step) {
     float x[NCH][8], g[NCH][8];
     from_raw<TY, AL, NCH>(rg, g);
@@ -398,7 +405,8 @@ __global__ void __launch_bounds__(1024) k_norm_reduce(const float* __restrict__ 
 }
 
 // (threads per row, chunks per thread) by the row's length: one wave up to
-// 2048 columns, then 256 threads up to 16384, then 1024
+// 2048 columns, then 256 threads up to 8192 and 512 up to 16384, then 1024
+// (which keep part of a backward row's sums in scratch memory)
 struct NormShape {
   int tpr, nch;
 };
@@ -408,7 +416,7 @@ NormShape shape_of(int64_t d) {
   if (d <= 2048) return {64, 4};
   if (d <= 4096) return {256, 2};
   if (d <= 8192) return {256, 4};
-  if (d <= 16384) return {256, 8};
+  if (d <= 16384) return {512, 4};
   return {1024, 8};
 }
 
@@ -422,9 +430,9 @@ hipError_t with_shape(int64_t d, F&& f) {
   }
   if (s.tpr == 256) {
     if (s.nch == 2) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
-    if (s.nch == 4) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
-    return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 8>{});
+    return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
   }
+  if (s.tpr == 512) return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 4>{});
   return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 8>{});
 }
 
