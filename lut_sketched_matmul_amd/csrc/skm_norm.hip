@@ -99,20 +99,20 @@ __device__ __forceinline__ void from_raw(const RawRow<T, AL, NCH>& r, float (&v)
     }
   }
 }
-// the same for a checkpoint's row (AL only)
+// the same for a checkpoint's row (AL only), `row` values from its start
 template <int NCH> struct RawCodes {
   u32x2 v[NCH];
   uint32_t s[NCH];
 };
 template <int TPR, int NCH>
-__device__ __forceinline__ void load_codes(const int8_t* codes, const uint8_t* scales, int64_t r, int d, int t,
+__device__ __forceinline__ void load_codes(const int8_t* codes, const uint8_t* scales, int64_t row, int d, int t,
                                            RawCodes<NCH>& o) {
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
     const int j0 = col_of<true, TPR>(t, c, 0);
     const bool in = j0 < d;
-    o.v[c] = in ? *reinterpret_cast<const u32x2*>(codes + r * d + j0) : u32x2{0u, 0u};
-    o.s[c] = in ? scales[(r * d + j0) >> 5] : 1u;
+    o.v[c] = in ? *reinterpret_cast<const u32x2*>(codes + row + j0) : u32x2{0u, 0u};
+    o.s[c] = in ? scales[(row + j0) >> 5] : 1u;
   }
 }
 
@@ -304,7 +304,7 @@ k_norm_bwd(const void* __restrict__ dY, const T* __restrict__ X, const int8_t* _
   float mu = 0.0f, rs = 0.0f;
   auto load = [&](int64_t r) {
     load_raw<TY, AL, TPR, NCH>((const TY*)dY + r * d, d, t, rg);
-    if constexpr (CK) load_codes<TPR, NCH>(codes, scales, r, d, t, rc);
+    if constexpr (CK) load_codes<TPR, NCH>(codes, scales, r * d, d, t, rc);
     else load_raw<T, AL, TPR, NCH>(X + r * d, d, t, rx);
     mu = mean ? mean[r] : 0.0f;
     rs = rstd[r];
@@ -372,6 +372,89 @@ k_norm_bwd(const void* __restrict__ dY, const T* __restrict__ X, const int8_t* _
   if (part_b) put(part_b, ab);
 }
 
+// Rows of more than 16384 columns: a thread's columns and their sums do not fit
+// its registers (in scratch memory 4096 x 20000 took 3.5 ms). dX reads its row
+// twice, the second time from the caches; dw and db come from a pass by columns.
+
+// x and g = dy of 8 columns of chunk c of row r, as fp32
+template <typename T, bool AL, int TPR, bool DYF, bool CK>
+__device__ __forceinline__ void load_pair(const void* dY, const T* X, const int8_t* codes, const uint8_t* scales,
+                                          int64_t r, int d, int t, int c, float (&x)[1][8], float (&g)[1][8]) {
+  typedef std::conditional_t<DYF, float, T> TY;
+  const int base = c * 8 * TPR;
+  load_row<TY, AL, TPR, 1>((const TY*)dY + r * d + base, d - base, t, g);
+  if constexpr (CK) {
+    RawCodes<1> q;
+    load_codes<TPR, 1>(codes + base, scales + base / 32, r * d, d - base, t, q);
+    ckpt_unpack8(q.v[0], q.s[0], x[0]);
+  } else {
+    load_row<T, AL, TPR, 1>(X + r * d + base, d - base, t, x);
+  }
+}
+
+template <typename T, bool AL, bool DYF, bool CK>
+__global__ void __launch_bounds__(1024)
+k_norm_bwd_wide(const void* __restrict__ dY, const T* __restrict__ X, const int8_t* __restrict__ codes,
+                const uint8_t* __restrict__ scales, const void* __restrict__ w, int p_f32,
+                const float* __restrict__ mean, const float* __restrict__ rstd, int64_t m, int d,
+                T* __restrict__ dX) {
+  constexpr int TPR = 1024;
+  __shared__ float red[2 * (TPR / 64)];
+  const int t = (int)threadIdx.x, chunks = (d + 8 * TPR - 1) / (8 * TPR);
+  const float inv_d = 1.0f / (float)d;
+  for (int64_t r = blockIdx.x; r < m; r += gridDim.x) {
+    const float mu = mean ? mean[r] : 0.0f, rs = rstd[r];
+    float s1 = 0.0f, s2 = 0.0f;  // sums of g xh and of g, g = dy w
+    for (int c = 0; c < chunks; ++c) {
+      float x[1][8], g[1][8], p[8];
+      load_pair<T, AL, TPR, DYF, CK>(dY, X, codes, scales, r, d, t, c, x, g);
+      load_param<T, AL, TPR>(w, p_f32, d, t, c, 1.0f, p);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float gw = g[0][j] * p[j];  // (past the row's end dy is 0)
+        s1 = __builtin_fmaf(gw, (x[0][j] - mu) * rs, s1);
+        s2 += gw;
+      }
+    }
+    row_sum2<TPR>(s1, s2, red);
+    s1 *= inv_d;
+    s2 = mean ? s2 * inv_d : 0.0f;
+    for (int c = 0; c < chunks; ++c) {
+      float x[1][8], g[1][8], p[8];
+      load_pair<T, AL, TPR, DYF, CK>(dY, X, codes, scales, r, d, t, c, x, g);
+      load_param<T, AL, TPR>(w, p_f32, d, t, c, 1.0f, p);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[0][j] = rs * (g[0][j] * p[j] - s2 - (x[0][j] - mu) * rs * s1);
+      store_row<T, AL, TPR, 1>(dX + r * d + c * 8 * TPR, d - c * 8 * TPR, t, x);
+    }
+  }
+}
+
+// dw and db of 2048 columns over the rows of slab blockIdx.y
+template <typename T, bool AL, bool DYF, bool CK>
+__global__ void __launch_bounds__(256)
+k_norm_cols(const void* __restrict__ dY, const T* __restrict__ X, const int8_t* __restrict__ codes,
+            const uint8_t* __restrict__ scales, const float* __restrict__ mean, const float* __restrict__ rstd, int64_t m,
+            int d, float* __restrict__ part_w, float* __restrict__ part_b) {
+  constexpr int TPR = 256;
+  const int t = (int)threadIdx.x, c = (int)blockIdx.x, base = c * 8 * TPR;
+  const int64_t per = (m + gridDim.y - 1) / gridDim.y, r0 = per * blockIdx.y, r1 = r0 + per < m ? r0 + per : m;
+  float aw[1][8] = {}, ab[1][8] = {};
+#pragma unroll 4
+  for (int64_t r = r0; r < r1; ++r) {
+    float x[1][8], g[1][8];
+    load_pair<T, AL, TPR, DYF, CK>(dY, X, codes, scales, r, d, t, c, x, g);
+    const float mu = mean ? mean[r] : 0.0f, rs = rstd[r];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      aw[0][j] = __builtin_fmaf(g[0][j], (x[0][j] - mu) * rs, aw[0][j]);
+      ab[0][j] += g[0][j];
+    }
+  }
+  if (part_w) store_row<float, AL, TPR, 1>(part_w + (int64_t)blockIdx.y * d + base, d - base, t, aw);
+  if (part_b) store_row<float, AL, TPR, 1>(part_b + (int64_t)blockIdx.y * d + base, d - base, t, ab);
+}
+
 // out[j] = (accumulate ? out[j] : 0) + the sum over the blocks' rows of part:
 // 64 columns per block, 16 slices of rows summed apart and then in slice order.
 // blockIdx.y: dw, db (the one that is wanted when there is one)
@@ -406,10 +489,10 @@ __global__ void __launch_bounds__(1024) k_norm_reduce(const float* __restrict__ 
 
 // (threads per row, chunks per thread) by the row's length: one wave up to
 // 2048 columns, then 256 threads up to 8192 and 512 up to 16384, then 1024
-// (which keep part of a backward row's sums in scratch memory)
 struct NormShape {
   int tpr, nch;
 };
+constexpr int64_t WIDE = 16384;  // beyond: k_norm_bwd_wide, k_norm_cols
 NormShape shape_of(int64_t d) {
   if (d <= 512) return {64, 1};
   if (d <= 1024) return {64, 2};
@@ -460,6 +543,7 @@ hipError_t norm_fwd_t(const NormArgs& a, const T* X, T* Y, float* mean, float* r
 // Blocks of the backward walk, each with one partial row of dw and of db: at
 // most two per CU.
 int64_t bwd_blocks(int64_t m, int64_t d) {
+  if (d > WIDE) return m < 64 ? m : 64;  // slabs of k_norm_cols
   const int rpb = shape_of(d).tpr < 256 ? 256 / shape_of(d).tpr : 1;
   const int64_t need = (m + rpb - 1) / rpb;
   return need < 512 ? need : 512;
@@ -476,8 +560,31 @@ struct NormBwd {
   float *part_w, *part_b;
 };
 
+template <typename T, bool AL, bool DYF, bool CK>
+hipError_t norm_bwd_wide(const NormArgs& a, const NormBwd& q, hipStream_t s) {
+  if (q.dX) {
+    hipLaunchKernelGGL((k_norm_bwd_wide<T, AL, DYF, CK>), dim3((unsigned)(a.m < 512 ? a.m : 512)), dim3(1024), 0, s, q.dY,
+                       (const T*)q.X, q.codes, q.scales, a.w, a.p_f32, q.mean, q.rstd, a.m, (int)a.d, (T*)q.dX);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (!q.part_w && !q.part_b) return hipSuccess;
+  hipLaunchKernelGGL((k_norm_cols<T, AL, DYF, CK>), dim3((unsigned)((a.d + 2047) / 2048), (unsigned)bwd_blocks(a.m, a.d)),
+                     dim3(256), 0, s, q.dY, (const T*)q.X, q.codes, q.scales, q.mean, q.rstd, a.m, (int)a.d, q.part_w,
+                     q.part_b);
+  return hipGetLastError();
+}
+
 template <typename T>
 hipError_t norm_bwd_t(const NormArgs& a, const NormBwd& q, hipStream_t s) {
+  constexpr bool F = __is_same(T, float);  // (an fp32 dY of fp32 rows is of their own type)
+  const bool f = q.dy_f32 && !F;
+  if (a.d > WIDE) {
+    if (q.codes) return f ? norm_bwd_wide<T, true, !F, true>(a, q, s) : norm_bwd_wide<T, true, false, true>(a, q, s);
+    if (a.d % 8 == 0)
+      return f ? norm_bwd_wide<T, true, !F, false>(a, q, s) : norm_bwd_wide<T, true, false, false>(a, q, s);
+    return f ? norm_bwd_wide<T, false, !F, false>(a, q, s) : norm_bwd_wide<T, false, false, false>(a, q, s);
+  }
   return with_shape(a.d, [&](auto tpr, auto nch) {
     constexpr int TPR = decltype(tpr)::value, NCH = decltype(nch)::value;
     auto go = [&](auto kern) {
@@ -486,12 +593,15 @@ hipError_t norm_bwd_t(const NormArgs& a, const NormBwd& q, hipStream_t s) {
                          q.part_w, q.part_b);
       return hipGetLastError();
     };
-    constexpr bool F = __is_same(T, float);  // (an fp32 dY of fp32 rows is of their own type)
-    const bool f = q.dy_f32 && !F;
-    if (q.codes) return f ? go(k_norm_bwd<T, true, TPR, NCH, !F, true>) : go(k_norm_bwd<T, true, TPR, NCH, false, true>);
-    if (a.d % 8 == 0)
-      return f ? go(k_norm_bwd<T, true, TPR, NCH, !F, false>) : go(k_norm_bwd<T, true, TPR, NCH, false, false>);
-    return f ? go(k_norm_bwd<T, false, TPR, NCH, !F, false>) : go(k_norm_bwd<T, false, TPR, NCH, false, false>);
+    if constexpr (TPR == 1024) {
+      return hipErrorNotSupported;  // (no such call comes here)
+    } else {
+      if (q.codes)
+        return f ? go(k_norm_bwd<T, true, TPR, NCH, !F, true>) : go(k_norm_bwd<T, true, TPR, NCH, false, true>);
+      if (a.d % 8 == 0)
+        return f ? go(k_norm_bwd<T, true, TPR, NCH, !F, false>) : go(k_norm_bwd<T, true, TPR, NCH, false, false>);
+      return f ? go(k_norm_bwd<T, false, TPR, NCH, !F, false>) : go(k_norm_bwd<T, false, TPR, NCH, false, false>);
+    }
   });
 }
 

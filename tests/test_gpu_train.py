@@ -236,6 +236,13 @@ def test_norm_forward_backward(m, d, dtype, kind, params):
         within(to_f64(w1), to_f64(dw) + 1.0, 8 * U * (1.0 + np.abs(to_f64(dw))), "accumulate")
 
 
+@pytest.mark.parametrize("m,d,dtype,kind", [(600, 16392, "bf16", "layer"), (70, 16385, "f16", "rms"),
+                                            (130, 8232, "bf16", "layer")])
+def test_norm_many_long_rows(m, d, dtype, kind):
+    """Blocks that walk several long rows, and slabs of several rows per column sum."""
+    test_norm_forward_backward(m, d, dtype, kind, "f32")
+
+
 @pytest.mark.parametrize("kind", ["layer", "rms"])
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("m,d", [(1, 32), (5, 96), (3, 2048), (6, 4096), (2, 8224), (2, 17024)])
