@@ -388,8 +388,8 @@ hipError_t dlut_piece_launch(const TX* dY, const TX* X, const uint8_t* idx, cons
   const DlutSplit sp = dlut_split_of(p);
   const int64_t count = p.n * p.gpr * p.k();
   const bool split = sp.parts() > 1;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(rb * p.gpr * sp.parts())), dim3(512), DpStage<TWO>::LDS, s, dY, X, idx, p.m, p.n,
-                     p.d, p.gpr, gband, split ? part : dLUT, split ? 0 : accumulate, sp.tsplits, sp.csplits,
+  hipLaunchKernelGGL(kern, dim3((unsigned)(rb * p.gpr * sp.parts())), dim3(512), DpStage<TWO>::LDS, s, dY, X, idx, p.m,
+                     p.n, p.d, p.gpr, gband, split ? part : dLUT, split ? 0 : accumulate, sp.tsplits, sp.csplits,
                      sp.tokens, sp.cols, count, pa);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && split) e = dlut_reduce(part, sp.parts(), count, dLUT, accumulate, s);

@@ -434,8 +434,8 @@ k_norm_bwd_wide(const void* __restrict__ dY, const T* __restrict__ X, const int8
 template <typename T, bool AL, bool DYF, bool CK>
 __global__ void __launch_bounds__(256)
 k_norm_cols(const void* __restrict__ dY, const T* __restrict__ X, const int8_t* __restrict__ codes,
-            const uint8_t* __restrict__ scales, const float* __restrict__ mean, const float* __restrict__ rstd, int64_t m,
-            int d, float* __restrict__ part_w, float* __restrict__ part_b) {
+            const uint8_t* __restrict__ scales, const float* __restrict__ mean, const float* __restrict__ rstd,
+            int64_t m, int d, float* __restrict__ part_w, float* __restrict__ part_b) {
   constexpr int TPR = 256;
   const int t = (int)threadIdx.x, c = (int)blockIdx.x, base = c * 8 * TPR;
   const int64_t per = (m + gridDim.y - 1) / gridDim.y, r0 = per * blockIdx.y, r1 = r0 + per < m ? r0 + per : m;
@@ -563,14 +563,14 @@ struct NormBwd {
 template <typename T, bool AL, bool DYF, bool CK>
 hipError_t norm_bwd_wide(const NormArgs& a, const NormBwd& q, hipStream_t s) {
   if (q.dX) {
-    hipLaunchKernelGGL((k_norm_bwd_wide<T, AL, DYF, CK>), dim3((unsigned)(a.m < 512 ? a.m : 512)), dim3(1024), 0, s, q.dY,
-                       (const T*)q.X, q.codes, q.scales, a.w, a.p_f32, q.mean, q.rstd, a.m, (int)a.d, (T*)q.dX);
+    hipLaunchKernelGGL((k_norm_bwd_wide<T, AL, DYF, CK>), dim3((unsigned)(a.m < 512 ? a.m : 512)), dim3(1024), 0, s,
+                       q.dY, (const T*)q.X, q.codes, q.scales, a.w, a.p_f32, q.mean, q.rstd, a.m, (int)a.d, (T*)q.dX);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (!q.part_w && !q.part_b) return hipSuccess;
-  hipLaunchKernelGGL((k_norm_cols<T, AL, DYF, CK>), dim3((unsigned)((a.d + 2047) / 2048), (unsigned)bwd_blocks(a.m, a.d)),
-                     dim3(256), 0, s, q.dY, (const T*)q.X, q.codes, q.scales, q.mean, q.rstd, a.m, (int)a.d, q.part_w,
+  const dim3 grid((unsigned)((a.d + 2047) / 2048), (unsigned)bwd_blocks(a.m, a.d));
+  hipLaunchKernelGGL((k_norm_cols<T, AL, DYF, CK>), grid, dim3(256), 0, s, q.dY, (const T*)q.X, q.codes, q.scales, q.mean, q.rstd, a.m, (int)a.d, q.part_w,
                      q.part_b);
   return hipGetLastError();
 }

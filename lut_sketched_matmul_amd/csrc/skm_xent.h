@@ -39,8 +39,9 @@
 //
 // Tokens whose target is ignore_index are left out: the index kernel lists the
 // others, and every kernel works on that list with its length read on the
-// device. Nothing is read from an ignored token's row of X (it may hold
-// anything); its loss, lse and dX are zeros.
+// device. (The few-token kernel computes their logits and drops them.) No value
+// of an ignored token's row of X, which may hold anything, reaches a result; its
+// loss, lse and dX are zeros.
 #pragma once
 
 #include "skm_common.h"

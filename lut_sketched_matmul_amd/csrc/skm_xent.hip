@@ -369,7 +369,8 @@ template <int B, typename TX, typename TL>
 __global__ void __launch_bounds__(256) k_xent_dx_out(const float* __restrict__ acc, int lanes,
                                                      const int32_t* __restrict__ pos,
                                                      const XentHead* __restrict__ head,
-                                                     const float* __restrict__ rest, const int64_t* __restrict__ targets,
+                                                     const float* __restrict__ rest,
+                                                     const int64_t* __restrict__ targets,
                                                      const uint8_t* __restrict__ idx_packed,
                                                      const TL* __restrict__ lut, int64_t V, int64_t d, int gpr,
                                                      TX* __restrict__ dX) {
@@ -681,8 +682,8 @@ hipError_t launch_xent_bwd(const XentArgs& a, const float* lse, const float* dlo
     e = f.few ? xent_few_grad(g, out, pos, s) : xent_grad(g, out, s);
     if (e == hipSuccess && dX) {
       // every range of the first piece is written; later pieces add to some or all
-      e = launch_dx_piece(f.own ? dxv : hi, a.lut_dtype, idx, lut, a.lut_dtype, q, acc, nullptr, &head->count, ld, v0 > 0,
-                          {}, &head->dx, f.dx_blocks, s);
+      e = launch_dx_piece(f.own ? dxv : hi, a.lut_dtype, idx, lut, a.lut_dtype, q, acc, nullptr, &head->count, ld,
+                          v0 > 0, {}, &head->dx, f.dx_blocks, s);
     }
     if (e == hipSuccess && dLUT) {
       const Problem qc{f.cap, n, p.d, p.b, p.gpr};
