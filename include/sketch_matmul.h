@@ -335,10 +335,12 @@ size_t sketch_xent_fwd_workspace(int64_t m, int64_t n, int64_t d, int b, int gpr
  *   dLUT = table gradient      [n][gpr][2^b] fp32; accumulate == 1 adds to it
  * each NULL = skip. The logits are recomputed a piece of the vocabulary at a
  * time. dX is the fp32 sum of products with dZ rounded once to the tables'
- * dtype (the target's term with its fp32 remainder); dLUT takes dZ to 23 bits.
- * f16 operands hold |dZ| down to 2^-28 of the largest |dloss| (for dLUT of bf16
- * X: |dloss| times the row's scale of X) at full precision and end at 2^-39 of
- * it. Both are deterministic (no atomics). workspace: at least
+ * dtype (the target's term with its fp32 remainder; f16 operands hold |dZ| down
+ * to 2^-28 of the largest |dloss| at full precision and end at 2^-39 of it).
+ * dLUT takes dZ to 2^-23 of itself, or to 2^-39 of the largest |dloss| where
+ * that is more; for bf16 X the tokens are compared by |dloss| times the largest
+ * |X| of their row, and X is taken exactly down to 2^-28 of that largest |X|
+ * and to 2^-39 of it below. Both are deterministic (no atomics). workspace: at least
  * sketch_xent_bwd_workspace(...) bytes (up to 256 MiB of dZ, two or more fp32
  * dX, and for dLUT one X); need_dx / need_dlut = 0 where the output is NULL.
  * With m == 0 and accumulate == 0 dLUT is written as zeros. Dtypes, sizes and

@@ -115,11 +115,16 @@ __device__ __forceinline__ int lane_id() { return (int)(threadIdx.x & 63); }
 // Both scale factors are normal fp32 numbers for every e in that range.
 constexpr bool scaled_pair(bool x_is_bf16, bool lut_is_f16) { return x_is_bf16 && lut_is_f16; }
 
+// The second case for every row: e is then continuous in the row's magnitude,
+// which matters where rows meet under one common scale (the table gradient of
+// the cross entropy, skm_xent.h).
+__device__ __forceinline__ int row_top_exp_of(uint32_t absmax_bits) {
+  const int e = (int)(absmax_bits >> 7) - 141;
+  return e < -126 ? -126 : (e > 113 ? 113 : e);
+}
 __device__ __forceinline__ int row_exp_of(uint32_t absmax_bits) {
   const int E = (int)(absmax_bits >> 7);
-  if (E >= 125 && E <= 142) return 0;
-  const int e = E - 141;
-  return e < -126 ? -126 : (e > 113 ? 113 : e);
+  return E >= 125 && E <= 142 ? 0 : row_top_exp_of(absmax_bits);
 }
 
 // Rows of exponent -101 <= e <= 0 (and no others in a block) may be scaled by

@@ -72,8 +72,10 @@ hipError_t launch_decode_sets(const void* X, int x_dtype, const uint8_t* idx, co
                               const int32_t* lut_set, int n_sets, const Problem& p, void* Y, hipStream_t s);
 
 // per-row exponents of the bf16 -> f16 operand prescale (skm_common.h) of a
-// bf16 matrix A [rows][cols] into e [rows]
-hipError_t launch_row_exp(const void* A, int64_t rows, int64_t cols, int32_t* e, hipStream_t s);
+// bf16 matrix A [rows][cols] into e [rows] and those without the window of
+// e = 0 into top [rows] (NULL = not wanted)
+hipError_t launch_row_exp(const void* A, int64_t rows, int64_t cols, int32_t* e, hipStream_t s,
+                          int32_t* top = nullptr);
 
 // prefill / training forward: m > 16, tiled matrix-core GEMM. rexp: the row
 // exponents of X (read only for bf16 activations with f16 tables)

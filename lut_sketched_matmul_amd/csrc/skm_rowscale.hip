@@ -1,8 +1,8 @@
-// Row exponents of the per-row power-of-two prescale (see skm_common.h):
-// e[r] = clamp(E - 141, -126, 113), E the biased exponent of the largest
-// |value| of row r of a bf16 matrix A [rows][cols]. Computed once per call
-// into the caller's workspace for the kernels that convert bf16 activations
-// (X of the forward GEMM, dY of dX) to f16 matrix-core operands.
+// Row exponents of the per-row power-of-two prescale (see skm_common.h) of a
+// bf16 matrix A [rows][cols]: row_exp_of in e, row_top_exp_of in top (NULL =
+// not wanted). Computed once per call into the caller's workspace for the
+// kernels that convert bf16 activations (X of the forward GEMM, dY of dX, X
+// and dZ of the cross entropy's dLUT) to f16 matrix-core operands.
 //
 // One wave per row; HBM-bound (the row is read once, 2 bytes per element).
 #include "skm_common.h"
@@ -14,7 +14,8 @@ namespace {
 
 template <bool VEC>
 __global__ void __launch_bounds__(256) k_row_exp(const uint16_t* __restrict__ A, int64_t rows, int64_t cols,
-                                                  int32_t* __restrict__ e) {
+                                                  int32_t* __restrict__ e,
+                                                  int32_t* __restrict__ top) {
   const int lane = lane_id();
   const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (r >= rows) return;  // wave-uniform
@@ -49,17 +50,20 @@ __global__ void __launch_bounds__(256) k_row_exp(const uint16_t* __restrict__ A,
     const uint32_t v = (uint32_t)__shfl_xor((int)mx, o, 64);
     mx = mx > v ? mx : v;
   }
-  if (lane == 0) e[r] = row_exp_of(mx);
+  if (lane == 0) {
+    if (e) e[r] = row_exp_of(mx);
+    if (top) top[r] = row_top_exp_of(mx);
+  }
 }
 
 }  // namespace
 
-hipError_t launch_row_exp(const void* A, int64_t rows, int64_t cols, int32_t* e, hipStream_t s) {
+hipError_t launch_row_exp(const void* A, int64_t rows, int64_t cols, int32_t* e, hipStream_t s, int32_t* top) {
   const dim3 grid((unsigned)((rows + 3) / 4));
   if (cols % 8 == 0)
-    hipLaunchKernelGGL(k_row_exp<true>, grid, dim3(256), 0, s, (const uint16_t*)A, rows, cols, e);
+    hipLaunchKernelGGL(k_row_exp<true>, grid, dim3(256), 0, s, (const uint16_t*)A, rows, cols, e, top);
   else
-    hipLaunchKernelGGL(k_row_exp<false>, grid, dim3(256), 0, s, (const uint16_t*)A, rows, cols, e);
+    hipLaunchKernelGGL(k_row_exp<false>, grid, dim3(256), 0, s, (const uint16_t*)A, rows, cols, e, top);
   return hipGetLastError();
 }
 

@@ -23,13 +23,17 @@
 // remainder in fp32 and k_xent_dx_out adds it times the target's weights. dLUT
 // is fp32: it takes dZ as the sum hi + lo of two f16 values, which leaves 2^-23
 // of each term. f16 rather than X's dtype, since two bf16 values leave 2^-17;
-// bf16 rows of X are prescaled by 2^-e to f16 as for a forward pass
-// (skm_common.h) and their rows of dZ multiplied by 2^e. (dX has a form of its
-// own then: a row of X near zero has no gradient to give to the tables, but
-// takes one itself.)
+// bf16 rows of X are scaled by 2^-e to f16, every row so that its largest value
+// lies in [2^14, 2^15) (row_top_exp_of), and their rows of dZ by 2^e: a row's
+// dZ is as large as what the row gives to the tables. (The logits' exponents
+// jump from 0 to -17 where a row's largest value falls below 2^-2; rows on
+// both sides under one scale lost up to 17 of the 23 bits.) dX has a form of
+// its own then: a row of X near zero has no gradient to give to the tables, but
+// takes one itself.
 // The f16 forms are scaled by one power of two that puts the largest row
-// factor, |dloss| 2^e or |dloss|, into [2^14, 2^15), so that f16 holds a
-// softmax value down to 2^-28 of the largest gradient at full precision; the
+// factor, |dloss| 2^e or |dloss|, into [2^14, 2^15): a term of dLUT keeps 2^-23
+// of itself or 2^-39 of that factor, whichever is more, and dX's operand holds
+// a softmax value down to 2^-28 of the largest |dloss| at full precision; the
 // results are scaled back in fp32 (exact). bf16 dZ (dX with bf16 tables) needs
 // no scale.
 //

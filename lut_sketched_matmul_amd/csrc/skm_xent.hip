@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(1024) k_xent_mean(const float* __restrict__ lo
 // ---- backward --------------------------------------------------------------------------
 
 // Xc[c] = X[rows[c]] in f16 for the listed tokens (bf16 rows prescaled by 2^-e,
-// e = zexp), zeros up to the next multiple of 32 (whole steps of the table
+// e = zexp: their largest value then lies in [2^14, 2^15)), zeros up to the next multiple of 32 (whole steps of the table
 // gradient's tiles); 16 bytes per thread and round
 template <typename TX>
 __global__ void __launch_bounds__(256) k_xent_gather(const TX* __restrict__ X, const int32_t* __restrict__ rows,
@@ -503,8 +503,8 @@ struct BwdPlan {
   DxShape dx;
   bool few, streams;
   bool own;            // dX's operand is a form of its own
-  bool exps;           // row exponents of X are needed: logits' or dLUT's f16 operands of bf16 rows
-  size_t rows, pos, rexp, hi, lo, dxv, rest, acc, xc, xp, part, bytes;
+  bool rexps, zexps;   // bf16 rows in f16: exponents of the logits' operand rows, of dLUT's
+  size_t rows, pos, rexp, zexp, hi, lo, dxv, rest, acc, xc, xp, part, bytes;
 };
 
 // The pieces: dZ of a piece takes 2 bytes per (token, word) and form, and is
@@ -516,7 +516,8 @@ BwdPlan bwd_plan(const Problem& p, int x_dtype, int lut_dtype, bool need_dx, boo
   BwdPlan f;
   f.own = x_dtype == DT_BF16;
   const bool has_hi = need_dlut || !f.own, has_dxv = need_dx && f.own;
-  f.exps = x_dtype == DT_BF16 && (need_dlut || lut_dtype == DT_F16);
+  f.rexps = mixed(x_dtype, lut_dtype);
+  f.zexps = x_dtype == DT_BF16 && need_dlut;
   const int forms = (has_hi ? 1 : 0) + (need_dlut ? 1 : 0) + (has_dxv ? 1 : 0);
   f.few = xent_few(p);
   f.streams = !f.few && xent_streams(p);
@@ -542,7 +543,8 @@ BwdPlan bwd_plan(const Problem& p, int x_dtype, int lut_dtype, bool need_dx, boo
   const size_t dz = (size_t)f.cap * (size_t)((n1 + 7) / 8 * 8) * 2;
   f.rows = take(true, (size_t)p.m * 4);
   f.pos = take(true, (size_t)p.m * 4);
-  f.rexp = take(f.exps, (size_t)p.m * 4);
+  f.rexp = take(f.rexps, (size_t)p.m * 4);
+  f.zexp = take(f.zexps, (size_t)p.m * 4);
   f.rest = take(need_dx, (size_t)p.m * 4);
   f.hi = take(has_hi, dz);
   f.lo = take(need_dlut, dz);
@@ -640,7 +642,9 @@ hipError_t launch_xent_bwd(const XentArgs& a, const float* lse, const float* dlo
   XentHead* head = at<XentHead>(ws, 0);
   int32_t* rows = at<int32_t>(ws, f.rows);
   int32_t* pos = at<int32_t>(ws, f.pos);
-  int32_t* rexp = f.exps ? at<int32_t>(ws, f.rexp) : nullptr;
+  int32_t* rexp = f.rexps ? at<int32_t>(ws, f.rexp) : nullptr;
+  // dLUT's operands: bf16 rows of X are scaled by 2^-e, their rows of dZ by 2^e
+  int32_t* zexp = f.zexps ? at<int32_t>(ws, f.zexp) : nullptr;
   float* acc = dX ? at<float>(ws, f.acc) : nullptr;
   float* rest = dX ? at<float>(ws, f.rest) : nullptr;
   void* hi = dLUT || !f.own ? at<void>(ws, f.hi) : nullptr;
@@ -648,10 +652,10 @@ hipError_t launch_xent_bwd(const XentArgs& a, const float* lse, const float* dlo
   void* dxv = dX && f.own ? at<void>(ws, f.dxv) : nullptr;
   void* xc = dLUT ? at<void>(ws, f.xc) : nullptr;
   void* xp = f.streams ? at<void>(ws, f.xp) : nullptr;
-  // dLUT's operands: bf16 rows of X are scaled by 2^-e, their rows of dZ by 2^e
-  const int32_t* zexp = dLUT ? rexp : nullptr;
   hipError_t e = hipSuccess;
-  if (rexp) e = launch_row_exp(a.X, p.m, p.d, rexp, s);
+  // (xent_rows and the staging decode find the logits' exponents themselves)
+  int32_t* find = f.streams || (f.few && xent_decode_stages(p)) ? nullptr : rexp;
+  if (find || zexp) e = launch_row_exp(a.X, p.m, p.d, find, s, zexp);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k_xent_index<true>, dim3(1), dim3(1024), 0, s, a.targets, a.ignore, p.m, dloss, zexp, head, rows,
                      pos, f.dx, nullptr, nullptr);

@@ -1,0 +1,95 @@
+"""GPU tests of what the training operators keep of their operands: bounds derived term by term, in float64.
+
+U = 2^-24 is half a step of fp32, h(t) = finfo(t).eps / 2 half a relative step of a 16-bit type. An f16 operand that
+was scaled so that the largest factor lies in [2^14, 2^15) is off by h(f16) of itself or, below 2^-14, by 2^-25, which
+is at most 2^-39 of that factor.
+"""
+import numpy as np
+import pytest
+
+import oracle
+from lut_sketched_matmul_amd import synthetic as syn
+from oracle import train_oracle as to
+
+from gpu_util import to_dev, to_f64
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+H = {"f16": 2.0 ** -11, "bf16": 2.0 ** -8}
+TINY = {"f16": 2.0 ** -25, "bf16": 0.0}
+PAIRS = [("f16", "f16"), ("bf16", "f16"), ("bf16", "bf16")]
+
+
+def skm():
+    import lut_sketched_matmul_amd as m
+    return m
+
+
+def torch():
+    import torch as _t
+    return _t
+
+
+def head(name, V, d, b, gpr, ldt, sigma=0.05):
+    idx = syn.random_packed_indices(name + "/i", V, d, b)
+    lut = syn.random_lut(name + "/l", V, gpr, b, sigma, ldt)
+    W = oracle.dequantize(idx, syn.to_float64(lut, ldt), d, b, gpr)
+    return to_dev(idx, "u8"), to_dev(lut, ldt), idx, W
+
+
+def inputs(x, io):
+    s = syn.to_storage(x.astype(np.float32), io)
+    return to_dev(s, io), syn.to_float64(s, io)
+
+
+def within(got, ref, bound, what):
+    assert got.shape == ref.shape and np.isfinite(got).all(), what
+    off = np.abs(got - ref) - bound
+    assert off.max() <= 0.0, f"{what}: {int((off > 0).sum())} of {off.size} over the bound by up to {off.max():.3e}"
+
+
+def logit_error(x, W, io, ldt, d):
+    """Of every token's logits: fp32 sums of d products, and f16 operands of prescaled bf16 rows."""
+    dz = (d / 16 + 24) * U * (np.abs(x) @ np.abs(W).T).max(1)
+    if (io, ldt) == ("bf16", "f16"):
+        dz = dz + 2.0 ** -23 * np.abs(x).max(1) * np.abs(W).sum(1).max()
+    return dz
+
+
+def dz_error(P, w, lse, dz, T):
+    """Of dZ in fp32: the softmax's argument and exp, relative to the softmax; the target's also the subtraction."""
+    e = w[:, None] * P * (dz + 2 * U * np.abs(lse) + 60 * U)[:, None]
+    e[np.arange(len(T)), T] += 4 * U * w
+    return e
+
+
+@pytest.mark.parametrize("ldt", ["f16", "bf16"])
+@pytest.mark.parametrize("m", [24, 300])
+@pytest.mark.parametrize("big", ["half", "one"])
+def test_table_gradient_of_rows_around_a_quarter(m, ldt, big):
+    """Every bf16 row gives the tables its dZ to 22 bits, whether its largest value lies just below or above 2^-2."""
+    t = torch()
+    V, d, b, gpr = 12000, 64, 4, 1
+    name = f"quarter/{m}/{ldt}"
+    gi, gl, idx, W = head(name, V, d, b, gpr, ldt)
+    x = syn.to_float64(syn.random_normal(name + "/x", (m, d), 1.0, "f32"), "f32")
+    top = np.where(np.arange(m) % 2 == 1, 0.26, 0.24) if big == "half" else np.where(np.arange(m) == m // 2, 0.26, 0.24)
+    X, x = inputs(x * (top / np.abs(x).max(1))[:, None], "bf16")
+    T = syn.rng_for(name + "/t").integers(0, V, size=m)
+    w = np.ones(m)
+    gt = t.from_numpy(T).cuda()
+    _, lse = skm().sketch_xent_fwd(X, gi, gl, gt, b, gpr)
+    dL = skm().sketch_xent_bwd(X, gi, gl, gt, lse, t.ones(m, device="cuda"), b, gpr, need_dx=False)[1]
+    l64 = to_f64(lse)
+    Z = x @ W.T
+    dZ = to.xent_dz(Z, T, l64, w)
+    e = dz_error(np.exp(Z - l64[:, None]), w, l64, logit_error(x, W, "bf16", ldt, d), T)
+    # the scale of an operand's row: its largest value in [2^14, 2^15); of dZ's row: the inverse, times one power of two
+    step = np.exp2(np.floor(np.log2(np.abs(x).max(1))) - 14)
+    op = e + 2.0 ** -22 * np.abs(dZ) + (2.0 ** -39 * (w * step).max() / step)[:, None]
+    ref = oracle.backward_dlut(dZ, x, idx, b, gpr)
+    mag = oracle.backward_dlut(np.abs(dZ), np.abs(x), idx, b, gpr)
+    err = oracle.backward_dlut(op, np.abs(x), idx, b, gpr)
+    err += oracle.backward_dlut(np.abs(dZ), np.repeat(2.0 ** -25 * step[:, None], d, 1), idx, b, gpr)
+    within(to_f64(dL), ref, 1.01 * err + (2 * m / 16 + d // gpr + 40) * U * mag, "dLUT")
