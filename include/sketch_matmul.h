@@ -336,8 +336,8 @@ size_t sketch_xent_fwd_workspace(int64_t m, int64_t n, int64_t d, int b, int gpr
  * each NULL = skip. The logits are recomputed a piece of the vocabulary at a
  * time. dX is the fp32 sum of products with dZ rounded once to the tables'
  * dtype (the target's term with its fp32 remainder; f16 operands hold |dZ| down
- * to 2^-28 of the largest |dloss| at full precision and end at 2^-39 of it).
- * dLUT takes dZ to 2^-23 of itself, or to 2^-39 of the largest |dloss| where
+ * to 2^-28 of the token's |dloss| at full precision and end at 2^-39 of it, for
+ * F16 X with both gradients of the largest |dloss|). dLUT takes dZ to 2^-23 of itself, or to 2^-39 of the largest |dloss| where
  * that is more; for bf16 X the tokens are compared by |dloss| times the largest
  * |X| of their row, and X is taken exactly down to 2^-28 of that largest |X|
  * and to 2^-39 of it below. Both are deterministic (no atomics). workspace: at least

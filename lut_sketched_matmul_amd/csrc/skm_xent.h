@@ -30,12 +30,15 @@
 // both sides under one scale lost up to 17 of the 23 bits.) dX has a form of
 // its own then: a row of X near zero has no gradient to give to the tables, but
 // takes one itself.
-// The f16 forms are scaled by one power of two that puts the largest row
-// factor, |dloss| 2^e or |dloss|, into [2^14, 2^15): a term of dLUT keeps 2^-23
-// of itself or 2^-39 of that factor, whichever is more, and dX's operand holds
-// a softmax value down to 2^-28 of the largest |dloss| at full precision; the
-// results are scaled back in fp32 (exact). bf16 dZ (dX with bf16 tables) needs
-// no scale.
+// The f16 forms are scaled by powers of two; the results are scaled back in
+// fp32 (exact). dLUT's sum over the tokens takes one scale for all, which puts
+// the largest row factor, |dloss| 2^e, into [2^14, 2^15): a term keeps 2^-23 of
+// itself or 2^-39 of that factor, whichever is more. dX's rows are apart, so
+// every token's |dloss| is put there by itself (xent_token_exp) and a softmax
+// value down to 2^-28 keeps f16's full precision, however far the tokens'
+// weights lie apart. Only f16 X with both gradients shares one form, with
+// dLUT's scale: a third one would be written and read for tokens whose dX
+// hardly fills f16. bf16 dZ (dX with bf16 tables) needs no scale.
 //
 // Bound by the matrix tiles. 4096 tokens, three quarters of them scored, 32000
 // words of 4096 columns (b = 4, f16): statistics 724 us (1113 TFLOP/s), dZ 794, dX
@@ -58,10 +61,19 @@ struct XentHead {
   int32_t count;    // tokens that have a target
   float scale;      // of dLUT's f16 operands, a power of two, and its inverse
   float inv_scale;
-  float dx_scale;   // of dX's (equal for f16 X: one form serves both)
-  float dx_inv;
   DxPlan dx;        // ranges of dX's tiles (dx_plan)
 };
+
+// exponent of the power of two that puts a value of this magnitude pattern
+// into [2^14, 2^15) (0 for zero and what is smaller than fp32's normal values)
+__device__ __forceinline__ int scale_exp(uint32_t top) {
+  const int e = top >= 0x00800000u ? 14 + 127 - (int)(top >> 23) : 0;
+  return e > 126 ? 126 : (e < -112 ? -112 : e);
+}
+// of a token's dZ as dX's f16 operand
+__device__ __forceinline__ int xent_token_exp(float dloss) {
+  return scale_exp(__builtin_bit_cast(uint32_t, dloss) & 0x7FFFFFFFu);
+}
 
 // ---- pieces of the launchers, one translation unit each --------------------------
 

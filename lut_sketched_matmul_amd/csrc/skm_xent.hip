@@ -54,15 +54,11 @@ __device__ __forceinline__ DxPlan dx_plan(int32_t count, const DxShape& q, unsig
 // One block (the list is one scan over m targets, 8192 per round).
 // rows[c] = token of listed row c, in token order. Forward: loss and lse of the
 // others are zeroed. Backward: pos[t] = listed row of token t or -1, and the
-// powers of two that put the largest finite |dloss| 2^e (e from zexp, NULL = 0)
-// and the largest finite |dloss| into [2^14, 2^15) (1 when there is none).
+// power of two that puts the largest finite |dloss| 2^e (e from zexp, NULL = 0)
+// into [2^14, 2^15) (1 when there is none).
 __device__ __forceinline__ uint32_t larger_finite(uint32_t top, float f) {
   const uint32_t a = __builtin_bit_cast(uint32_t, f) & 0x7FFFFFFFu;
   return a < 0x7F800000u && a > top ? a : top;
-}
-__device__ __forceinline__ int scale_exp(uint32_t top) {
-  const int e = top >= 0x00800000u ? 14 + 127 - (int)(top >> 23) : 0;
-  return e > 126 ? 126 : (e < -112 ? -112 : e);
 }
 template <bool BWD>
 __global__ void __launch_bounds__(1024) k_xent_index(const int64_t* __restrict__ targets, int64_t ignore, int64_t m,
@@ -72,10 +68,10 @@ __global__ void __launch_bounds__(1024) k_xent_index(const int64_t* __restrict__
                                                      DxShape dx, float* __restrict__ loss, float* __restrict__ lse) {
   __shared__ int32_t before[129];  // listed tokens of a round in front of wave w's k-th 64: [16 k + w]
   __shared__ unsigned long long slot[16];
-  __shared__ uint32_t wmax[2][16];
+  __shared__ uint32_t wmax[16];
   const int t = (int)threadIdx.x, lane = t & 63, wave = t >> 6;
   int32_t base = 0;
-  uint32_t top = 0u, top_dx = 0u;
+  uint32_t top = 0u;
   for (int64_t r0 = 0; r0 < m; r0 += 8192) {
     unsigned long long on[8];
     float f[8] = {};
@@ -117,10 +113,7 @@ __global__ void __launch_bounds__(1024) k_xent_index(const int64_t* __restrict__
       if (mine) rows[c] = (int32_t)i;
       if constexpr (BWD) {
         pos[i] = mine ? c : -1;
-        if (mine) {
-          top_dx = larger_finite(top_dx, f[k]);
-          top = larger_finite(top, f[k] * pow2f(z[k]));
-        }
+        if (mine) top = larger_finite(top, f[k] * pow2f(z[k]));
       } else if (!mine) {
         loss[i] = 0.0f;
         lse[i] = 0.0f;
@@ -132,14 +125,10 @@ __global__ void __launch_bounds__(1024) k_xent_index(const int64_t* __restrict__
   if constexpr (BWD) {
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) {
-      const uint32_t v = (uint32_t)__shfl_xor((int)top, o, 64), w = (uint32_t)__shfl_xor((int)top_dx, o, 64);
+      const uint32_t v = (uint32_t)__shfl_xor((int)top, o, 64);
       top = top > v ? top : v;
-      top_dx = top_dx > w ? top_dx : w;
     }
-    if (lane == 0) {
-      wmax[0][wave] = top;
-      wmax[1][wave] = top_dx;
-    }
+    if (lane == 0) wmax[wave] = top;
     __syncthreads();
   }
   DxPlan plan{0, 1, 1, 1};
@@ -149,15 +138,10 @@ __global__ void __launch_bounds__(1024) k_xent_index(const int64_t* __restrict__
     head->count = base;
     head->dx = plan;
     if constexpr (BWD) {
-      for (int w = 0; w < 16; ++w) {
-        top = top > wmax[0][w] ? top : wmax[0][w];
-        top_dx = top_dx > wmax[1][w] ? top_dx : wmax[1][w];
-      }
-      const int e = scale_exp(top), e_dx = scale_exp(top_dx);
+      for (int w = 0; w < 16; ++w) top = top > wmax[w] ? top : wmax[w];
+      const int e = scale_exp(top);
       head->scale = pow2f(e);
       head->inv_scale = pow2f(-e);
-      head->dx_scale = pow2f(e_dx);
-      head->dx_inv = pow2f(-e_dx);
     }
   }
 }
@@ -362,13 +346,15 @@ __global__ void __launch_bounds__(256) k_xent_gather(const TX* __restrict__ X, c
 
 // dX[t] = (sum of the ranges' dX of t's listed row + what rounding took from the
 // target's term, times the target's weights), scaled back; zeros for an ignored
-// token. f16 operands (TL) carry the scale, bf16 ones none. A block sums 2048 /
-// lanes columns, 8 per thread, `lanes` threads taking every lanes-th range each:
-// a few rows have up to 256 ranges, which one thread would wait for one by one.
+// token. f16 operands (TL) carry the token's scale (dloss given) or dLUT's, bf16
+// ones none. A block sums 2048 / lanes columns, 8 per thread, `lanes` threads
+// taking every lanes-th range each: a few rows have up to 256 ranges, which one
+// thread would wait for one by one.
 template <int B, typename TX, typename TL>
 __global__ void __launch_bounds__(256) k_xent_dx_out(const float* __restrict__ acc, int lanes,
                                                      const int32_t* __restrict__ pos,
                                                      const XentHead* __restrict__ head,
+                                                     const float* __restrict__ dloss,
                                                      const float* __restrict__ rest,
                                                      const int64_t* __restrict__ targets,
                                                      const uint8_t* __restrict__ idx_packed,
@@ -428,7 +414,7 @@ __global__ void __launch_bounds__(256) k_xent_dx_out(const float* __restrict__ a
     for (int q = 0; q < 8; ++q) v[q] = __builtin_fmaf(r, to_f32(g[(w >> (B * q)) & (K - 1)]), v[q]);
   }
   if constexpr (!__is_same(TL, bf16_t)) {
-    const float back = head->dx_inv;
+    const float back = !dloss ? head->inv_scale : (c >= 0 ? pow2f(-xent_token_exp(dloss[t])) : 0.0f);
 #pragma unroll
     for (int q = 0; q < 8; ++q) v[q] *= back;
   }
@@ -440,6 +426,7 @@ struct DxOut {
   int ranges;
   const int32_t* pos;
   const XentHead* head;
+  const float* dloss;  // dX's operand is scaled token by token; NULL = as dLUT's
   const float* rest;
 };
 template <typename TX, typename TL>
@@ -451,7 +438,7 @@ hipError_t dx_out_t(const XentArgs& a, const DxOut& o, void* dX, hipStream_t s) 
   const int64_t cols = 2048 / lanes;
   auto go = [&](auto kern) {
     hipLaunchKernelGGL(kern, dim3((unsigned)p.m, (unsigned)((p.d + cols - 1) / cols)), dim3(256), 0, s, o.acc,
-                       lanes, o.pos, o.head, o.rest, a.targets, a.idx, (const TL*)a.lut, p.n, p.d, p.gpr, (TX*)dX);
+                       lanes, o.pos, o.head, o.dloss, o.rest, a.targets, a.idx, (const TL*)a.lut, p.n, p.d, p.gpr, (TX*)dX);
     return hipGetLastError();
   };
   if (p.b == 2) return go(k_xent_dx_out<2, TX, TL>);
@@ -696,7 +683,7 @@ hipError_t launch_xent_bwd(const XentArgs& a, const float* lse, const float* dlo
     }
   }
   if (e != hipSuccess || !dX) return e;
-  return dx_out(a, {acc, (int)f.slots, pos, head, rest}, dX, s);
+  return dx_out(a, {acc, (int)f.slots, pos, head, f.own || !dLUT ? dloss : nullptr, rest}, dX, s);
 }
 
 }  // namespace skm

@@ -77,8 +77,10 @@ template <typename TX, typename TL> struct EpDecodeGrad {
     if (c < 0) return;
     const int64_t target = ep.targets[t];
     const float dl = target >= 0 && target < ep.V ? ep.dloss[t] : __builtin_nanf("");
-    const float up = ep.zexp ? dl * pow2f(ep.zexp[t]) * ep.head->scale : dl * ep.head->scale;
-    const float dx = OWN ? (__is_same(TL, bf16_t) ? dl : dl * ep.head->dx_scale) : up;
+    const float own = __is_same(TL, bf16_t) ? dl : dl * pow2f(xent_token_exp(dl));
+    const float up =
+        !ep.lo ? own : (ep.zexp ? dl * pow2f(ep.zexp[t]) * ep.head->scale : dl * ep.head->scale);
+    const float dx = OWN ? own : up;
     const bool mine = ok && ep.v0 + row == target;
     const float p = __expf(v - ep.lse[t]) - (mine ? 1.0f : 0.0f);
     store(ep, c * ep.ld + row, ok ? p * up : 0.0f, ok ? p * dx : 0.0f);

@@ -109,8 +109,9 @@ __device__ __forceinline__ u32x4 pair_up(uint32_t a0, uint32_t a1, uint32_t b0, 
 
 // EpGrad: dZ of the block, [listed token][ld] in up to three forms (NULL = not
 // wanted): hi + lo in f16 for dLUT, scaled by head->scale 2^e of the token, and
-// dxv in the tables' dtype for dX, f16 scaled by head->dx_scale (f16 X: e = 0
-// and hi serves both). Columns n .. ld - 1 and listed rows past the count up to the next
+// dxv in the tables' dtype for dX, f16 scaled by the token's own 2^e
+// (xent_token_exp). f16 X: hi serves both, scaled for dLUT if there is a lo and
+// else for dX. Columns n .. ld - 1 and listed rows past the count up to the next
 // multiple of 32 are written as zeros. rest[c]: what rounding took from the
 // target's term in dX's operand.
 template <typename TX, typename TL> struct EpGrad {
@@ -136,7 +137,7 @@ template <typename TX, typename TL> struct EpGrad {
     const int cols = (int)(n - c0 < 64 ? n - c0 : 64) - 4 * (lane >> 5);
     const int stored = (int)(ep.ld - c0 < 64 ? ep.ld - c0 : 64);
     const bool ragged = n - c0 < 64 || m0 + G_BM > m;  // wave-uniform
-    const float scale = ep.head->scale, dx_scale = __is_same(TL, bf16_t) ? 1.0f : ep.head->dx_scale;
+    const float scale = ep.head->scale;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t tok = m0 + 128 * wm + 32 * i + (lane & 31);
@@ -149,8 +150,9 @@ template <typename TX, typename TL> struct EpGrad {
       const float lse = ep.lse[src];
       // a target outside the vocabulary gives NaN gradients (its loss is NaN)
       const float dl = target >= 0 && target < ep.V ? ep.dloss[src] : __builtin_nanf("");
-      const float up = ep.zexp ? dl * pow2f(ep.zexp[src]) * scale : dl * scale;
-      const float dx = OWN ? dl * dx_scale : up;
+      const float own = __is_same(TL, bf16_t) ? dl : dl * pow2f(xent_token_exp(dl));
+      const float up = !ep.lo ? own : (ep.zexp ? dl * pow2f(ep.zexp[src]) * scale : dl * scale);
+      const float dx = OWN ? own : up;
       // g[e] = dZ of output e over its row's factor. (The target's 1 and the
       // masks only where the wave has one: few waves hold a target of one of
       // their tokens, one column and one token block are ragged.)

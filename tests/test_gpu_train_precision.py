@@ -93,3 +93,42 @@ def test_table_gradient_of_rows_around_a_quarter(m, ldt, big):
     err = oracle.backward_dlut(op, np.abs(x), idx, b, gpr)
     err += oracle.backward_dlut(np.abs(dZ), np.repeat(2.0 ** -25 * step[:, None], d, 1), idx, b, gpr)
     within(to_f64(dL), ref, 1.01 * err + (2 * m / 16 + d // gpr + 40) * U * mag, "dLUT")
+
+
+def check_dx(name, m, V, d, b, gpr, io, ldt, w, sigma=0.05, x=None, weights=None, need_dlut=False):
+    """dX against float64, every token by its own dloss: H[ldt] of each term but the target's (2^-22: it keeps its
+    remainder in fp32) or 2^-39 of the token's |dloss|, where dX has an operand of its own."""
+    t = torch()
+    gi, gl, idx, W = weights if weights is not None else head(name, V, d, b, gpr, ldt, sigma)
+    if x is None:
+        x = syn.to_float64(syn.random_normal(name + "/x", (m, d), 1.0, "f32"), "f32")
+    X, x = inputs(x, io)
+    T = syn.rng_for(name + "/t").integers(0, V, size=m)
+    gt = t.from_numpy(T).cuda()
+    w = w.astype(np.float32).astype(np.float64)
+    _, lse = skm().sketch_xent_fwd(X, gi, gl, gt, b, gpr)
+    dX = skm().sketch_xent_bwd(X, gi, gl, gt, lse, t.from_numpy(w.astype(np.float32)).cuda(), b, gpr,
+                               need_dlut=need_dlut)[0]
+    l64 = to_f64(lse)
+    Z = x @ W.T
+    dZ = to.xent_dz(Z, T, l64, w)
+    e = dz_error(np.exp(Z - l64[:, None]), np.abs(w), l64, logit_error(x, W, io, ldt, d), T)
+    keep = np.full(dZ.shape, H[ldt])
+    keep[np.arange(m), T] = 2.0 ** -22
+    op = e + keep * (np.abs(dZ) + e) + (2.0 ** -39 * np.abs(w)[:, None] if ldt == "f16" else 0.0)
+    ref = dZ @ W
+    # fp32 sums of V terms: 16 at a time, the pieces, the ranges
+    err = op @ np.abs(W) + (V / 16 + 64) * U * (np.abs(dZ) @ np.abs(W))
+    within(to_f64(dX), ref, 1.01 * err + H[io] * (np.abs(ref) + err) + TINY[io], "dX")
+
+
+@pytest.mark.parametrize("m", [24, 300])
+@pytest.mark.parametrize("io,ldt,need_dlut,hi,lo", [
+    ("f16", "f16", False, 15, -12), ("bf16", "f16", False, 20, -60), ("bf16", "f16", True, 20, -60),
+    ("bf16", "bf16", False, 20, -60),
+])
+def test_dx_of_tokens_with_far_weights(io, ldt, need_dlut, hi, lo, m):
+    """A token's dX is as precise beside a token of 2^80 times its weight as alone."""
+    w = np.exp2(np.linspace(hi, lo, m))
+    w[1::2] *= -1.0
+    check_dx(f"farw/{io}/{ldt}/{m}", m, 9000, 64, 4, 1, io, ldt, w, need_dlut=need_dlut)
