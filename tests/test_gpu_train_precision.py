@@ -95,9 +95,9 @@ def test_table_gradient_of_rows_around_a_quarter(m, ldt, big):
     within(to_f64(dL), ref, 1.01 * err + (2 * m / 16 + d // gpr + 40) * U * mag, "dLUT")
 
 
-def check_dx(name, m, V, d, b, gpr, io, ldt, w, sigma=0.05, x=None, weights=None, need_dlut=False):
-    """dX against float64, every token by its own dloss: H[ldt] of each term but the target's (2^-22: it keeps its
-    remainder in fp32) or 2^-39 of the token's |dloss|, where dX has an operand of its own."""
+def check_dx(name, m, V, d, b, gpr, io, ldt, w, sigma=0.05, x=None, weights=None, need_dlut=False, others=None):
+    """dX against float64, every token by its own dloss: H[ldt] of each term (`others` if given) but the target's (2^-22:
+    it keeps its remainder in fp32) or 2^-39 of the token's |dloss|, where dX has an operand of its own."""
     t = torch()
     gi, gl, idx, W = weights if weights is not None else head(name, V, d, b, gpr, ldt, sigma)
     if x is None:
@@ -113,13 +113,15 @@ def check_dx(name, m, V, d, b, gpr, io, ldt, w, sigma=0.05, x=None, weights=None
     Z = x @ W.T
     dZ = to.xent_dz(Z, T, l64, w)
     e = dz_error(np.exp(Z - l64[:, None]), np.abs(w), l64, logit_error(x, W, io, ldt, d), T)
-    keep = np.full(dZ.shape, H[ldt])
+    keep = np.full(dZ.shape, H[ldt] if others is None else others)
     keep[np.arange(m), T] = 2.0 ** -22
     op = e + keep * (np.abs(dZ) + e) + (2.0 ** -39 * np.abs(w)[:, None] if ldt == "f16" else 0.0)
     ref = dZ @ W
     # fp32 sums of V terms: 16 at a time, the pieces, the ranges
     err = op @ np.abs(W) + (V / 16 + 64) * U * (np.abs(dZ) @ np.abs(W))
-    within(to_f64(dX), ref, 1.01 * err + H[io] * (np.abs(ref) + err) + TINY[io], "dX")
+    bound = 1.01 * err + H[io] * (np.abs(ref) + err) + TINY[io]
+    within(to_f64(dX), ref, bound, "dX")
+    return dZ[np.arange(m), T], W[T], bound
 
 
 @pytest.mark.parametrize("m", [24, 300])
@@ -132,3 +134,20 @@ def test_dx_of_tokens_with_far_weights(io, ldt, need_dlut, hi, lo, m):
     w = np.exp2(np.linspace(hi, lo, m))
     w[1::2] *= -1.0
     check_dx(f"farw/{io}/{ldt}/{m}", m, 9000, 64, 4, 1, io, ldt, w, need_dlut=need_dlut)
+
+
+@pytest.mark.parametrize("m", [20, 700])
+@pytest.mark.parametrize("io,ldt,V", [("f16", "f16", 4096), ("bf16", "f16", 4096), ("bf16", "bf16", 1024)])
+def test_dx_keeps_the_targets_remainder(io, ldt, V, m):
+    """Rows of zeros against words near 4: dX = mean(W) - W[target], the small difference of two large terms. The
+    softmax 1 / V is exact in 16 bits and 1 / V - 1 is not, so only its remainder saves the difference."""
+    d, b = 64, 4
+    g = syn.rng_for(f"rest/{ldt}")
+    idx = syn.random_packed_indices(f"rest/{ldt}/i", V, d, b)
+    lut = syn.to_storage((4.0 + g.integers(-2, 3, size=(V, 1, 16)) * 2.0 ** -5).astype(np.float32), ldt)
+    W = oracle.dequantize(idx, syn.to_float64(lut, ldt), d, b, 1)
+    dz, wt, bound = check_dx(f"rest/{io}/{ldt}/{m}", m, V, d, b, 1, io, ldt, np.ones(m), x=np.zeros((m, d)),
+                             weights=(to_dev(idx, "u8"), to_dev(lut, ldt), idx, W), need_dlut=m == 20, others=0.0)
+    # (the bound tells: the target's term rounded like the others would be outside it)
+    r = syn.to_float64(syn.to_storage((dz * 0.999999).astype(np.float32), ldt), ldt) - dz
+    assert (np.abs(r[:, None] * wt) > 2 * bound).all()
