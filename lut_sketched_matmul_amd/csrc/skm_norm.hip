@@ -7,11 +7,13 @@
 //   dx = r (g - xh mean(g xh) - [layer] mean(g)),  g = dy w
 //   dw = sum_rows dy xh,   db = sum_rows dy
 //
-// All arithmetic is fp32. A row is read once and stays in registers: TPR
-// threads of E = 8 NCH elements each, so the variance is taken from the
-// centred values (no cancellation) without a second read. Rows of whole
-// 8-column chunks (AL) move 8 consecutive columns per lane; other widths take
-// the same kernels with column j TPR + t in element j of thread t.
+// All arithmetic is fp32; means are quotients, rounded once. (As products with
+// a rounded 1 / d, the mean of 7 times 1000 was 1000.0001 and y of that row 0.02
+// instead of 0.) A row is read once and stays in registers: TPR threads of E = 8
+// NCH elements each, so the variance is taken from the centred values (no
+// cancellation) without a second read. Rows of whole 8-column chunks (AL) move 8
+// consecutive columns per lane; other widths take the same kernels with column
+// j TPR + t in element j of thread t.
 //
 // Backward: each block walks rows blockIdx, blockIdx + grid, ... and keeps its
 // columns' dw and db sums in registers, the next row's loads in flight while a
@@ -213,7 +215,7 @@ k_norm_fwd(const T* __restrict__ X, const void* __restrict__ w, const void* __re
   if (r >= m) return;  // uniform over the row's threads (the whole block when TPR > 64)
   float x[NCH][8];
   load_row<T, AL, TPR, NCH>(X + r * d, d, t, x);
-  const float inv_d = 1.0f / (float)d;
+  const float fd = (float)d;
   float mu = 0.0f, z = 0.0f;
   if (layer) {
 #pragma unroll
@@ -221,7 +223,7 @@ k_norm_fwd(const T* __restrict__ X, const void* __restrict__ w, const void* __re
 #pragma unroll
       for (int j = 0; j < 8; ++j) mu += x[c][j];
     row_sum2<TPR>(mu, z, red);
-    mu *= inv_d;
+    mu /= fd;
   }
   float var = 0.0f;
 #pragma unroll
@@ -233,7 +235,7 @@ k_norm_fwd(const T* __restrict__ X, const void* __restrict__ w, const void* __re
     }
   z = 0.0f;
   row_sum2<TPR>(var, z, red);
-  const float rs = 1.0f / sqrtf(var * inv_d + eps);
+  const float rs = 1.0f / sqrtf(var / fd + eps);
   if (t == 0) {
     rstd[r] = rs;
     if (mean) mean[r] = mu;
@@ -292,7 +294,7 @@ k_norm_bwd(const void* __restrict__ dY, const T* __restrict__ X, const int8_t* _
   typedef std::conditional_t<DYF, float, T> TY;
   __shared__ float red[2 * (TPR / 64)];
   const int t = (int)(threadIdx.x % TPR);
-  const float inv_d = 1.0f / (float)d;
+  const float fd = (float)d;
   float p[NCH][8], aw[NCH][8], ab[NCH][8];
 #pragma unroll
   for (int c = 0; c < NCH; ++c)
@@ -340,8 +342,8 @@ k_norm_bwd(const void* __restrict__ dY, const T* __restrict__ X, const int8_t* _
       }
     if (dX) {
       row_sum2<TPR>(s1, s2, red);
-      s1 *= inv_d;
-      s2 = mean ? s2 * inv_d : 0.0f;
+      s1 /= fd;
+      s2 = mean ? s2 / fd : 0.0f;
 #pragma unroll
       for (int c = 0; c < NCH; ++c)
 #pragma unroll
@@ -401,7 +403,7 @@ k_norm_bwd_wide(const void* __restrict__ dY, const T* __restrict__ X, const int8
   constexpr int TPR = 1024;
   __shared__ float red[2 * (TPR / 64)];
   const int t = (int)threadIdx.x, chunks = (d + 8 * TPR - 1) / (8 * TPR);
-  const float inv_d = 1.0f / (float)d;
+  const float fd = (float)d;
   for (int64_t r = blockIdx.x; r < m; r += gridDim.x) {
     const float mu = mean ? mean[r] : 0.0f, rs = rstd[r];
     float s1 = 0.0f, s2 = 0.0f;  // sums of g xh and of g, g = dy w
@@ -417,8 +419,8 @@ k_norm_bwd_wide(const void* __restrict__ dY, const T* __restrict__ X, const int8
       }
     }
     row_sum2<TPR>(s1, s2, red);
-    s1 *= inv_d;
-    s2 = mean ? s2 * inv_d : 0.0f;
+    s1 /= fd;
+    s2 = mean ? s2 / fd : 0.0f;
     for (int c = 0; c < chunks; ++c) {
       float x[1][8], g[1][8], p[8];
       load_pair<T, AL, TPR, DYF, CK>(dY, X, codes, scales, r, d, t, c, x, g);

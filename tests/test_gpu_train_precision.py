@@ -151,3 +151,24 @@ def test_dx_keeps_the_targets_remainder(io, ldt, V, m):
     # (the bound tells: the target's term rounded like the others would be outside it)
     r = syn.to_float64(syn.to_storage((dz * 0.999999).astype(np.float32), ldt), ldt) - dz
     assert (np.abs(r[:, None] * wt) > 2 * bound).all()
+
+
+@pytest.mark.parametrize("d", [7, 41, 56, 97, 112, 1001, 1792, 4280, 4512, 8560, 9024, 14336, 16826, 20000])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_norm_of_constant_rows_is_exact(d, dtype):
+    """The sums of 1000s and 4s are exact, so their means are, wherever the mean is a quotient rounded once: no
+    variance, y = bias, 1 / rms = 1 / 2; and the backward's mean of a constant g takes all of it away."""
+    t = torch()
+    X = to_dev(syn.to_storage(np.full((5, d), 1000.0, np.float32), dtype), dtype)
+    B = to_dev(syn.random_normal(f"const/{d}", (d,), 1.0, "f32"), "f32")
+    Y, mean, rstd, _, _ = skm().sketch_norm_fwd(X, None, B, kind="layer", eps=1e-5)
+    assert (mean == 1000.0).all() and t.equal(Y, B.to(Y.dtype).expand(5, d))
+    assert (rstd == rstd[0]).all() and abs(float(rstd[0]) * 1e-5 ** 0.5 - 1.0) <= 4 * U
+    dX, dw, db = skm().sketch_norm_bwd(t.full((5, d), 3.0, device="cuda"), X, None, mean, rstd, kind="layer")
+    assert (dX == 0).all() and (dw == 0).all() and (db == 15.0).all()
+    X = to_dev(syn.to_storage(np.full((5, d), -2.0, np.float32), dtype), dtype)
+    Y, mean, rstd, _, _ = skm().sketch_norm_fwd(X, kind="rms", eps=0.0)
+    assert mean is None and (rstd == 0.5).all() and (Y == -1.0).all()
+    # g xh = -3 in every column: mean(g xh) = -3 and dx = r (g - xh mean(g xh)) = 0
+    dX = skm().sketch_norm_bwd(t.full((5, d), 3.0, device="cuda"), X, None, None, rstd, kind="rms")[0]
+    assert (dX == 0).all()
