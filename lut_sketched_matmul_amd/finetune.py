@@ -16,9 +16,9 @@ projection with its cross entropy loss, whose logits are never stored.
 Every compute step runs in the HIP library (forward, dX, dLUT, norms, loss,
 optimizer step); this module only marshals arguments. Three small torch
 operations remain in the glue: the fp32 input gradient is cast to the
-activations' dtype (autograd requires a gradient in its input's dtype), a
-grouped layer's output gradient is made contiguous before the backward launch,
-and the gradient of a mean loss is multiplied by the tokens' weights.
+activations' dtype (autograd requires a gradient in its input's dtype),
+inputs and output gradients that are not contiguous or not aligned to 16 bytes
+are copied, and the gradient of a mean loss is multiplied by the tokens' weights.
 """
 from __future__ import annotations
 
@@ -27,6 +27,16 @@ from typing import Iterable, List, Optional, Sequence
 import torch
 
 from . import _lib
+
+
+def _packed(t):
+    """t as the library takes it: contiguous, from a multiple of 16 bytes on.
+
+    Slices start anywhere, and so do the gradients autograd hands out: those of the parts of a concatenation are
+    contiguous views into one tensor.
+    """
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
 class SketchMatmulFunction(torch.autograd.Function):
@@ -38,7 +48,7 @@ class SketchMatmulFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, X, lut_master, lut, idx_packed, b: int, gpr: int):
-        Y = _lib.sketch_matmul_fwd(X.contiguous(), idx_packed, lut, b, gpr)
+        Y = _lib.sketch_matmul_fwd(_packed(X), idx_packed, lut, b, gpr)
         ctx.save_for_backward(X, lut, idx_packed)
         ctx.b, ctx.gpr = b, gpr
         return Y
@@ -49,10 +59,10 @@ class SketchMatmulFunction(torch.autograd.Function):
         need_dx, need_dlut = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
         if not (need_dx or need_dlut):
             return None, None, None, None, None, None
-        dY = dY.contiguous()
+        dY = _packed(dY)
         if dY.dtype != X.dtype:
             raise TypeError("the output gradient must have the activations' dtype")
-        dX, dL = _lib.sketch_matmul_bwd(dY, X.contiguous() if need_dlut else None, idx_packed, lut, ctx.b, ctx.gpr,
+        dX, dL = _lib.sketch_matmul_bwd(dY, _packed(X) if need_dlut else None, idx_packed, lut, ctx.b, ctx.gpr,
                                         d=X.shape[1], need_dx=need_dx, need_dlut=need_dlut)
         if dX is not None and dX.dtype != X.dtype:
             dX = dX.to(X.dtype)
@@ -67,7 +77,7 @@ def sketch_matmul(X, lut_master, lut, idx_packed, b: int, gpr: int):
 def _check_dy(dY, dtype):
     if dY.dtype != dtype:
         raise TypeError("the output gradient must have the activations' dtype")
-    return dY.contiguous()
+    return _packed(dY)
 
 
 class CheckpointedMatmulFunction(torch.autograd.Function):
@@ -79,7 +89,7 @@ class CheckpointedMatmulFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, X, lut_master, lut, idx_packed, b: int, gpr: int):
-        X = X.contiguous()
+        X = _packed(X)
         Y = _lib.sketch_matmul_fwd(X, idx_packed, lut, b, gpr)
         codes, scales = _lib.sketch_act_quant(X) if ctx.needs_input_grad[1] else (None, None)
         ctx.save_for_backward(codes, scales, lut, idx_packed)
@@ -108,7 +118,7 @@ class NormFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, X, weight, bias, kind: str, eps: float):
-        X = X.contiguous()
+        X = _packed(X)
         Y, mean, rstd, _, _ = _lib.sketch_norm_fwd(X, weight, bias, kind=kind, eps=eps)
         ctx.save_for_backward(X, weight, mean, rstd)
         ctx.kind = kind
@@ -118,7 +128,7 @@ class NormFunction(torch.autograd.Function):
     def backward(ctx, dY):
         X, weight, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
-        dX, dw, db = _lib.sketch_norm_bwd(dY.contiguous(), X, weight, mean, rstd, kind=ctx.kind, need_dx=need[0],
+        dX, dw, db = _lib.sketch_norm_bwd(_packed(dY), X, weight, mean, rstd, kind=ctx.kind, need_dx=need[0],
                                           need_dw=need[1], need_db=need[2])
         return dX, dw, db, None, None
 
@@ -133,7 +143,7 @@ class NormMatmulFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, weight, bias, lut_master, lut, idx_packed, b: int, gpr: int, kind: str, eps: float,
                 checkpoint: bool):
-        X = X.contiguous()
+        X = _packed(X)
         need = ctx.needs_input_grad
         Xn, mean, rstd, codes, scales = _lib.sketch_norm_fwd(X, weight, bias, kind=kind, eps=eps,
                                                              checkpoint=checkpoint and need[3])
@@ -171,7 +181,7 @@ class CrossEntropyFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, X, lut_master, lut, idx_packed, targets, b: int, gpr: int, ignore_index: int):
-        X, targets = X.contiguous(), targets.contiguous()
+        X, targets = _packed(X), targets.contiguous()
         loss, lse = _lib.sketch_xent_fwd(X, idx_packed, lut, targets, b, gpr, ignore_index=ignore_index)
         ctx.save_for_backward(X, lut, idx_packed, targets, lse)
         ctx.b, ctx.gpr, ctx.ignore_index = b, gpr, ignore_index
@@ -181,7 +191,7 @@ class CrossEntropyFunction(torch.autograd.Function):
     def backward(ctx, dloss):
         X, lut, idx_packed, targets, lse = ctx.saved_tensors
         need_dx, need_dlut = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
-        dX, dL = _lib.sketch_xent_bwd(X, idx_packed, lut, targets, lse, dloss.contiguous(), ctx.b, ctx.gpr,
+        dX, dL = _lib.sketch_xent_bwd(X, idx_packed, lut, targets, lse, _packed(dloss), ctx.b, ctx.gpr,
                                       ignore_index=ctx.ignore_index, need_dx=need_dx, need_dlut=need_dlut)
         return dX, dL, None, None, None, None, None, None
 
@@ -247,7 +257,7 @@ class SketchedLinear(torch.nn.Module):
             raise ValueError("table or index shape does not match (n, gpr, 2^b) / (n, d*b/8)")
         self.d, self.b, self.gpr = d, b, gpr
         self.checkpoint, self.norm = bool(checkpoint), norm
-        self.register_buffer("idx_packed", idx_packed.contiguous())
+        self.register_buffer("idx_packed", _packed(idx_packed))
         self.lut_master = torch.nn.Parameter(lut.detach().to(torch.float32).contiguous().clone())
         if compute_dtype == torch.float32:
             self.lut = None
@@ -374,7 +384,7 @@ class LutAdam(torch.optim.Optimizer):
                     st["exp_avg"] = torch.zeros_like(p, memory_format=torch.contiguous_format)
                     st["exp_avg_sq"] = torch.zeros_like(p, memory_format=torch.contiguous_format)
                 st["step"] += 1
-                _lib.sketch_lut_adam_step(p, p.grad.contiguous(), st["exp_avg"], st["exp_avg_sq"], st["step"],
+                _lib.sketch_lut_adam_step(p, _packed(p.grad), st["exp_avg"], st["exp_avg_sq"], st["step"],
                                           group["lr"], b1, b2, group["eps"], group["weight_decay"],
                                           group["grad_scale"], lut=_copy_of(p))
         return loss
@@ -400,7 +410,7 @@ class LutSGD(torch.optim.Optimizer):
                     if "momentum_buffer" not in st:
                         st["momentum_buffer"] = torch.zeros_like(p, memory_format=torch.contiguous_format)
                     buf = st["momentum_buffer"]
-                _lib.sketch_lut_sgd_step(p, p.grad.contiguous(), group["lr"], group["momentum"],
+                _lib.sketch_lut_sgd_step(p, _packed(p.grad), group["lr"], group["momentum"],
                                          group["weight_decay"], group["grad_scale"], momentum_buf=buf,
                                          lut=_copy_of(p))
         return loss
