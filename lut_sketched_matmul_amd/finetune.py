@@ -10,7 +10,8 @@ tried (SpaLLM, appendix B.1, Table 7) but name no optimizer.
 
 A layer can keep its input for the table gradient as an 8-bit checkpoint
 (``checkpoint=True``) and take the norm in front of it (``norm=``), which then
-writes that checkpoint in its own pass. :class:`SketchedHead` is the vocabulary
+writes that checkpoint in its own pass (and keeps its own input in 8 bits for
+its backward: dX is then that of the checkpoint). :class:`SketchedHead` is the vocabulary
 projection with its cross entropy loss, whose logits are never stored.
 
 Every compute step runs in the HIP library (forward, dX, dLUT, norms, loss,
@@ -137,7 +138,8 @@ class NormMatmulFunction(torch.autograd.Function):
     """Y = norm(X) Wᵀ in two launches; its backward hands the matmul's fp32 dX to the norm without a cast.
 
     checkpoint: keep the normed input (written by the norm's own pass) and X as 8-bit checkpoints instead of
-    16-bit copies.
+    16-bit copies, 16.5 bits per value for both. The table gradient is then that of the normed input's checkpoint,
+    and the norm's backward (dX, dweight, dbias) that of X's. Without a table gradient nothing is quantised.
     """
 
     @staticmethod
@@ -151,7 +153,7 @@ class NormMatmulFunction(torch.autograd.Function):
         x0, x1 = X, None
         if not any(need[:3]):
             x0 = None
-        elif checkpoint:
+        elif checkpoint and need[3]:
             x0, x1 = _lib.sketch_act_quant(X)
         ctx.save_for_backward(x0, x1, weight, mean, rstd, codes, scales,
                               Xn if need[3] and not checkpoint else None, lut, idx_packed)
@@ -245,6 +247,11 @@ class SketchedLinear(torch.nn.Module):
     for the fp32 path, where the master itself is read). checkpoint: keep the input for the table gradient as
     its 8-bit checkpoint (8.25 bits per value). norm: a :class:`SketchNorm` applied to the input first (its
     pass then writes the checkpoint).
+
+    With checkpoint alone the table gradient is that of the 8-bit input and dX is unchanged. With both, the norm's
+    own input is kept in 8 bits too, so dX and the gradients of the norm's weight and bias are those of that
+    checkpoint (each value off by at most half a step of its 32-column block). While the tables need no gradient
+    (``lut_master.requires_grad_(False)``) checkpoint changes nothing.
     """
 
     def __init__(self, idx_packed, lut, d: int, b: int, gpr: int, compute_dtype=torch.float16,

@@ -167,3 +167,23 @@ def test_inputs_that_start_anywhere(calls):
     head.token_losses(X, T).sum().backward()
     head.token_losses(want, T).sum().backward()
     assert torch.equal(X.grad, want.grad)
+
+
+def test_checkpoint_is_for_the_table_gradient(calls):
+    """Frozen tables: nothing is quantised and the gradients of X and of the norm are those of X itself."""
+    idx, lut = sketch(8, 32, 1, 13)
+    x, dY = normal((4, 32), 14), normal((4, 8), 15)
+    grads = []
+    for checkpoint in (False, True):
+        norm = finetune.SketchNorm(32, "rms", device="cpu")
+        layer = finetune.SketchedLinear(idx, lut, 32, 4, 1, compute_dtype=torch.float32, checkpoint=checkpoint, norm=norm)
+        layer.lut_master.requires_grad_(False)
+        X = x.clone().requires_grad_()
+        layer(X).backward(dY)
+        grads.append((X.grad, norm.weight.grad))
+    assert all(torch.equal(p, q) for p, q in zip(*grads))
+    assert "norm_bwd" in calls.log and not {"quant", "norm_fwd_ckpt", "norm_bwd_ckpt"} & set(calls.log)
+    # trained tables: both checkpoints, as asked for
+    layer.lut_master.requires_grad_(True)
+    layer(x.clone().requires_grad_()).backward(dY)
+    assert {"quant", "norm_fwd_ckpt", "norm_bwd_ckpt"} <= set(calls.log)
