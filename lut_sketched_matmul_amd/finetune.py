@@ -291,11 +291,13 @@ class SketchedLinear(torch.nn.Module):
 
     def forward(self, X):
         self._link_copy()
+        # (a function's needs_input_grad names parameters under no_grad too, where no backward will come)
+        checkpoint = self.checkpoint and torch.is_grad_enabled()
         if self.norm is not None:
             n = self.norm
             return NormMatmulFunction.apply(X, n.weight, n.bias, self.lut_master, self.compute_tables(),
-                                            self.idx_packed, self.b, self.gpr, n.kind, n.eps, self.checkpoint)
-        if self.checkpoint:
+                                            self.idx_packed, self.b, self.gpr, n.kind, n.eps, checkpoint)
+        if checkpoint:
             return CheckpointedMatmulFunction.apply(X, self.lut_master, self.compute_tables(), self.idx_packed,
                                                     self.b, self.gpr)
         return sketch_matmul(X, self.lut_master, self.compute_tables(), self.idx_packed, self.b, self.gpr)

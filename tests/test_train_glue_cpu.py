@@ -187,3 +187,16 @@ def test_checkpoint_is_for_the_table_gradient(calls):
     layer.lut_master.requires_grad_(True)
     layer(x.clone().requires_grad_()).backward(dY)
     assert {"quant", "norm_fwd_ckpt", "norm_bwd_ckpt"} <= set(calls.log)
+
+
+def test_nothing_is_kept_without_gradients(calls):
+    """Under no_grad a checkpointed layer does the plain layer's calls: there is no backward to keep anything for."""
+    idx, lut = sketch(8, 32, 1, 16)
+    x = normal((4, 32), 17)
+    layer = finetune.SketchedLinear(idx, lut, 32, 4, 1, compute_dtype=torch.float32, checkpoint=True)
+    normed = finetune.SketchedLinear(idx, lut, 32, 4, 1, compute_dtype=torch.float32, checkpoint=True,
+                                     norm=finetune.SketchNorm(32, "rms", device="cpu"))
+    with torch.no_grad():
+        layer(x)
+        normed(x)
+    assert calls.log == ["matmul_fwd", "norm_fwd", "matmul_fwd"]
