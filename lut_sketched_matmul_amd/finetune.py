@@ -356,7 +356,10 @@ class SketchedHead(SketchedLinear):
 
     def forward(self, X, targets):
         """Mean loss over the tokens whose target is not ignore_index (0 when there is none)."""
-        return _MeanFunction.apply(self.token_losses(X, targets), targets.contiguous(), self.ignore_index)
+        losses = self.token_losses(X, targets)
+        if losses.numel() == 0:
+            return losses.sum()
+        return _MeanFunction.apply(losses, targets.contiguous(), self.ignore_index)
 
     def logits(self, X):
         """X Wᵀ [m, n] in X's dtype."""

@@ -200,3 +200,15 @@ def test_nothing_is_kept_without_gradients(calls):
         layer(x)
         normed(x)
     assert calls.log == ["matmul_fwd", "norm_fwd", "matmul_fwd"]
+
+
+def test_head_of_an_empty_batch(calls, monkeypatch):
+    """No token is scored: loss 0, gradients 0, as for a batch whose every target is ignored."""
+    monkeypatch.setattr(finetune._lib, "sketch_xent_mean", lambda *a, **k: pytest.fail("takes at least one token"))
+    idx, lut = sketch(8, 32, 1, 18)
+    head = finetune.SketchedHead(idx, lut, 32, 4, 1)
+    X = torch.zeros((0, 32), dtype=torch.float16, requires_grad=True)
+    loss = head(X, torch.zeros(0, dtype=torch.int64))
+    assert loss.dim() == 0 and loss.dtype == torch.float32 and float(loss.detach()) == 0.0
+    loss.backward()
+    assert X.grad.shape == (0, 32) and (head.lut_master.grad == 0).all()
