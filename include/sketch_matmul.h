@@ -243,8 +243,8 @@ int sketch_act_dequant(const int8_t* codes, const uint8_t* scales, int64_t m, in
  * workspace: at least sketch_matmul_bwd_ckpt_workspace(...) bytes (one X in
  * io_dtype for dLUT, up to 128 MiB of partial sums of dX when its tiles are
  * few, one dY when n is not a multiple of 8, split table gradients); need_dx /
- * need_dlut = 0 where the output is NULL. m * n and m * d at most 2^34.
- * Everything else as for sketch_matmul_bwd.
+ * need_dlut = 0 where the output is NULL. m * n and m * d at most 2^34, n rounded
+ * up to 128 times gpr at most 2^29. Everything else as for sketch_matmul_bwd.
  */
 int sketch_matmul_bwd_ckpt(const void* dY, const int8_t* codes, const uint8_t* scales, int io_dtype,
                            const uint8_t* idx_packed, const void* lut, int lut_dtype,

@@ -324,11 +324,18 @@ int sketch_act_dequant(const int8_t* codes, const uint8_t* scales, int64_t m, in
   return status_of(skm::launch_act_dequant(codes, scales, m * d, X, x_dtype, stream));
 }
 
+static int check_bwd_ckpt(int64_t m, int64_t n, int64_t d, int b, int gpr) {
+  int st = check_shape(m, n, d, b, gpr);
+  if (st == SKM_OK) st = check_ckpt_shape(m, d);
+  if (st != SKM_OK) return st;
+  // (and the table gradient's blocks of 128 weight rows x a group have 512)
+  if ((m > 0 && n > (int64_t(1) << 34) / m) || (n + 127) / 128 > (int64_t(1) << 22) / gpr) return SKM_EINVAL;
+  return SKM_OK;
+}
+
 size_t sketch_matmul_bwd_ckpt_workspace(int64_t m, int64_t n, int64_t d, int b, int gpr, int io_dtype, int lut_dtype,
                                         int need_dx, int need_dlut) {
-  if (m < 1 || check_shape(m, n, d, b, gpr) != SKM_OK || check_ckpt_shape(m, d) != SKM_OK ||
-      !supported_pair(io_dtype, lut_dtype))
-    return 0;
+  if (m < 1 || check_bwd_ckpt(m, n, d, b, gpr) != SKM_OK || !supported_pair(io_dtype, lut_dtype)) return 0;
   if (io_dtype == SKM_F32) return need_dlut ? align256((size_t)m * (size_t)d * 4) : 0;
   return skm::bwd_ckpt_bytes(Problem{m, n, d, b, gpr}, io_dtype, lut_dtype, need_dx != 0, need_dlut != 0);
 }
@@ -337,10 +344,8 @@ int sketch_matmul_bwd_ckpt(const void* dY, const int8_t* codes, const uint8_t* s
                            const uint8_t* idx_packed, const void* lut, int lut_dtype, int64_t m, int64_t n, int64_t d,
                            int b, int gpr, float* dX, float* dLUT, int accumulate, void* workspace,
                            size_t workspace_bytes, hipStream_t stream) {
-  int st = check_shape(m, n, d, b, gpr);
-  if (st == SKM_OK) st = check_ckpt_shape(m, d);
+  int st = check_bwd_ckpt(m, n, d, b, gpr);
   if (st != SKM_OK) return st;
-  if (m > 0 && n > (int64_t(1) << 34) / m) return SKM_EINVAL;
   if (!supported_pair(io_dtype, lut_dtype)) return SKM_EUNSUPPORTED;
   if (accumulate != 0 && accumulate != 1) return SKM_EINVAL;
   if (!idx_packed || !lut) return SKM_EINVAL;

@@ -237,3 +237,11 @@ def test_wrappers_check_tensors_before_the_call():
         _lib.sketch_xent_bwd(X, idx, lut, t, torch.zeros(3), torch.zeros(4), 4, 2)
     with pytest.raises(TypeError, match="dloss"):
         _lib.sketch_xent_bwd(X, idx, lut, t, torch.zeros(4), torch.zeros(4, dtype=torch.float16), 4, 2)
+
+
+def test_bwd_ckpt_of_more_rows_than_a_launch_takes(lib):
+    """2^22 blocks of 128 weight rows x a group, 512 threads each, is what one launch of the table gradient takes."""
+    most = (1 << 29) // 2
+    assert bwd(lib, m=1, n=most + 1) == EINVAL and bwd(lib, m=1, n=1 << 31, gpr=1, d=32) == EINVAL
+    assert bwd(lib, m=1, n=most, ws=None) == EWS
+    assert _lib.sketch_matmul_bwd_ckpt_workspace(1, most + 1, 512, 4, 2, F16, F16) == 0
