@@ -563,13 +563,19 @@ template <typename T> T* at(void* ws, size_t off) { return reinterpret_cast<T*>(
 // 4096 columns, 16 / 32 / 64 tokens 36 / 64 / 117 against 105; 16000 of 2048, 32
 // / 64 / 160 tokens 31 / 54 / 121 against 59; 4000 of 4096, 64 / 160 / 300 / 500
 // tokens 23 / 45 / 77 / 124 against 100; 2048 of 1024, 160 / 500 tokens 19 / 46
-// against 38.
+// against 38. The gradient takes the same rule (its dZ has to come from the
+// logits that lse came from); there the decode's two-byte stores bring the
+// crossover forward a little, at most 8 % of a call (dX alone, us): 32000 of
+// 4096, 16 / 32 / 48 / 64 tokens 115 / 145 / 176 / 207 against 172 to 180; 16000
+// of 2048, 32 / 64 / 160 tokens 70 / 100 / 184 against 88 / 93 / 103; 4000 of
+// 4096, 160 / 300 / 500 tokens 78 / 120 / 175 against 134 / 141 / 146.
 bool xent_few(const Problem& p) {
   const int64_t groups = (p.m + 15) / 16, tiles = (p.m + 255) / 256 * ((p.n + XENT_BN - 1) / XENT_BN);
   const double decode = (double)(groups * p.n) * (0.4e-3 + 0.14e-6 * (double)p.d);
   const int64_t blocks = ((p.n + 15) / 16 + 7) / 8 * 8 * groups;
   return decode <= (double)((tiles + 255) / 256) * (10.0 + 0.021 * (double)p.d) &&
-         blocks <= (int64_t(1) << 22) &&  // (a launch has fewer than 2^32 threads)
+         // (a launch has fewer than 2^32 threads: 512 per block here, 1024 per token in k_xent_merge_few)
+         blocks <= (int64_t(1) << 22) && p.m < (int64_t(1) << 22) &&
          decode_supported(Problem{p.m < 16 ? p.m : 16, p.n, p.d, p.b, p.gpr});
 }
 
