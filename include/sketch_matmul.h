@@ -341,8 +341,11 @@ size_t sketch_xent_fwd_workspace(int64_t m, int64_t n, int64_t d, int b, int gpr
  * that is more; for bf16 X the tokens are compared by |dloss| times the largest
  * |X| of their row, and X is taken exactly down to 2^-28 of that largest |X|
  * and to 2^-39 of it below. Both are deterministic (no atomics). workspace: at least
- * sketch_xent_bwd_workspace(...) bytes (up to 256 MiB of dZ, two or more fp32
- * dX, and for dLUT one X); need_dx / need_dlut = 0 where the output is NULL.
+ * sketch_xent_bwd_workspace(...) bytes (dZ in one 16-bit form for dX, two for
+ * dLUT, three for both of BF16 X: together up to 256 MiB, or 256 words of every
+ * token where that is more, 512 bytes per token and form; two or more fp32 dX;
+ * for dLUT one X, and one more copy of X for b = 4); need_dx / need_dlut = 0
+ * where the output is NULL.
  * With m == 0 and accumulate == 0 dLUT is written as zeros. Dtypes, sizes and
  * alignment as for sketch_xent_fwd.
  */

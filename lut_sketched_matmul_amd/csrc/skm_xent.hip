@@ -496,7 +496,9 @@ struct BwdPlan {
 
 // The pieces: dZ of a piece takes 2 bytes per (token, word) and form, and is
 // written once and read by two products; 256 MB of it stays in the memory-side
-// cache, and more rows per piece only save re-reading dX's fp32 sums.
+// cache, and more rows per piece only save re-reading dX's fp32 sums. A piece
+// has at least one tile of words, which is more than that from 175 000 tokens
+// (three forms) to 524 000 (one) on.
 constexpr size_t XENT_PIECE_BYTES = size_t(256) << 20;
 
 BwdPlan bwd_plan(const Problem& p, int x_dtype, int lut_dtype, bool need_dx, bool need_dlut) {

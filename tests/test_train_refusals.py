@@ -245,3 +245,19 @@ def test_bwd_ckpt_of_more_rows_than_a_launch_takes(lib):
     assert bwd(lib, m=1, n=most + 1) == EINVAL and bwd(lib, m=1, n=1 << 31, gpr=1, d=32) == EINVAL
     assert bwd(lib, m=1, n=most, ws=None) == EWS
     assert _lib.sketch_matmul_bwd_ckpt_workspace(1, most + 1, 512, 4, 2, F16, F16) == 0
+
+
+@pytest.mark.parametrize("m,n,dt,need,forms", [
+    (4096, 128256, BF16, (True, False), 1), (4096, 128256, F16, (True, True), 2), (4096, 128256, BF16, (True, True), 3),
+    (1 << 22, 512, F16, (True, False), 1), (1 << 22, 512, F16, (False, True), 2), (1 << 22, 512, BF16, (True, True), 3),
+])
+def test_xent_bwd_workspace_is_as_stated(m, n, dt, need, forms):
+    """dZ: 256 MiB, or 512 bytes per token and form; beside it the other terms of the header, d = 32 columns."""
+    d, gpr = 32, 1
+    got = _lib.sketch_xent_bwd_workspace(m, n, d, 4, gpr, dt, F16, *need)
+    tiles = m // 256
+    dx = max(2, 512 // tiles) * m * d * 4 if need[0] else 0
+    tables = 64 * n * gpr * 16 * 4 if need[1] else 0                 # partial tables, when the row blocks are few
+    vectors = 6 * (m * 4 + 256)
+    assert got <= max(1 << 28, 512 * m * forms) + dx + 2 * (2 * m * d + 256) + tables + vectors
+    assert got >= min(1 << 28, 512 * m * forms) // 2
