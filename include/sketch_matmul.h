@@ -334,20 +334,22 @@ size_t sketch_xent_fwd_workspace(int64_t m, int64_t n, int64_t d, int b, int gpr
  *   dX   = dZ * W              [m][d] x_dtype, zeros for ignored tokens
  *   dLUT = table gradient      [n][gpr][2^b] fp32; accumulate == 1 adds to it
  * each NULL = skip. The logits are recomputed a piece of the vocabulary at a
- * time. dX is the fp32 sum of products with dZ rounded once to the tables'
- * dtype (the target's term with its fp32 remainder; f16 operands hold |dZ| down
- * to 2^-28 of the token's |dloss| at full precision and end at 2^-39 of it, for
- * F16 X with both gradients of the largest |dloss|). dLUT takes dZ to 2^-23 of itself, or to 2^-39 of the largest |dloss| where
- * that is more; for bf16 X the tokens are compared by |dloss| times the largest
- * |X| of their row, and X is taken exactly down to 2^-28 of that largest |X|
- * and to 2^-39 of it below. Both are deterministic (no atomics). workspace: at least
- * sketch_xent_bwd_workspace(...) bytes (dZ in one 16-bit form for dX, two for
- * dLUT, three for both of BF16 X: together up to 256 MiB, or 256 words of every
- * token where that is more, 512 bytes per token and form; two or more fp32 dX;
- * for dLUT one X, and one more copy of X for b = 4); need_dx / need_dlut = 0
- * where the output is NULL.
- * With m == 0 and accumulate == 0 dLUT is written as zeros. Dtypes, sizes and
- * alignment as for sketch_xent_fwd.
+ * time. Both gradients are fp32 sums in a fixed order (deterministic, no
+ * atomics) of products whose dZ is an operand of the matrix cores:
+ *   dX    takes dZ rounded once to the tables' dtype, the target's term with its
+ *         fp32 remainder. F16 operands hold |dZ| down to 2^-28 of the token's
+ *         |dloss| at full precision and end at 2^-39 of it (F16 X with both
+ *         gradients: of the largest |dloss|).
+ *   dLUT  takes dZ to 2^-23 of itself, or to 2^-39 of the largest |dloss| where
+ *         that is more. For BF16 X the tokens are compared by |dloss| times the
+ *         largest |X| of their row, and X is taken exactly down to 2^-28 of
+ *         that largest |X| and to 2^-39 of it below.
+ * workspace: at least sketch_xent_bwd_workspace(...) bytes (dZ in one 16-bit
+ * form for dX, two for dLUT or for both of F16 X, three for both of BF16 X:
+ * together up to 256 MiB, or 512 bytes per token and form where that is more;
+ * two or more fp32 dX; for dLUT one X; one more copy of X for b = 4); need_dx /
+ * need_dlut = 0 where the output is NULL. With m == 0 and accumulate == 0 dLUT
+ * is written as zeros. Dtypes, sizes and alignment as for sketch_xent_fwd.
  */
 int sketch_xent_bwd(const void* X, int x_dtype, const uint8_t* idx_packed, const void* lut, int lut_dtype,
                     const int64_t* targets, int64_t ignore_index, const float* lse, const float* dloss,

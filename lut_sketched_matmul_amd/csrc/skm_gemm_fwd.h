@@ -431,12 +431,14 @@ k_gemm_fwd(const TX* __restrict__ X, const uint8_t* __restrict__ idx_packed, con
   #pragma unroll
       for (int i = 0; i < 4; ++i)
   #pragma unroll
-        for (int jj = 0; jj < 2; ++jj) acc[i][jj] = EP::SWAP ? MF::run(fb0[jj], fa0[i], acc[i][jj]) : MF::run(fa0[i], fb0[jj], acc[i][jj]);
+        for (int jj = 0; jj < 2; ++jj)
+          acc[i][jj] = EP::SWAP ? MF::run(fb0[jj], fa0[i], acc[i][jj]) : MF::run(fa0[i], fb0[jj], acc[i][jj]);
       load_frags(fa1, fb1, k, 1);
   #pragma unroll
       for (int i = 0; i < 4; ++i)
   #pragma unroll
-        for (int jj = 0; jj < 2; ++jj) acc[i][jj] = EP::SWAP ? MF::run(fb1[jj], fa1[i], acc[i][jj]) : MF::run(fa1[i], fb1[jj], acc[i][jj]);
+        for (int jj = 0; jj < 2; ++jj)
+          acc[i][jj] = EP::SWAP ? MF::run(fb1[jj], fa1[i], acc[i][jj]) : MF::run(fa1[i], fb1[jj], acc[i][jj]);
       __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);  // reads of the first half
   #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -739,7 +741,9 @@ k_gemm_fwd64(const TX* __restrict__ X, const uint8_t* __restrict__ idx_packed, c
   #pragma unroll
         for (int i = 0; i < 4; ++i)
   #pragma unroll
-          for (int jj = 0; jj < 2; ++jj) acc[i][jj] = EP::SWAP ? MF::run(fb[ks][jj], fa[ks][i], acc[i][jj]) : MF::run(fa[ks][i], fb[ks][jj], acc[i][jj]);
+          for (int jj = 0; jj < 2; ++jj)
+            acc[i][jj] = EP::SWAP ? MF::run(fb[ks][jj], fa[ks][i], acc[i][jj])
+                                  : MF::run(fa[ks][i], fb[ks][jj], acc[i][jj]);
       // each quarter's fragment reads interleaved with the previous quarter's MFMAs
       __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
   #pragma unroll

@@ -572,8 +572,8 @@ hipError_t norm_bwd_wide(const NormArgs& a, const NormBwd& q, hipStream_t s) {
   }
   if (!q.part_w && !q.part_b) return hipSuccess;
   const dim3 grid((unsigned)((a.d + 2047) / 2048), (unsigned)bwd_blocks(a.m, a.d));
-  hipLaunchKernelGGL((k_norm_cols<T, AL, DYF, CK>), grid, dim3(256), 0, s, q.dY, (const T*)q.X, q.codes, q.scales, q.mean, q.rstd, a.m, (int)a.d, q.part_w,
-                     q.part_b);
+  hipLaunchKernelGGL((k_norm_cols<T, AL, DYF, CK>), grid, dim3(256), 0, s, q.dY, (const T*)q.X, q.codes, q.scales,
+                     q.mean, q.rstd, a.m, (int)a.d, q.part_w, q.part_b);
   return hipGetLastError();
 }
 

@@ -318,8 +318,9 @@ __global__ void __launch_bounds__(1024) k_xent_mean(const float* __restrict__ lo
 // ---- backward --------------------------------------------------------------------------
 
 // Xc[c] = X[rows[c]] in f16 for the listed tokens (bf16 rows prescaled by 2^-e,
-// e = zexp: their largest value then lies in [2^14, 2^15)), zeros up to the next multiple of 32 (whole steps of the table
-// gradient's tiles); 16 bytes per thread and round
+// e = zexp: their largest value then lies in [2^14, 2^15)), zeros up to the next
+// multiple of 32 (whole steps of the table gradient's tiles); 16 bytes per thread
+// and round
 template <typename TX>
 __global__ void __launch_bounds__(256) k_xent_gather(const TX* __restrict__ X, const int32_t* __restrict__ rows,
                                                      const int32_t* __restrict__ zexp,
@@ -438,7 +439,8 @@ hipError_t dx_out_t(const XentArgs& a, const DxOut& o, void* dX, hipStream_t s) 
   const int64_t cols = 2048 / lanes;
   auto go = [&](auto kern) {
     hipLaunchKernelGGL(kern, dim3((unsigned)p.m, (unsigned)((p.d + cols - 1) / cols)), dim3(256), 0, s, o.acc,
-                       lanes, o.pos, o.head, o.dloss, o.rest, a.targets, a.idx, (const TL*)a.lut, p.n, p.d, p.gpr, (TX*)dX);
+                       lanes, o.pos, o.head, o.dloss, o.rest, a.targets, a.idx, (const TL*)a.lut, p.n, p.d, p.gpr,
+                       (TX*)dX);
     return hipGetLastError();
   };
   if (p.b == 2) return go(k_xent_dx_out<2, TX, TL>);

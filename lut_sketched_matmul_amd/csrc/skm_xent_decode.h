@@ -12,7 +12,7 @@ namespace skm {
 namespace {
 
 // part[t0 + token][block] = (max, sum of exp(z - max)) over the block's 16 words
-template <typename TX> struct EpDecodeStats {
+struct EpDecodeStats {
   static constexpr bool GROUPS = true;
   struct Args {
     const int64_t* targets;  // [m]

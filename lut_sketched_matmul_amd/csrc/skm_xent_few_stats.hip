@@ -8,7 +8,7 @@ namespace {
 
 template <typename TX, typename TL>
 hipError_t few_t(const XentGemm& g, float2* part, int64_t blocks, float* tlogit, hipStream_t s) {
-  typedef EpDecodeStats<TX> EP;
+  typedef EpDecodeStats EP;
   const typename EP::Args a{g.targets, part, blocks, tlogit, 0};
   if (g.p.b == 2) return xent_decode<2, TX, TL, EP>(g, a, s);
   if (g.p.b == 3) return xent_decode<3, TX, TL, EP>(g, a, s);

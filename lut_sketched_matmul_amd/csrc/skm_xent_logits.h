@@ -134,7 +134,8 @@ k_xent_logits(const TL* __restrict__ Xp, const uint8_t* __restrict__ idx_packed,
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj)
-          acc[i][jj] = EP::SWAP ? MF::run(fb[ks][jj], fa[ks][i], acc[i][jj]) : MF::run(fa[ks][i], fb[ks][jj], acc[i][jj]);
+          acc[i][jj] = EP::SWAP ? MF::run(fb[ks][jj], fa[ks][i], acc[i][jj])
+                                : MF::run(fa[ks][i], fb[ks][jj], acc[i][jj]);
     __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
 #pragma unroll
     for (int ks = 1; ks < 4; ++ks) {

@@ -8,7 +8,7 @@ namespace {
 
 template <int B, typename TX, typename TL>
 hipError_t stats_b(const XentGemm& g, float2* part, int64_t stride, float* tlogit, hipStream_t s) {
-  typedef EpStats<TX> EP;
+  typedef EpStats EP;
   typename EP::Args a;
   a.rows = g.rows;
   a.count = &g.head->count;

@@ -31,7 +31,7 @@ constexpr int col_of_output(int e) { return 32 * (e >> 4) + 8 * ((e & 15) >> 2) 
 // EpStats: part[(n0 / 256) * stride + c] = (max, sum of exp(z - max)) over the
 // block's columns for listed token c; tlogit[c] = the target's logit (written
 // by the one lane that holds it).
-template <typename TX> struct EpStats {
+struct EpStats {
   static constexpr bool SWAP = true, ROWS = true;
   struct Args : XentRows {
     float2* part;
