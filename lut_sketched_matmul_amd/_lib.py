@@ -211,6 +211,14 @@ def _matrix(t, name: str):
     return t.shape
 
 
+def _gradient(out, shape, accumulate: bool, device):
+    """The fp32 output a call writes, or adds to: `out`, else a new one (of zeros when there is to be added)."""
+    if out is not None:
+        return out
+    torch = _torch()
+    return (torch.zeros if accumulate else torch.empty)(shape, dtype=torch.float32, device=device)
+
+
 def sketch_matmul_fwd_workspace(m: int, n: int, d: int, b: int, gpr: int, x_dtype: int, lut_dtype: int) -> int:
     """Bytes of device workspace sketch_matmul_fwd needs for these sizes and dtypes."""
     return int(lib().sketch_matmul_fwd_workspace(m, n, d, b, gpr, x_dtype, lut_dtype))
@@ -317,7 +325,8 @@ def sketch_matmul_bwd(dY, X, idx_packed, lut, b: int, gpr: int, d: Optional[int]
     dX = torch.empty((m, d), dtype=torch.float32, device=dY.device) if need_dx else None
     dL = None
     if need_dlut:
-        dL = dlut_out if dlut_out is not None else torch.empty((n, gpr, K), dtype=torch.float32, device=dY.device)
+        with torch.cuda.stream(stream):  # (where a new output's zeros have to be written)
+            dL = _gradient(dlut_out, (n, gpr, K), accumulate, dY.device)
     workspace = _workspace(workspace, sketch_matmul_bwd_workspace(m, n, d, b, gpr, dtype_code(dY), dtype_code(lut)),
                            dY.device)
     st = lib().sketch_matmul_bwd(
@@ -627,7 +636,7 @@ def sketch_matmul_bwd_ckpt(dY, codes, scales, idx_packed, lut, b: int, gpr: int,
         dX = torch.empty((m, d), dtype=torch.float32, device=dY.device) if need_dx else None
         dL = None
         if need_dlut:
-            dL = dlut_out if dlut_out is not None else torch.empty((n, gpr, K), dtype=torch.float32, device=dY.device)
+            dL = _gradient(dlut_out, (n, gpr, K), accumulate, dY.device)
         ws = _workspace(workspace, sketch_matmul_bwd_ckpt_workspace(m, n, d, b, gpr, io, lt, need_dx, need_dlut),
                         dY.device)
         st = lib().sketch_matmul_bwd_ckpt(_ptr(dY), _ptr(codes), _ptr(scales), io, idx_packed.data_ptr(),
@@ -749,9 +758,9 @@ def sketch_norm_bwd(dY, X, weight, mean, rstd, kind: str = "layer", need_dx: boo
         dX = torch.empty((m, d), dtype=xt, device=dev) if need_dx else None
         dw = db = None
         if need_dw:
-            dw = dw_out if dw_out is not None else torch.empty(d, dtype=torch.float32, device=dev)
+            dw = _gradient(dw_out, (d,), accumulate, dev)
         if need_db:
-            db = db_out if db_out is not None else torch.empty(d, dtype=torch.float32, device=dev)
+            db = _gradient(db_out, (d,), accumulate, dev)
         need = sketch_norm_bwd_workspace(m, d) if need_dw or need_db else 0
         ws = _workspace(workspace, need, dev)
         st = lib().sketch_norm_bwd(_ptr(dY), dtype_code(dY), _ptr(X), xc, _ptr(codes), _ptr(scales),
@@ -843,7 +852,7 @@ def sketch_xent_bwd(X, idx_packed, lut, targets, lse, dloss, b: int, gpr: int, i
     """(dX, dLUT) of sketch_xent_fwd's losses: dX [m, d] in X's dtype, dLUT fp32 [n, gpr, 2^b]; None if not asked.
 
     lse [m] as sketch_xent_fwd gave it, dloss [m] fp32 the gradient of every token's loss. dlut_out: optional
-    fp32 [n, gpr, 2^b] to write (accumulate=True adds to it). The other arguments are the forward's.
+    fp32 [n, gpr, 2^b] to write (accumulate=True adds to it; to zeros without it). The other arguments are the forward's.
     """
     torch = _torch()
     m, n, d = _check_xent(X, idx_packed, lut, targets, b, gpr, lse=lse, dloss=dloss)
@@ -856,7 +865,7 @@ def sketch_xent_bwd(X, idx_packed, lut, targets, lse, dloss, b: int, gpr: int, i
         dX = torch.empty((m, d), dtype=X.dtype, device=X.device) if need_dx else None
         dL = None
         if need_dlut:
-            dL = dlut_out if dlut_out is not None else torch.empty((n, gpr, K), dtype=torch.float32, device=X.device)
+            dL = _gradient(dlut_out, (n, gpr, K), accumulate, X.device)
         ws = _workspace(workspace, sketch_xent_bwd_workspace(m, n, d, b, gpr, xc, lc, need_dx, need_dlut), X.device)
         st = lib().sketch_xent_bwd(_ptr(X), xc, idx_packed.data_ptr(), lut.data_ptr(), lc, _ptr(targets), ignore_index,
                                    _ptr(lse), _ptr(dloss), m, n, d, b, gpr, _ptr(dX), _ptr(dL),
