@@ -371,6 +371,121 @@ int sketch_xent_mean(const float* loss, const int64_t* targets, int64_t ignore_i
                      float* mean, float* weight, hipStream_t stream);
 
 /*
+ * Dropout, with the residual it is added to:
+ *   Y[i] = [residual[i] +] (keep(i) ? X[i] / (1 - p') : 0),  i < count
+ * p' = round(65536 p) / 65536. keep(i) is computed, not stored: half-word i % 8
+ * (low halves first) of Philox4x32-10 (Salmon et al., "Parallel random numbers:
+ * as easy as 1, 2, 3") with key seed[0] and counter (i / 8, seed[1]) is at least
+ * 65536 p'. The same seed gives the same mask, so the gradient of X is the same
+ * call on Y's gradient without a residual.
+ *   X, residual, Y  [count] x_dtype (F32, F16 or BF16); residual NULL = none.
+ *                   Computed in fp32, rounded once. Values that do not stay do not
+ *                   count, whatever they hold.
+ *   seed            int64 [2] on the device (read when the work runs, so a
+ *                   captured call follows what is written there; NULL if p' == 0)
+ * 0 <= p <= 1 (1 keeps none), 0 <= count <= 2^40. Pointers 16-byte aligned, seed
+ * 8-byte; Y must not overlap an input.
+ */
+int sketch_dropout(const void* X, int x_dtype, const void* residual, int64_t count, double p, const int64_t* seed,
+                   void* Y, hipStream_t stream);
+
+/*
+ * Low-rank adapters of many requests beside one shared projection, s = adapter[t]:
+ *   H[t] = A[s] D(X[t]),   Y[t] = base[t] + scale[s] B[s] H[t]
+ * with D dropout as above over the elements of X (p == 0: none).
+ *   X [m][d], A [n_adapters][r][d], B [n_adapters][n][r], base [m][n], Y [m][n]
+ *               all in `dtype` (F16 or BF16). base NULL = zeros; Y may be base.
+ *   adapter     int32 [m] (device), NULL = every token has adapter 0. Tokens
+ *               whose value is outside [0, n_adapters) have none: Y is base.
+ *   scale       fp32 [n_adapters], NULL = ones
+ *   H           fp32 [m][r], zeros for tokens without an adapter; NULL = not
+ *               wanted (the backward pass takes it)
+ * H and its sums are fp32 (as operand of the second product two 16-bit terms);
+ * Y is rounded once. Adapters of smaller rank are filled up with zeros. An
+ * infinity or NaN in a token or an adapter gives infinities or NaN in what it
+ * reaches and nothing elsewhere.
+ * m <= 2^22, n <= 2^24, d a multiple of 32 and <= 2^20, m * n and m * d <= 2^34,
+ * 1 <= r <= 128, 1 <= n_adapters <= 2^20. Pointers 16-byte aligned (adapter and
+ * scale 4, seed 8); outputs must not overlap inputs or each other, except Y the
+ * base. workspace: sketch_adapter_fwd_workspace(...) bytes; has_ids: whether
+ * adapter is given. m == 0 is a no-op.
+ */
+int sketch_adapter_fwd(const void* X, const void* A, const void* B, int dtype, const int32_t* adapter, int n_adapters,
+                       const float* scale, const void* base, double p, const int64_t* seed, int64_t m, int64_t n,
+                       int64_t d, int r, void* Y, float* H, void* workspace, size_t workspace_bytes,
+                       hipStream_t stream);
+
+size_t sketch_adapter_fwd_workspace(int64_t m, int64_t n, int64_t d, int r, int n_adapters, int has_ids);
+
+/*
+ * Its backward pass, from the H it wrote and the same X, A, B, adapter, scale, p
+ * and seed, with dH[t] = scale[s] B[s]^T dY[t]:
+ *   dX[t] = base_dx[t] + D'(A[s]^T dH[t])      [m][d] dtype, rounded once
+ *   dA[s] = sum over s's tokens of dH[t] D(X[t])^T          [n_adapters][r][d] fp32
+ *   dB[s] = sum over s's tokens of scale[s] dY[t] H[t]^T    [n_adapters][n][r] fp32
+ * each NULL = skip. base_dx fp32 [m][d] (the dX of sketch_matmul_bwd; NULL = zeros)
+ * is all that reaches dX for tokens without an adapter; adapters without tokens get
+ * zeros. accumulate == 1 adds to dA and dB. The sums over tokens are fp32 in a
+ * fixed order (deterministic, no atomics) of products that keep 24 bits. X is read
+ * for dA only, H for dB only (NULL otherwise). n_adapters <= 4096; everything else
+ * as above. With m == 0 and accumulate == 0 dA and dB are written as zeros.
+ */
+int sketch_adapter_bwd(const void* dY, const void* X, const float* H, const void* A, const void* B, int dtype,
+                       const int32_t* adapter, int n_adapters, const float* scale, const float* base_dx, double p,
+                       const int64_t* seed, int64_t m, int64_t n, int64_t d, int r, void* dX, float* dA, float* dB,
+                       int accumulate, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t sketch_adapter_bwd_workspace(int64_t m, int64_t n, int64_t d, int r, int n_adapters, int has_ids, int need_dx,
+                                    int need_da, int need_db);
+
+/*
+ * The query and key heads between a projection and attention: the root-mean-
+ * square norm of every head (norm == 1) and the rotation by its position, for
+ * head x [head_dim] of token t:
+ *   z = norm ? x / sqrt(mean(x^2) + eps) * weight : x
+ *   (y[a], y[b]) = (z[a] c - z[b] s, z[a] s + z[b] c),  c, s = cos, sin(positions[t] inv_freq[i])
+ * for the rot_dim / 2 pairs (a, b) = (i, i + rot_dim / 2) (SKM_PAIRS_HALVES) or
+ * (2 i, 2 i + 1) (SKM_PAIRS_NEIGHBOURS); columns from rot_dim on are z.
+ *   Q, K       row t at Q + t * ldq, its q_heads (k_heads) heads side by side; the
+ *              columns of a joined q/k/v projection are taken where they lie.
+ *              x_dtype F32, F16 or BF16. k_heads == 0: no K (K, Kout NULL).
+ *   Qout, Kout row t at Qout + t * ldqo; may be Q and K with their strides (in
+ *              place), else must not overlap an input.
+ *   positions  int64 [m], of magnitude up to 2^40. inv_freq fp64 [rot_dim / 2]
+ *              (e.g. theta^(-2 i / rot_dim)). Angles are fp64, computed here.
+ *   weights    fp32 [head_dim], NULL = ones (unread without the norm)
+ * fp32 inside, rounded once. 0 <= m < 2^31, head_dim and rot_dim even, 2 <= rot_dim
+ * <= head_dim <= 1024, at most 65536 heads a side, strides (in elements) at least
+ * a row and m strides at most 2^40. Rows are aligned to an element (16-byte rows,
+ * head_dim and rot_dim multiples of 16 are the fast case), positions and inv_freq
+ * to 8 bytes, weights to 16.
+ */
+enum { SKM_PAIRS_HALVES = 0, SKM_PAIRS_NEIGHBOURS = 1 };
+
+int sketch_rotary_fwd(const void* Q, int64_t ldq, int q_heads, const void* K, int64_t ldk, int k_heads, int x_dtype,
+                      const int64_t* positions, const double* inv_freq, const float* q_weight, const float* k_weight,
+                      int64_t m, int head_dim, int rot_dim, int pairs, int norm, float eps, void* Qout, int64_t ldqo,
+                      void* Kout, int64_t ldko, hipStream_t stream);
+
+/*
+ * Its backward pass: dXq, dXk the gradients of Q and K from dQ, dK (of Qout, Kout),
+ * all strided rows of x_dtype, and with the norm dq_weight, dk_weight fp32
+ * [head_dim] (NULL = skip; accumulate == 1 adds; sums in a fixed order). Q and K
+ * are read with the norm only. dXq and dXk may lie in one joined buffer; outputs
+ * must not overlap inputs. workspace: sketch_rotary_bwd_workspace(head_dim) bytes when a
+ * weight gradient is given. With m == 0 and accumulate == 0 those are written as
+ * zeros (k_heads == 0: dk_weight too).
+ */
+int sketch_rotary_bwd(const void* dQ, int64_t lddq, int q_heads, const void* dK, int64_t lddk, int k_heads,
+                      int x_dtype, const void* Q, int64_t ldq, const void* K, int64_t ldk, const int64_t* positions,
+                      const double* inv_freq, const float* q_weight, const float* k_weight, int64_t m, int head_dim,
+                      int rot_dim, int pairs, int norm, float eps, void* dXq, int64_t ldxq, void* dXk, int64_t ldxk,
+                      float* dq_weight, float* dk_weight, int accumulate, void* workspace, size_t workspace_bytes,
+                      hipStream_t stream);
+
+size_t sketch_rotary_bwd_workspace(int head_dim);
+
+/*
  * Dequantise W[i][j] = lut[i][j/G][idx[i][j]] into a dense [n][d] array of
  * lut_dtype (SpaLLM Eq. (1) with groups per row). A checking aid: the matmul
  * entry points never build W.

@@ -13,8 +13,13 @@ from ._lib import (  # noqa: F401
     lib,
     sketch_act_dequant,
     sketch_act_quant,
+    sketch_adapter_bwd,
+    sketch_adapter_bwd_workspace,
+    sketch_adapter_fwd,
+    sketch_adapter_fwd_workspace,
     sketch_column_weights,
     sketch_dequant,
+    sketch_dropout,
     sketch_hessian_factor,
     sketch_lloyd,
     sketch_lut_adam_step,
@@ -31,6 +36,9 @@ from ._lib import (  # noqa: F401
     sketch_norm_bwd,
     sketch_norm_bwd_workspace,
     sketch_norm_fwd,
+    sketch_rotary_bwd,
+    sketch_rotary_bwd_workspace,
+    sketch_rotary_fwd,
     sketch_unpack_indices,
     sketch_xent_bwd,
     sketch_xent_bwd_workspace,

@@ -81,6 +81,22 @@ _SIGNATURES = {
     "sketch_xent_bwd": (_c_int, [_c_vp, _c_int, _c_vp, _c_vp, _c_int, _c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_i64,
                                  _c_i64, _c_int, _c_int, _c_vp, _c_vp, _c_int, _c_vp, _c_size, _c_vp]),
     "sketch_xent_bwd_workspace": (_c_size, [_c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int]),
+    "sketch_dropout": (_c_int, [_c_vp, _c_int, _c_vp, _c_i64, ctypes.c_double, _c_vp, _c_vp, _c_vp]),
+    "sketch_adapter_fwd": (_c_int, [_c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_int, _c_vp, _c_vp, ctypes.c_double, _c_vp,
+                                    _c_i64, _c_i64, _c_i64, _c_int, _c_vp, _c_vp, _c_vp, _c_size, _c_vp]),
+    "sketch_adapter_fwd_workspace": (_c_size, [_c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int]),
+    "sketch_adapter_bwd": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_int, _c_vp, _c_vp,
+                                    ctypes.c_double, _c_vp, _c_i64, _c_i64, _c_i64, _c_int, _c_vp, _c_vp, _c_vp,
+                                    _c_int, _c_vp, _c_size, _c_vp]),
+    "sketch_adapter_bwd_workspace": (_c_size, [_c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                               _c_int]),
+    "sketch_rotary_fwd": (_c_int, [_c_vp, _c_i64, _c_int, _c_vp, _c_i64, _c_int, _c_int, _c_vp, _c_vp, _c_vp, _c_vp,
+                                   _c_i64, _c_int, _c_int, _c_int, _c_int, _c_f32, _c_vp, _c_i64, _c_vp, _c_i64,
+                                   _c_vp]),
+    "sketch_rotary_bwd": (_c_int, [_c_vp, _c_i64, _c_int, _c_vp, _c_i64, _c_int, _c_int, _c_vp, _c_i64, _c_vp, _c_i64,
+                                   _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_f32, _c_vp,
+                                   _c_i64, _c_vp, _c_i64, _c_vp, _c_vp, _c_int, _c_vp, _c_size, _c_vp]),
+    "sketch_rotary_bwd_workspace": (_c_size, [_c_int]),
     "sketch_status_str": (ctypes.c_char_p, [_c_int]),
     "sketch_version": (_c_int, []),
 }
@@ -874,3 +890,273 @@ def sketch_xent_bwd(X, idx_packed, lut, targets, lse, dloss, b: int, gpr: int, i
         _leave(context)
     _check("sketch_xent_bwd", st)
     return dX, dL
+
+
+# --------------------------------------------------------------------------
+# dropout, low-rank adapters, norm and rotation of heads
+# --------------------------------------------------------------------------
+
+def _check_dropout(p: float, seed, size: str = "p"):
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"{size} = {p} is not a probability")
+    _expect(seed, "seed", shape=(2,), dtypes=("int64",))
+    if seed is None and p * 65536 + 0.5 >= 1.0:
+        raise ValueError("dropout needs a seed")
+
+
+def sketch_dropout(X, p: float, seed=None, residual=None, out=None, stream=None):
+    """residual + dropout(X): every value of X is 0 with probability p, else divided by 1 - p (p to 2^-16).
+
+    X (f32/f16/bf16, any shape), residual and out of X's shape and dtype. seed: int64 [2] on the GPU, (key, stream
+    number), read when the work runs; the mask is computed from it and from a value's number and is never stored, so
+    the gradient of X is the same call on the gradient.
+    """
+    torch = _torch()
+    _expect(X, "X", dtypes=_FLOAT_DTYPES)
+    _check_dropout(p, seed)
+    name = (_dtype_name(X),)
+    _expect(residual, "residual", shape=X.shape, dtypes=name)
+    _expect(out, "out", shape=X.shape, dtypes=name)
+    sp, context = _enter(stream, X, residual, seed, out)
+    try:
+        if out is None:
+            out = torch.empty_like(X)
+        st = lib().sketch_dropout(_ptr(X), dtype_code(X), _ptr(residual), X.numel(), p, _ptr(seed), _ptr(out), sp)
+    finally:
+        _leave(context)
+    _check("sketch_dropout", st)
+    return out
+
+
+def _check_adapter(X, A, B, adapter, scale):
+    """(m, n, d, r, n_adapters) of X [m, d], A [n_adapters, r, d], B [n_adapters, n, r] in one 16-bit dtype."""
+    m, d = _matrix(X, "X")
+    if A.dim() != 3 or B.dim() != 3:
+        raise ValueError("A and B must have the adapters as the first of three dimensions")
+    S, r = A.shape[0], A.shape[1]
+    n = B.shape[1]
+    name = (_dtype_name(X),)
+    _expect(X, "X", dtypes=("float16", "bfloat16"))
+    _expect(A, "A", shape=(S, r, d), dtypes=name)
+    _expect(B, "B", shape=(S, n, r), dtypes=name)
+    _expect(adapter, "adapter", shape=(m,), dtypes=("int32",))
+    _expect(scale, "scale", shape=(S,), dtypes=("float32",))
+    return m, n, d, r, S
+
+
+def sketch_adapter_fwd_workspace(m: int, n: int, d: int, r: int, n_adapters: int, has_ids: bool = True) -> int:
+    """Bytes of device workspace sketch_adapter_fwd needs for these sizes (has_ids: with a token's adapter given)."""
+    return int(lib().sketch_adapter_fwd_workspace(m, n, d, r, n_adapters, 1 if has_ids else 0))
+
+
+def sketch_adapter_fwd(X, A, B, base=None, adapter=None, scale=None, p: float = 0.0, seed=None, out=None,
+                       need_h: bool = False, workspace=None, stream=None) -> Tuple[object, object]:
+    """(Y, H): Y[t] = base[t] + scale[s] B[s] H[t], H[t] = A[s] dropout(X[t]), s = adapter[t].
+
+    X [m, d], A [n_adapters, r, d], B [n_adapters, n, r] and base [m, n] (None = zeros) f16 or bf16, all the same.
+    adapter int32 [m]: a token's adapter, outside [0, n_adapters) = none (None: all have adapter 0); scale fp32
+    [n_adapters] (None = ones). p, seed: dropout of X as in sketch_dropout. out: optional output, may be base itself.
+    need_h: also return H, fp32 [m, r], which the backward pass takes (None otherwise).
+    """
+    torch = _torch()
+    m, n, d, r, S = _check_adapter(X, A, B, adapter, scale)
+    _check_dropout(p, seed)
+    name = (_dtype_name(X),)
+    _expect(base, "base", shape=(m, n), dtypes=name)
+    _expect(out, "out", shape=(m, n), dtypes=name)
+    _expect(workspace, "workspace", dtypes=("uint8",))
+    sp, context = _enter(stream, X, A, B, base, adapter, scale, seed, out, workspace)
+    try:
+        if out is None:
+            out = X.new_empty((m, n))
+        H = X.new_empty((m, r), dtype=torch.float32) if need_h else None
+        ws = _workspace(workspace, sketch_adapter_fwd_workspace(m, n, d, r, S, adapter is not None), X.device)
+        st = lib().sketch_adapter_fwd(_ptr(X), _ptr(A), _ptr(B), dtype_code(X), _ptr(adapter), S, _ptr(scale),
+                                      _ptr(base), p, _ptr(seed), m, n, d, r, _ptr(out), _ptr(H), _ptr(ws), _size(ws),
+                                      sp)
+    finally:
+        _leave(context)
+    _check("sketch_adapter_fwd", st)
+    return out, H
+
+
+def sketch_adapter_bwd_workspace(m: int, n: int, d: int, r: int, n_adapters: int, has_ids: bool = True,
+                                 need_dx: bool = True, need_da: bool = True, need_db: bool = True) -> int:
+    """Bytes of device workspace sketch_adapter_bwd needs for these sizes."""
+    return int(lib().sketch_adapter_bwd_workspace(m, n, d, r, n_adapters, 1 if has_ids else 0, 1 if need_dx else 0,
+                                                  1 if need_da else 0, 1 if need_db else 0))
+
+
+def sketch_adapter_bwd(dY, X, H, A, B, base_dx=None, adapter=None, scale=None, p: float = 0.0, seed=None,
+                       need_dx: bool = True, need_da: bool = True, need_db: bool = True, da_out=None, db_out=None,
+                       accumulate: bool = False, workspace=None, stream=None):
+    """(dX, dA, dB) of sketch_adapter_fwd; None where not asked for.
+
+    dY [m, n] in X's dtype, H as the forward gave it (None if dB is not asked for), the other arguments the forward's.
+    dX [m, d] in X's dtype is base_dx (fp32 [m, d], None = zeros) plus the adapters' part; dA, dB fp32 in the shapes
+    of A and B (da_out / db_out: optional outputs, accumulate=True adds to them).
+    """
+    torch = _torch()
+    m, n, d, r, S = _check_adapter(X, A, B, adapter, scale)
+    _check_dropout(p, seed)
+    _expect(dY, "dY", shape=(m, n), dtypes=(_dtype_name(X),))
+    if need_db and H is None:
+        raise ValueError("the gradient of B needs H")
+    _expect(H, "H", shape=(m, r), dtypes=("float32",))
+    _expect(base_dx, "base_dx", shape=(m, d), dtypes=("float32",))
+    _expect(da_out, "da_out", shape=(S, r, d), dtypes=("float32",))
+    _expect(db_out, "db_out", shape=(S, n, r), dtypes=("float32",))
+    _expect(workspace, "workspace", dtypes=("uint8",))
+    sp, context = _enter(stream, dY, X, H, A, B, base_dx, adapter, scale, seed, da_out, db_out, workspace)
+    try:
+        dev = X.device
+        dX = torch.empty_like(X) if need_dx else None
+        dA = dB = None
+        if need_da:
+            dA = _gradient(da_out, (S, r, d), accumulate, dev)
+        if need_db:
+            dB = _gradient(db_out, (S, n, r), accumulate, dev)
+        ws = _workspace(workspace, sketch_adapter_bwd_workspace(m, n, d, r, S, adapter is not None, need_dx, need_da,
+                                                                need_db), dev)
+        st = lib().sketch_adapter_bwd(_ptr(dY), _ptr(X), _ptr(H), _ptr(A), _ptr(B), dtype_code(X), _ptr(adapter), S,
+                                      _ptr(scale), _ptr(base_dx), p, _ptr(seed), m, n, d, r, _ptr(dX), _ptr(dA),
+                                      _ptr(dB), 1 if accumulate else 0, _ptr(ws), _size(ws), sp)
+    finally:
+        _leave(context)
+    _check("sketch_adapter_bwd", st)
+    return dX, dA, dB
+
+
+_PAIRS = {"halves": 0, "neighbours": 1}
+
+
+def _pairs(pairs: str) -> int:
+    if pairs not in _PAIRS:
+        raise ValueError(f"pairs = {pairs!r}: supported are 'halves' and 'neighbours'")
+    return _PAIRS[pairs]
+
+
+def _head_rows(t, name: str, like=None):
+    """(address, elements from token to token) of heads [m, heads, head_dim] whose heads lie side by side."""
+    if t is None:
+        return None, 0
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have three dimensions (tokens, heads, columns), got {t.dim()}")
+    m, h, dh = t.shape
+    if like is not None:
+        _expect(t, name, shape=like.shape, dtypes=(_dtype_name(like),))
+        if t.get_device() != like.get_device():
+            raise ValueError(f"{name} must live where the heads do")
+    if not t.is_cuda:
+        raise ValueError("tensors must live on the GPU")
+    ld, sh, sc = t.stride()
+    if (dh > 1 and sc != 1) or (h > 1 and sh != dh) or (m > 1 and ld < h * dh):
+        raise ValueError(f"{name}: the heads of a token must lie side by side")
+    return t.data_ptr(), (ld if m > 1 else h * dh)
+
+
+def _check_rotary(q, k, positions, inv_freq, q_weight, k_weight, eps):
+    qp, ldq = _head_rows(q, "q")
+    m, hq, dh = q.shape
+    _expect(q, "q", dtypes=_FLOAT_DTYPES)
+    kp, ldk = _head_rows(k, "k")
+    hk = 0
+    if k is not None:
+        hk = k.shape[1]
+        _expect(k, "k", shape=(m, hk, dh), dtypes=(_dtype_name(q),))
+        if k.get_device() != q.get_device():
+            raise ValueError("q and k must live on one GPU")
+    _expect(positions, "positions", shape=(m,), dtypes=("int64",))
+    _expect(inv_freq, "inv_freq", dtypes=("float64",))
+    if inv_freq.dim() != 1 or not 1 <= inv_freq.numel() <= dh // 2:
+        raise ValueError(f"inv_freq must be a vector of 1 to {dh // 2} frequencies, got {tuple(inv_freq.shape)}")
+    if eps is None and (q_weight is not None or k_weight is not None):
+        raise ValueError("weights belong to a norm: give its eps")
+    _expect(q_weight, "q_weight", shape=(dh,), dtypes=("float32",))
+    _expect(k_weight, "k_weight", shape=(dh,), dtypes=("float32",))
+    if positions.get_device() != q.get_device():
+        raise ValueError("positions must live where the heads do")
+    return m, hq, hk, dh, qp, ldq, kp, ldk
+
+
+def sketch_rotary_fwd(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: Optional[float] = None,
+                      pairs: str = "halves", q_out=None, k_out=None, stream=None) -> Tuple[object, object]:
+    """(q', k'): the heads q [m, heads, head_dim] and k (None = none) normed and turned by their positions.
+
+    f32/f16/bf16; rows may be strided (the q and k columns of a joined projection). positions int64 [m], inv_freq
+    float64 [rot_dim / 2]: pair i of a head turns by positions[t] * inv_freq[i], columns from rot_dim on stay. pairs:
+    "halves" (i, i + rot_dim / 2) or "neighbours" (2 i, 2 i + 1). eps: of the root-mean-square norm of every head
+    (None = no norm), q_weight / k_weight its fp32 [head_dim] weights (None = ones). q_out / k_out: optional outputs,
+    also q and k themselves.
+    """
+    m, hq, hk, dh, qp, ldq, kp, ldk = _check_rotary(q, k, positions, inv_freq, q_weight, k_weight, eps)
+    pc = _pairs(pairs)
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    sp, context = _enter(stream, positions, inv_freq, q_weight, k_weight)
+    try:
+        if q_out is None:
+            q_out = q.new_empty((m, hq, dh))
+        if k is not None and k_out is None:
+            k_out = q.new_empty((m, hk, dh))
+        qo, ldqo = _head_rows(q_out, "q_out", q)
+        ko, ldko = _head_rows(k_out, "k_out", k)
+        st = lib().sketch_rotary_fwd(qp, ldq, hq, kp, ldk, hk, dtype_code(q), _ptr(positions), _ptr(inv_freq),
+                                     _ptr(q_weight), _ptr(k_weight), m, dh, 2 * inv_freq.numel(), pc,
+                                     0 if eps is None else 1, 0.0 if eps is None else eps, qo, ldqo, ko, ldko, sp)
+    finally:
+        _leave(context)
+    _check("sketch_rotary_fwd", st)
+    return q_out, k_out
+
+
+def sketch_rotary_bwd_workspace(head_dim: int) -> int:
+    """Bytes of device workspace sketch_rotary_bwd needs for weight gradients."""
+    return int(lib().sketch_rotary_bwd_workspace(head_dim))
+
+
+def sketch_rotary_bwd(dq, dk, q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: Optional[float] = None,
+                      pairs: str = "halves", need_dw: bool = True, q_out=None, k_out=None, qw_out=None, kw_out=None,
+                      accumulate: bool = False, workspace=None, stream=None):
+    """(dq_in, dk_in, dq_weight, dk_weight) of sketch_rotary_fwd; the weights' gradients fp32 [head_dim], with a norm
+    and need_dw only (else None).
+
+    dq, dk: gradients of the outputs, strided rows of the heads' dtype; the other arguments the forward's. q_out /
+    k_out: optional outputs for the heads' gradients (strided rows, e.g. of one joined buffer); qw_out / kw_out for
+    the weights' (accumulate=True adds to them).
+    """
+    m, hq, hk, dh, qp, ldq, kp, ldk = _check_rotary(q, k, positions, inv_freq, q_weight, k_weight, eps)
+    pc = _pairs(pairs)
+    if (dk is None) != (k is None) or (k is None and (k_out is not None or kw_out is not None)):
+        raise ValueError("dk, k_out and kw_out go with k")
+    if eps is None and (qw_out is not None or kw_out is not None):
+        raise ValueError("weights belong to a norm: give its eps")
+    dqp, lddq = _head_rows(dq, "dq", q)
+    dkp, lddk = _head_rows(dk, "dk", k)
+    _expect(qw_out, "qw_out", shape=(dh,), dtypes=("float32",))
+    _expect(kw_out, "kw_out", shape=(dh,), dtypes=("float32",))
+    _expect(workspace, "workspace", dtypes=("uint8",))
+    need_dw = need_dw and eps is not None
+    sp, context = _enter(stream, positions, inv_freq, q_weight, k_weight, qw_out, kw_out, workspace)
+    try:
+        dev = q.device
+        if q_out is None:
+            q_out = q.new_empty((m, hq, dh))
+        if k is not None and k_out is None:
+            k_out = q.new_empty((m, hk, dh))
+        qo, ldqo = _head_rows(q_out, "q_out", q)
+        ko, ldko = _head_rows(k_out, "k_out", k)
+        dqw = dkw = ws = None
+        if need_dw:
+            dqw = _gradient(qw_out, (dh,), accumulate, dev)
+            if k is not None:
+                dkw = _gradient(kw_out, (dh,), accumulate, dev)
+            ws = _workspace(workspace, sketch_rotary_bwd_workspace(dh), dev)
+        st = lib().sketch_rotary_bwd(dqp, lddq, hq, dkp, lddk, hk, dtype_code(q), qp, ldq, kp, ldk, _ptr(positions),
+                                     _ptr(inv_freq), _ptr(q_weight), _ptr(k_weight), m, dh, 2 * inv_freq.numel(), pc,
+                                     0 if eps is None else 1, 0.0 if eps is None else eps, qo, ldqo, ko, ldko,
+                                     _ptr(dqw), _ptr(dkw), 1 if accumulate else 0, _ptr(ws), _size(ws), sp)
+    finally:
+        _leave(context)
+    _check("sketch_rotary_bwd", st)
+    return q_out, k_out, dqw, dkw

@@ -5,6 +5,7 @@
 #include <cmath>
 #include <mutex>
 
+#include "skm_abi_util.h"
 #include "skm_common.h"
 #include "skm_launch.h"
 
@@ -15,18 +16,14 @@
 constexpr size_t kScratchBytes = size_t(8) << 20;
 __device__ __align__(256) unsigned char scratch[kScratchBytes];
 
+using namespace skm::abi;
+
 namespace {
 
 using skm::Problem;
 
 constexpr int kVersion = 100;  // 0.1.0
 constexpr int64_t kMaxFactorD = int64_t(1) << 16;  // sketch_hessian_factor: the tile grid stays below 2^31 blocks
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int elem_bytes(int dt) { return dt == SKM_F32 ? 4 : 2; }
-
-bool valid_dtype(int dt) { return dt == SKM_F32 || dt == SKM_F16 || dt == SKM_BF16; }
 
 // (activation dtype, table dtype) pairs with a kernel
 bool supported_pair(int x_dt, int lut_dt) {
@@ -45,24 +42,6 @@ int check_shape(int64_t m, int64_t n, int64_t d, int b, int gpr) {
   if (n > (int64_t(1) << 31) || d > (int64_t(1) << 31) || m > (int64_t(1) << 31)) return SKM_EINVAL;
   return SKM_OK;
 }
-
-struct Range {
-  const void* p;
-  int64_t bytes;
-};
-
-bool overlap(Range a, Range b) {
-  if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-  return a0 < b0 + (uintptr_t)b.bytes && b0 < a0 + (uintptr_t)a.bytes;
-}
-
-int status_of(hipError_t e) { return e == hipSuccess ? SKM_OK : SKM_EHIP; }
-
-// finite and at least lo
-bool finite_in(float v, float lo) { return std::isfinite(v) && v >= lo; }
-
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // bf16 activations with f16 tables: the matrix-core operands are f16, and
 // the activations (forward) or output gradients (dX) are prescaled per row

@@ -176,6 +176,63 @@ size_t xent_bwd_bytes(const Problem& p, int x_dtype, int lut_dtype, bool need_dx
 hipError_t launch_xent_bwd(const XentArgs& a, const float* lse, const float* dloss, void* dX, float* dLUT,
                            int accumulate, void* ws, hipStream_t s);
 
+// dropout (skm_philox.h): values whose 16 random bits are below `threshold` go,
+// the others are divided by the share that stays; threshold 0 = none go (seed unread)
+struct Dropout {
+  uint32_t threshold;  // 0..65536
+  const int64_t* seed;
+  float stay() const { return (float)(65536 - threshold) / 65536.f; }
+  float inv() const { return threshold < 65536 ? (float)(65536.0 / (65536 - threshold)) : 0.f; }
+};
+hipError_t launch_dropout(const void* X, int x_dtype, const void* residual, int64_t count, const Dropout& d, void* Y,
+                          hipStream_t s);
+
+// norm and rotation of the query and key heads (skm_rotary.hip); row strides in elements
+constexpr int kMaxHeadDim = 1024;
+struct RotarySide {
+  const void* x;   // heads (backward: NULL without a norm)
+  const void* dy;  // backward: the outputs' gradient
+  void* y;         // outputs, or the heads' gradient
+  int64_t ldx, lddy, ldy;
+  const float* w;  // NULL = ones
+  int heads;       // 0 = no such side
+};
+struct RotaryArgs {
+  RotarySide q, k;
+  const int64_t* pos;
+  const double* freq;
+  int64_t m;
+  int dh, rot, neighbours, norm;
+  float eps;
+};
+hipError_t launch_rotary_fwd(const RotaryArgs& a, int x_dtype, hipStream_t s);
+// weight gradients into dqw / dkw (NULL = skip) through part (NULL = neither)
+size_t rotary_bwd_part_bytes(int64_t dh);
+hipError_t launch_rotary_bwd(const RotaryArgs& a, int x_dtype, float* dqw, float* dkw, int accumulate, float* part,
+                             hipStream_t s);
+
+// low-rank adapters beside a projection (skm_adapter.h), 16-bit operands
+struct AdapterArgs {
+  const void* X;       // [m][d]
+  int dtype;           // DT_F16 or DT_BF16, of X, A, B, base and Y
+  const void* A;       // [S][r][d]
+  const void* B;       // [S][n][r]
+  const int32_t* ids;  // [m], NULL = all 0
+  const float* scale;  // [S], NULL = ones
+  Dropout drop;
+  int64_t m, n, d;
+  int r, S;
+};
+constexpr int kMaxAdapterRank = 128;
+constexpr int kMaxGradAdapters = 4096;  // adapters of one backward call (skm_adapter_grad.hip: one LDS counter each)
+size_t adapter_fwd_bytes(const AdapterArgs& a);
+// Y = base (NULL = zeros) + the adapters' products; H [m][r] fp32 (NULL = not wanted)
+hipError_t launch_adapter_fwd(const AdapterArgs& a, const void* base, void* Y, float* H, void* ws, hipStream_t s);
+size_t adapter_bwd_bytes(const AdapterArgs& a, bool need_dx, bool need_da, bool need_db);
+// dX = base_dx (fp32, NULL = zeros) + the adapters' part; dX, dA, dB: NULL = skip
+hipError_t launch_adapter_bwd(const AdapterArgs& a, const void* dY, const float* H, const float* base_dx, void* dX,
+                              float* dA, float* dB, int accumulate, void* ws, hipStream_t s);
+
 // sketch construction: column weights 1 / [H^-1]_jj from the factor U, the
 // weighted Lloyd tables, and the error-compensated mapping (Wc is overwritten;
 // E holds map_workspace_bytes(n))

@@ -14,6 +14,10 @@ writes that checkpoint in its own pass (and keeps its own input in 8 bits for
 its backward: dX is then that of the checkpoint). :class:`SketchedHead` is the vocabulary
 projection with its cross entropy loss, whose logits are never stored.
 
+Beside a layer can stand low-rank adapters of many requests (``adapter=SketchAdapter(...)``, with dropout in front
+while training). :class:`SketchDropout` drops and adds a residual, :class:`SketchRotary` norms and turns the query and
+key heads of a projection; no mask and no angle is stored.
+
 Every compute step runs in the HIP library (forward, dX, dLUT, norms, loss,
 optimizer step); this module only marshals arguments. Three small torch
 operations remain in the glue: the fp32 input gradient is cast to the
@@ -213,6 +217,205 @@ class _MeanFunction(torch.autograd.Function):
         return weight * dmean, None, None
 
 
+class DropoutFunction(torch.autograd.Function):
+    """residual + dropout(X); the mask is computed again from the seed in the backward pass."""
+
+    @staticmethod
+    def forward(ctx, X, residual, p: float, seed):
+        ctx.save_for_backward(seed)
+        ctx.p = p
+        return _lib.sketch_dropout(_packed(X), p, seed, residual=None if residual is None else _packed(residual))
+
+    @staticmethod
+    def backward(ctx, dY):
+        (seed,) = ctx.saved_tensors
+        dX = _lib.sketch_dropout(_packed(dY), ctx.p, seed) if ctx.needs_input_grad[0] else None
+        return dX, dY if ctx.needs_input_grad[1] else None, None, None
+
+
+class AdapterMatmulFunction(torch.autograd.Function):
+    """Y = X Wᵀ + the adapters' products; gradients for X, the master tables and the adapters' masters.
+
+    The matmul's fp32 dX goes into the adapters' backward, which adds its part and rounds once.
+    """
+
+    @staticmethod
+    def forward(ctx, X, lut_master, lut, idx_packed, b: int, gpr: int, A_master, B_master, A, B, ids, scale,
+                p: float, seed):
+        X = _packed(X)
+        Y = _lib.sketch_matmul_fwd(X, idx_packed, lut, b, gpr)
+        Y, H = _lib.sketch_adapter_fwd(X, A, B, Y, adapter=ids, scale=scale, p=p, seed=seed, out=Y,
+                                       need_h=ctx.needs_input_grad[7])
+        need = ctx.needs_input_grad
+        ctx.save_for_backward(X if need[1] or need[6] else None, H, lut, idx_packed, A, B, ids, scale, seed)
+        ctx.b, ctx.gpr, ctx.p, ctx.shape, ctx.dtype = b, gpr, p, X.shape, X.dtype
+        return Y
+
+    @staticmethod
+    def backward(ctx, dY):
+        X, H, lut, idx_packed, A, B, ids, scale, seed = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dY = _check_dy(dY, ctx.dtype)
+        base_dx = dL = None
+        if need[0] or need[1]:
+            base_dx, dL = _lib.sketch_matmul_bwd(dY, X if need[1] else None, idx_packed, lut, ctx.b, ctx.gpr,
+                                                 d=ctx.shape[1], need_dx=need[0], need_dlut=need[1])
+        if X is None:  # (not read, its shape and dtype are)
+            X = dY.new_empty(ctx.shape)
+        dX, dA, dB = _lib.sketch_adapter_bwd(dY, X, H, A, B, base_dx, adapter=ids, scale=scale, p=ctx.p, seed=seed,
+                                             need_dx=need[0], need_da=need[6], need_db=need[7])
+        return (dX, dL, None, None, None, None, dA, dB) + (None,) * 6
+
+
+class RotaryFunction(torch.autograd.Function):
+    """Heads q [m, heads, head_dim] and k (or None), normed (eps given) and turned; gradients for both and the weights."""
+
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, eps, pairs: str):
+        q, k = _heads(q), _heads(k)
+        out = _lib.sketch_rotary_fwd(q, k, positions, inv_freq, q_weight, k_weight, eps=eps, pairs=pairs)
+        ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
+        ctx.eps, ctx.pairs = eps, pairs
+        return out
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        q, k, q_weight, k_weight, positions, inv_freq = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        out = _lib.sketch_rotary_bwd(_heads(dq), _heads(dk), q, k, positions, inv_freq, q_weight, k_weight, eps=ctx.eps,
+                                     pairs=ctx.pairs, need_dw=need[2] or need[3])
+        return tuple(g if n else None for g, n in zip(out, need)) + (None,) * 4
+
+
+def _heads(t):
+    """t [m, heads, head_dim] with every token's heads side by side, as the library takes them."""
+    if t is None or (t.stride(2) == 1 and t.stride(1) == t.shape[2] and t.stride(0) >= t.shape[1] * t.shape[2]):
+        return t
+    return t.contiguous()
+
+
+class _Seed(torch.nn.Module):
+    """A dropout's random numbers: a key and the number of the next mask, on the GPU and in the state dict.
+
+    seed: the key (None = from torch's generator, so that modules differ and torch.manual_seed repeats them). The
+    number moves on in the stream's order, in replays of a captured step too.
+    """
+
+    def __init__(self, seed: Optional[int], device):
+        super().__init__()
+        key = int(torch.randint(0, (1 << 63) - 1, ()).item()) if seed is None else int(seed)
+        self.register_buffer("state", torch.tensor([key, 0], dtype=torch.int64, device=device))
+
+    @torch.no_grad()
+    def next(self):
+        seed = self.state.clone()
+        self.state[1:] += 1
+        return seed
+
+
+def _check_p(p: float) -> float:
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p = {p} is not a probability")
+    return float(p)
+
+
+class SketchDropout(torch.nn.Module):
+    """residual + dropout(X) while training, residual + X else (the residual may be left out)."""
+
+    def __init__(self, p: float, seed: Optional[int] = None, device="cuda"):
+        super().__init__()
+        self.p = _check_p(p)
+        self.seed = _Seed(seed, device)
+
+    def forward(self, X, residual=None):
+        if self.training and self.p > 0.0:
+            return DropoutFunction.apply(X, residual, self.p, self.seed.next())
+        return X if residual is None else DropoutFunction.apply(X, residual, 0.0, None)
+
+
+class SketchAdapter(torch.nn.Module):
+    """Low-rank adapters of rank r beside a sketched layer of n rows and d columns.
+
+    A [n_adapters, r, d] and B [n_adapters, n, r] are fp32 parameters with a 16-bit copy that the kernels read, as a
+    layer's tables (trained by :class:`LutAdam` / :class:`LutSGD`, which refresh the copy). A starts uniform in
+    +-1 / sqrt(d), B with zeros. scale: alpha / r for every adapter (alpha = r unless given). dropout: of the layer's
+    input in front of A, while training. compute_dtype must be the activations' dtype.
+    """
+
+    def __init__(self, n: int, d: int, r: int, n_adapters: int = 1, alpha: Optional[float] = None,
+                 dropout: float = 0.0, compute_dtype=torch.float16, seed: Optional[int] = None, device="cuda"):
+        super().__init__()
+        if compute_dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError("adapters compute in float16 or bfloat16")
+        if not 1 <= r <= 128 or n_adapters < 1:
+            raise ValueError(f"{n_adapters} adapters of rank {r}: at least one, of rank 1 to 128")
+        self.p = _check_p(dropout)
+        self.A_master = torch.nn.Parameter((torch.rand((n_adapters, r, d), device=device) * 2 - 1) / d ** 0.5)
+        self.B_master = torch.nn.Parameter(torch.zeros((n_adapters, n, r), device=device))
+        self.register_buffer("A", self.A_master.detach().to(compute_dtype))
+        self.register_buffer("B", self.B_master.detach().to(compute_dtype))
+        scale = (r if alpha is None else float(alpha)) / r
+        self.register_buffer("scale", torch.full((n_adapters,), scale, dtype=torch.float32, device=device))
+        self.seed = _Seed(seed, device)
+        self._link_copies()
+
+    def _link_copies(self) -> None:
+        # (as SketchedLinear._link_copy)
+        self.A_master._skm_copy, self.B_master._skm_copy = self.A, self.B
+
+    def refresh_copies(self) -> None:
+        """Round the masters into the compute copies (after changing them outside the optimizers)."""
+        self.A.copy_(self.A_master.detach())
+        self.B.copy_(self.B_master.detach())
+
+    def arguments(self):
+        """(p, seed) of this pass: dropout while training only."""
+        self._link_copies()
+        return (self.p, self.seed.next()) if self.training and self.p > 0.0 else (0.0, None)
+
+
+class SketchRotary(torch.nn.Module):
+    """Norm (optional) and position rotation of the query and key heads of a projection, in one pass.
+
+    theta: frequencies theta^(-2 i / rot_dim), or give inv_freq (float64 [rot_dim / 2]). rot_dim: leading columns of a
+    head that turn (all unless given). norm: root-mean-square norm of every head, with fp32 weights for query and key
+    heads (ones unless given). pairs: "halves" or "neighbours". forward(q, k, positions): heads [m, heads, head_dim],
+    also as strided views of a joined projection (``q.unflatten(1, (heads, head_dim))``), positions int64 [m].
+    """
+
+    def __init__(self, head_dim: int, theta: float = 10000.0, rot_dim: Optional[int] = None, inv_freq=None,
+                 norm: bool = False, eps: float = 1e-6, pairs: str = "halves", q_weight=None, k_weight=None,
+                 device="cuda"):
+        super().__init__()
+        _lib._pairs(pairs)
+        if inv_freq is None:
+            rot = head_dim if rot_dim is None else rot_dim
+            if rot % 2 or not 2 <= rot <= head_dim:
+                raise ValueError(f"rot_dim = {rot} of {head_dim} columns: an even number of them")
+            inv_freq = float(theta) ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+        elif rot_dim is not None and rot_dim != 2 * inv_freq.numel():
+            raise ValueError(f"{inv_freq.numel()} frequencies for {rot_dim} columns")
+        if not norm and (q_weight is not None or k_weight is not None):
+            raise ValueError("weights belong to a norm")
+        self.pairs, self.eps = pairs, float(eps) if norm else None
+        self.register_buffer("inv_freq", inv_freq.to(device=device, dtype=torch.float64).contiguous().clone())
+
+        def param(t):
+            if not norm:
+                return None
+            if t is None:
+                return torch.nn.Parameter(torch.ones(head_dim, dtype=torch.float32, device=device))
+            if tuple(t.shape) != (head_dim,):
+                raise ValueError(f"heads of {head_dim} columns given {tuple(t.shape)} weights")
+            return torch.nn.Parameter(t.detach().to(torch.float32).contiguous().clone())
+
+        self.q_weight, self.k_weight = param(q_weight), param(k_weight)
+
+    def forward(self, q, k, positions):
+        return RotaryFunction.apply(q, k, self.q_weight, self.k_weight if k is not None else None, positions.contiguous(),
+                                    self.inv_freq, self.eps, self.pairs)
+
+
 class SketchNorm(torch.nn.Module):
     """Layer norm (kind "layer", with a bias) or root-mean-square norm (kind "rms") of rows of d columns.
 
@@ -252,18 +455,29 @@ class SketchedLinear(torch.nn.Module):
     own input is kept in 8 bits too, so dX and the gradients of the norm's weight and bias are those of that
     checkpoint (each value off by at most half a step of its 32-column block). While the tables need no gradient
     (``lut_master.requires_grad_(False)``) checkpoint changes nothing.
+
+    adapter: a :class:`SketchAdapter` whose products are added to the output; forward then takes the adapter of every
+    token too (int32 [m], outside [0, n_adapters) = none; left out: the first one). It reads the layer's input in full,
+    so it does not go with checkpoint.
     """
 
     def __init__(self, idx_packed, lut, d: int, b: int, gpr: int, compute_dtype=torch.float16,
-                 checkpoint: bool = False, norm: Optional[SketchNorm] = None):
+                 checkpoint: bool = False, norm: Optional[SketchNorm] = None,
+                 adapter: Optional[SketchAdapter] = None):
         super().__init__()
+        if adapter is not None:
+            if checkpoint:
+                raise ValueError("an adapter reads its layer's input in full: not with checkpoint")
+            if adapter.A.shape[2] != d or adapter.B.shape[1] != idx_packed.shape[0]:
+                raise ValueError(f"an adapter of {adapter.B.shape[1]} x {adapter.A.shape[2]} beside a layer of "
+                                 f"{idx_packed.shape[0]} x {d}")
         if norm is not None and norm.weight.numel() != d:
             raise ValueError(f"a norm of {norm.weight.numel()} columns in front of a layer of {d}")
         n = idx_packed.shape[0]
         if tuple(lut.shape) != (n, gpr, 1 << b) or idx_packed.shape[1] * 8 != d * b:
             raise ValueError("table or index shape does not match (n, gpr, 2^b) / (n, d*b/8)")
         self.d, self.b, self.gpr = d, b, gpr
-        self.checkpoint, self.norm = bool(checkpoint), norm
+        self.checkpoint, self.norm, self.adapter = bool(checkpoint), norm, adapter
         self.register_buffer("idx_packed", _packed(idx_packed))
         self.lut_master = torch.nn.Parameter(lut.detach().to(torch.float32).contiguous().clone())
         if compute_dtype == torch.float32:
@@ -289,8 +503,17 @@ class SketchedLinear(torch.nn.Module):
         if self.lut is not None:
             self.lut.copy_(self.lut_master.detach())
 
-    def forward(self, X):
+    def forward(self, X, adapter_ids=None):
         self._link_copy()
+        if self.adapter is not None:
+            a = self.adapter
+            p, seed = a.arguments()
+            X = X if self.norm is None else self.norm(X)
+            return AdapterMatmulFunction.apply(X, self.lut_master, self.compute_tables(), self.idx_packed, self.b,
+                                               self.gpr, a.A_master, a.B_master, a.A, a.B, adapter_ids, a.scale, p,
+                                               seed)
+        if adapter_ids is not None:
+            raise ValueError("adapter_ids for a layer without adapters")
         # (a function's needs_input_grad names parameters under no_grad too, where no backward will come)
         checkpoint = self.checkpoint and torch.is_grad_enabled()
         if self.norm is not None:
@@ -307,16 +530,18 @@ class GroupedSketchedLinear(torch.nn.Module):
     """Several sketched projections of the same input (q/k/v, gate/up) in one launch per pass.
 
     The projections' rows are stored back to back (indices and tables), so the forward, dX and dLUT
-    each run as one launch over all rows; forward returns one view per projection.
+    each run as one launch over all rows; forward returns one view per projection. An adapter spans all
+    of the rows.
     """
 
     def __init__(self, idx_list: Sequence, lut_list: Sequence, d: int, b: int, gpr: int,
-                 compute_dtype=torch.float16, checkpoint: bool = False, norm: Optional[SketchNorm] = None):
+                 compute_dtype=torch.float16, checkpoint: bool = False, norm: Optional[SketchNorm] = None,
+                 adapter: Optional[SketchAdapter] = None):
         super().__init__()
         self.sizes = [int(i.shape[0]) for i in idx_list]
         self.inner = SketchedLinear(torch.cat([i.contiguous() for i in idx_list], 0),
                                     torch.cat([t.detach() for t in lut_list], 0), d, b, gpr, compute_dtype,
-                                    checkpoint=checkpoint, norm=norm)
+                                    checkpoint=checkpoint, norm=norm, adapter=adapter)
 
     @property
     def lut_master(self):
@@ -326,8 +551,8 @@ class GroupedSketchedLinear(torch.nn.Module):
         """The master tables of each projection (views into the shared parameter)."""
         return list(torch.split(self.inner.lut_master, self.sizes, 0))
 
-    def forward(self, X):
-        Y = self.inner(X)
+    def forward(self, X, adapter_ids=None):
+        Y = self.inner(X, adapter_ids)
         return tuple(torch.split(Y, self.sizes, dim=1))
 
 
