@@ -33,6 +33,15 @@ namespace skm {
 namespace adapt {
 
 constexpr int WAVES = 4;  // of a block
+// Over this many tokens the waves of a block take tiles of their own and share the weights through LDS; up to it they
+// share a tile and take other columns. Forward calls of both forms (shared / not): 8 adapters of rank 16, 4096 ->
+// 11008, 256 tokens 16.0 / 10.7 us, 512 15.7 / 16.0, 1024 22.2 / 25.6; 4 of rank 64, 8192 -> 8192, 256 tokens 20.1 /
+// 18.2, 512 22.2 / 27.4, 1024 30.5 / 48.5; one of rank 16, 4096 -> 4096, within 10 % from 64 to 2048 tokens.
+constexpr int64_t kManyTokens = 512;
+// With many tokens and ranks over this one the waves of "down" share the weights, too (8 adapters of rank 64, 2048
+// tokens of 8192 columns: 25 us with the ranges' sum, against 27 to 33); below, a wave keeps its own (4096
+// columns, rank 16, 8192 tokens: 18 us against 19 and a sum more).
+constexpr int kSharedRank = 32;
 
 template <typename T> __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c);
 template <> __device__ __forceinline__ f32x4 mma<half_t>(u32x4 a, u32x4 b, f32x4 c) {
@@ -75,25 +84,17 @@ __device__ __forceinline__ float unpack(uint32_t w, int half) {
   return to_f32(__builtin_bit_cast(T, (uint16_t)(half ? w >> 16 : w & 0xFFFFu)));
 }
 
-// Term `term` of eight fp32 values in T: v rounded, then what is left of it
-// rounded, and so on (zeros behind a term that is not finite)
+// Eight fp32 values as two terms of T: rounded, and what that takes away rounded (zero beside a term that is not
+// finite)
 template <typename T>
-__device__ __forceinline__ u32x4 term_of(float (&v)[8], int term) {
-  u32x4 o = kZero4;
+__device__ __forceinline__ void split8(const float (&v)[8], u32x4& hi, u32x4& lo) {
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    if (i > term) break;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      o[j] = pack2<T>(v[2 * j], v[2 * j + 1]);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float t = unpack<T>(o[j], k), rest = v[2 * j + k] - t;
-        v[2 * j + k] = __builtin_isfinite(t) ? rest : 0.f;
-      }
-    }
+  for (int j = 0; j < 4; ++j) {
+    const float a = v[2 * j], b = v[2 * j + 1];
+    hi[j] = pack2<T>(a, b);
+    const float c = unpack<T>(hi[j], 0), d = unpack<T>(hi[j], 1);
+    lo[j] = pack2<T>(__builtin_isfinite(c) ? a - c : 0.f, __builtin_isfinite(d) ? b - d : 0.f);
   }
-  return o;
 }
 
 // Rows e = 0..7 of eight values each, turned: out[e] holds value e of every row
@@ -137,8 +138,9 @@ struct Down {
   Dropout drop;  // of P (threshold 0 = none)
   float* parts;
 };
-int down_splits(int64_t m, int64_t K, int S, int64_t& per);
-hipError_t launch_down(const Down& a, int dtype, hipStream_t s);
+int down_splits(int64_t m, int64_t K, int r, int S, int64_t& per);
+// (a.splits is what is left for the reader to add up)
+hipError_t launch_down(Down& a, int dtype, hipStream_t s);
 
 // "up": out [m][N] = base + sum over ranks of factor_t h_t[k] W[column][k], h_t the sum of
 // `splits` parts; forward: W = B, base and out of T; backward: W = A, base fp32, dropout

@@ -63,14 +63,23 @@ __device__ __forceinline__ int block_scan(int v, int* sh, int& all) {
 
 __device__ __forceinline__ int chunks_of(int count, int chunk) { return (count + chunk - 1) / chunk; }
 
-// One block per adapter: counts all adapters' tokens, then writes its own list, chunks and owner. The last block
-// marks the chunks nobody has. Sums over integers only: the order of the LDS atomics cannot show.
-__global__ __launch_bounds__(PLAN_THREADS) void k_adapt_plan(const int32_t* __restrict__ ids, int64_t m, int S,
-                                                             int chunk, int max_chunks, int32_t* order, Chunk* chunks,
-                                                             Owner* owners) {
-  extern __shared__ __align__(16) int hist[];  // [S]
-  __shared__ int sh[PLAN_THREADS / 64], mine[3];
-  const int me = blockIdx.x, lane = lane_id();
+struct Plan {
+  const int32_t* ids;
+  int64_t m;
+  int S, chunk, max_chunks, blocks;  // blocks: S, or 0 without a plan
+  int32_t* order;
+  Chunk* chunks;
+  Owner* owners;
+};
+// Block `me` of S: counts all adapters' tokens, then writes its own list, chunks and owner. The last block marks the
+// chunks nobody has. Sums over integers only: the order of the LDS atomics cannot show.
+__device__ __forceinline__ void plan_block(const Plan& a, int me, int* hist, int* sh, int* mine) {
+  const int32_t* __restrict__ ids = a.ids;
+  const int64_t m = a.m;
+  const int S = a.S, chunk = a.chunk, max_chunks = a.max_chunks, lane = lane_id();
+  int32_t* order = a.order;
+  Chunk* chunks = a.chunks;
+  Owner* owners = a.owners;
   for (int i = threadIdx.x; i < S; i += PLAN_THREADS) hist[i] = 0;
   __syncthreads();
   for (int64_t t = threadIdx.x; t < (m + 63) / 64 * 64; t += PLAN_THREADS) {
@@ -127,25 +136,38 @@ __global__ __launch_bounds__(PLAN_THREADS) void k_adapt_plan(const int32_t* __re
   }
 }
 
-// ---- operands --------------------------------------------------------------------
-
-// B [S][n][r] -> [S][r][ld], zeros from n on
-__global__ __launch_bounds__(256) void k_adapt_turn(const uint16_t* __restrict__ B, int64_t n, int r, int64_t ld,
-                                                    uint16_t* __restrict__ out) {
-  __shared__ uint16_t tile[64][kMaxAdapterRank + 2];
-  const int64_t i0 = (int64_t)blockIdx.x * 64, s = blockIdx.y;
-  const uint16_t* b = B + (s * n + i0) * r;
-  const int rows = (int)(n - i0 < 64 ? (n > i0 ? n - i0 : 0) : 64);
-  for (int e = threadIdx.x; e < 64 * r; e += 256) {
+// B [S][n][r] -> [S][r][ld], zeros from n on: block i turns 64 rows of one adapter
+struct Turn {
+  const uint16_t* B;
+  int64_t n, ld;
+  int r;
+  uint16_t* out;
+};
+__device__ __forceinline__ void turn_block(const Turn& a, int64_t block, uint16_t* tile) {
+  const int64_t per = a.ld / 64, s = block / per, i0 = block % per * 64, n = a.n;
+  const int r = a.r, ldt = r + 2;
+  const uint16_t* b = a.B + (s * n + i0) * r;
+  const int rows = (int)(n - i0 < 64 ? n - i0 : 64);
+  for (int e = threadIdx.x; e < 64 * r; e += PLAN_THREADS) {
     const int i = e / r, k = e - i * r;
-    tile[i][k] = i < rows ? b[e] : (uint16_t)0;
+    tile[i * ldt + k] = i < rows ? b[e] : (uint16_t)0;
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < 64 * r; e += 256) {
+  for (int e = threadIdx.x; e < 64 * r; e += PLAN_THREADS) {
     const int k = e >> 6, i = e & 63;
-    out[(s * r + k) * ld + i0 + i] = tile[i][k];
+    a.out[(s * r + k) * a.ld + i0 + i] = tile[i * ldt + k];
   }
 }
+
+// both, neither of which waits for the other: the first p.blocks blocks plan, the others turn
+__global__ __launch_bounds__(PLAN_THREADS) void k_adapt_prepare(Plan p, Turn t) {
+  extern __shared__ __align__(16) unsigned char smem[];  // S counters, or a tile of B
+  __shared__ int sh[PLAN_THREADS / 64], mine[3];
+  if ((int64_t)blockIdx.x < p.blocks) plan_block(p, blockIdx.x, (int*)smem, sh, mine);
+  else turn_block(t, (int64_t)blockIdx.x - p.blocks, (uint16_t*)smem);
+}
+
+// ---- operands --------------------------------------------------------------------
 
 struct Terms {
   const float* parts;  // [splits][m][ld]
@@ -154,8 +176,9 @@ struct Terms {
   uint32_t* out;       // NULL = not wanted
 };
 
-// The terms of h (or dh) by position: [step][term][rank][32 positions] bf16, ranks padded to 16, zeros where there
-// is no token or rank. A thread: two positions of one rank.
+// The terms of h (or dh) by position, as a matrix instruction's lanes want them: [step][term][16 ranks][lane][8
+// positions] bf16, lane l rank l % 16 and positions 8 (l / 16) .. of the step's 32; zeros where there is no token or
+// rank. A thread: two positions of one rank.
 __global__ __launch_bounds__(256) void k_adapt_terms(Terms a, Terms b, const int32_t* __restrict__ ids,
                                                      const float* __restrict__ scale,
                                                      const int32_t* __restrict__ order, int64_t m, int64_t positions,
@@ -183,7 +206,7 @@ __global__ __launch_bounds__(256) void k_adapt_terms(Terms a, Terms b, const int
 #pragma unroll
   for (int k = 0; k < GTERMS; ++k) {
     const uint32_t w = pack2<bf16_t>(v[0], v[1]);
-    t.out[((step * GTERMS + k) * rp16 + rank) * (STEP / 2) + pair] = w;
+    t.out[((step * GTERMS + k) * rp16 + (rank & ~15)) * (STEP / 2) + ((rank & 15) + 16 * (pair >> 2)) * 4 + (pair & 3)] = w;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const float u = unpack<bf16_t>(w, j);
@@ -205,47 +228,52 @@ struct Grad {
 };
 struct GradGrid {
   Grad b, a;            // dB, dA (columns 0 = not wanted)
-  int64_t strips_b;     // 128-column strips of dB
+  int64_t strips_b, strips;  // 128-column strips of dB, and of both
+  int64_t shuffle;
   const int32_t* order;
   const Chunk* chunks;  // NULL: chunk i is tokens [i chunk, (i + 1) chunk)
   int64_t m;
   int chunk, r, rp16, accumulate, single;  // single: without ids, one chunk in all
 };
 
-// a step's 32 tokens: eight rows of eight columns a lane, zeros where there is no token or column
+// a lane's eight tokens of a step, -1 past the chunk
+__device__ __forceinline__ void load_tokens(const GradGrid& a, int p0, int end, int (&tk)[8]) {
+  if (a.order) {
+    // (whole steps are listed: both vectors are there)
+    const int at = p0 < end ? p0 : 0;
+    const u32x4 lo = reinterpret_cast<const u32x4*>(a.order + at)[0], hi = reinterpret_cast<const u32x4*>(a.order + at)[1];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) tk[i] = p0 + i < end ? (int)(i < 4 ? lo[i & 3] : hi[i & 3]) : -1;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) tk[i] = p0 + i < end ? p0 + i : -1;
+  }
+}
+// their eight columns from col on, zeros where there is no token or column
 template <typename T, bool ALIGNED>
-__device__ __forceinline__ void load_rows(const Grad& g, const GradGrid& a, int64_t p0, int64_t end, int64_t col,
-                                          u32x4 (&row)[8], int64_t (&tk)[8]) {
+__device__ __forceinline__ void load_rows(const Grad& g, int64_t col, const int (&tk)[8], u32x4 (&row)[8]) {
+  if (ALIGNED || col + 8 <= g.N) {
+    const int64_t c = col < g.N ? col : 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t p = p0 + i;
-    tk[i] = p < end ? (a.order ? a.order[p] : p) : -1;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t t = tk[i] < 0 ? 0 : tk[i];
-    const T* ptr = (const T*)g.P + t * g.N + col;
-    if constexpr (ALIGNED) {
-      row[i] = *reinterpret_cast<const u32x4*>((const T*)g.P + t * g.N + (col + 8 <= g.N ? col : 0));
-      if (col + 8 > g.N) row[i] = kZero4;
-    } else {
-      if (col + 8 <= g.N) row[i] = load_any(ptr);
-      else row[i] = load_some(ptr, g.N - col);
+    for (int i = 0; i < 8; ++i) {
+      const T* p = (const T*)g.P + (int64_t)(tk[i] < 0 ? 0 : tk[i]) * g.N + c;
+      row[i] = ALIGNED ? *reinterpret_cast<const u32x4*>(p) : load_any(p);
     }
-  }
+  } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (tk[i] < 0) row[i] = kZero4;
+    for (int i = 0; i < 8; ++i)
+      row[i] = load_some((const T*)g.P + (int64_t)(tk[i] < 0 ? 0 : tk[i]) * g.N + col, g.N - col);
+  }
 }
 
-// two bf16 terms of packed f16 values (both exact together; see skm_adapter.h)
+// two bf16 terms of packed f16 values (exact together; an infinity's rest is NaN, and its sums are)
 __device__ __forceinline__ void split_f16(u32x4 v, u32x4& hi, u32x4& lo) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float a = unpack<half_t>(v[j], 0), b = unpack<half_t>(v[j], 1);
     hi[j] = pack2<bf16_t>(a, b);
     const float c = a - unpack<bf16_t>(hi[j], 0), d = b - unpack<bf16_t>(hi[j], 1);
-    lo[j] = pack2<bf16_t>(__builtin_isfinite(a) ? c : 0.f, __builtin_isfinite(b) ? d : 0.f);
+    lo[j] = pack2<bf16_t>(c, d);
   }
 }
 
@@ -253,16 +281,20 @@ template <typename T, int RT, bool ALIGNED>
 __global__ __launch_bounds__(64 * WAVES) void k_adapt_grad(GradGrid a) {
   __shared__ __align__(16) f32x4 sums[WAVES][8][64];
   const int lane = lane_id(), wave = threadIdx.x >> 6, row = lane & 15, q = lane >> 4;
-  const bool is_a = (int64_t)blockIdx.x >= a.strips_b;
+  // dA's blocks draw random numbers and take longer: block i takes the work of i times a number without a common
+  // divisor with their count, so that every CU gets some of both
+  const int64_t work = (int64_t)blockIdx.x * a.shuffle % gridDim.x;
+  const int64_t strip = work % a.strips, chunk_at = work / a.strips;
+  const bool is_a = strip >= a.strips_b;
   const Grad& g = is_a ? a.a : a.b;
-  const int64_t c0 = ((int64_t)blockIdx.x - (is_a ? a.strips_b : 0)) * 128, col = c0 + 8 * row;
-  const int r0 = (int)blockIdx.z * 16 * RT;
+  const int64_t c0 = (strip - (is_a ? a.strips_b : 0)) * 128, col = c0 + 8 * row;
+  const int r0 = (int)blockIdx.y * 16 * RT;
   Chunk ch;
   if (a.chunks) {
-    ch = a.chunks[blockIdx.y];
+    ch = a.chunks[chunk_at];
   } else {
-    const int64_t b = (int64_t)blockIdx.y * a.chunk, e = b + a.chunk;
-    ch = Chunk{(int32_t)b, (int32_t)(e < a.m ? e : a.m), 0, a.single ? -1 : (int32_t)blockIdx.y};
+    const int64_t b = chunk_at * a.chunk, e = b + a.chunk;
+    ch = Chunk{(int32_t)b, (int32_t)(e < a.m ? e : a.m), 0, a.single ? -1 : (int32_t)chunk_at};
   }
   if (ch.end <= ch.begin) return;
   const Philox rng = g.drop.threshold ? philox_of(g.drop.seed) : Philox{0u, 0u, 0u, 0u};
@@ -272,27 +304,40 @@ __global__ __launch_bounds__(64 * WAVES) void k_adapt_grad(GradGrid a) {
   for (int j = 0; j < RT; ++j)
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[j][e] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int64_t p0 = ch.begin + STEP * wave; p0 < ch.end; p0 += STEP * WAVES) {
-    u32x4 x[8], y[8];
-    int64_t tk[8];
-    load_rows<T, ALIGNED>(g, a, p0 + 8 * q, ch.end, col, x, tk);
+  const PhiloxMask mask = philox_mask_of(g.drop.threshold);
+
+  // one step: its terms, the next step's rows and the tokens of the one behind that on their way, then the products
+  constexpr int TURN = STEP * WAVES;
+  auto step = [&](int p0, u32x4 (&x)[8], int (&tk)[8], u32x4 (&x_next)[8], int (&tk_next)[8]) {
     u32x4 h[GTERMS][RT];
-    const uint16_t* tp = g.terms + (p0 / STEP) * (GTERMS * a.rp16 * STEP) + 8 * q;
+    const uint16_t* tp = g.terms + (int64_t)(p0 / STEP) * (GTERMS * a.rp16 * STEP) + 8 * lane;
 #pragma unroll
     for (int k = 0; k < GTERMS; ++k)
 #pragma unroll
       for (int j = 0; j < RT; ++j) {
-        const int rank = r0 + 16 * j + row;
+        const int rank = r0 + 16 * j;  // (ranks past the last are not kept)
         h[k][j] = *reinterpret_cast<const u32x4*>(tp + (k * a.rp16 + (rank < a.rp16 ? rank : 0)) * STEP);
       }
+    if (p0 + TURN < ch.end) load_rows<T, ALIGNED>(g, col, tk_next, x_next);
+    if (p0 + STEP > ch.end) {  // (the last step of a chunk)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (tk[i] < 0) x[i] = kZero4;
+    }
+    if (ALIGNED && col >= g.N) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = kZero4;
+    }
     if (g.drop.threshold) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const u32x4 rnd = philox_block(rng, (uint64_t)((tk[i] < 0 ? 0 : tk[i]) * g.N + col) / 8);
+        const u32x4 rnd = philox_block(rng, (uint64_t)((int64_t)(tk[i] < 0 ? 0 : tk[i]) * g.N + col) / 8);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[i][j] = philox_mask2(rnd, j, g.drop.threshold, x[i][j]);
+        for (int j = 0; j < 4; ++j) x[i][j] = philox_mask2(rnd[j], mask, x[i][j]);
       }
     }
+    load_tokens(a, p0 + 2 * TURN + 8 * q, ch.end, tk);
+    u32x4 y[8];
     turn8x8(x, y);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -315,6 +360,32 @@ __global__ __launch_bounds__(64 * WAVES) void k_adapt_grad(GradGrid a) {
           acc[j][e] = mma<bf16_t>(h[1][j], y[e], acc[j][e]);
           acc[j][e] = mma<bf16_t>(h[0][j], y[e], acc[j][e]);
         }
+      }
+    }
+  };
+  int t0[8], t1[8];
+  u32x4 x0[8], x1[8];
+  int p0 = ch.begin + STEP * wave;
+  load_tokens(a, p0 + 8 * q, ch.end, t0);
+  load_tokens(a, p0 + TURN + 8 * q, ch.end, t1);
+  if (p0 < ch.end) load_rows<T, ALIGNED>(g, col, t0, x0);
+  if constexpr (RT == 1) {
+    while (p0 < ch.end) {
+      step(p0, x0, t0, x1, t1);
+      p0 += TURN;
+      if (p0 >= ch.end) break;
+      step(p0, x1, t1, x0, t0);
+      p0 += TURN;
+    }
+  } else {  // (two copies of the step do not fit the registers)
+    for (; p0 < ch.end; p0 += TURN) {
+      step(p0, x0, t0, x1, t1);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int t = t0[i];
+        x0[i] = x1[i];
+        t0[i] = t1[i];
+        t1[i] = t;
       }
     }
   }
@@ -402,11 +473,11 @@ Layout layout_of(const AdapterArgs& a, bool need_dx, bool need_da, bool need_db)
   l.rp = padded_rank(a.r);
   l.rp16 = (a.r + 15) / 16 * 16;
   l.ldt = (a.n + 63) / 64 * 64;
-  l.splits = down_splits(a.m, a.n, (int)S, l.per);
-  // Chunks: as long as the launch keeps about four blocks per CU, since every chunk costs a partial gradient
-  // (written and read again); whole turns of the block's waves.
+  l.splits = down_splits(a.m, a.n, a.r, (int)S, l.per);
+  // Chunks: as long as the launch keeps 512 blocks, since every chunk costs a partial gradient (written and read
+  // again); whole turns of the block's waves.
   const int64_t strips = (need_db ? (a.n + 127) / 128 : 0) + (need_da ? (a.d + 127) / 128 : 0);
-  int64_t chunk = a.m * strips / 1024;
+  int64_t chunk = a.m * strips / 512;
   const int64_t least = 16 * a.r;  // a partial gradient is then at most a quarter of the data read
   if (chunk < least) chunk = least;
   if (chunk > 4096) chunk = 4096;
@@ -443,6 +514,20 @@ Layout layout_of(const AdapterArgs& a, bool need_dx, bool need_da, bool need_db)
   return l;
 }
 
+// a number near 0.62 n without a common divisor with n
+int64_t shuffle_of(int64_t n) {
+  int64_t p = n * 618 / 1000 | 1;
+  for (;; p += 2) {
+    int64_t a = n, b = p;
+    while (b) {
+      const int64_t t = a % b;
+      a = b;
+      b = t;
+    }
+    if (a == 1) return p;
+  }
+}
+
 struct FwdLayout {
   int64_t per;
   int splits, rp;
@@ -451,7 +536,7 @@ struct FwdLayout {
 FwdLayout fwd_layout(const AdapterArgs& a) {
   FwdLayout l{};
   l.rp = padded_rank(a.r);
-  l.splits = down_splits(a.m, a.d, a.ids ? a.S : 1, l.per);
+  l.splits = down_splits(a.m, a.d, a.r, a.ids ? a.S : 1, l.per);
   l.bytes = up256((size_t)l.splits * a.m * l.rp * 4);
   return l;
 }
@@ -470,7 +555,7 @@ hipError_t launch_adapter_fwd(const AdapterArgs& a, const void* base, void* Y, f
   Down dn{a.X, a.A, a.d, (int64_t)a.r * a.d, a.m, a.d, l.per, a.r, l.rp, S, l.splits, a.ids, a.drop, (float*)ws};
   const hipError_t e = launch_down(dn, a.dtype, s);
   if (e != hipSuccess) return e;
-  Up up{(const float*)ws, l.splits, l.rp, a.r, S, a.B, a.m, a.n, a.ids, a.scale, 1.f, base, Y, H, Dropout{0, nullptr}};
+  Up up{(const float*)ws, dn.splits, l.rp, a.r, S, a.B, a.m, a.n, a.ids, a.scale, 1.f, base, Y, H, Dropout{0, nullptr}};
   return launch_up(up, a.dtype, false, s);
 }
 
@@ -488,24 +573,28 @@ hipError_t launch_adapter_bwd(const AdapterArgs& a, const void* dY, const float*
   Chunk* chunks = a.ids ? (Chunk*)(w + l.chunks) : nullptr;
   Owner* owners = a.ids ? (Owner*)(w + l.owners) : nullptr;
   hipError_t e = hipSuccess;
-  if (dX || dA) {
-    uint16_t* turned = (uint16_t*)(w + l.turned);
-    hipLaunchKernelGGL(k_adapt_turn, dim3((unsigned)(l.ldt / 64), (unsigned)S), dim3(256), 0, s,
-                       (const uint16_t*)a.B, a.n, a.r, l.ldt, turned);
+  int splits = l.splits;  // left to add up
+  const bool dh = dX || dA, plan = (dA || dB) && a.ids;
+  uint16_t* turned = (uint16_t*)(w + l.turned);
+  if (dh || plan) {
+    const Plan p{a.ids, a.m, S, l.chunk, (int)l.max_chunks, plan ? S : 0, order, chunks, owners};
+    const Turn t{(const uint16_t*)a.B, a.n, l.ldt, a.r, turned};
+    const int64_t turns = dh ? l.ldt / 64 * S : 0;
+    const size_t counters = plan ? (size_t)S * 4 : 0, tile = dh ? (size_t)64 * (a.r + 2) * 2 : 0;
+    hipLaunchKernelGGL(k_adapt_prepare, dim3((unsigned)(p.blocks + turns)), dim3(PLAN_THREADS),
+                       counters > tile ? counters : tile, s, p, t);
     if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (dh) {
     Down dn{dY,  turned, l.ldt, a.r * l.ldt, a.m, a.n, l.per, a.r, l.rp, S, l.splits, a.ids, Dropout{0, nullptr},
             parts};
     if ((e = launch_down(dn, a.dtype, s)) != hipSuccess) return e;
+    splits = dn.splits;
   }
   if (dA || dB) {
-    if (a.ids) {
-      hipLaunchKernelGGL(k_adapt_plan, dim3((unsigned)S), dim3(PLAN_THREADS), (size_t)S * 4, s, a.ids, a.m, S, l.chunk,
-                         (int)l.max_chunks, order, chunks, owners);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
     const float inv = a.drop.threshold ? a.drop.inv() : 1.f;
     const Terms th{H, 1, a.r, 1.f, dB ? (uint32_t*)(w + l.terms_h) : nullptr};
-    const Terms td{parts, l.splits, l.rp, inv, dA ? (uint32_t*)(w + l.terms_dh) : nullptr};
+    const Terms td{parts, splits, l.rp, inv, dA ? (uint32_t*)(w + l.terms_dh) : nullptr};
     const int64_t threads = l.positions / STEP * 16 * l.rp16;
     hipLaunchKernelGGL(k_adapt_terms, dim3((unsigned)((threads + 255) / 256), 2), dim3(256), 0, s, th, td, a.ids,
                        a.scale, order, a.m, l.positions, a.r, l.rp16, S);
@@ -513,11 +602,12 @@ hipError_t launch_adapter_bwd(const AdapterArgs& a, const void* dY, const float*
     const Grad gb{dY, a.n, (const uint16_t*)(w + l.terms_h), dB, (float*)(w + l.part_b), Dropout{0, nullptr}, 0};
     const Grad ga{a.X, a.d, (const uint16_t*)(w + l.terms_dh), dA, (float*)(w + l.part_a), a.drop, 1};
     const int64_t sb = dB ? (a.n + 127) / 128 : 0, sa = dA ? (a.d + 127) / 128 : 0;
-    const GradGrid g{gb, ga, sb, order, chunks, a.m, l.chunk, a.r, l.rp16, accumulate, l.max_chunks == 1};
+    const int64_t blocks = (sb + sa) * l.max_chunks;
+    const GradGrid g{gb, ga, sb, sb + sa, shuffle_of(blocks), order, chunks, a.m, l.chunk, a.r, l.rp16, accumulate, l.max_chunks == 1};
     auto go = [&](auto t, auto rt, auto al) {
       constexpr int RT = decltype(rt)::value;
       hipLaunchKernelGGL((k_adapt_grad<typename decltype(t)::type, RT, decltype(al)::value>),
-                         dim3((unsigned)(sb + sa), (unsigned)l.max_chunks, (unsigned)((l.rp16 + 16 * RT - 1) / (16 * RT))),
+                         dim3((unsigned)blocks, (unsigned)((l.rp16 + 16 * RT - 1) / (16 * RT))),
                          dim3(64 * WAVES), 0, s, g);
       return hipGetLastError();
     };
@@ -542,7 +632,7 @@ hipError_t launch_adapter_bwd(const AdapterArgs& a, const void* dY, const float*
   }
   if (dX) {
     const float inv = a.drop.threshold ? a.drop.inv() : 1.f;
-    Up up{parts, l.splits, l.rp, a.r, S, a.A, a.m, a.d, a.ids, a.scale, inv, base_dx, dX, nullptr, a.drop};
+    Up up{parts, splits, l.rp, a.r, S, a.A, a.m, a.d, a.ids, a.scale, inv, base_dx, dX, nullptr, a.drop};
     if ((e = launch_up(up, a.dtype, true, s)) != hipSuccess) return e;
   }
   return hipSuccess;

@@ -23,15 +23,20 @@ __device__ __forceinline__ Philox philox_of(const int64_t* seed) {
   return Philox{(uint32_t)key, (uint32_t)(key >> 32), (uint32_t)stream, (uint32_t)(stream >> 32)};
 }
 
+// (one instruction; from a ^ b ^ c the compiler makes two)
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) {
+  return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96);
+}
+
 __device__ __forceinline__ u32x4 philox_block(const Philox& p, uint64_t block) {
   uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32), c2 = p.s0, c3 = p.s1;
   uint32_t k0 = p.k0, k1 = p.k1;
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t a = (uint64_t)0xD2511F53u * c0, b = (uint64_t)0xCD9E8D57u * c2;
-    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+    c0 = xor3((uint32_t)(b >> 32), c1, k0);
     c1 = (uint32_t)b;
-    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c2 = xor3((uint32_t)(a >> 32), c3, k1);
     c3 = (uint32_t)a;
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
@@ -45,10 +50,21 @@ __device__ __forceinline__ bool philox_stays(u32x4 u, int j, uint32_t threshold)
   return (j & 1 ? w >> 16 : w & 0xFFFFu) >= threshold;
 }
 
-// Two packed 16-bit values (2 j and 2 j + 1 of the block) with those that do not stay cleared
-__device__ __forceinline__ uint32_t philox_mask2(u32x4 u, int j, uint32_t threshold, uint32_t v) {
-  const uint32_t lo = (u[j] & 0xFFFFu) >= threshold ? v & 0xFFFFu : 0u;
-  return lo | ((u[j] >> 16) >= threshold ? v & 0xFFFF0000u : 0u);
+// The same for packed 16-bit values, in three packed instructions and an and: those that go are cleared.
+struct PhiloxMask {
+  uint32_t least;  // the threshold in both halves
+  uint32_t all;    // 0 where none stays (a threshold of 65536 has no 16 bits)
+};
+__device__ __forceinline__ PhiloxMask philox_mask_of(uint32_t threshold) {
+  return threshold < 65536u ? PhiloxMask{threshold * 0x00010001u, ~0u} : PhiloxMask{0u, 0u};
+}
+__device__ __forceinline__ uint32_t philox_mask2(uint32_t u, const PhiloxMask& m, uint32_t v) {
+  uint32_t t;
+  const uint32_t one = 0x00010001u;
+  asm("v_pk_sub_u16 %0, %1, %2 clamp" : "=v"(t) : "s"(m.least), "v"(u));  // 0 where u >= least
+  asm("v_pk_min_u16 %0, %1, %2" : "=v"(t) : "v"(t), "s"(one));
+  asm("v_pk_sub_u16 %0, %1, %2" : "=v"(t) : "v"(t), "s"(one));            // all bits, or none
+  return __builtin_amdgcn_bitop3_b32(t, v, m.all, 0x80);                  // and of the three
 }
 
 }  // namespace skm

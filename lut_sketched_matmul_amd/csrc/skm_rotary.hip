@@ -296,20 +296,23 @@ __global__ __launch_bounds__(THREADS) void k_rotary(RotaryGrid a) {
   }
 }
 
-// dw[c] (+)= sum over the blocks' rows; 16 threads a column, each every 16th row
+// dw[c] (+)= sum over the blocks' rows: four columns a block, 64 threads a column, each every 64th row
 __global__ __launch_bounds__(256) void k_rotary_reduce(const float* __restrict__ part, int rows, int dh, float* dqw,
                                                        float* dkw, int accumulate) {
-  __shared__ float sh[16][17];
-  const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
-  const int c = blockIdx.x * 16 + x, side = blockIdx.y;
+  __shared__ float sh[64][4];
+  const int x = threadIdx.x & 3, y = threadIdx.x >> 2;
+  const int c = blockIdx.x * 4 + x, side = blockIdx.y;
   float* out = side ? dkw : dqw;
   float t = 0.f;
-  if (c < dh)
-    for (int r = y; r < rows; r += 16) t += part[((int64_t)r * 2 + side) * dh + c];
+  if (c < dh) {
+#pragma unroll 8
+    for (int r = y; r < rows; r += 64) t += part[((int64_t)r * 2 + side) * dh + c];
+  }
   sh[y][x] = t;
   __syncthreads();
   if (y || c >= dh || !out) return;
-  for (int k = 1; k < 16; ++k) t += sh[k][x];
+  t = 0.f;
+  for (int k = 0; k < 64; ++k) t += sh[k][x];
   out[c] = accumulate ? out[c] + t : t;
 }
 
@@ -356,7 +359,7 @@ hipError_t rotary_t(const RotaryArgs& a, float* dqw, float* dkw, int accumulate,
     hipLaunchKernelGGL((k_rotary<T, V, L, NS, BWD>), dim3(g.gx, g.gy), dim3(THREADS), 0, s, r);
     hipError_t e = hipGetLastError();
     if (!BWD || e != hipSuccess || !part) return e;
-    hipLaunchKernelGGL(k_rotary_reduce, dim3((unsigned)((a.dh + 15) / 16), 2), dim3(256), 0, s, part,
+    hipLaunchKernelGGL(k_rotary_reduce, dim3((unsigned)((a.dh + 3) / 4), 2), dim3(256), 0, s, part,
                        (int)(g.gx * g.gy), a.dh, dqw, dkw, accumulate);
     return hipGetLastError();
   };
