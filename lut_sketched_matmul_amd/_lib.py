@@ -550,7 +550,7 @@ def _enter(stream, first, *others):
         if stream.device_index != index:
             raise ValueError(f"a stream of cuda:{stream.device_index} for tensors on cuda:{index}")
         context = torch.cuda.stream(stream)
-    elif torch.cuda.current_device() != index:
+    elif torch._C._cuda_getDevice() != index:
         context = torch.cuda.device(index)
     if context is not None:
         context.__enter__()
@@ -896,12 +896,16 @@ def sketch_xent_bwd(X, idx_packed, lut, targets, lse, dloss, b: int, gpr: int, i
 # dropout, low-rank adapters, norm and rotation of heads
 # --------------------------------------------------------------------------
 
-def _check_dropout(p: float, seed, size: str = "p"):
+# These calls are short on the device, so what is right is found in one expression; the checks one by one word the error.
+
+def _check_dropout(p: float, seed):
     if not 0.0 <= p <= 1.0:
-        raise ValueError(f"{size} = {p} is not a probability")
-    _expect(seed, "seed", shape=(2,), dtypes=("int64",))
-    if seed is None and p * 65536 + 0.5 >= 1.0:
-        raise ValueError("dropout needs a seed")
+        raise ValueError(f"p = {p} is not a probability")
+    if seed is None:
+        if p * 65536 + 0.5 >= 1.0:
+            raise ValueError("dropout needs a seed")
+    else:
+        _expect(seed, "seed", shape=(2,), dtypes=("int64",))
 
 
 def sketch_dropout(X, p: float, seed=None, residual=None, out=None, stream=None):
@@ -912,16 +916,18 @@ def sketch_dropout(X, p: float, seed=None, residual=None, out=None, stream=None)
     the gradient of X is the same call on the gradient.
     """
     torch = _torch()
-    _expect(X, "X", dtypes=_FLOAT_DTYPES)
+    dt, code = X.dtype, _dtype_codes.get(X.dtype)
+    if code is None:
+        _expect(X, "X", dtypes=_FLOAT_DTYPES)
     _check_dropout(p, seed)
-    name = (_dtype_name(X),)
-    _expect(residual, "residual", shape=X.shape, dtypes=name)
-    _expect(out, "out", shape=X.shape, dtypes=name)
+    for name, t in (("residual", residual), ("out", out)):
+        if t is not None and (t.dtype is not dt or t.shape != X.shape):
+            _expect(t, name, shape=X.shape, dtypes=(_dtype_name(X),))
     sp, context = _enter(stream, X, residual, seed, out)
     try:
         if out is None:
             out = torch.empty_like(X)
-        st = lib().sketch_dropout(_ptr(X), dtype_code(X), _ptr(residual), X.numel(), p, _ptr(seed), _ptr(out), sp)
+        st = lib().sketch_dropout(_ptr(X), code, _ptr(residual), X.numel(), p, _ptr(seed), _ptr(out), sp)
     finally:
         _leave(context)
     _check("sketch_dropout", st)
@@ -930,17 +936,23 @@ def sketch_dropout(X, p: float, seed=None, residual=None, out=None, stream=None)
 
 def _check_adapter(X, A, B, adapter, scale):
     """(m, n, d, r, n_adapters) of X [m, d], A [n_adapters, r, d], B [n_adapters, n, r] in one 16-bit dtype."""
+    torch = _torch()
     m, d = _matrix(X, "X")
     if A.dim() != 3 or B.dim() != 3:
         raise ValueError("A and B must have the adapters as the first of three dimensions")
-    S, r = A.shape[0], A.shape[1]
-    n = B.shape[1]
-    name = (_dtype_name(X),)
-    _expect(X, "X", dtypes=("float16", "bfloat16"))
-    _expect(A, "A", shape=(S, r, d), dtypes=name)
-    _expect(B, "B", shape=(S, n, r), dtypes=name)
-    _expect(adapter, "adapter", shape=(m,), dtypes=("int32",))
-    _expect(scale, "scale", shape=(S,), dtypes=("float32",))
+    S, r, da = A.shape
+    sb, n, rb = B.shape
+    dt = X.dtype
+    if not (da == d and sb == S and rb == r and A.dtype is dt and B.dtype is dt
+            and (dt is torch.float16 or dt is torch.bfloat16)
+            and (adapter is None or (adapter.dtype is torch.int32 and adapter.shape == (m,)))
+            and (scale is None or (scale.dtype is torch.float32 and scale.shape == (S,)))):
+        name = (_dtype_name(X),)
+        _expect(X, "X", dtypes=("float16", "bfloat16"))
+        _expect(A, "A", shape=(S, r, d), dtypes=name)
+        _expect(B, "B", shape=(S, n, r), dtypes=name)
+        _expect(adapter, "adapter", shape=(m,), dtypes=("int32",))
+        _expect(scale, "scale", shape=(S,), dtypes=("float32",))
     return m, n, d, r, S
 
 
@@ -961,10 +973,11 @@ def sketch_adapter_fwd(X, A, B, base=None, adapter=None, scale=None, p: float = 
     torch = _torch()
     m, n, d, r, S = _check_adapter(X, A, B, adapter, scale)
     _check_dropout(p, seed)
-    name = (_dtype_name(X),)
-    _expect(base, "base", shape=(m, n), dtypes=name)
-    _expect(out, "out", shape=(m, n), dtypes=name)
-    _expect(workspace, "workspace", dtypes=("uint8",))
+    for name, t in (("base", base), ("out", out)):
+        if t is not None and (t.dtype is not X.dtype or t.shape != (m, n)):
+            _expect(t, name, shape=(m, n), dtypes=(_dtype_name(X),))
+    if workspace is not None:
+        _expect(workspace, "workspace", dtypes=("uint8",))
     sp, context = _enter(stream, X, A, B, base, adapter, scale, seed, out, workspace)
     try:
         if out is None:
@@ -1042,13 +1055,12 @@ def _head_rows(t, name: str, like=None):
         return None, 0
     if t.dim() != 3:
         raise ValueError(f"{name} must have three dimensions (tokens, heads, columns), got {t.dim()}")
-    m, h, dh = t.shape
-    if like is not None:
+    if like is not None and (t.shape != like.shape or t.dtype is not like.dtype or t.get_device() != like.get_device()):
         _expect(t, name, shape=like.shape, dtypes=(_dtype_name(like),))
-        if t.get_device() != like.get_device():
-            raise ValueError(f"{name} must live where the heads do")
+        raise ValueError(f"{name} must live where the heads do")
     if not t.is_cuda:
         raise ValueError("tensors must live on the GPU")
+    m, h, dh = t.shape
     ld, sh, sc = t.stride()
     if (dh > 1 and sc != 1) or (h > 1 and sh != dh) or (m > 1 and ld < h * dh):
         raise ValueError(f"{name}: the heads of a token must lie side by side")
@@ -1056,27 +1068,51 @@ def _head_rows(t, name: str, like=None):
 
 
 def _check_rotary(q, k, positions, inv_freq, q_weight, k_weight, eps):
+    torch = _torch()
     qp, ldq = _head_rows(q, "q")
     m, hq, dh = q.shape
-    _expect(q, "q", dtypes=_FLOAT_DTYPES)
-    kp, ldk = _head_rows(k, "k")
-    hk = 0
+    dt, index = q.dtype, q.get_device()
+    kp, ldk, hk = None, 0, 0
     if k is not None:
+        kp, ldk = _head_rows(k, "k")
         hk = k.shape[1]
-        _expect(k, "k", shape=(m, hk, dh), dtypes=(_dtype_name(q),))
-        if k.get_device() != q.get_device():
+        if k.dtype is not dt or k.shape != (m, hk, dh):
+            _expect(k, "k", shape=(m, hk, dh), dtypes=(_dtype_name(q),))
+        if k.get_device() != index:
             raise ValueError("q and k must live on one GPU")
-    _expect(positions, "positions", shape=(m,), dtypes=("int64",))
-    _expect(inv_freq, "inv_freq", dtypes=("float64",))
+    if dt not in _dtype_codes:
+        _expect(q, "q", dtypes=_FLOAT_DTYPES)
+    if positions.dtype is not torch.int64 or positions.shape != (m,):
+        _expect(positions, "positions", shape=(m,), dtypes=("int64",))
+    if inv_freq.dtype is not torch.float64:
+        _expect(inv_freq, "inv_freq", dtypes=("float64",))
     if inv_freq.dim() != 1 or not 1 <= inv_freq.numel() <= dh // 2:
         raise ValueError(f"inv_freq must be a vector of 1 to {dh // 2} frequencies, got {tuple(inv_freq.shape)}")
-    if eps is None and (q_weight is not None or k_weight is not None):
-        raise ValueError("weights belong to a norm: give its eps")
-    _expect(q_weight, "q_weight", shape=(dh,), dtypes=("float32",))
-    _expect(k_weight, "k_weight", shape=(dh,), dtypes=("float32",))
-    if positions.get_device() != q.get_device():
+    if q_weight is not None or k_weight is not None:
+        if eps is None:
+            raise ValueError("weights belong to a norm: give its eps")
+        _expect(q_weight, "q_weight", shape=(dh,), dtypes=("float32",))
+        _expect(k_weight, "k_weight", shape=(dh,), dtypes=("float32",))
+    if positions.get_device() != index:
         raise ValueError("positions must live where the heads do")
     return m, hq, hk, dh, qp, ldq, kp, ldk
+
+
+def _head_outputs(q, k, q_out, k_out, m: int, hq: int, hk: int, dh: int):
+    """The outputs beside q and k (new ones where none are given) and their addresses and strides."""
+    if q_out is None:
+        q_out = q.new_empty((m, hq, dh))
+        qo, ldqo = q_out.data_ptr(), hq * dh
+    else:
+        qo, ldqo = _head_rows(q_out, "q_out", q)
+    ko, ldko = None, 0
+    if k is not None:
+        if k_out is None:
+            k_out = q.new_empty((m, hk, dh))
+            ko, ldko = k_out.data_ptr(), hk * dh
+        else:
+            ko, ldko = _head_rows(k_out, "k_out", k)
+    return q_out, k_out, qo, ldqo, ko, ldko
 
 
 def sketch_rotary_fwd(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: Optional[float] = None,
@@ -1095,12 +1131,7 @@ def sketch_rotary_fwd(q, k, positions, inv_freq, q_weight=None, k_weight=None, e
         raise ValueError("k_out without k")
     sp, context = _enter(stream, positions, inv_freq, q_weight, k_weight)
     try:
-        if q_out is None:
-            q_out = q.new_empty((m, hq, dh))
-        if k is not None and k_out is None:
-            k_out = q.new_empty((m, hk, dh))
-        qo, ldqo = _head_rows(q_out, "q_out", q)
-        ko, ldko = _head_rows(k_out, "k_out", k)
+        q_out, k_out, qo, ldqo, ko, ldko = _head_outputs(q, k, q_out, k_out, m, hq, hk, dh)
         st = lib().sketch_rotary_fwd(qp, ldq, hq, kp, ldk, hk, dtype_code(q), _ptr(positions), _ptr(inv_freq),
                                      _ptr(q_weight), _ptr(k_weight), m, dh, 2 * inv_freq.numel(), pc,
                                      0 if eps is None else 1, 0.0 if eps is None else eps, qo, ldqo, ko, ldko, sp)
@@ -1133,19 +1164,14 @@ def sketch_rotary_bwd(dq, dk, q, k, positions, inv_freq, q_weight=None, k_weight
         raise ValueError("weights belong to a norm: give its eps")
     dqp, lddq = _head_rows(dq, "dq", q)
     dkp, lddk = _head_rows(dk, "dk", k)
-    _expect(qw_out, "qw_out", shape=(dh,), dtypes=("float32",))
-    _expect(kw_out, "kw_out", shape=(dh,), dtypes=("float32",))
+    for name, t in (("qw_out", qw_out), ("kw_out", kw_out)):
+        _expect(t, name, shape=(dh,), dtypes=("float32",))
     _expect(workspace, "workspace", dtypes=("uint8",))
     need_dw = need_dw and eps is not None
     sp, context = _enter(stream, positions, inv_freq, q_weight, k_weight, qw_out, kw_out, workspace)
     try:
         dev = q.device
-        if q_out is None:
-            q_out = q.new_empty((m, hq, dh))
-        if k is not None and k_out is None:
-            k_out = q.new_empty((m, hk, dh))
-        qo, ldqo = _head_rows(q_out, "q_out", q)
-        ko, ldko = _head_rows(k_out, "k_out", k)
+        q_out, k_out, qo, ldqo, ko, ldko = _head_outputs(q, k, q_out, k_out, m, hq, hk, dh)
         dqw = dkw = ws = None
         if need_dw:
             dqw = _gradient(qw_out, (dh,), accumulate, dev)

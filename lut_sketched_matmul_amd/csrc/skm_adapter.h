@@ -159,6 +159,10 @@ struct Up {
 };
 hipError_t launch_up(const Up& a, int dtype, bool back, hipStream_t s);
 
+// the whole forward of a few tokens in one launch, without a workspace
+bool few_tokens(const AdapterArgs& a);
+hipError_t launch_few(const AdapterArgs& a, const void* base, void* Y, float* H, hipStream_t s);
+
 // ranks padded to whole groups of eight in the parts
 inline int padded_rank(int r) { return (r + 7) / 8 * 8; }
 

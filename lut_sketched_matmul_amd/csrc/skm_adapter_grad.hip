@@ -550,6 +550,7 @@ using namespace adapt;
 size_t adapter_fwd_bytes(const AdapterArgs& a) { return fwd_layout(a).bytes; }
 
 hipError_t launch_adapter_fwd(const AdapterArgs& a, const void* base, void* Y, float* H, void* ws, hipStream_t s) {
+  if (few_tokens(a)) return launch_few(a, base, Y, H, s);
   const FwdLayout l = fwd_layout(a);
   const int S = a.ids ? a.S : 1;
   Down dn{a.X, a.A, a.d, (int64_t)a.r * a.d, a.m, a.d, l.per, a.r, l.rp, S, l.splits, a.ids, a.drop, (float*)ws};

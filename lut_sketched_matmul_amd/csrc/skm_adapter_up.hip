@@ -200,6 +200,7 @@ __global__ __launch_bounds__(64 * WAVES, WT > 1 ? (KS < 4 ? 2 : 1) : (KS < 2 ? 2
     return true;
   };
   bool found = next();
+  if (WT == 1 && !found && zi != 0) return;  // (fewer adapters than blocks for them)
 
   if (a.H && group == 0 && zi == 0 && wave < WT) {
     for (int e = lane; e < 16 * a.r; e += 64) {
@@ -383,11 +384,12 @@ hipError_t launch_up(const Up& a, int dtype, bool back, hipStream_t s) {
     if (ready != hipSuccess) return ready;
     const int64_t tiles = (a.m + 16 * WT - 1) / (16 * WT);
     // Blocks: as many as run at once (two per CU), or twice that where they are many, then several chunks to a wave, whose
-    // operands serve all of them. A few tiles (decoding) may hold an adapter per token: a block for each. More
-    // tiles are requests of many tokens, and a block walks its tile's adapters.
+    // operands serve all of them. A few tiles (decoding) may hold an adapter per token: a block for each. Up to 256
+    // tokens may be some of both: four blocks (128 tokens with 64 adapters, 4096 -> 11008 at rank 16, 33 -> 26 us; 128
+    // of 8 requests 9.1 either way). More are requests of many tokens, and a block walks its tile's adapters.
     const int most = a.S < 16 * WT ? a.S : 16 * WT;
-    const int64_t Z = tiles <= 4 ? most : 1;
-    int64_t want = (tiles <= 4 ? 512 : 1024) / (tiles * Z);
+    const int64_t Z = tiles <= 4 ? most : (tiles > 16 ? 1 : (most < 4 ? most : 4));
+    int64_t want = tiles <= 4 ? 512 / (tiles * Z) : 1024 / tiles;
     if (want < 1) want = 1;
     const int64_t each = (chunks + WC * want - 1) / (WC * want);  // chunks of a wave
     const int64_t groups = (chunks + WC * each - 1) / (WC * each);

@@ -26,6 +26,7 @@ namespace skm {
 namespace {
 
 constexpr int THREADS = 256;
+constexpr int64_t kBwdBlocks = 768;  // of the backward at most: three per CU run at once (512 blocks: 46 us, 768: 44, 1024: 49)
 constexpr int MAX_TRIG = kMaxHeadDim / 2;  // (token, pair) angles a block holds
 
 // cos and sin of pos * freq
@@ -345,7 +346,7 @@ Plan plan_of(const RotaryArgs& a, int L, bool bwd) {
     gy = 512 / groups;
     if (gy > steps) gy = steps;
   }
-  const int64_t most = bwd ? (512 / gy > 1 ? 512 / gy : 1) : 65536;
+  const int64_t most = bwd ? (kBwdBlocks / gy > 1 ? kBwdBlocks / gy : 1) : 65536;
   return Plan{t, (unsigned)(groups < most ? groups : most), (unsigned)gy};
 }
 
@@ -386,8 +387,7 @@ hipError_t rotary_t(const RotaryArgs& a, float* dqw, float* dkw, int accumulate,
 
 }  // namespace
 
-// (blocks of the backward: at most 512 of any shape, see plan_of)
-size_t rotary_bwd_part_bytes(int64_t dh) { return (size_t)512 * 2 * (size_t)dh * 4; }
+size_t rotary_bwd_part_bytes(int64_t dh) { return (size_t)kBwdBlocks * 2 * (size_t)dh * 4; }
 
 hipError_t launch_rotary_fwd(const RotaryArgs& a, int x_dtype, hipStream_t s) {
   if (x_dtype == DT_F32) return rotary_t<float, false>(a, nullptr, nullptr, 0, nullptr, s);
