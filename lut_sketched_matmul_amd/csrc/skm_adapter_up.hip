@@ -388,8 +388,8 @@ hipError_t launch_up(const Up& a, int dtype, bool back, hipStream_t s) {
     // tokens may be some of both: four blocks (128 tokens with 64 adapters, 4096 -> 11008 at rank 16, 33 -> 26 us; 128
     // of 8 requests 9.1 either way). More are requests of many tokens, and a block walks its tile's adapters.
     const int most = a.S < 16 * WT ? a.S : 16 * WT;
-    const int64_t Z = tiles <= 4 ? most : (tiles > 16 ? 1 : (most < 4 ? most : 4));
-    int64_t want = tiles <= 4 ? 512 / (tiles * Z) : 1024 / tiles;
+    const int64_t Z = WT > 1 || tiles > 16 ? 1 : (tiles <= 4 || most < 4 ? most : 4);
+    int64_t want = WT == 1 && tiles <= 4 ? 512 / (tiles * Z) : 1024 / tiles;
     if (want < 1) want = 1;
     const int64_t each = (chunks + WC * want - 1) / (WC * want);  // chunks of a wave
     const int64_t groups = (chunks + WC * each - 1) / (WC * each);
