@@ -407,15 +407,17 @@ int sketch_dropout(const void* X, int x_dtype, const void* residual, int64_t cou
  * m <= 2^22, n <= 2^24, d a multiple of 32 and <= 2^20, m * n and m * d <= 2^34,
  * 1 <= r <= 128, 1 <= n_adapters <= 2^20. Pointers 16-byte aligned (adapter and
  * scale 4, seed 8); outputs must not overlap inputs or each other, except Y the
- * base. workspace: sketch_adapter_fwd_workspace(...) bytes; has_ids: whether
- * adapter is given. m == 0 is a no-op.
+ * base. workspace: sketch_adapter_fwd_workspace(...) bytes, NULL when that is 0;
+ * has_ids: whether adapter is given, has_dropout: whether p' > 0 (a few tokens
+ * without dropout need none). m == 0 is a no-op.
  */
 int sketch_adapter_fwd(const void* X, const void* A, const void* B, int dtype, const int32_t* adapter, int n_adapters,
                        const float* scale, const void* base, double p, const int64_t* seed, int64_t m, int64_t n,
                        int64_t d, int r, void* Y, float* H, void* workspace, size_t workspace_bytes,
                        hipStream_t stream);
 
-size_t sketch_adapter_fwd_workspace(int64_t m, int64_t n, int64_t d, int r, int n_adapters, int has_ids);
+size_t sketch_adapter_fwd_workspace(int64_t m, int64_t n, int64_t d, int r, int n_adapters, int has_ids,
+                                    int has_dropout);
 
 /*
  * Its backward pass, from the H it wrote and the same X, A, B, adapter, scale, p

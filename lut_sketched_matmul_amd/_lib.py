@@ -84,7 +84,7 @@ _SIGNATURES = {
     "sketch_dropout": (_c_int, [_c_vp, _c_int, _c_vp, _c_i64, ctypes.c_double, _c_vp, _c_vp, _c_vp]),
     "sketch_adapter_fwd": (_c_int, [_c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_int, _c_vp, _c_vp, ctypes.c_double, _c_vp,
                                     _c_i64, _c_i64, _c_i64, _c_int, _c_vp, _c_vp, _c_vp, _c_size, _c_vp]),
-    "sketch_adapter_fwd_workspace": (_c_size, [_c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int]),
+    "sketch_adapter_fwd_workspace": (_c_size, [_c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_int]),
     "sketch_adapter_bwd": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_int, _c_vp, _c_vp,
                                     ctypes.c_double, _c_vp, _c_i64, _c_i64, _c_i64, _c_int, _c_vp, _c_vp, _c_vp,
                                     _c_int, _c_vp, _c_size, _c_vp]),
@@ -956,9 +956,11 @@ def _check_adapter(X, A, B, adapter, scale):
     return m, n, d, r, S
 
 
-def sketch_adapter_fwd_workspace(m: int, n: int, d: int, r: int, n_adapters: int, has_ids: bool = True) -> int:
-    """Bytes of device workspace sketch_adapter_fwd needs for these sizes (has_ids: with a token's adapter given)."""
-    return int(lib().sketch_adapter_fwd_workspace(m, n, d, r, n_adapters, 1 if has_ids else 0))
+def sketch_adapter_fwd_workspace(m: int, n: int, d: int, r: int, n_adapters: int, has_ids: bool = True,
+                                 has_dropout: bool = True) -> int:
+    """Bytes of device workspace sketch_adapter_fwd needs for these sizes (has_ids: with a token's adapter given;
+    has_dropout: with p > 0; a few tokens without dropout need none)."""
+    return int(lib().sketch_adapter_fwd_workspace(m, n, d, r, n_adapters, 1 if has_ids else 0, 1 if has_dropout else 0))
 
 
 def sketch_adapter_fwd(X, A, B, base=None, adapter=None, scale=None, p: float = 0.0, seed=None, out=None,
@@ -983,7 +985,7 @@ def sketch_adapter_fwd(X, A, B, base=None, adapter=None, scale=None, p: float = 
         if out is None:
             out = X.new_empty((m, n))
         H = X.new_empty((m, r), dtype=torch.float32) if need_h else None
-        ws = _workspace(workspace, sketch_adapter_fwd_workspace(m, n, d, r, S, adapter is not None), X.device)
+        ws = _workspace(workspace, sketch_adapter_fwd_workspace(m, n, d, r, S, adapter is not None, p > 0.0), X.device)
         st = lib().sketch_adapter_fwd(_ptr(X), _ptr(A), _ptr(B), dtype_code(X), _ptr(adapter), S, _ptr(scale),
                                       _ptr(base), p, _ptr(seed), m, n, d, r, _ptr(out), _ptr(H), _ptr(ws), _size(ws),
                                       sp)

@@ -105,9 +105,12 @@ static skm::AdapterArgs adapter_sizes(int64_t m, int64_t n, int64_t d, int r, in
 
 constexpr int kMaxAdapters = 1 << 20;
 
-size_t sketch_adapter_fwd_workspace(int64_t m, int64_t n, int64_t d, int r, int n_adapters, int has_ids) {
+size_t sketch_adapter_fwd_workspace(int64_t m, int64_t n, int64_t d, int r, int n_adapters, int has_ids,
+                                    int has_dropout) {
   if (m < 1 || check_adapter(m, n, d, r, n_adapters, kMaxAdapters, SKM_F16) != SKM_OK) return 0;
-  return skm::adapter_fwd_bytes(adapter_sizes(m, n, d, r, n_adapters, has_ids));
+  skm::AdapterArgs a = adapter_sizes(m, n, d, r, n_adapters, has_ids);
+  a.drop.threshold = has_dropout ? 1 : 0;
+  return skm::adapter_fwd_bytes(a);
 }
 
 int sketch_adapter_fwd(const void* X, const void* A, const void* B, int dtype, const int32_t* adapter, int n_adapters,
@@ -123,10 +126,11 @@ int sketch_adapter_fwd(const void* X, const void* A, const void* B, int dtype, c
     if (!aligned16(q)) return SKM_EALIGN;
   if (((uintptr_t)adapter & 3u) || ((uintptr_t)scale & 3u) || ((uintptr_t)seed & 7u)) return SKM_EALIGN;
   if (m == 0) return SKM_OK;
-  const size_t need = sketch_adapter_fwd_workspace(m, n, d, r, n_adapters, adapter != nullptr);
-  if (workspace_bytes < need || !workspace) return SKM_EWORKSPACE;
+  const size_t need =
+      sketch_adapter_fwd_workspace(m, n, d, r, n_adapters, adapter != nullptr, drop.threshold != 0);
+  if (workspace_bytes < need || (need && !workspace)) return SKM_EWORKSPACE;
   const int64_t S = n_adapters;
-  const Range w[3] = {{Y, m * n * 2}, {H, m * r * 4}, {workspace, (int64_t)need}};
+  const Range w[3] = {{Y, m * n * 2}, {H, m * r * 4}, {need ? workspace : nullptr, (int64_t)need}};
   // (Y may be the base itself: an element is read before it is written, by the same lane)
   const Range in[7] = {{X, m * d * 2},     {A, S * r * d * 2}, {B, S * n * r * 2}, {adapter, m * 4},
                        {scale, S * 4},     {seed, 16},         {base == Y ? nullptr : base, m * n * 2}};

@@ -547,7 +547,7 @@ FwdLayout fwd_layout(const AdapterArgs& a) {
 
 using namespace adapt;
 
-size_t adapter_fwd_bytes(const AdapterArgs& a) { return fwd_layout(a).bytes; }
+size_t adapter_fwd_bytes(const AdapterArgs& a) { return few_tokens(a) ? 0 : fwd_layout(a).bytes; }
 
 hipError_t launch_adapter_fwd(const AdapterArgs& a, const void* base, void* Y, float* H, void* ws, hipStream_t s) {
   if (few_tokens(a)) return launch_few(a, base, Y, H, s);

@@ -274,7 +274,8 @@ class RotaryFunction(torch.autograd.Function):
     def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, eps, pairs: str):
         q, k = _heads(q), _heads(k)
         out = _lib.sketch_rotary_fwd(q, k, positions, inv_freq, q_weight, k_weight, eps=eps, pairs=pairs)
-        ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
+        kept = (q, k) if eps is not None else (None, None)  # (the rotation alone reads no heads going back)
+        ctx.save_for_backward(*kept, q_weight, k_weight, positions, inv_freq)
         ctx.eps, ctx.pairs = eps, pairs
         return out
 
@@ -282,7 +283,10 @@ class RotaryFunction(torch.autograd.Function):
     def backward(ctx, dq, dk):
         q, k, q_weight, k_weight, positions, inv_freq = ctx.saved_tensors
         need = ctx.needs_input_grad
-        out = _lib.sketch_rotary_bwd(_heads(dq), _heads(dk), q, k, positions, inv_freq, q_weight, k_weight, eps=ctx.eps,
+        dq, dk = _heads(dq), _heads(dk)
+        if ctx.eps is None:
+            q, k = dq, dk  # (not read, their shape and dtype are)
+        out = _lib.sketch_rotary_bwd(dq, dk, q, k, positions, inv_freq, q_weight, k_weight, eps=ctx.eps,
                                      pairs=ctx.pairs, need_dw=need[2] or need[3])
         return tuple(g if n else None for g, n in zip(out, need)) + (None,) * 4
 
@@ -298,7 +302,8 @@ class _Seed(torch.nn.Module):
     """A dropout's random numbers: a key and the number of the next mask, on the GPU and in the state dict.
 
     seed: the key (None = from torch's generator, so that modules differ and torch.manual_seed repeats them). The
-    number moves on in the stream's order, in replays of a captured step too.
+    number moves on in the stream's order, in replays of a captured step too. A forward that is run again (activation
+    recomputation) draws a new mask.
     """
 
     def __init__(self, seed: Optional[int], device):

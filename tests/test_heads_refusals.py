@@ -76,6 +76,10 @@ def test_adapter_forward_refusals(lib):
     assert afwd(lib, Y=addr(8)) == EALIAS and afwd(lib, H=addr(5)) == EALIAS
     assert afwd(lib, Y=addr(5) + 16) == EALIAS           # over the base, but not the base itself
     assert afwd(lib, m=0, X=None, Y=None, seed=None, ws=None, wsb=0) == 0
+    # a few tokens without dropout take none
+    assert skm.sketch_adapter_fwd_workspace(40, 50, 64, 8, 3, has_dropout=False) == 0
+    assert skm.sketch_adapter_fwd_workspace(400, 50, 64, 8, 3, has_dropout=False) >= 400 * 8 * 4
+    assert afwd(lib, m=400, p=0.0, seed=None, wsb=400 * 8 * 4 - 1) == EWS
     assert skm.sketch_adapter_fwd_workspace(40, 50, 48, 8, 3) == 0 and skm.sketch_adapter_fwd_workspace(0, 50, 64, 8, 3) == 0
 
 
