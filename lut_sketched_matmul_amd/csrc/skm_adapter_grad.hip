@@ -369,7 +369,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_adapt_grad(GradGrid a) {
   load_tokens(a, p0 + 8 * q, ch.end, t0);
   load_tokens(a, p0 + TURN + 8 * q, ch.end, t1);
   if (p0 < ch.end) load_rows<T, ALIGNED>(g, col, t0, x0);
-  if constexpr (RT == 1) {
+  if constexpr (RT == 1 && ALIGNED) {
     while (p0 < ch.end) {
       step(p0, x0, t0, x1, t1);
       p0 += TURN;
@@ -377,7 +377,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_adapt_grad(GradGrid a) {
       step(p0, x1, t1, x0, t0);
       p0 += TURN;
     }
-  } else {  // (two copies of the step do not fit the registers)
+  } else {  // (two copies of the step do not fit the registers, or leave them for two waves per SIMD instead of three)
     for (; p0 < ch.end; p0 += TURN) {
       step(p0, x0, t0, x1, t1);
 #pragma unroll
@@ -475,9 +475,11 @@ Layout layout_of(const AdapterArgs& a, bool need_dx, bool need_da, bool need_db)
   l.ldt = (a.n + 63) / 64 * 64;
   l.splits = down_splits(a.m, a.n, a.r, (int)S, l.per);
   // Chunks: as long as the launch keeps 512 blocks, since every chunk costs a partial gradient (written and read
-  // again); whole turns of the block's waves.
+  // again); whole turns of the block's waves. (8192 tokens, 4096 -> 4096, rank 16: 34.5 us, with 1024 blocks 37.5.)
+  // Several adapters' tokens do not come in whole chunks, and shorter ones even that out (4001 tokens, 4096 -> 4095,
+  // rank 12, 5 adapters: 1024 blocks 40 us, 512 48 to 56).
   const int64_t strips = (need_db ? (a.n + 127) / 128 : 0) + (need_da ? (a.d + 127) / 128 : 0);
-  int64_t chunk = a.m * strips / 512;
+  int64_t chunk = a.m * strips / (a.ids ? 1024 : 512);
   const int64_t least = 16 * a.r;  // a partial gradient is then at most a quarter of the data read
   if (chunk < least) chunk = least;
   if (chunk > 4096) chunk = 4096;
