@@ -139,6 +139,9 @@ __device__ __forceinline__ void put_some(const Up& a, int64_t at, int64_t count,
     }
 }
 
+// whether the groups come out even on eight XCDs
+__host__ __device__ __forceinline__ bool by_xcd(int64_t groups) { return groups % 8 == 0 || groups >= 32; }
+
 // WT: waves of a block along the tokens, 16 each, sharing the weights; the others along the columns.
 // WAL: rows of W aligned (forward: r % 8 == 0); ALIGNED: rows of base and out
 template <typename T, int KS, bool PACKED, int WT, bool BACK, bool DROP, bool WAL, bool ALIGNED>
@@ -148,9 +151,12 @@ __global__ __launch_bounds__(64 * WAVES, WT > 1 ? (KS < 4 ? 2 : 1) : (KS < 2 ? 2
   constexpr int RG = PACKED ? 2 : 4 * KS;     // groups of eight ranks
   constexpr int WC = WAVES / WT, BUFS = WT > 1 ? 2 : 1;
   const int lane = lane_id(), wave = threadIdx.x >> 6, row = lane & 15, q = lane >> 4;
-  // column groups go over the XCDs (blocks i, i + 8, .. run on one), all tiles of a group one after the other, so an
-  // XCD's L2 holds its columns of the weights
-  const int tile_at = (int)(blockIdx.x / 8) % tiles, group = (int)(blockIdx.x % 8) + (int)(blockIdx.x / 8) / tiles * 8;
+  // Column groups go over the XCDs (blocks i, i + 8, .. run on one) where that leaves none of them idle: all tiles of a
+  // group one after the other, so an XCD's L2 holds its columns of the weights. Else neighbouring blocks take a tile's
+  // groups.
+  const int at_x = (int)(blockIdx.x / 8);
+  const int tile_at = by_xcd(groups) ? at_x % tiles : (int)(blockIdx.x / groups);
+  const int group = by_xcd(groups) ? (int)(blockIdx.x % 8) + at_x / tiles * 8 : (int)(blockIdx.x % groups);
   if (group >= groups) return;
   const int64_t t0 = (int64_t)tile_at * (16 * WT);
   const int own = 16 * (wave % WT);  // this wave's tokens: t0 + own .. + 15
@@ -391,10 +397,12 @@ hipError_t launch_up(const Up& a, int dtype, bool back, hipStream_t s) {
     const int64_t Z = WT > 1 || tiles > 16 ? 1 : (tiles <= 4 || most < 4 ? most : 4);
     int64_t want = WT == 1 && tiles <= 4 ? 512 / (tiles * Z) : 1024 / tiles;
     if (want < 1) want = 1;
+    if (want > 8) want = want / 8 * 8;
     const int64_t each = (chunks + WC * want - 1) / (WC * want);  // chunks of a wave
     const int64_t groups = (chunks + WC * each - 1) / (WC * each);
-    hipLaunchKernelGGL(kern, dim3((unsigned)((groups + 7) / 8 * 8 * tiles), (unsigned)Z), dim3(64 * WAVES), lds, s, a,
-                       (int)Z, (int)tiles, (int)groups);
+    const int64_t blocks = (by_xcd(groups) ? (groups + 7) / 8 * 8 : groups) * tiles;
+    hipLaunchKernelGGL(kern, dim3((unsigned)blocks, (unsigned)Z), dim3(64 * WAVES), lds, s, a, (int)Z, (int)tiles,
+                       (int)groups);
     return hipGetLastError();
   };
   std::true_type yes;

@@ -162,7 +162,9 @@ def test_adapter_many_tokens(dt, n, r, ids, p):
 @pytest.mark.parametrize("dt,m,d,n,r,S,ids,p", [("bf16", 700, 2080, 520, 64, 70, "mixed", 0.0),
                                                 ("f16", 530, 4096, 264, 33, 5, "ragged", 0.1),
                                                 ("bf16", 513, 4096, 1001, 16, 600, "mixed", 0.0),
-                                                ("f16", 512, 1056, 300, 48, 9, "ragged", 0.0)])
+                                                ("f16", 512, 1056, 300, 48, 9, "ragged", 0.0),
+                                                ("bf16", 10007, 64, 2056, 16, 2, "ragged", 0.0),
+                                                ("f16", 33001, 32, 200, 24, 1, None, 0.0)])
 def test_adapter_ranges_and_many_adapters(dt, m, d, n, r, S, ids, p):
     """The contraction in several ranges, added up in between; a tile with an adapter per token."""
     check(case(d, m, d, n, r, S, dt, ids, p=p))
