@@ -7,7 +7,11 @@
 //
 // Few tokens are split along the contraction until the launch has about 512
 // blocks, and over the adapters: one token of 4096 columns is 16 blocks of 256
-// columns. The splits' sums are added by their reader, in order.
+// columns (3.3 us; 64 tokens with 64 adapters 6 us). The ranges' sums are added by
+// their reader, in order.
+//
+// Many tokens: 8192 x 4096, rank 16, 17.7 us (3.8 TB/s of a read that a copy's rate would do in 12), with dropout
+// 19.6; what is left is the start and the end of 512 blocks that all run at once.
 #include <type_traits>
 
 #include "skm_adapter.h"

@@ -14,6 +14,10 @@
 // from k_adapt_terms in the order the lanes want it. An adapter of one chunk
 // is written at once; the others' chunks are added up in order by
 // k_adapt_reduce (deterministic, no atomics).
+//
+// 8192 tokens, 4096 -> 4096, rank 16, bf16 with dropout: 33.5 us for the 134 MB of dY and X (4 TB/s), bound by the
+// vector ALU's share beside the loads (random numbers and turning: 40 % of its cycles) at two waves per SIMD; f16
+// rows of 4095 values 39 us for 65 MB, their conversions and split lines more.
 #include <type_traits>
 
 #include "skm_adapter.h"
@@ -606,7 +610,8 @@ hipError_t launch_adapter_bwd(const AdapterArgs& a, const void* dY, const float*
     const Grad ga{a.X, a.d, (const uint16_t*)(w + l.terms_dh), dA, (float*)(w + l.part_a), a.drop, 1};
     const int64_t sb = dB ? (a.n + 127) / 128 : 0, sa = dA ? (a.d + 127) / 128 : 0;
     const int64_t blocks = (sb + sa) * l.max_chunks;
-    const GradGrid g{gb, ga, sb, sb + sa, shuffle_of(blocks), order, chunks, a.m, l.chunk, a.r, l.rp16, accumulate, l.max_chunks == 1};
+    const GradGrid g{gb, ga, sb, sb + sa, shuffle_of(blocks), order, chunks, a.m,
+                     l.chunk, a.r, l.rp16, accumulate, l.max_chunks == 1};
     auto go = [&](auto t, auto rt, auto al) {
       constexpr int RT = decltype(rt)::value;
       hipLaunchKernelGGL((k_adapt_grad<typename decltype(t)::type, RT, decltype(al)::value>),

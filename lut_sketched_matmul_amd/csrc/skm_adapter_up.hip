@@ -8,8 +8,13 @@
 // rows of a group are read as they lie and turned in registers. B's columns (their
 // ranks are consecutive) go through LDS: read straight into operands, neighbouring
 // lanes are eight columns apart and every lane is an access of its own to the L1,
-// which bound the kernel (2048 tokens, 28672 columns, rank 64: 121 us). Read in
-// order and turned around in LDS, once for the block's four tiles of tokens, ...
+// which bound the kernel (2048 tokens, 28672 columns, rank 64, 8 adapters: 121 us). Read
+// in order and turned around in LDS, once for the block's four tiles of tokens, 84 us.
+//
+// Bound by memory and the latency that two waves per SIMD leave: 8192 x 4096, rank 16, 31 us for the 134 MB of
+// base and result (4.4 TB/s; a copy of them takes 26); dx with dropout 42 us for 201 MB (4.8 TB/s). With the base of
+// two chunks and the weights behind them on their way (256 registers) 36 and 47 us; three waves per SIMD (168
+// registers) 33 and 51. A tile on the border between two requests takes a pass for each.
 #include <type_traits>
 
 #include "skm_adapter.h"
@@ -144,8 +149,10 @@ __host__ __device__ __forceinline__ bool by_xcd(int64_t groups) { return groups 
 
 // WT: waves of a block along the tokens, 16 each, sharing the weights; the others along the columns.
 // WAL: rows of W aligned (forward: r % 8 == 0); ALIGNED: rows of base and out
+// Two waves per SIMD where the operands fit their registers, else one.
 template <typename T, int KS, bool PACKED, int WT, bool BACK, bool DROP, bool WAL, bool ALIGNED>
-__global__ __launch_bounds__(64 * WAVES, WT > 1 ? (KS < 4 ? 2 : 1) : (KS < 2 ? 2 : 1)) void k_adapt_up(Up a, int Z, int tiles, int groups) {
+__global__ __launch_bounds__(64 * WAVES, WT > 1 ? (KS < 4 ? 2 : 1) : (KS < 2 ? 2 : 1))
+void k_adapt_up(Up a, int Z, int tiles, int groups) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int NT = PACKED ? 1 : 2;          // instructions of a step
   constexpr int RG = PACKED ? 2 : 4 * KS;     // groups of eight ranks

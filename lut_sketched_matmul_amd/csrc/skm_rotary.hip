@@ -13,6 +13,10 @@
 // no exchange; a head's sums go over its 1 to 64 lanes. V = 8 (16-byte vectors of a
 // 16-bit type) where the heads and rows allow it, else V = 1.
 //
+// Bound by memory: 8192 tokens, 72 heads of 128, bf16 with norm 59 us (5.1 TB/s); backward of 4096 tokens, 64 heads,
+// f16, 44 us (4.6 TB/s) and 4.6 us for the blocks' sums; one token's 40 heads 5.3 us. Fetching the next heads early
+// measured the same or worse (59.8 and 48 us: more registers, fewer waves).
+//
 // The weight gradients: each block keeps its lanes' sums in registers over the
 // tokens it walks, adds them up in LDS, and k_rotary_reduce adds the blocks'
 // rows in block order (deterministic, no atomics).

@@ -241,11 +241,11 @@ class AdapterMatmulFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, X, lut_master, lut, idx_packed, b: int, gpr: int, A_master, B_master, A, B, ids, scale,
-                p: float, seed):
+                p: float, seed, back: bool):
         X = _packed(X)
         Y = _lib.sketch_matmul_fwd(X, idx_packed, lut, b, gpr)
         Y, H = _lib.sketch_adapter_fwd(X, A, B, Y, adapter=ids, scale=scale, p=p, seed=seed, out=Y,
-                                       need_h=ctx.needs_input_grad[7])
+                                       need_h=back and ctx.needs_input_grad[7])
         need = ctx.needs_input_grad
         ctx.save_for_backward(X if need[1] or need[6] else None, H, lut, idx_packed, A, B, ids, scale, seed)
         ctx.b, ctx.gpr, ctx.p, ctx.shape, ctx.dtype = b, gpr, p, X.shape, X.dtype
@@ -264,7 +264,7 @@ class AdapterMatmulFunction(torch.autograd.Function):
             X = dY.new_empty(ctx.shape)
         dX, dA, dB = _lib.sketch_adapter_bwd(dY, X, H, A, B, base_dx, adapter=ids, scale=scale, p=ctx.p, seed=seed,
                                              need_dx=need[0], need_da=need[6], need_db=need[7])
-        return (dX, dL, None, None, None, None, dA, dB) + (None,) * 6
+        return (dX, dL, None, None, None, None, dA, dB) + (None,) * 7
 
 
 class RotaryFunction(torch.autograd.Function):
@@ -514,9 +514,11 @@ class SketchedLinear(torch.nn.Module):
             a = self.adapter
             p, seed = a.arguments()
             X = X if self.norm is None else self.norm(X)
+            if adapter_ids is not None:
+                adapter_ids = adapter_ids.contiguous()
             return AdapterMatmulFunction.apply(X, self.lut_master, self.compute_tables(), self.idx_packed, self.b,
                                                self.gpr, a.A_master, a.B_master, a.A, a.B, adapter_ids, a.scale, p,
-                                               seed)
+                                               seed, torch.is_grad_enabled())
         if adapter_ids is not None:
             raise ValueError("adapter_ids for a layer without adapters")
         # (a function's needs_input_grad names parameters under no_grad too, where no backward will come)

@@ -196,6 +196,7 @@ def test_only_what_is_asked_for(calls):
     layer(X).float().sum().backward()                       # all frozen: neither X nor H is kept
     assert calls.log == [("adapter_fwd", 0.0, False, True), ("matmul_bwd", True, False), ("adapter_bwd", True, False, False)]
     calls.log.clear()
+    a.A_master.requires_grad_(True), a.B_master.requires_grad_(True)
     with torch.no_grad():
         layer(X)
     assert calls.log == [("adapter_fwd", 0.0, False, True)]

@@ -210,7 +210,8 @@ def test_binding_checks():
         a.update(bad)
         with pytest.raises(kind):
             skm.sketch_rotary_fwd(**a)
-    for bad, kind in ((dict(dq=t(4, 8, 32)), ValueError), (dict(dk=None), ValueError), (dict(dk=t(4, 2, 64, dtype=f32)), TypeError),
+    for bad, kind in ((dict(dq=t(4, 8, 32)), ValueError), (dict(dk=None), ValueError),
+                      (dict(dk=t(4, 2, 64, dtype=f32)), TypeError),
                       (dict(qw_out=w), ValueError), (dict(eps=1e-6, qw_out=t(64)), TypeError)):
         a = dict(dq=q, dk=k, q=q, k=k, positions=pos, inv_freq=f)
         a.update(bad)
