@@ -152,7 +152,7 @@ __host__ __device__ __forceinline__ bool by_xcd(int64_t groups) { return groups 
 // Two waves per SIMD where the operands fit their registers, else one.
 template <typename T, int KS, bool PACKED, int WT, bool BACK, bool DROP, bool WAL, bool ALIGNED>
 __global__ __launch_bounds__(64 * WAVES, WT > 1 ? (KS < 4 ? 2 : 1) : (KS < 2 ? 2 : 1))
-void k_adapt_up(Up a, int Z, int tiles, int groups) {
+void k_adapt_up(Up a, int Z, int tiles, int groups, int each) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int NT = PACKED ? 1 : 2;          // instructions of a step
   constexpr int RG = PACKED ? 2 : 4 * KS;     // groups of eight ranks
@@ -172,8 +172,10 @@ void k_adapt_up(Up a, int Z, int tiles, int groups) {
   const uint64_t any = tile.left;
   const uint64_t here = __ballot(lane < 16 * WT && t0 + lane < a.m);
 
-  const int64_t chunks = (a.N + 127) / 128;
-  const int64_t first = (int64_t)group * WC + wave / WT, step = (int64_t)groups * WC;
+  // a wave's chunks lie side by side: where rows start anywhere, neighbouring chunks share lines (4001 x 4095, f16,
+  // 34 -> 32 us)
+  const int64_t all = (a.N + 127) / 128, first = ((int64_t)group * WC + wave / WT) * each;
+  const int64_t chunks = first + each < all ? first + each : all;
   u32x4* lds = reinterpret_cast<u32x4*>(smem) + (wave / WT) * (BUFS * 128 * RG);
   const int stage_lane = lane + 64 * (wave % WT);
   const bool based = a.base && a.N >= 8;
@@ -299,14 +301,14 @@ void k_adapt_up(Up a, int Z, int tiles, int groups) {
       else __builtin_amdgcn_wave_barrier();
     }
     // (all waves of a block have the same chunks when they share the weights)
-    for (int64_t ch = first; ch < chunks; ch += step) {
-      const bool more = ch + step < chunks;
+    for (int64_t ch = first; ch < chunks; ++ch) {
+      const bool more = ch + 1 < chunks;
       const int64_t col = ch * 128 + 8 * row;
       const bool whole = col + 8 <= a.N;
       RawBase<BACK> b[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) b[c] = ahead[c];
-      if (AHEAD && more) weights.load(a, w, ch + step, stage_lane);
+      if (AHEAD && more) weights.load(a, w, ch + 1, stage_lane);
       if (works) {
         f32x4 acc[8];
 #pragma unroll
@@ -321,7 +323,7 @@ void k_adapt_up(Up a, int Z, int tiles, int groups) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = lds[buf * (128 * RG) + slot_of<RG>(e, grp, row)];
           }
-          if ((BACK || AHEAD) && s == KS - 1 && based && more) fetch(ch + step);
+          if ((BACK || AHEAD) && s == KS - 1 && based && more) fetch(ch + 1);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
 #pragma unroll
@@ -350,8 +352,8 @@ void k_adapt_up(Up a, int Z, int tiles, int groups) {
       } else if constexpr (!BACK) {
         __builtin_amdgcn_wave_barrier();
         if (more) {
-          if (!AHEAD) weights.load(a, w, ch + step, stage_lane);
-          if (!AHEAD && works && based) fetch(ch + step);
+          if (!AHEAD) weights.load(a, w, ch + 1, stage_lane);
+          if (!AHEAD && works && based) fetch(ch + 1);
           weights.store(a, lds, stage_lane);
         }
         __builtin_amdgcn_wave_barrier();
@@ -362,7 +364,7 @@ void k_adapt_up(Up a, int Z, int tiles, int groups) {
   // tokens without an adapter: the base alone
   const uint64_t rest = ((here & ~any) >> own) & 0xFFFFu;
   if (!rest || zi != 0 || (!BACK && a.base == a.out)) return;
-  for (int64_t ch = first; ch < chunks; ch += step) {
+  for (int64_t ch = first; ch < chunks; ++ch) {
     const int64_t col = ch * 128 + 8 * row;
     const float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -409,7 +411,7 @@ hipError_t launch_up(const Up& a, int dtype, bool back, hipStream_t s) {
     const int64_t groups = (chunks + WC * each - 1) / (WC * each);
     const int64_t blocks = (by_xcd(groups) ? (groups + 7) / 8 * 8 : groups) * tiles;
     hipLaunchKernelGGL(kern, dim3((unsigned)blocks, (unsigned)Z), dim3(64 * WAVES), lds, s, a, (int)Z, (int)tiles,
-                       (int)groups);
+                       (int)groups, (int)each);
     return hipGetLastError();
   };
   std::true_type yes;
