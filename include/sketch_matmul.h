@@ -429,8 +429,8 @@ size_t sketch_adapter_fwd_workspace(int64_t m, int64_t n, int64_t d, int r, int 
  * is all that reaches dX for tokens without an adapter; adapters without tokens get
  * zeros. accumulate == 1 adds to dA and dB. The sums over tokens are fp32 in a
  * fixed order (deterministic, no atomics) of products that keep 24 bits. X is read
- * for dA only, H for dB only (NULL otherwise). n_adapters <= 4096; everything else
- * as above. With m == 0 and accumulate == 0 dA and dB are written as zeros.
+ * for dA only, H for dB only (NULL otherwise). n_adapters <= 4096, and (n + d) / 128
+ * times (m / 128 + 1 + min(m, n_adapters)) below 2^24; everything else as above. With m == 0 and accumulate == 0 dA and dB are written as zeros.
  */
 int sketch_adapter_bwd(const void* dY, const void* X, const float* H, const void* A, const void* B, int dtype,
                        const int32_t* adapter, int n_adapters, const float* scale, const float* base_dx, double p,

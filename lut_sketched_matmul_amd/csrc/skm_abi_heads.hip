@@ -92,6 +92,15 @@ static int check_adapter(int64_t m, int64_t n, int64_t d, int r, int n_adapters,
   return dtype == SKM_F16 || dtype == SKM_BF16 ? SKM_OK : SKM_EUNSUPPORTED;
 }
 
+// its gradients' launch has a block of 256 threads per 128 columns of dY and X and chunk of tokens (of 128 at least,
+// and one per adapter), fewer than 2^32 threads in all
+static int check_adapter_bwd(int64_t m, int64_t n, int64_t d, int r, int n_adapters, int dtype) {
+  const int st = check_adapter(m, n, d, r, n_adapters, skm::kMaxGradAdapters, dtype);
+  if (st != SKM_OK) return st;
+  const int64_t strips = (n + 127) / 128 + (d + 127) / 128, chunks = m / 128 + 1 + (n_adapters < m ? n_adapters : m);
+  return strips * chunks < (int64_t(1) << 24) ? SKM_OK : SKM_EINVAL;
+}
+
 static skm::AdapterArgs adapter_sizes(int64_t m, int64_t n, int64_t d, int r, int n_adapters, int has_ids) {
   skm::AdapterArgs a{};
   a.m = m;
@@ -142,7 +151,7 @@ int sketch_adapter_fwd(const void* X, const void* A, const void* B, int dtype, c
 size_t sketch_adapter_bwd_workspace(int64_t m, int64_t n, int64_t d, int r, int n_adapters, int has_ids, int need_dx,
                                     int need_da, int need_db) {
   if (m < 1 || (!need_dx && !need_da && !need_db)) return 0;
-  if (check_adapter(m, n, d, r, n_adapters, skm::kMaxGradAdapters, SKM_F16) != SKM_OK) return 0;
+  if (check_adapter_bwd(m, n, d, r, n_adapters, SKM_F16) != SKM_OK) return 0;
   return skm::adapter_bwd_bytes(adapter_sizes(m, n, d, r, n_adapters, has_ids), need_dx != 0, need_da != 0,
                                 need_db != 0);
 }
@@ -151,7 +160,7 @@ int sketch_adapter_bwd(const void* dY, const void* X, const float* H, const void
                        const int32_t* adapter, int n_adapters, const float* scale, const float* base_dx, double p,
                        const int64_t* seed, int64_t m, int64_t n, int64_t d, int r, void* dX, float* dA, float* dB,
                        int accumulate, void* workspace, size_t workspace_bytes, hipStream_t stream) {
-  int st = check_adapter(m, n, d, r, n_adapters, skm::kMaxGradAdapters, dtype);
+  int st = check_adapter_bwd(m, n, d, r, n_adapters, dtype);
   if (st != SKM_OK) return st;
   skm::Dropout drop;
   if (!dropout_of(p, seed, drop) || (accumulate != 0 && accumulate != 1)) return SKM_EINVAL;

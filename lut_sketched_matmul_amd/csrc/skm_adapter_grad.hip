@@ -145,11 +145,13 @@ struct Turn {
   const uint16_t* B;
   int64_t n, ld;
   int r;
+  int64_t blocks;
   uint16_t* out;
 };
 __device__ __forceinline__ void turn_block(const Turn& a, int64_t block, uint16_t* tile) {
   const int64_t per = a.ld / 64, s = block / per, i0 = block % per * 64, n = a.n;
   const int r = a.r, ldt = r + 2;
+  __syncthreads();  // (an earlier tile is still read)
   const uint16_t* b = a.B + (s * n + i0) * r;
   const int rows = (int)(n - i0 < 64 ? n - i0 : 64);
   for (int e = threadIdx.x; e < 64 * r; e += PLAN_THREADS) {
@@ -168,7 +170,9 @@ __global__ __launch_bounds__(PLAN_THREADS) void k_adapt_prepare(Plan p, Turn t) 
   extern __shared__ __align__(16) unsigned char smem[];  // S counters, or a tile of B
   __shared__ int sh[PLAN_THREADS / 64], mine[3];
   if ((int64_t)blockIdx.x < p.blocks) plan_block(p, blockIdx.x, (int*)smem, sh, mine);
-  else turn_block(t, (int64_t)blockIdx.x - p.blocks, (uint16_t*)smem);
+  else
+    for (int64_t b = (int64_t)blockIdx.x - p.blocks; b < t.blocks; b += gridDim.x - p.blocks)
+      turn_block(t, b, (uint16_t*)smem);
 }
 
 // ---- operands --------------------------------------------------------------------
@@ -585,8 +589,8 @@ hipError_t launch_adapter_bwd(const AdapterArgs& a, const void* dY, const float*
   uint16_t* turned = (uint16_t*)(w + l.turned);
   if (dh || plan) {
     const Plan p{a.ids, a.m, S, l.chunk, (int)l.max_chunks, plan ? S : 0, order, chunks, owners};
-    const Turn t{(const uint16_t*)a.B, a.n, l.ldt, a.r, turned};
-    const int64_t turns = dh ? l.ldt / 64 * S : 0;
+    const Turn t{(const uint16_t*)a.B, a.n, l.ldt, a.r, dh ? l.ldt / 64 * S : 0, turned};
+    const int64_t most = int64_t(1) << 20, turns = t.blocks < most ? t.blocks : most;
     const size_t counters = plan ? (size_t)S * 4 : 0, tile = dh ? (size_t)64 * (a.r + 2) * 2 : 0;
     hipLaunchKernelGGL(k_adapt_prepare, dim3((unsigned)(p.blocks + turns)), dim3(PLAN_THREADS),
                        counters > tile ? counters : tile, s, p, t);

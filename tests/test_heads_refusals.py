@@ -85,6 +85,9 @@ def test_adapter_forward_refusals(lib):
 
 def test_adapter_backward_refusals(lib):
     assert abwd(lib, S=4097) == EINVAL and abwd(lib, acc=2) == EINVAL
+    assert abwd(lib, m=1024, n=1 << 24, S=512) == EINVAL     # more blocks than one launch takes
+    assert skm.sketch_adapter_bwd_workspace(1024, 1 << 24, 64, 8, 512) == 0
+    assert skm.sketch_adapter_bwd_workspace(1024, 1 << 24, 64, 8, 16) > 0
     assert abwd(lib, dY=None) == EINVAL and abwd(lib, H=None) == EINVAL
     need = skm.sketch_adapter_bwd_workspace(40, 50, 64, 8, 3)
     assert abwd(lib, wsb=need - 1) == EWS
