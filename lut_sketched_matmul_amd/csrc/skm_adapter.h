@@ -8,7 +8,7 @@
 // Everything is bound by memory from a few hundred tokens on (r is small beside
 // d and n) and by launches and latency below.
 //
-// Tokens are not sorted for the first four: a tile of 16 or 32 tokens walks the
+// Tokens are not sorted for the first four: a tile of 16 or 64 tokens walks the
 // distinct adapters among its tokens, multiplies all of its rows by each and
 // keeps the rows that are the adapter's. With requests one after the other a
 // tile has one or two; in a decode batch of different adapters each adapter's

@@ -1,6 +1,6 @@
 // The adapters' first product, h = A_s D(x) and dh = B_s^T dy (skm_adapter.h).
 //
-// A block takes 16 TT tokens, one range of the contraction and (of the distinct
+// A block takes 16 tokens, one range of the contraction and (of the distinct
 // adapters in the tile) every Z-th; its waves take turns over 64 columns of that
 // range and add up in LDS. Fragments come straight from memory, 16 bytes a
 // lane; with dropout each of X's fragments is one generator call.
@@ -22,19 +22,15 @@ namespace adapt {
 namespace {
 
 // P's and W's fragments of 64 columns from k on, and their products
-template <typename T, int TT, int RT, bool DROP, bool WHOLE, bool ALIGNED>
-__device__ __forceinline__ void down_chunk(const T* const (&p)[TT], const T* const (&w)[RT], const uint64_t (&block)[TT],
-                                           int64_t k, int64_t K, const Philox& g, const PhiloxMask& mask,
-                                           f32x4 (&acc)[TT][RT]) {
-  u32x4 x[2][TT], y[2][RT];
+template <typename T, int RT, bool DROP, bool WHOLE, bool ALIGNED>
+__device__ __forceinline__ void down_chunk(const T* p, const T* const (&w)[RT], uint64_t block, int64_t k, int64_t K,
+                                           const Philox& g, const PhiloxMask& mask, f32x4 (&acc)[RT]) {
+  u32x4 x[2], y[2][RT];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int64_t at = k + 32 * u;
-#pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      if constexpr (WHOLE) x[u][i] = ALIGNED ? *reinterpret_cast<const u32x4*>(p[i] + at) : load_any(p[i] + at);
-      else x[u][i] = load_some(p[i] + at, K - at);
-    }
+    if constexpr (WHOLE) x[u] = ALIGNED ? *reinterpret_cast<const u32x4*>(p + at) : load_any(p + at);
+    else x[u] = load_some(p + at, K - at);
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
       if constexpr (WHOLE) y[u][j] = *reinterpret_cast<const u32x4*>(w[j] + at);
@@ -44,42 +40,31 @@ __device__ __forceinline__ void down_chunk(const T* const (&p)[TT], const T* con
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     if constexpr (DROP) {
+      const u32x4 rnd = philox_block(g, block + (uint64_t)(k + 32 * u) / 8);
 #pragma unroll
-      for (int i = 0; i < TT; ++i) {
-        const u32x4 rnd = philox_block(g, block[i] + (uint64_t)(k + 32 * u) / 8);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[u][i][j] = philox_mask2(rnd[j], mask, x[u][i][j]);
-      }
+      for (int j = 0; j < 4; ++j) x[u][j] = philox_mask2(rnd[j], mask, x[u][j]);
     }
 #pragma unroll
-    for (int i = 0; i < TT; ++i)
-#pragma unroll
-      for (int j = 0; j < RT; ++j) acc[i][j] = mma<T>(x[u][i], y[u][j], acc[i][j]);
+    for (int j = 0; j < RT; ++j) acc[j] = mma<T>(x[u], y[u][j], acc[j]);
   }
 }
 
-template <typename T, int TT, int RT, bool DROP, bool ALIGNED>
+template <typename T, int RT, bool DROP, bool ALIGNED>
 __global__ __launch_bounds__(64 * WAVES) void k_adapt_down(Down a, int Z, float factor) {
   extern __shared__ __align__(16) unsigned char smem[];
-  f32x4* sums = reinterpret_cast<f32x4*>(smem);  // [WAVES][TT][RT][64]
+  f32x4* sums = reinterpret_cast<f32x4*>(smem);  // [WAVES][RT][64]
   const int lane = lane_id(), wave = threadIdx.x >> 6, row = lane & 15, q = lane >> 4;
-  const int64_t t0 = (int64_t)blockIdx.x * (16 * TT);
+  const int64_t t0 = (int64_t)blockIdx.x * 16;
   const int zi = blockIdx.z % Z, r0 = (blockIdx.z / Z) * (16 * RT);
   const int64_t kb = (int64_t)blockIdx.y * a.per;
   const int64_t ke = kb + a.per < a.K ? kb + a.per : a.K;
   const Philox g = DROP ? philox_of(a.drop.seed) : Philox{0u, 0u, 0u, 0u};
   const PhiloxMask mask = philox_mask_of(a.drop.threshold);
 
-  const T* p[TT];
-  uint64_t block[TT];
-#pragma unroll
-  for (int i = 0; i < TT; ++i) {
-    int64_t t = t0 + 16 * i + row;
-    if (t >= a.m) t = a.m - 1;  // (its row is not kept)
-    p[i] = (const T*)a.P + t * a.K + 8 * q;
-    block[i] = (uint64_t)(t * a.K) / 8 + q;
-  }
-  TileIds tile(a.ids, a.S, t0 + lane, lane < 16 * TT && t0 + lane < a.m);
+  const int64_t t = t0 + row < a.m ? t0 + row : a.m - 1;  // (a row past the last is not kept)
+  const T* p = (const T*)a.P + t * a.K + 8 * q;
+  const uint64_t block = (uint64_t)(t * a.K) / 8 + q;
+  TileIds tile(a.ids, a.S, t0 + lane, lane < 16 && t0 + lane < a.m);
   int adapter, turn = 0;
   uint64_t lanes;
   while (tile.next(adapter, lanes)) {
@@ -91,36 +76,30 @@ __global__ __launch_bounds__(64 * WAVES) void k_adapt_down(Down a, int Z, float 
       if (k >= a.r) k = a.r - 1;  // (its column is not kept)
       w[j] = (const T*)a.W + adapter * a.wstride + k * a.ldw + 8 * q;
     }
-    f32x4 acc[TT][RT];
+    f32x4 acc[RT];
 #pragma unroll
-    for (int i = 0; i < TT; ++i)
-#pragma unroll
-      for (int j = 0; j < RT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < RT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int64_t stride = 64 * WAVES;
     int64_t k = kb + 64 * wave;
     for (; k + 64 <= ke; k += stride)
-      down_chunk<T, TT, RT, DROP, true, ALIGNED>(p, w, block, k, a.K - 8 * q, g, mask, acc);
-    if (k < ke) down_chunk<T, TT, RT, DROP, false, ALIGNED>(p, w, block, k, a.K - 8 * q, g, mask, acc);
+      down_chunk<T, RT, DROP, true, ALIGNED>(p, w, block, k, a.K - 8 * q, g, mask, acc);
+    if (k < ke) down_chunk<T, RT, DROP, false, ALIGNED>(p, w, block, k, a.K - 8 * q, g, mask, acc);
 
     __syncthreads();  // (the last adapter's sums are still read)
 #pragma unroll
-    for (int i = 0; i < TT; ++i)
-#pragma unroll
-      for (int j = 0; j < RT; ++j) sums[((wave * TT + i) * RT + j) * 64 + lane] = acc[i][j];
+    for (int j = 0; j < RT; ++j) sums[(wave * RT + j) * 64 + lane] = acc[j];
     __syncthreads();
-    for (int e = threadIdx.x; e < TT * RT * 64; e += 64 * WAVES) {
+    for (int e = threadIdx.x; e < RT * 64; e += 64 * WAVES) {
       f32x4 v = sums[e];
 #pragma unroll
-      for (int x = 1; x < WAVES; ++x) v += sums[x * TT * RT * 64 + e];
-      const int l = e & 63, j = (e >> 6) % RT, i = (e >> 6) / RT;
-      const int k = r0 + 16 * j + (l & 15);
-      if (k < a.rp) {
+      for (int x = 1; x < WAVES; ++x) v += sums[x * RT * 64 + e];
+      const int l = e & 63, k2 = r0 + 16 * (e >> 6) + (l & 15);
+      if (k2 >= a.rp) continue;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int tk = 16 * i + 4 * (l >> 4) + c;
-          if ((lanes >> tk) & 1)
-            a.parts[((int64_t)blockIdx.y * a.m + t0 + tk) * a.rp + k] = k < a.r ? v[c] * factor : 0.f;
-        }
+      for (int c = 0; c < 4; ++c) {
+        const int tk = 4 * (l >> 4) + c;
+        if ((lanes >> tk) & 1)
+          a.parts[((int64_t)blockIdx.y * a.m + t0 + tk) * a.rp + k2] = k2 < a.r ? v[c] * factor : 0.f;
       }
     }
   }
@@ -399,7 +378,7 @@ hipError_t launch_down(Down& a, int dtype, hipStream_t s) {
                          factor);
       return hipGetLastError();
     }
-    hipLaunchKernelGGL((k_adapt_down<T, 1, RT, decltype(drop)::value, decltype(aligned)::value>),
+    hipLaunchKernelGGL((k_adapt_down<T, RT, decltype(drop)::value, decltype(aligned)::value>),
                        dim3((unsigned)tiles, (unsigned)a.splits, (unsigned)(Z * groups)), dim3(64 * WAVES),
                        WAVES * RT * 64 * 16, s, a, (int)Z, factor);
     return hipGetLastError();

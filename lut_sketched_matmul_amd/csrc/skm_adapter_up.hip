@@ -1,7 +1,7 @@
 // The adapters' second product, y = base + scale_s B_s h and
 // dx = base_dx + D'(A_s^T dh) (skm_adapter.h).
 //
-// A wave takes 16 TT tokens (the rows of the matrix instruction) and 128
+// A wave takes 16 tokens (the rows of the matrix instruction) and 128
 // columns at a time: column 8 c + e of the chunk is column c of instruction e, so a
 // lane ends with eight consecutive columns of four tokens, 16 lanes with 256
 // consecutive bytes of a row, and base and result move 16 bytes a lane. A's eight

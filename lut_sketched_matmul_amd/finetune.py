@@ -23,7 +23,8 @@ optimizer step); this module only marshals arguments. Three small torch
 operations remain in the glue: the fp32 input gradient is cast to the
 activations' dtype (autograd requires a gradient in its input's dtype),
 inputs and output gradients that are not contiguous or not aligned to 16 bytes
-are copied, and the gradient of a mean loss is multiplied by the tokens' weights.
+are copied, and the gradient of a mean loss is multiplied by the tokens' weights. A dropout's two whole numbers (key
+and number of the mask) are copied and counted on.
 """
 from __future__ import annotations
 
