@@ -28,6 +28,7 @@ and number of the mask) are copied and counted on.
 """
 from __future__ import annotations
 
+import threading
 from typing import Iterable, List, Optional, Sequence
 
 import torch
@@ -299,12 +300,45 @@ def _heads(t):
     return t.contiguous()
 
 
+_masks = threading.local()  # .stack: the contexts of replay_masks that this thread is in, innermost last
+
+
+class _Masks:
+    """One of the two contexts of :func:`replay_masks`: seeds that forwards draw in it are noted in order, or (replay)
+    handed out again from the first one. It may be left out of turn and from another thread: a checkpointed forward
+    that raises leaves it when its frame is collected."""
+
+    def __init__(self, drawn: list, replay: bool):
+        self.drawn, self.replay, self.open = drawn, replay, []
+
+    def __enter__(self):
+        stack = _masks.__dict__.setdefault("stack", [])
+        entry = [self.drawn, iter(self.drawn) if self.replay else None]
+        stack.append(entry)
+        self.open.append((stack, entry))
+
+    def __exit__(self, *exc):
+        stack, entry = self.open.pop()
+        stack[:] = [e for e in stack if e is not entry]
+
+
+def replay_masks():
+    """``context_fn=replay_masks`` of ``torch.utils.checkpoint.checkpoint(.., use_reentrant=False, ..)``: where a
+    forward with dropout is recomputed in the backward pass, it drops what it dropped the first time.
+
+    Without it such a recomputation is refused (it would draw other masks than the output had, whatever the state of
+    torch's generators), also with use_reentrant=True: there, draw the seed outside (``module.seed.next()``) and
+    hand it in as an argument of the checkpointed function, on to ``forward(.., seed=seed)``.
+    """
+    drawn = []
+    return _Masks(drawn, False), _Masks(drawn, True)
+
+
 class _Seed(torch.nn.Module):
     """A dropout's random numbers: a key and the number of the next mask, on the GPU and in the state dict.
 
     seed: the key (None = from torch's generator, so that modules differ and torch.manual_seed repeats them). The
-    number moves on in the stream's order, in replays of a captured step too. A forward that is run again (activation
-    recomputation) draws a new mask.
+    number moves on in the stream's order, in replays of a captured step too.
     """
 
     def __init__(self, seed: Optional[int], device):
@@ -314,8 +348,23 @@ class _Seed(torch.nn.Module):
 
     @torch.no_grad()
     def next(self):
-        seed = self.state.clone()
-        self.state[1:] += 1
+        """The seed of the next mask, int64 [2]; where :func:`replay_masks` runs a forward again, of the mask it had."""
+        seen, stack = [], _masks.__dict__.get("stack", ())
+        for drawn, again in reversed(stack):  # (checkpoints inside a recomputed function record what it replays)
+            if again is not None:
+                owner, seed = next(again, (None, None))
+                if owner is not self:
+                    raise RuntimeError("a recomputed forward went through other dropouts than the first time")
+                break
+            seen.append(drawn)
+        else:
+            if torch._C._current_graph_task_id() != -1:
+                raise RuntimeError("dropout in a forward that is recomputed in the backward pass: give checkpoint() "
+                                   "context_fn=replay_masks, or the forward its seed")
+            seed = self.state.clone()
+            self.state[1:] += 1
+        for drawn in seen:
+            drawn.append((self, seed))
         return seed
 
 
@@ -326,16 +375,20 @@ def _check_p(p: float) -> float:
 
 
 class SketchDropout(torch.nn.Module):
-    """residual + dropout(X) while training, residual + X else (the residual may be left out)."""
+    """residual + dropout(X) while training, residual + X else (the residual may be left out).
+
+    Every forward has the next mask, or that of `seed` (int64 [2] on the GPU, e.g. from ``module.seed.next()``). A
+    forward that is recomputed in the backward pass needs :func:`replay_masks` or its seed given.
+    """
 
     def __init__(self, p: float, seed: Optional[int] = None, device="cuda"):
         super().__init__()
         self.p = _check_p(p)
         self.seed = _Seed(seed, device)
 
-    def forward(self, X, residual=None):
+    def forward(self, X, residual=None, seed=None):
         if self.training and self.p > 0.0:
-            return DropoutFunction.apply(X, residual, self.p, self.seed.next())
+            return DropoutFunction.apply(X, residual, self.p, self.seed.next() if seed is None else seed)
         return X if residual is None else DropoutFunction.apply(X, residual, 0.0, None)
 
 
@@ -345,7 +398,8 @@ class SketchAdapter(torch.nn.Module):
     A [n_adapters, r, d] and B [n_adapters, n, r] are fp32 parameters with a 16-bit copy that the kernels read, as a
     layer's tables (trained by :class:`LutAdam` / :class:`LutSGD`, which refresh the copy). A starts uniform in
     +-1 / sqrt(d), B with zeros. scale: alpha / r for every adapter (alpha = r unless given). dropout: of the layer's
-    input in front of A, while training. compute_dtype must be the activations' dtype.
+    input in front of A, while training, with masks as :class:`SketchDropout` (a forward that is recomputed needs
+    :func:`replay_masks` or its seed given). compute_dtype must be the activations' dtype.
     """
 
     def __init__(self, n: int, d: int, r: int, n_adapters: int = 1, alpha: Optional[float] = None,
@@ -374,10 +428,12 @@ class SketchAdapter(torch.nn.Module):
         self.A.copy_(self.A_master.detach())
         self.B.copy_(self.B_master.detach())
 
-    def arguments(self):
-        """(p, seed) of this pass: dropout while training only."""
+    def arguments(self, seed=None):
+        """(p, seed) of this pass: dropout while training only, with the next mask unless its seed is given."""
         self._link_copies()
-        return (self.p, self.seed.next()) if self.training and self.p > 0.0 else (0.0, None)
+        if not self.training or self.p == 0.0:
+            return 0.0, None
+        return self.p, self.seed.next() if seed is None else seed
 
 
 class SketchRotary(torch.nn.Module):
@@ -463,8 +519,8 @@ class SketchedLinear(torch.nn.Module):
     (``lut_master.requires_grad_(False)``) checkpoint changes nothing.
 
     adapter: a :class:`SketchAdapter` whose products are added to the output; forward then takes the adapter of every
-    token too (int32 [m], outside [0, n_adapters) = none; left out: the first one). It reads the layer's input in full,
-    so it does not go with checkpoint.
+    token too (int32 [m], outside [0, n_adapters) = none; left out: the first one), and the seed of its dropout's mask
+    (left out: the next one). It reads the layer's input in full, so it does not go with checkpoint.
     """
 
     def __init__(self, idx_packed, lut, d: int, b: int, gpr: int, compute_dtype=torch.float16,
@@ -509,19 +565,19 @@ class SketchedLinear(torch.nn.Module):
         if self.lut is not None:
             self.lut.copy_(self.lut_master.detach())
 
-    def forward(self, X, adapter_ids=None):
+    def forward(self, X, adapter_ids=None, seed=None):
         self._link_copy()
         if self.adapter is not None:
             a = self.adapter
-            p, seed = a.arguments()
+            p, seed = a.arguments(seed)
             X = X if self.norm is None else self.norm(X)
             if adapter_ids is not None:
                 adapter_ids = adapter_ids.contiguous()
             return AdapterMatmulFunction.apply(X, self.lut_master, self.compute_tables(), self.idx_packed, self.b,
                                                self.gpr, a.A_master, a.B_master, a.A, a.B, adapter_ids, a.scale, p,
                                                seed, torch.is_grad_enabled())
-        if adapter_ids is not None:
-            raise ValueError("adapter_ids for a layer without adapters")
+        if adapter_ids is not None or seed is not None:
+            raise ValueError("adapter_ids or a seed for a layer without adapters")
         # (a function's needs_input_grad names parameters under no_grad too, where no backward will come)
         checkpoint = self.checkpoint and torch.is_grad_enabled()
         if self.norm is not None:
@@ -559,8 +615,8 @@ class GroupedSketchedLinear(torch.nn.Module):
         """The master tables of each projection (views into the shared parameter)."""
         return list(torch.split(self.inner.lut_master, self.sizes, 0))
 
-    def forward(self, X, adapter_ids=None):
-        Y = self.inner(X, adapter_ids)
+    def forward(self, X, adapter_ids=None, seed=None):
+        Y = self.inner(X, adapter_ids, seed)
         return tuple(torch.split(Y, self.sizes, dim=1))
 
 

@@ -627,3 +627,56 @@ def test_captured_layer_draws_new_masks():
             assert torch.equal(got, run_layer(parts, X, ids, pos))
             assert not any(torch.equal(got, o) for o in seen)
             seen.append(got)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_recomputed_layer_has_its_own_masks(captured):
+    """A layer whose activations are recomputed in the backward pass (there, by autograd's own thread) gives the output
+    and gradients of one that keeps them; without its masks the recomputation is refused."""
+    from torch.utils.checkpoint import checkpoint
+    from lut_sketched_matmul_amd import finetune
+    m, d = 70, 256
+    ids = torch.tensor(([0] * 30 + [1] * 25 + [-1] * 15), dtype=torch.int32, device="cuda")
+    pos = torch.cat([torch.arange(30), torch.arange(40)]).to("cuda")
+    dY = normal(gen(2), (m, d), 0.1, torch.bfloat16)
+
+    def both(around):
+        torch.manual_seed(11)
+        parts = layer_parts("bf16")
+        a, rot = parts[2], parts[3]
+        X = normal(gen(1), (m, d), 1.0, torch.bfloat16).requires_grad_()
+        leaves = [X, a.A_master, a.B_master, rot.q_weight, rot.k_weight]
+
+        def step():  # (two runs through one layer: masks 0 and 1 of its dropouts)
+            Y = around(lambda x: run_layer(parts, x, ids, pos), around(lambda x: run_layer(parts, x, ids, pos), X))
+            return [Y.detach(), *torch.autograd.grad(Y, leaves, dY)]
+
+        if not captured:
+            return [step()]
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            step()
+        torch.cuda.current_stream().wait_stream(s)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = step()
+        turns = []
+        for _ in range(3):
+            g.replay()
+            turns.append([t.clone() for t in out])
+            torch.cuda.synchronize()
+        return turns
+
+    def replayed(fn, X):
+        return checkpoint(fn, X, use_reentrant=False, preserve_rng_state=False, context_fn=finetune.replay_masks)
+
+    want, got = both(lambda fn, X: fn(X)), both(replayed)
+    for a, b in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    if captured:
+        assert not torch.equal(want[0][0], want[1][0])
+    else:
+        with pytest.raises(RuntimeError, match="recomputed"):
+            both(lambda fn, X: checkpoint(fn, X, use_reentrant=False))

@@ -1,7 +1,10 @@
 """The modules around adapters, dropout and head rotation, without a GPU: the library's calls are replaced by
 stand-ins that compute the same with torch and refuse what the library refuses."""
+import threading
+
 import pytest
 import torch
+from torch.utils.checkpoint import checkpoint
 
 from lut_sketched_matmul_amd import finetune
 
@@ -268,3 +271,110 @@ def test_refusals(calls):
                 dict(norm=True, q_weight=torch.ones(8)), dict(inv_freq=torch.ones(4), rot_dim=16)):
         with pytest.raises(ValueError):
             finetune.SketchRotary(16, device="cpu", **bad)
+
+
+# ---- activations that are computed again in the backward pass -------------------------------------------
+
+
+def dropping_parts():
+    """A run of an adapted layer with dropout in front, and a dropout used twice, all from the same seeds every time."""
+    n, d = 64, 64
+    idx, lut = sketch(n, d, 2, 1)
+    torch.manual_seed(3)
+    layer = finetune.SketchedLinear(idx, lut, d, 4, 2, compute_dtype=torch.bfloat16, adapter=adapter(n, d, 4, 2, p=0.3))
+    drop = finetune.SketchDropout(0.5, seed=9, device="cpu")
+    ids = torch.tensor([0, 1, -1, 1, 0], dtype=torch.int32)
+    return layer, drop, ids
+
+
+def step(parts, around, runs=1):
+    """(output, gradients) of layer -> dropout -> tanh -> dropout + residual, each run handed to `around(fn, X)`."""
+    layer, drop, ids = parts
+
+    def fn(X):
+        return drop(torch.tanh(drop(layer(X, ids))), X)
+
+    X = normal((5, 64), 2).bfloat16().requires_grad_()
+    Y = X
+    for _ in range(runs):
+        Y = around(fn, Y)
+    Y.backward(normal((5, 64), 4).bfloat16())
+    return [Y.detach(), X.grad, layer.adapter.A_master.grad, layer.adapter.B_master.grad, layer.lut_master.grad]
+
+
+def replayed(fn, X):
+    return checkpoint(fn, X, use_reentrant=False, context_fn=finetune.replay_masks)
+
+
+@pytest.mark.parametrize("around", [replayed, lambda fn, X: replayed(lambda x: replayed(fn, x), X)])
+@pytest.mark.parametrize("runs", [1, 3])
+def test_recomputed_forward_has_its_own_masks(calls, around, runs):
+    """Run again in the backward pass, once or in nested checkpoints, a forward has the masks that it had."""
+    want, got = (step(dropping_parts(), a, runs) for a in (lambda fn, X: fn(X), around))
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_recomputed_twice(calls):
+    """A graph that is kept and gone through again."""
+    drop = finetune.SketchDropout(0.5, seed=9, device="cpu")
+    X = normal((4, 32), 1).requires_grad_()
+    Y = replayed(lambda x: drop(torch.tanh(drop(x))), X)
+    one, = torch.autograd.grad(Y.sum(), X, retain_graph=True)
+    two, = torch.autograd.grad(Y.sum(), X)
+    assert torch.equal(one, two) and drop.seed.state.tolist() == [9, 2]
+
+
+@pytest.mark.parametrize("reentrant", [False, True])
+def test_recomputation_without_the_masks_is_refused(calls, reentrant):
+    """It would draw other masks than the output had."""
+    with pytest.raises(RuntimeError, match="recomputed"):
+        step(dropping_parts(), lambda fn, X: checkpoint(fn, X, use_reentrant=reentrant))
+    parts = dropping_parts()  # (nothing is drawn here)
+    parts[0].eval(), parts[1].eval()
+    step(parts, lambda fn, X: checkpoint(fn, X, use_reentrant=reentrant))
+
+
+@pytest.mark.parametrize("reentrant", [False, True])
+def test_masks_given_by_their_seeds(calls, reentrant):
+    layer, drop, ids = dropping_parts()
+    X = normal((5, 64), 2).bfloat16().requires_grad_()
+    dY = normal((5, 64), 4).bfloat16()
+    want = drop(layer(X, ids), X)
+    want.backward(dY)
+    first, X.grad = X.grad, None
+    layer, drop, ids = dropping_parts()
+
+    def fn(X, a, b):
+        return drop(layer(X, ids, seed=a), X, seed=b)
+
+    got = checkpoint(fn, X, layer.adapter.seed.next(), drop.seed.next(), use_reentrant=reentrant)
+    got.backward(dY)
+    assert torch.equal(got, want) and torch.equal(X.grad, first)
+    assert drop.seed.state.tolist() == [9, 1]
+    with pytest.raises(ValueError):
+        finetune.SketchedLinear(*sketch(64, 64, 2, 1), 64, 4, 2, compute_dtype=torch.bfloat16)(X, seed=drop.seed.next())
+
+
+def test_contexts_left_late_and_from_another_thread():
+    """A forward that raises leaves its context when it is collected: whenever, wherever."""
+    drop = finetune.SketchDropout(0.5, seed=9, device="cpu")
+    (a, again), (b, _) = finetune.replay_masks(), finetune.replay_masks()
+    a.__enter__()
+    one = drop.seed.next()
+    b.__enter__()
+    two = drop.seed.next()
+    t = threading.Thread(target=a.__exit__, args=(None, None, None))
+    t.start(), t.join()
+    three = drop.seed.next()
+    b.__exit__(None, None, None)
+    drop.seed.next()
+    assert [s.tolist() for _, s in a.drawn] == [one.tolist(), two.tolist()]
+    assert [s.tolist() for _, s in b.drawn] == [two.tolist(), three.tolist()]
+    for _ in range(2):
+        with again:
+            assert torch.equal(drop.seed.next(), one) and torch.equal(drop.seed.next(), two)
+            with pytest.raises(RuntimeError, match="other dropouts"):
+                drop.seed.next()
+    with again, pytest.raises(RuntimeError, match="other dropouts"):
+        finetune.SketchDropout(0.5, seed=9, device="cpu").seed.next()
+    assert drop.seed.next().tolist() == [9, 4]
