@@ -148,6 +148,7 @@ __device__ __forceinline__ void side_units(const RotaryGrid& a, const Side& p, i
   for (int i = 0; i < NS; ++i) {
     const int s = lane + L * i;
     slot_cols<V>(a, s < slots ? s : 0, c0[i], c1[i], turns[i]);
+    turns[i] = turns[i] && s < slots;  // (a lane behind the last slot has no angles)
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       w[i][0][j] = p.w ? p.w[c0[i] + j] : 1.f;

@@ -366,6 +366,14 @@ def test_rotary_wide_heads(dh, rot):
     rotary_check(dh, 7, 3, 0, dh, rot, "f32", 1e-6, "neighbours")
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("pairs", ["halves", "neighbours"])
+@pytest.mark.parametrize("dh,rot", [(528, 16), (1008, 32), (514, 2), (1022, 32), (80, 20), (96, 24)])
+def test_rotary_lanes_behind_a_wide_head(dh, rot, pairs, dt):
+    """Heads that leave lanes of their group idle, with so many tokens that a block holds the angles of several."""
+    rotary_check(dh + rot, 8200, 1, 1, dh, rot, dt, 1e-6, pairs)
+
+
 def test_rotary_many_tokens_and_no_weights():
     rotary_check(1, 4099, 8, 2, 128, 128, "bf16", 1e-5, "halves", weights=False, joined=False)
     rotary_check(2, 2500, 40, 10, 64, 64, "f16", 1e-5, "neighbours")
