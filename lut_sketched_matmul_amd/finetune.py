@@ -338,13 +338,18 @@ class _Seed(torch.nn.Module):
     """A dropout's random numbers: a key and the number of the next mask, on the GPU and in the state dict.
 
     seed: the key (None = from torch's generator, so that modules differ and torch.manual_seed repeats them). The
-    number moves on in the stream's order, in replays of a captured step too.
+    number moves on in the stream's order, in replays of a captured step too. A deep copy has a key of its own, from
+    torch's generator: layers that are copies of one must not drop the same values.
     """
 
     def __init__(self, seed: Optional[int], device):
         super().__init__()
         key = int(torch.randint(0, (1 << 63) - 1, ()).item()) if seed is None else int(seed)
         self.register_buffer("state", torch.tensor([key, 0], dtype=torch.int64, device=device))
+
+    def __deepcopy__(self, memo):
+        new = memo[id(self)] = type(self)(None, self.state.device)
+        return new.train(self.training)
 
     @torch.no_grad()
     def next(self):
@@ -378,7 +383,8 @@ class SketchDropout(torch.nn.Module):
     """residual + dropout(X) while training, residual + X else (the residual may be left out).
 
     Every forward has the next mask, or that of `seed` (int64 [2] on the GPU, e.g. from ``module.seed.next()``). A
-    forward that is recomputed in the backward pass needs :func:`replay_masks` or its seed given.
+    forward that is recomputed in the backward pass needs :func:`replay_masks` or its seed given. A deep copy has masks
+    of its own.
     """
 
     def __init__(self, p: float, seed: Optional[int] = None, device="cuda"):

@@ -1,5 +1,7 @@
 """The modules around adapters, dropout and head rotation, without a GPU: the library's calls are replaced by
 stand-ins that compute the same with torch and refuse what the library refuses."""
+import copy
+import pickle
 import threading
 
 import pytest
@@ -378,3 +380,22 @@ def test_contexts_left_late_and_from_another_thread():
     with again, pytest.raises(RuntimeError, match="other dropouts"):
         finetune.SketchDropout(0.5, seed=9, device="cpu").seed.next()
     assert drop.seed.next().tolist() == [9, 4]
+
+
+def test_copied_layers_have_keys_of_their_own(calls):
+    """Layers stacked as deep copies of one drop different values; a module shared within a copy stays shared."""
+    first = torch.nn.ModuleDict(dict(a=finetune.SketchDropout(0.5, seed=9, device="cpu"), ad=adapter(8, 64, 4, 1, p=0.1)))
+    first["b"] = first["a"]
+    first.eval()["a"].train()
+    torch.manual_seed(2)
+    second, third = copy.deepcopy(first), copy.deepcopy(first)
+    keys = {int(m["a"].seed.state[0]) for m in (first, second, third)} | {int(m["ad"].seed.state[0]) for m in (first, second, third)}
+    assert len(keys) == 6
+    assert second["a"] is second["b"] and second["a"].training and second["a"].seed.training and not second["ad"].seed.training
+    assert second["a"].seed.state.tolist()[1] == 0 and second["a"].seed.state.device == first["a"].seed.state.device
+    torch.manual_seed(2)
+    assert torch.equal(copy.deepcopy(first)["a"].seed.state, second["a"].seed.state)
+    X = torch.ones(4, 32)
+    assert not torch.equal(second["a"](X), third["a"](X))
+    again = pickle.loads(pickle.dumps(first))  # (saved and loaded it goes on where it was)
+    assert torch.equal(again["a"].seed.state, first["a"].seed.state)
