@@ -25,6 +25,8 @@ activations' dtype (autograd requires a gradient in its input's dtype),
 inputs and output gradients that are not contiguous or not aligned to 16 bytes
 are copied, and the gradient of a mean loss is multiplied by the tokens' weights. A dropout's two whole numbers (key
 and number of the mask) are copied and counted on.
+
+The library's gradients carry no graph, so a second derivative through them is refused.
 """
 from __future__ import annotations
 
@@ -32,6 +34,7 @@ import threading
 from typing import Iterable, List, Optional, Sequence
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 
@@ -61,6 +64,7 @@ class SketchMatmulFunction(torch.autograd.Function):
         return Y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         X, lut, idx_packed = ctx.saved_tensors
         need_dx, need_dlut = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
@@ -104,6 +108,7 @@ class CheckpointedMatmulFunction(torch.autograd.Function):
         return Y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         codes, scales, lut, idx_packed = ctx.saved_tensors
         dX, dL = _matmul_bwd(_check_dy(dY, ctx.dtype), codes, scales, idx_packed, lut, ctx)
@@ -132,6 +137,7 @@ class NormFunction(torch.autograd.Function):
         return Y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         X, weight, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -167,6 +173,7 @@ class NormMatmulFunction(torch.autograd.Function):
         return Y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         x0, x1, weight, mean, rstd, codes, scales, Xn, lut, idx_packed = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -196,6 +203,7 @@ class CrossEntropyFunction(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dloss):
         X, lut, idx_packed, targets, lse = ctx.saved_tensors
         need_dx, need_dlut = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
@@ -229,6 +237,7 @@ class DropoutFunction(torch.autograd.Function):
         return _lib.sketch_dropout(_packed(X), p, seed, residual=None if residual is None else _packed(residual))
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         (seed,) = ctx.saved_tensors
         dX = _lib.sketch_dropout(_packed(dY), ctx.p, seed) if ctx.needs_input_grad[0] else None
@@ -254,6 +263,7 @@ class AdapterMatmulFunction(torch.autograd.Function):
         return Y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         X, H, lut, idx_packed, A, B, ids, scale, seed = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -282,6 +292,7 @@ class RotaryFunction(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk):
         q, k, q_weight, k_weight, positions, inv_freq = ctx.saved_tensors
         need = ctx.needs_input_grad

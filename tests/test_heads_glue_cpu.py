@@ -399,3 +399,27 @@ def test_copied_layers_have_keys_of_their_own(calls):
     assert not torch.equal(second["a"](X), third["a"](X))
     again = pickle.loads(pickle.dumps(first))  # (saved and loaded it goes on where it was)
     assert torch.equal(again["a"].seed.state, first["a"].seed.state)
+
+
+@pytest.mark.parametrize("which", ["dropout", "adapter", "rotary", "matmul"])
+def test_second_derivatives_are_refused(calls, which, monkeypatch):
+    """The library's gradients carry no graph: a second derivative through them would miss its terms without a word."""
+    for name in dir(Calls):  # (as the library, the stand-ins then give tensors without a graph)
+        if name.startswith("sketch_"):
+            monkeypatch.setattr(finetune._lib, name, torch.no_grad()(getattr(calls, name)))
+    n = d = 64
+    idx, lut = sketch(n, d, 2, 1)
+    X = normal((5, d), 2).bfloat16().requires_grad_()
+    if which == "rotary":
+        rot = finetune.SketchRotary(16, norm=True, device="cpu")
+        run = lambda x: rot(x.unflatten(1, (4, 16)), None, torch.arange(5))[0].flatten(1)
+    elif which == "dropout":
+        run = finetune.SketchDropout(0.5, seed=1, device="cpu")
+    else:
+        run = finetune.SketchedLinear(idx, lut, d, 4, 2, compute_dtype=torch.bfloat16,
+                                      adapter=adapter(n, d, 4, 1) if which == "adapter" else None)
+    Y = run(X)
+    g, = torch.autograd.grad((Y * X).float().square().sum(), X, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.float().square().sum().backward()
+    run(X).float().square().sum().backward()  # (the first derivatives stay)
