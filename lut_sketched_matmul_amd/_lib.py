@@ -1009,10 +1009,16 @@ def sketch_adapter_bwd(dY, X, H, A, B, base_dx=None, adapter=None, scale=None, p
 
     dY [m, n] in X's dtype, H as the forward gave it (None if dB is not asked for), the other arguments the forward's.
     dX [m, d] in X's dtype is base_dx (fp32 [m, d], None = zeros) plus the adapters' part; dA, dB fp32 in the shapes
-    of A and B (da_out / db_out: optional outputs, accumulate=True adds to them).
+    of A and B (da_out / db_out: optional outputs, accumulate=True adds to them). At most 4096 adapters (the forward
+    takes 2^20), and (n / 128 + d / 128) (m / 128 + 1 + min(m, n_adapters)) blocks below 2^24.
     """
     torch = _torch()
     m, n, d, r, S = _check_adapter(X, A, B, adapter, scale)
+    if S > 4096:
+        raise ValueError(f"{S} adapters: a backward call takes at most 4096")
+    if (-(-n // 128) - (-d // 128)) * (m // 128 + 1 + min(m, S)) >= 1 << 24:
+        raise ValueError(f"{m} tokens of {S} adapters with {n} rows and {d} columns: a backward call takes less than 2^24 "
+                         "blocks of 128 rows or columns and 128 tokens or an adapter's")
     _check_dropout(p, seed)
     _expect(dY, "dY", shape=(m, n), dtypes=(_dtype_name(X),))
     if need_db and H is None:

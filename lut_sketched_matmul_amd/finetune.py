@@ -416,7 +416,8 @@ class SketchAdapter(torch.nn.Module):
     layer's tables (trained by :class:`LutAdam` / :class:`LutSGD`, which refresh the copy). A starts uniform in
     +-1 / sqrt(d), B with zeros. scale: alpha / r for every adapter (alpha = r unless given). dropout: of the layer's
     input in front of A, while training, with masks as :class:`SketchDropout` (a forward that is recomputed needs
-    :func:`replay_masks` or its seed given). compute_dtype must be the activations' dtype.
+    :func:`replay_masks` or its seed given). compute_dtype must be the activations' dtype. A backward pass takes at most
+    4096 adapters; the forward alone 2^20.
     """
 
     def __init__(self, n: int, d: int, r: int, n_adapters: int = 1, alpha: Optional[float] = None,

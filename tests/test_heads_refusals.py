@@ -222,3 +222,17 @@ def test_binding_checks():
             skm.sketch_rotary_bwd(**a)
     with pytest.raises(ValueError):
         skm.sketch_dropout(torch.zeros(8), 0.0)               # not on the GPU
+
+
+def meta(*shape, dtype=torch.bfloat16):
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+@pytest.mark.parametrize("m,n,d,r,S,word", [(5, 64, 64, 1, 4097, "4096"), (1024, 1 << 24, 64, 8, 512, "2\\^24")])
+def test_adapter_backward_names_its_limits(m, n, d, r, S, word):
+    """What the forward takes and the backward does not is refused with the reason, not with a bare status."""
+    args = (meta(m, n), meta(m, d), meta(m, r, dtype=torch.float32), meta(S, r, d), meta(S, n, r))
+    with pytest.raises(ValueError, match=word):
+        skm.sketch_adapter_bwd(*args)
+    with pytest.raises(ValueError, match="GPU"):  # (in range: the next check's)
+        skm.sketch_adapter_bwd(meta(m, 64), args[1], args[2], meta(4, r, d), meta(4, 64, r))
