@@ -54,6 +54,15 @@ template <> __device__ __forceinline__ f32x4 mma<bf16_t>(u32x4 a, u32x4 b, f32x4
 
 constexpr u32x4 kZero4 = {0u, 0u, 0u, 0u};
 
+// Between lanes of one wave that hand values to each other through LDS: what was stored before is there for every lane's
+// loads behind it. The hardware completes a wave's LDS operations in order, so this is no instruction; the fences say so
+// to the compiler, which may otherwise move a load before a store of another address.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // eight 16-bit values from any address of theirs
 template <typename T>
 __device__ __forceinline__ u32x4 load_any(const T* p) {

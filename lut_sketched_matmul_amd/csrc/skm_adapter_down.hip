@@ -179,7 +179,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_adapt_down_lds(Down a, float fac
     for (; k < ke; k += COLS * WAVES) {
       // (a wave's LDS operations complete in order: no barrier between its own)
       store(k);
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
       if (k + COLS * WAVES < ke) load(k + COLS * WAVES);
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
@@ -188,7 +188,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_adapt_down_lds(Down a, float fac
         for (int j = 0; j < RT; ++j)
           acc[j] = mma<T>(p, lds[256 + (16 * j + row) * 16 + ((4 * s + q) ^ row)], acc[j]);
       }
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
     }
     __syncthreads();
 #pragma unroll

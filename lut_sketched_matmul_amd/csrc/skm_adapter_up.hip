@@ -298,7 +298,7 @@ void k_adapt_up(Up a, int Z, int tiles, int groups, int each) {
     if constexpr (!BACK) {
       if (first < chunks) weights.store(a, lds + buf * (128 * RG), stage_lane);
       if (WT > 1) __syncthreads();
-      else __builtin_amdgcn_wave_barrier();
+      else wave_sync();
     }
     // (all waves of a block have the same chunks when they share the weights)
     for (int64_t ch = first; ch < chunks; ++ch) {
@@ -350,13 +350,13 @@ void k_adapt_up(Up a, int Z, int tiles, int groups, int each) {
         if (more) weights.store(a, lds + buf * (128 * RG), stage_lane);
         __syncthreads();
       } else if constexpr (!BACK) {
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
         if (more) {
           if (!AHEAD) weights.load(a, w, ch + 1, stage_lane);
           if (!AHEAD && works && based) fetch(ch + 1);
           weights.store(a, lds, stage_lane);
         }
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
       }
     }
     found = next();
