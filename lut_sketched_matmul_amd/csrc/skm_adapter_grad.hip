@@ -237,7 +237,6 @@ struct Grad {
 struct GradGrid {
   Grad b, a;            // dB, dA (columns 0 = not wanted)
   int64_t strips_b, strips;  // 128-column strips of dB, and of both
-  int64_t shuffle;
   const int32_t* order;
   const Chunk* chunks;  // NULL: chunk i is tokens [i chunk, (i + 1) chunk)
   int64_t m;
@@ -289,10 +288,7 @@ template <typename T, int RT, bool ALIGNED>
 __global__ __launch_bounds__(64 * WAVES) void k_adapt_grad(GradGrid a) {
   __shared__ __align__(16) f32x4 sums[WAVES][8][64];
   const int lane = lane_id(), wave = threadIdx.x >> 6, row = lane & 15, q = lane >> 4;
-  // dA's blocks draw random numbers and take longer: block i takes the work of i times a number without a common
-  // divisor with their count, so that every CU gets some of both
-  const int64_t work = (int64_t)blockIdx.x * a.shuffle % gridDim.x;
-  const int64_t strip = work % a.strips, chunk_at = work / a.strips;
+  const int64_t strip = (int64_t)blockIdx.x % a.strips, chunk_at = (int64_t)blockIdx.x / a.strips;
   const bool is_a = strip >= a.strips_b;
   const Grad& g = is_a ? a.a : a.b;
   const int64_t c0 = (strip - (is_a ? a.strips_b : 0)) * 128, col = c0 + 8 * row;
@@ -524,20 +520,6 @@ Layout layout_of(const AdapterArgs& a, bool need_dx, bool need_da, bool need_db)
   return l;
 }
 
-// a number near 0.62 n without a common divisor with n
-int64_t shuffle_of(int64_t n) {
-  int64_t p = n * 618 / 1000 | 1;
-  for (;; p += 2) {
-    int64_t a = n, b = p;
-    while (b) {
-      const int64_t t = a % b;
-      a = b;
-      b = t;
-    }
-    if (a == 1) return p;
-  }
-}
-
 struct FwdLayout {
   int64_t per;
   int splits, rp;
@@ -614,7 +596,7 @@ hipError_t launch_adapter_bwd(const AdapterArgs& a, const void* dY, const float*
     const Grad ga{a.X, a.d, (const uint16_t*)(w + l.terms_dh), dA, (float*)(w + l.part_a), a.drop, 1};
     const int64_t sb = dB ? (a.n + 127) / 128 : 0, sa = dA ? (a.d + 127) / 128 : 0;
     const int64_t blocks = (sb + sa) * l.max_chunks;
-    const GradGrid g{gb, ga, sb, sb + sa, shuffle_of(blocks), order, chunks, a.m,
+    const GradGrid g{gb, ga, sb, sb + sa, order, chunks, a.m,
                      l.chunk, a.r, l.rp16, accumulate, l.max_chunks == 1};
     auto go = [&](auto t, auto rt, auto al) {
       constexpr int RT = decltype(rt)::value;
