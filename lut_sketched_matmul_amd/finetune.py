@@ -538,7 +538,9 @@ class SketchedLinear(torch.nn.Module):
 
     adapter: a :class:`SketchAdapter` whose products are added to the output; forward then takes the adapter of every
     token too (int32 [m], outside [0, n_adapters) = none; left out: the first one), and the seed of its dropout's mask
-    (left out: the next one). It reads the layer's input in full, so it does not go with checkpoint.
+    (left out: the next one). It reads the layer's input in full, so it does not go with checkpoint. With a norm in front
+    as well, the normed input's gradient is rounded to the activations' dtype on its way to the norm's backward (the
+    adapters' backward sums it in fp32 and rounds once; without an adapter the norm takes it in fp32).
     """
 
     def __init__(self, idx_packed, lut, d: int, b: int, gpr: int, compute_dtype=torch.float16,
@@ -588,6 +590,7 @@ class SketchedLinear(torch.nn.Module):
         if self.adapter is not None:
             a = self.adapter
             p, seed = a.arguments(seed)
+            # (a function of its own: its backward takes the adapters' 16-bit dX, half a step of the activations' type)
             X = X if self.norm is None else self.norm(X)
             if adapter_ids is not None:
                 adapter_ids = adapter_ids.contiguous()

@@ -688,3 +688,55 @@ def test_recomputed_layer_has_its_own_masks(captured):
     else:
         with pytest.raises(RuntimeError, match="recomputed"):
             both(lambda fn, X: checkpoint(fn, X, use_reentrant=False))
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_norm_in_front_of_an_adapted_layer(dt, kind):
+    """norm -> projection + adapters, against the same in float64.
+
+    Norms of the whole. The normed input is rounded (in every gradient of a weight), its gradient once more before the
+    norm's backward, and each result: at most three half steps in a row. The norm's backward scales a row's error as
+    the row, its weights (1 +- 0.6) those of a column by up to 1.6 / 1: twice that, and a rest for fp32 sums.
+    """
+    from gpu_util import to_dev
+    from lut_sketched_matmul_amd import finetune as ft, sketch_dequant, synthetic as syn
+    m, n, d, r, S, eps = 90, 384, 256, 8, 2, 1e-5
+    idx = to_dev(syn.random_packed_indices("normed/i", n, d, 4), "u8")
+    lut = to_dev(syn.random_lut("normed/l", n, 2, 4, 0.05, "f16"), "f16").to(T[dt])
+    g = gen(1)
+    a = ft.SketchAdapter(n, d, r, S, dropout=0.1, compute_dtype=T[dt], seed=3)
+    with torch.no_grad():
+        a.A_master.copy_(torch.randn(a.A_master.shape, generator=g, device="cuda") / 16)
+        a.B_master.copy_(torch.randn(a.B_master.shape, generator=g, device="cuda") / 16)
+    a.refresh_copies()
+    norm = ft.SketchNorm(d, kind=kind, eps=eps)
+    with torch.no_grad():
+        norm.weight += 0.6 * (2 * torch.rand(d, generator=g, device="cuda") - 1)
+    layer = ft.SketchedLinear(idx, lut, d, 4, 2, compute_dtype=T[dt], norm=norm, adapter=a)
+    X = normal(g, (m, d), 2.0, T[dt]).requires_grad_()
+    ids = torch.arange(m, device="cuda", dtype=torch.int32) % 3  # (2 is no adapter)
+    dY = normal(g, (m, n), 0.1, T[dt])
+    Y = layer(X, ids)
+    Y.backward(dY)
+
+    x, w, A, B = (t.detach().double().requires_grad_() for t in (X, norm.weight, a.A, a.B))
+    W = sketch_dequant(layer.idx_packed, layer.lut, d, 4, 2).double().requires_grad_()
+    c = x - x.mean(1, keepdim=True) if kind == "layer" else x
+    xn = c / torch.sqrt((c * c).mean(1, keepdim=True) + eps) * w
+    z = xn * hu.multiplier((m, d), 0.1, [3, 0], "cuda")
+    on = [(ids == s).double()[:, None] for s in range(S)]
+    want = xn @ W.T + sum(on[s] * ((z @ A[s].T) @ B[s].T) for s in range(S))
+    want.backward(dY.double())
+    code = sketch_codes(layer.idx_packed)
+    dL = torch.zeros(n, 2, 16, device="cuda", dtype=torch.float64).scatter_add_(2, code.reshape(n, 2, d // 2),
+                                                                            W.grad.reshape(n, 2, d // 2))
+    pairs = [(Y, want), (X.grad, x.grad), (norm.weight.grad, w.grad), (a.A_master.grad, A.grad),
+             (a.B_master.grad, B.grad), (layer.lut_master.grad, dL)]
+    for got, ref in pairs:
+        assert float((got.detach().double() - ref.detach()).norm()) <= 8 * hu.U[T[dt]] * float(ref.detach().norm())
+
+
+def sketch_codes(idx):
+    """The 4-bit indices [n, d] of packed rows."""
+    return torch.stack([idx & 15, idx >> 4], 2).reshape(idx.shape[0], -1).long()
