@@ -1,17 +1,25 @@
 // The adapters' first product, h = A_s D(x) and dh = B_s^T dy (skm_adapter.h).
 //
-// A block takes 16 tokens, one range of the contraction and (of the distinct
-// adapters in the tile) every Z-th; its waves take turns over 64 columns of that
-// range and add up in LDS. Fragments come straight from memory, 16 bytes a
-// lane; with dropout each of X's fragments is one generator call.
+// Three kernels, a wave with 16 tokens in each:
+//   k_adapt_down        up to kManyTokens tokens. A block takes 16 tokens, one range
+//                       of the contraction and (of the distinct adapters in the tile)
+//                       every Z-th; its waves take turns over 64 columns of that range
+//                       and add up in LDS. Fragments come straight from memory, 16
+//                       bytes a lane.
+//   k_adapt_down_lds    more tokens, ranks up to kSharedRank: the same tile, 128 columns
+//                       at a time through LDS of the wave's own.
+//   k_adapt_down_tiles  more tokens and ranks: 64 tokens a block, whose waves share
+//                       the weights in LDS.
+// With dropout each of X's fragments is one generator call.
 //
 // Few tokens are split along the contraction until the launch has about 512
-// blocks, and over the adapters: one token of 4096 columns is 16 blocks of 256
-// columns (3.3 us; 64 tokens with 64 adapters 6 us). The ranges' sums are added by
-// their reader, in order.
+// blocks, and over the adapters: 64 tokens of 4096 columns with 64 adapters are 8
+// ranges and 16 blocks for a tile's adapters, 5.8 us. (Most calls of a few tokens
+// with rank <= 32 and no dropout do not come here: skm_adapter_few.hip.) The ranges'
+// sums are added by their reader, in order.
 //
-// Many tokens: 8192 x 4096, rank 16, 17.7 us (3.8 TB/s of a read that a copy's rate would do in 12), with dropout
-// 19.6; what is left is the start and the end of 512 blocks that all run at once.
+// Many tokens: 8192 x 4096, rank 16, 18.4 us (3.7 TB/s of a read that a copy's rate would do in 12), with dropout
+// 19.8; what is left is the start and the end of 512 blocks that all run at once.
 #include <type_traits>
 
 #include "skm_adapter.h"

@@ -2,7 +2,7 @@
 // dA_s = sum_t dh_t D(x_t)^T over the tokens of adapter s (skm_adapter.h), and
 // the calls that order all of the adapters' kernels.
 //
-// Positions. k_adapt_plan lists every adapter's tokens in order, each list
+// Positions. k_adapt_prepare lists every adapter's tokens in order, each list
 // padded to whole steps of 32 positions (-1) and cut into chunks of at most
 // `chunk` tokens. Without ids the list is the tokens themselves.
 //
@@ -15,7 +15,7 @@
 // is written at once; the others' chunks are added up in order by
 // k_adapt_reduce (deterministic, no atomics).
 //
-// 8192 tokens, 4096 -> 4096, rank 16, bf16 with dropout: 33.5 us for the 134 MB of dY and X (4 TB/s), bound by the
+// 8192 tokens, 4096 -> 4096, rank 16, bf16 with dropout: 34 us for the 134 MB of dY and X (4 TB/s), bound by the
 // vector ALU's share beside the loads (random numbers and turning: 40 % of its cycles) at two waves per SIMD; f16
 // rows of 4095 values 39 us for 65 MB, their conversions and split lines more.
 #include <type_traits>
@@ -479,9 +479,9 @@ Layout layout_of(const AdapterArgs& a, bool need_dx, bool need_da, bool need_db)
   l.ldt = (a.n + 63) / 64 * 64;
   l.splits = down_splits(a.m, a.n, a.r, (int)S, l.per);
   // Chunks: as long as the launch keeps 512 blocks, since every chunk costs a partial gradient (written and read
-  // again); whole turns of the block's waves. (8192 tokens, 4096 -> 4096, rank 16: 34.5 us, with 1024 blocks 37.5.)
+  // again); whole turns of the block's waves. (8192 tokens, 4096 -> 4096, rank 16: 34 us, with 1024 blocks 36.5.)
   // Several adapters' tokens do not come in whole chunks, and shorter ones even that out (4001 tokens, 4096 -> 4095,
-  // rank 12, 5 adapters: 1024 blocks 40 us, 512 48 to 56).
+  // rank 12, 5 adapters: 1024 blocks 39 us, 512 54).
   const int64_t strips = (need_db ? (a.n + 127) / 128 : 0) + (need_da ? (a.d + 127) / 128 : 0);
   int64_t chunk = a.m * strips / (a.ids ? 1024 : 512);
   const int64_t least = 16 * a.r;  // a partial gradient is then at most a quarter of the data read
